@@ -16,12 +16,13 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libhisa.so")
 
 HISA_OK, HISA_EINVAL, HISA_EDTYPE, HISA_EWORKSPACE, HISA_ECUDA, HISA_EDEVICE = 0, -1, -2, -3, -4, -5
-HISA_F32, HISA_BF16 = 0, 1
+HISA_F32, HISA_BF16, HISA_E4M3 = 0, 1, 2
+ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN = range(3)
 FLAG_CHAINED = 0x1
 DEV_BAD_OFFSETS, DEV_GATE, DEV_BAD_ID, DEV_NONFINITE, DEV_BAD_BLOCK, DEV_TIMEOUT = \
     0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 FLAT_NOALLOC_MAX_SCORES = 1 << 22
-OP_COMPRESS = 6
+OP_COMPRESS, OP_PREFIX_ATTEND = 6, 7
 OP_INDEX_SCORES, OP_BLOCK_MEANS, OP_BLOCK_FILTER, OP_SELECT_TOPK, OP_FLAT_TOPK, OP_SPARSE_ATTEND = \
     range(6)
 
@@ -58,6 +59,38 @@ class CompressDesc(ctypes.Structure):
                 ("means_rows", ctypes.c_int64), ("flags", ctypes.c_int32)]
 
 
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("scale_group", ctypes.c_int32), ("scale_pow2", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("flags", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_res", ctypes.c_int64),
+                ("ld_out", ctypes.c_int64)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("rope_dims", ctypes.c_int32), ("kind", ctypes.c_int32), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("orig_len", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("heads", ctypes.c_int32), ("heads2", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("rope_dims", ctypes.c_int32), ("rope_first", ctypes.c_int32),
+                ("half", ctypes.c_int32), ("inverse", ctypes.c_int32), ("src_dtype", ctypes.c_int32),
+                ("dst_dtype", ctypes.c_int32), ("mscale", ctypes.c_float), ("flags", ctypes.c_int32),
+                ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64), ("y_token", ctypes.c_int64),
+                ("y_head", ctypes.c_int64), ("x2_token", ctypes.c_int64), ("x2_head", ctypes.c_int64),
+                ("y2_token", ctypes.c_int64), ("y2_head", ctypes.c_int64)]
+
+
+class PrefixDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("L", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("Dh", ctypes.c_int32), ("window", ctypes.c_int32), ("W_max", ctypes.c_int32),
+                ("r", ctypes.c_int32), ("flags", ctypes.c_int32), ("prefix_rows", ctypes.c_int64),
+                ("Np_max", ctypes.c_int64), ("kv_rows", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("q_dtype", ctypes.c_int32), ("kv_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
 _lib = None
 _lock = threading.Lock()
 _P = ctypes.c_void_p
@@ -75,6 +108,10 @@ _SIG = {
     "hisa_flat_topk_noalloc": (ctypes.c_int32, [_P] * 9),
     "hisa_sparse_attend": (ctypes.c_int32, [_P] * 12 + [ctypes.c_size_t, _P]),
     "hisa_compress_append": (ctypes.c_int32, [_P] * 13 + [ctypes.c_size_t, _P]),
+    "hisa_rms_norm": (ctypes.c_int32, [_P] * 8),
+    "hisa_rope_table": (ctypes.c_int32, [_P] * 2),
+    "hisa_rope": (ctypes.c_int32, [_P] * 8),
+    "hisa_prefix_attend": (ctypes.c_int32, [_P] * 12 + [ctypes.c_size_t, _P]),
 }
 
 
@@ -225,6 +262,37 @@ def compress_append(desc, kv, gate, tok_off, p_first, n_new, ape, norm_w, keys, 
                                       _ptr(keys), _ptr(key_off), _ptr(means), _ptr(means_off),
                                       _ptr(ws), ws.numel(), _stream(stream)),
            "hisa_compress_append")
+
+
+# ----------------------------------------------------------------------------
+# around the step
+# ----------------------------------------------------------------------------
+def rms_norm(desc, x, residual, w, residual_out, out, scales=None, stream=None):
+    _check(lib().hisa_rms_norm(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(w),
+                               _ptr(residual_out), _ptr(out), _ptr(scales), _stream(stream)),
+           "hisa_rms_norm")
+
+
+def rope_table(scaling, device="cuda"):
+    """The frequency table of hisa_rope as an int64 tensor on `device` (the uint64 bit patterns)."""
+    import torch
+    host = np.zeros(max(int(scaling.rope_dims), 0) // 2, dtype=np.uint64)
+    _check(lib().hisa_rope_table(ctypes.byref(scaling), ctypes.c_void_p(host.ctypes.data)),
+           "hisa_rope_table")
+    return torch.from_numpy(host.view(np.int64)).to(device)
+
+
+def rope(desc, table, pos, x, y, x2=None, y2=None, stream=None):
+    _check(lib().hisa_rope(ctypes.byref(desc), _ptr(table), _ptr(pos), _ptr(x), _ptr(y), _ptr(x2),
+                           _ptr(y2), _stream(stream)), "hisa_rope")
+
+
+def prefix_attend(desc, q, local_kv, local_len, local_pos0, prefix_kv, pooled_kv, kv_off, sinks, t0,
+                  out, ws, stream=None):
+    _check(lib().hisa_prefix_attend(ctypes.byref(desc), _ptr(q), _ptr(local_kv), _ptr(local_len),
+                                    _ptr(local_pos0), _ptr(prefix_kv), _ptr(pooled_kv), _ptr(kv_off),
+                                    _ptr(sinks), _ptr(t0), _ptr(out), _ptr(ws), ws.numel(),
+                                    _stream(stream)), "hisa_prefix_attend")
 
 
 # ----------------------------------------------------------------------------

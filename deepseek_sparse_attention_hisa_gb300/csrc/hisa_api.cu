@@ -4,6 +4,7 @@
 #include <cstring>
 
 #include "hisa_internal.cuh"
+#include "ops_internal.cuh"
 
 using namespace hisa;
 
@@ -252,6 +253,7 @@ size_t hisa_workspace_bytes(int32_t op, const void *desc) {
     if (op == HISA_OP_COMPRESS)
         return check_compress_desc(static_cast<const hisa_compress_desc *>(desc)) == HISA_OK
                    ? kStatusBytes : 0;
+    if (op == HISA_OP_PREFIX_ATTEND) return prefix_workspace_bytes(static_cast<const hisa_prefix_desc *>(desc));
     if (op == HISA_OP_SPARSE_ATTEND) {
         const hisa_attn_desc *d = static_cast<const hisa_attn_desc *>(desc);
         if (check_attn_desc(d) != HISA_OK) return 0;

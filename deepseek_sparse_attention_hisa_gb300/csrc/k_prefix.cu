@@ -1,0 +1,268 @@
+// Shared-prefix combine: the CUDA-core segments and the merge of all segments.
+//
+// One softmax over  [local window | P shared rows | own pooled rows | sink]  per query row and
+// head, K = V. Its statistics join over disjoint sets of rows: a segment s with logits z_i and
+// rows v_i keeps m_s = max z_i, l_s = sum e^{z_i - m_s}, O_s = sum e^{z_i - m_s} v_i, and
+//   M = max(max_s m_s, sink),  out = sum_s e^{m_s - M} O_s / (sum_s e^{m_s - M} l_s + e^{sink - M}).
+// So the shared rows, which every query row of the batch sees whole, become segments whose query
+// rows are stacked across sequences (one staged chunk of shared rows serves R stacked rows),
+// and the local and own rows become segments of one query row each.
+//
+// The kernel here: R query rows x 32 list rows per chunk, 16 threads per row group, scores and
+// sums in f32 registers, the running maximum and sum per row (a rescale per chunk). Bound by the
+// FMA pipe and its shared-memory operands.
+#include "ops_internal.cuh"
+
+namespace hisa {
+namespace {
+
+constexpr int kChunk = 32;
+
+template <int R, int DH>
+struct Smem {
+    static constexpr int kStride = DH + 4;               // floats per staged row: 16 bytes of pad
+    static constexpr size_t bytes = (size_t)((R + kChunk) * kStride + R * (kChunk + 1)) * sizeof(float);
+};
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p) {
+    if constexpr (sizeof(T) == 4) {
+        return *reinterpret_cast<const float4 *>(p);
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                           __uint_as_float(u.y & 0xffff0000u));
+    }
+}
+
+// The visible part of query row q's own list: local rows [lo, lo + nloc) of its window buffer,
+// then own pooled rows [0, nown).
+struct Tail {
+    int64_t lo, nloc, k0, nown;
+};
+__device__ __forceinline__ Tail tail_of(const PrefixParams &p, int row, bool report) {
+    const int b = row / p.L, j = row - b * p.L;
+    const int64_t t = (int64_t)p.t0[b] + j;
+    Tail x{0, 0, 0, 0};
+    int64_t nl = p.W_max > 0 ? p.local_len[b] : 0;
+    nl = nl < 0 ? 0 : (nl > p.W_max ? p.W_max : nl);
+    if (nl > 0) {
+        const int64_t pos0 = p.local_pos0[b];
+        int64_t lo = t - p.window + 1 - pos0, hi = t - pos0 + 1;
+        lo = lo < 0 ? 0 : lo;
+        hi = hi > nl ? nl : hi;
+        x.lo = lo;
+        x.nloc = hi > lo ? hi - lo : 0;
+    }
+    if (p.Np_max > 0) {
+        if (seq_ok(p.kv_off, b, p.Np_max, p.kv_rows)) {
+            x.k0 = p.kv_off[b];
+            x.nown = p.kv_off[b + 1] - x.k0;
+            if (p.L > 1) {
+                const int64_t v = visible_len(t, p.r, p.P + x.nown) - p.P;
+                x.nown = v < 0 ? 0 : (v < x.nown ? v : x.nown);
+            }
+        } else if (report) {
+            flag(p.status, HISA_DEV_BAD_OFFSETS);
+        }
+    }
+    return x;
+}
+
+// One item: R stacked query rows (shared rows) or the R = H heads of one query row (its own
+// list), and one segment of the list. TR x 16 threads; thread (tr, tc) owns rows tr + TR i,
+// scores of chunk rows tc + 16 j, and dims 4 tc + 64 j of the sums.
+template <int R, int DH, typename T>
+__global__ void __launch_bounds__((R < 16 ? R : 16) * 16) k_prefix_simt(PrefixParams p, int tail) {
+    using S = Smem<R, DH>;
+    constexpr int TR = R < 16 ? R : 16, RP = R / TR, NT = TR * 16, DJ = DH / 64;
+    extern __shared__ __align__(16) float sm[];
+    float *sq = sm, *skv = sq + R * S::kStride, *sp = skv + kChunk * S::kStride;
+    const int tid = threadIdx.x, tr = tid / 16, tc = tid % 16;
+    const int seg = blockIdx.y;
+    const int64_t rows = (int64_t)p.B * p.L * p.H;
+    const int64_t g0 = (int64_t)blockIdx.x * R;
+    grid_dep_wait();
+    Tail x{0, 0, 0, 0};
+    int64_t e0, e1;
+    if (tail) {
+        x = tail_of(p, blockIdx.x, seg == 0 && tid == 0);
+        e0 = (int64_t)seg * p.tail_rows;
+        e1 = e0 + p.tail_rows;
+        const int64_t n = x.nloc + x.nown;
+        e1 = e1 < n ? e1 : n;
+    } else {
+        e0 = (int64_t)seg * p.pre_rows;
+        e1 = e0 + p.pre_rows;
+        e1 = e1 < p.P ? e1 : p.P;
+    }
+    const T *q = static_cast<const T *>(p.q);
+    for (int i = tid; i < R * (DH / 4); i += NT) {
+        const int r = i / (DH / 4), d = (i % (DH / 4)) * 4;
+        const float4 v = g0 + r < rows ? load4(q + (g0 + r) * DH + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(sq + r * S::kStride + d) = v;
+    }
+    const int b = tail ? (int)blockIdx.x / p.L : 0;
+    const T *loc = static_cast<const T *>(p.local_kv) + ((int64_t)b * p.W_max + x.lo) * DH;
+    const T *own = static_cast<const T *>(p.pooled_kv) + x.k0 * DH;
+    const T *pre = static_cast<const T *>(p.prefix_kv);
+
+    float4 acc[RP][DJ];
+    float m[RP], l[RP];
+#pragma unroll
+    for (int i = 0; i < RP; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < DJ; ++j) acc[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int64_t c0 = e0; c0 < e1; c0 += kChunk) {
+        __syncthreads();                                  // the previous chunk has been read
+        for (int i = tid; i < kChunk * (DH / 4); i += NT) {
+            const int r = i / (DH / 4), d = (i % (DH / 4)) * 4;
+            const int64_t e = c0 + r;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (e < e1) v = load4((tail ? (e < x.nloc ? loc + e * DH : own + (e - x.nloc) * DH) : pre + e * DH) + d);
+            *reinterpret_cast<float4 *>(skv + r * S::kStride + d) = v;
+        }
+        __syncthreads();
+        float s[RP][2];
+#pragma unroll
+        for (int i = 0; i < RP; ++i) s[i][0] = s[i][1] = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < DH; d += 4) {
+            const float4 k0 = *reinterpret_cast<const float4 *>(skv + tc * S::kStride + d);
+            const float4 k1 = *reinterpret_cast<const float4 *>(skv + (tc + 16) * S::kStride + d);
+#pragma unroll
+            for (int i = 0; i < RP; ++i) {
+                const float4 a = *reinterpret_cast<const float4 *>(sq + (tr + TR * i) * S::kStride + d);
+                s[i][0] += a.x * k0.x + a.y * k0.y + a.z * k0.z + a.w * k0.w;
+                s[i][1] += a.x * k1.x + a.y * k1.y + a.z * k1.z + a.w * k1.w;
+            }
+        }
+        float al[RP];
+#pragma unroll
+        for (int i = 0; i < RP; ++i) {
+            const float z0 = c0 + tc < e1 ? s[i][0] * p.scale : -INFINITY;
+            const float z1 = c0 + tc + 16 < e1 ? s[i][1] * p.scale : -INFINITY;
+            float mx = fmaxf(z0, z1);
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float mn = fmaxf(m[i], mx);
+            const float ref = mn == -INFINITY ? 0.f : mn; // every logit so far is -inf: e^{-inf} = 0
+            al[i] = expf(m[i] - ref);
+            m[i] = mn;
+            const float p0 = expf(z0 - ref), p1 = expf(z1 - ref);
+            float sum = p0 + p1;
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l[i] = l[i] * al[i] + sum;
+            sp[(tr + TR * i) * (kChunk + 1) + tc] = p0;
+            sp[(tr + TR * i) * (kChunk + 1) + tc + 16] = p1;
+        }
+        __syncwarp();                                     // a row's 16 threads sit in one warp
+#pragma unroll
+        for (int i = 0; i < RP; ++i)
+#pragma unroll
+            for (int j = 0; j < DJ; ++j) {
+                acc[i][j].x *= al[i]; acc[i][j].y *= al[i]; acc[i][j].z *= al[i]; acc[i][j].w *= al[i];
+            }
+        const int nk = e1 - c0 < kChunk ? (int)(e1 - c0) : kChunk;
+        for (int k = 0; k < nk; ++k) {
+            float w[RP];
+#pragma unroll
+            for (int i = 0; i < RP; ++i) w[i] = sp[(tr + TR * i) * (kChunk + 1) + k];
+#pragma unroll
+            for (int j = 0; j < DJ; ++j) {
+                const float4 v = *reinterpret_cast<const float4 *>(skv + k * S::kStride + 4 * tc + 64 * j);
+#pragma unroll
+                for (int i = 0; i < RP; ++i) {
+                    acc[i][j].x += w[i] * v.x; acc[i][j].y += w[i] * v.y;
+                    acc[i][j].z += w[i] * v.z; acc[i][j].w += w[i] * v.w;
+                }
+            }
+        }
+        __syncwarp();                                     // sp is read before the next chunk's is written
+    }
+    const int64_t at = (int64_t)((tail ? 0 : p.tail_split) + seg) * rows;
+#pragma unroll
+    for (int i = 0; i < RP; ++i) {
+        const int64_t g = g0 + tr + TR * i;
+        if (g >= rows) continue;
+        if (tc == 0) *reinterpret_cast<float2 *>(p.part_ml + (at + g) * 2) = make_float2(m[i], l[i]);
+#pragma unroll
+        for (int j = 0; j < DJ; ++j)
+            *reinterpret_cast<float4 *>(p.part_o + (at + g) * DH + 4 * tc + 64 * j) = acc[i][j];
+    }
+}
+
+// Joins the segments of one (query row, head) and the sink: DH / 4 threads, four dims each.
+// Bound by memory: every segment's sums are read once.
+template <int DH>
+__global__ void k_prefix_merge(PrefixParams p) {
+    constexpr int kPer = 128 / (DH / 4);                  // (query row, head) pairs per CTA
+    grid_dep_wait();
+    const int64_t rows = (int64_t)p.B * p.L * p.H;
+    const int sub = threadIdx.x / (DH / 4), d = (threadIdx.x % (DH / 4)) * 4;
+    const int64_t g = (int64_t)blockIdx.x * kPer + sub;
+    if (g >= rows) return;
+    const int nseg = p.tail_split + p.pre_split;
+    const float sink = p.sinks ? p.sinks[g % p.H] : -INFINITY;
+    float M = sink;
+    for (int s = 0; s < nseg; ++s) M = fmaxf(M, p.part_ml[(s * rows + g) * 2]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float den = expf(sink - ref);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < nseg; ++s) {
+        const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + (s * rows + g) * 2);
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;   // a segment that holds nothing
+        const float a = expf(ml.x - ref);
+        den += ml.y * a;
+        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p.part_o + (s * rows + g) * DH + d));
+        o.x += v.x * a; o.y += v.y * a; o.z += v.z * a; o.w += v.w * a;
+    }
+    const float f = den == 0.f ? 0.f : 1.f / den;         // nothing visible, no sink: 0
+    o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+    if (p.out_bf16) {
+        const __nv_bfloat162 u = __floats2bfloat162_rn(o.x, o.y), v = __floats2bfloat162_rn(o.z, o.w);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + g * DH + d) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + g * DH + d) = o;
+    }
+}
+
+template <int R, int DH, typename T>
+cudaError_t go(const PrefixParams &p, int tail, cudaStream_t s) {
+    const size_t bytes = Smem<R, DH>::bytes;
+    const cudaError_t e = smem_attr_once<k_prefix_simt<R, DH, T>>((int)bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = (int64_t)p.B * p.L * p.H;
+    const int64_t tiles = (rows + R - 1) / R;
+    return launch_pdl(k_prefix_simt<R, DH, T>, dim3((unsigned)tiles, (unsigned)(tail ? p.tail_split : p.pre_split)),
+                      dim3((R < 16 ? R : 16) * 16), bytes, s, 1, p, tail);
+}
+
+template <typename T>
+cudaError_t pick(const PrefixParams &p, int tail, cudaStream_t s) {
+    if (p.Dh == 64) return tail ? go<8, 64, T>(p, 1, s) : go<64, 64, T>(p, 0, s);
+    if (p.Dh == 128) return tail ? go<16, 128, T>(p, 1, s) : go<64, 128, T>(p, 0, s);
+    return go<64, 512, T>(p, tail, s);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_simt(const PrefixParams &p, int tail, cudaStream_t s) {
+    return p.bf16 ? pick<__nv_bfloat16>(p, tail, s) : pick<float>(p, tail, s);
+}
+
+cudaError_t launch_prefix_merge(const PrefixParams &p, cudaStream_t s) {
+    const int64_t rows = (int64_t)p.B * p.L * p.H;
+    const int per = 128 / (p.Dh / 4);
+    const dim3 grid((unsigned)((rows + per - 1) / per));
+    if (p.Dh == 64) return launch_pdl(k_prefix_merge<64>, grid, dim3(128), 0, s, 1, p);
+    if (p.Dh == 128) return launch_pdl(k_prefix_merge<128>, grid, dim3(128), 0, s, 1, p);
+    return launch_pdl(k_prefix_merge<512>, grid, dim3(128), 0, s, 1, p);
+}
+
+}  // namespace hisa

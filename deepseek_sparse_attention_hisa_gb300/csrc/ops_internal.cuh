@@ -1,0 +1,73 @@
+// Internal declarations of the operators around the step (norm, rotary positions,
+// shared-prefix combine). Nothing here is part of the C ABI (see include/hisa.h).
+#pragma once
+
+#include "hisa_internal.cuh"
+
+namespace hisa {
+
+struct NormParams {
+    int64_t rows;
+    int cols;
+    int x_bf16, res_bf16;
+    int out_dtype;            // hisa_dtype
+    int group;                // columns per scale (0: the row)
+    int pow2;
+    float eps;
+    int64_t ld_x, ld_res, ld_out;
+    const void *x;            // [rows, cols]
+    const void *res;          // [rows, cols] or nullptr
+    const float *w;           // [cols]
+    void *res_out;            // [rows, cols] or nullptr
+    void *out;                // [rows, cols]
+    float *scales;            // [rows, cols / group] (8-bit output)
+    int wide;                 // every row start is 16-byte aligned (8-byte for 8-bit codes), cols % 8 == 0
+    int chained;
+};
+
+struct RopeParams {
+    int64_t rows;             // tokens * (heads + heads2)
+    int heads, heads_all;     // of x; of x and x2
+    int D, dims, first, half;
+    int src_bf16, dst_bf16;
+    int inplace;
+    float mscale, sin_sign;
+    const uint64_t *table;
+    const int32_t *pos;
+    const void *x, *x2;
+    void *y, *y2;
+    int64_t x_token, x_head, y_token, y_head, x2_token, x2_head, y2_token, y2_head;
+    int rows_per_cta;         // set by launch_rope
+    int wide;                 // 8 elements per access fit every boundary
+    int chained;
+};
+
+// One shared-prefix combine. Partials of a segment (a range of the shared rows, or of a query
+// row's own list) are unnormalised sums with their running maximum and sum of exponentials.
+struct PrefixParams {
+    int B, L, H, Dh, window, W_max, r;
+    int64_t P, Np_max, kv_rows;
+    float scale;
+    const void *q, *local_kv, *prefix_kv, *pooled_kv;
+    const int32_t *local_len, *local_pos0, *t0;
+    const int64_t *kv_off;
+    const float *sinks;       // or nullptr
+    void *out;
+    int bf16, out_bf16;
+    int tail_split;           // segments [0, tail_split): a query row's local and own rows
+    int tail_rows;            // list rows of one of them
+    int pre_split;            // segments [tail_split, tail_split + pre_split): shared rows
+    int64_t pre_rows;         // shared rows of one of them
+    float *part_o;            // [segments, B * L * H, Dh]
+    float *part_ml;           // [segments, B * L * H, 2]: maximum (of the logits), sum
+    uint32_t *status;
+};
+
+size_t prefix_workspace_bytes(const hisa_prefix_desc *d);
+
+cudaError_t launch_rms_norm(const NormParams &p, cudaStream_t s);
+cudaError_t launch_rope(const RopeParams &p, cudaStream_t s);
+cudaError_t launch_prefix_simt(const PrefixParams &p, int tail, cudaStream_t s);
+cudaError_t launch_prefix_merge(const PrefixParams &p, cudaStream_t s);
+
+}  // namespace hisa

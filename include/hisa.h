@@ -5,7 +5,9 @@
  * hierarchical sparse attention" (cited as [HiSA issue] with its section): score
  * pooled indexer keys, select index_topk pooled rows (flat or hierarchical), gather
  * the selected pooled KV rows and combine them with the local window and the
- * per-head sinks in one split softmax.
+ * per-head sinks in one split softmax. Beside it stand the operators that a layer runs
+ * around the step: hisa_rms_norm, hisa_rope and, for a batch that shares a long prefix,
+ * hisa_prefix_attend.
  *
  * Conventions shared by every entry point
  *  - Tensor pointers are DEVICE pointers owned by the caller; tensors are dense,
@@ -22,10 +24,12 @@
  *    output. Set the flag only when the kernel just before the call on the stream is
  *    another libhisa call and none of those early-read inputs is written by it (the
  *    usual chain: hisa_block_filter(_append) -> hisa_select_topk -> hisa_sparse_attend).
+ *    With it hisa_rms_norm reads w, and hisa_rope its table, before that kernel has completed.
  *    Without the flag (flags = 0) a call's kernels start after the previous work on the
  *    stream has completed, as with any ordinary launch, except kernels that read nothing
- *    before the previous grid has completed (the coarse stage's pipeline, and the selects
- *    and merges that follow a call's scoring or combine kernel), which may always overlap
+ *    before the previous grid has completed (the coarse stage's pipeline, the selects and
+ *    merges that follow a call's scoring or combine kernel, and the kernels of
+ *    hisa_prefix_attend), which may always overlap
  *    its end.
  *  - Ragged batches: sequence b owns pooled rows [key_off[b], key_off[b+1]) of the
  *    packed key / KV arrays, so Np_b = key_off[b+1] - key_off[b] (int64, device).
@@ -80,7 +84,11 @@ typedef enum {
     HISA_EDEVICE = -5     /* hisa_device_status(): a kernel flagged bad data */
 } hisa_status;
 
-typedef enum { HISA_F32 = 0, HISA_BF16 = 1 } hisa_dtype;
+typedef enum {
+    HISA_F32 = 0,
+    HISA_BF16 = 1,
+    HISA_E4M3 = 2         /* 8-bit float, 4 exponent bits, largest 448 (hisa_rms_norm's out only) */
+} hisa_dtype;
 
 /* Bits of the device status word. */
 #define HISA_DEV_BAD_OFFSETS 0x1u /* offsets not monotone, past keys_rows / means_rows / kv_rows, Np_b > Np_max,
@@ -102,6 +110,7 @@ typedef enum { HISA_F32 = 0, HISA_BF16 = 1 } hisa_dtype;
 #define HISA_OP_FLAT_TOPK     4
 #define HISA_OP_SPARSE_ATTEND 5
 #define HISA_OP_COMPRESS      6
+#define HISA_OP_PREFIX_ATTEND 7
 
 /* Indexer problem ([HiSA issue] "Configuration", "Flat selection", "HiSA decode path"). */
 typedef struct {
@@ -161,8 +170,84 @@ typedef struct {
     int32_t flags;        /* HISA_FLAG_* bits (0 = none) */
 } hisa_compress_desc;
 
+/* The norm ahead of a layer's projections: the residual's addition, the root-mean-square
+ * norm, and the output in f32, bf16 or in 8 bits with scales (hisa_rms_norm). */
+typedef struct {
+    int64_t rows;         /* tokens (>= 0; 0 = nothing to do) */
+    int32_t cols;         /* hidden size, 1..32768 */
+    int32_t x_dtype;      /* hisa_dtype of x: HISA_F32 or HISA_BF16 */
+    int32_t res_dtype;    /* hisa_dtype of residual and residual_out: HISA_F32 or HISA_BF16 */
+    int32_t out_dtype;    /* hisa_dtype of out: HISA_F32, HISA_BF16 or HISA_E4M3 */
+    int32_t scale_group;  /* HISA_E4M3: columns that share a scale: 32, 64, 128 or 256 (a divisor of
+                             cols), or 0 for one scale per row; else 0 */
+    int32_t scale_pow2;   /* HISA_E4M3: 1 rounds each scale up to a power of two; else 0 */
+    float eps;            /* > 0 */
+    int32_t flags;        /* HISA_FLAG_* bits (0 = none) */
+    int64_t ld_x, ld_res, ld_out; /* elements from one row to the next of x, of residual and
+                             residual_out, of out (>= cols; ld_res is ignored without a residual) */
+} hisa_norm_desc;
+
+/* The frequencies of rotary positions ([HiSA issue] "Configuration": compress_rope_theta,
+ * qk_rope_head_dim), for hisa_rope_table. Pair i of rope_dims / 2 turns by f_i radians per
+ * position, f_i = theta^(-2i / rope_dims), scaled for contexts longer than the trained one: */
+#define HISA_ROPE_PLAIN  0   /* f_i */
+#define HISA_ROPE_LINEAR 1   /* f_i / factor: positions squeezed into the trained range */
+#define HISA_ROPE_YARN   2   /* f_i / factor * g_i + f_i * (1 - g_i): the pairs that turn more than
+                              * beta_fast times over orig_len positions stay, those that turn fewer
+                              * than beta_slow times are squeezed, a ramp linear in i between:
+                              * g_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1), with c(n) =
+                              * rope_dims * ln(orig_len / (2 pi n)) / (2 ln theta), lo =
+                              * max(floor(c(beta_fast)), 0), hi = min(ceil(c(beta_slow)), rope_dims - 1) */
+typedef struct {
+    int32_t rope_dims;    /* rotated dims, even, 2..1024 */
+    int32_t kind;         /* HISA_ROPE_* */
+    double theta;         /* base (> 1) */
+    double factor;        /* LINEAR, YARN: > 0 (ignored otherwise) */
+    double orig_len;      /* YARN: the trained length (> 0) */
+    double beta_fast;     /* YARN: > 0 */
+    double beta_slow;     /* YARN: > 0 */
+} hisa_rope_scaling;
+
+/* Rotary positions of one or two tensors of heads (hisa_rope), for instance queries and the
+ * shared KV row of each token. All strides in elements; heads need not be dense. */
+typedef struct {
+    int64_t tokens;       /* >= 0 (0 = nothing to do) */
+    int32_t heads;        /* heads of x (>= 1) */
+    int32_t heads2;       /* heads of x2 (0 = no second tensor) */
+    int32_t D;            /* head dim, 2..1024 */
+    int32_t rope_dims;    /* rotated dims, even, 2..D */
+    int32_t rope_first;   /* first rotated dim, 0..D - rope_dims */
+    int32_t half;         /* pairs: 0 = (2i, 2i + 1), interleaved; 1 = (i, i + rope_dims / 2), halves */
+    int32_t inverse;      /* 1 turns back (the angle's sign is changed) */
+    int32_t src_dtype;    /* hisa_dtype of x and x2: HISA_F32 or HISA_BF16 */
+    int32_t dst_dtype;    /* hisa_dtype of y and y2 */
+    float mscale;         /* factor of the rotated dims (1 = none) */
+    int32_t flags;        /* HISA_FLAG_* bits (0 = none) */
+    int64_t x_token, x_head, y_token, y_head;       /* strides of x and y */
+    int64_t x2_token, x2_head, y2_token, y2_head;   /* strides of x2 and y2 */
+} hisa_rope_desc;
+
+/* The dense combine of a batch whose sequences share their first pooled rows
+ * (hisa_prefix_attend). */
+typedef struct {
+    int32_t B, L;         /* sequences, query rows per sequence */
+    int32_t H;            /* query heads sharing the single KV head: 8, 16 or 64 */
+    int32_t Dh;           /* head dim: 64, 128 or 512 (with H = 8, 16, 64 respectively) */
+    int32_t window;       /* sliding window: local row s is visible to t iff 0 <= t-s < window */
+    int32_t W_max;        /* rows allocated per sequence in local_kv */
+    int32_t r;            /* compress ratio, for V(t) */
+    int32_t flags;        /* HISA_FLAG_* bits (0 = none) */
+    int64_t prefix_rows;  /* P: pooled rows that every sequence shares (>= 0) */
+    int64_t Np_max;       /* an upper bound of the sequences' own pooled rows Np_b */
+    int64_t kv_rows;      /* rows allocated in pooled_kv (>= kv_off[B]); no read goes past it */
+    float scale;          /* softmax scale; <= 0 selects Dh^-1/2 */
+    int32_t q_dtype;      /* hisa_dtype of q; must equal kv_dtype */
+    int32_t kv_dtype;     /* hisa_dtype of local_kv, prefix_kv and pooled_kv */
+    int32_t out_dtype;    /* hisa_dtype of out: HISA_F32 or HISA_BF16 */
+} hisa_prefix_desc;
+
 /* Bytes of device workspace `op` needs for `desc` (a hisa_index_desc* for ops 0-4,
- * a hisa_attn_desc* for op 5, a hisa_compress_desc* for op 6). Always >= 256 for a valid desc; 0 for an invalid one.
+ * a hisa_attn_desc* for op 5, a hisa_compress_desc* for op 6, a hisa_prefix_desc* for op 7). Always >= 256 for a valid desc; 0 for an invalid one.
  * Pure host arithmetic: needs no GPU. */
 HISA_API size_t hisa_workspace_bytes(int32_t op, const void *desc);
 
@@ -322,6 +407,70 @@ HISA_API hisa_status hisa_compress_append(const hisa_compress_desc *desc, const 
 HISA_API hisa_status hisa_sparse_attend(const hisa_attn_desc *desc, const void *q, const void *local_kv,
                                const int32_t *local_len, const int32_t *local_pos0,
                                const void *pooled_kv, const int64_t *kv_off, const int32_t *I,
+                               const float *sinks, const int32_t *t0, void *out, void *ws,
+                               size_t ws_bytes, hisa_stream_t stream);
+
+/* Residual addition, root-mean-square norm and output in one pass over the rows:
+ *   h = x + residual (f32), rounded to res_dtype where there is a residual; residual_out = h;
+ *   y = h / sqrt(mean(h^2) + eps) * w  (f32, over the row as stored);
+ *   out = y rounded once, or in 8 bits: per group of scale_group columns (the row if 0) of
+ *   largest magnitude a, scale = max(a, 1e-10) / 448, with scale_pow2 the next power of two at
+ *   or above it, and out = y / scale rounded to nearest even (|y / scale| <= 448 but for f32
+ *   rounding, which saturates). A row that holds a NaN or an infinity gives NaN where the
+ *   formula does; the other rows are not affected.
+ *   x            [rows, cols] x_dtype, rows ld_x apart
+ *   residual     [rows, cols] res_dtype, rows ld_res apart, or NULL (h = x)
+ *   w            [cols] f32
+ *   residual_out [rows, cols] res_dtype, rows ld_res apart, or NULL (the sum is not kept); may be
+ *                residual itself
+ *   out          [rows, cols] out_dtype, rows ld_out apart; may be x itself when dtype and stride
+ *                are the same
+ *   scales       [rows, cols / scale_group] f32 dense ([rows] if scale_group is 0): HISA_E4M3 only,
+ *                else NULL
+ * Apart from those two cases no output may overlap an input. Every pointer is aligned to its
+ * element; rows whose starts are all 16-byte aligned are moved 16 bytes at a time. No workspace. */
+HISA_API hisa_status hisa_rms_norm(const hisa_norm_desc *desc, const void *x, const void *residual,
+                          const float *w, void *residual_out, void *out, float *scales,
+                          hisa_stream_t stream);
+
+/* Fills table[rope_dims / 2] (HOST memory; pure host arithmetic) for hisa_rope: the turns per
+ * position of each pair in units of 2^-64, so that position * table[i] modulo 2^64 is the
+ * angle's fraction of a turn, exact at any position. The caller copies it to the device once. */
+HISA_API hisa_status hisa_rope_table(const hisa_rope_scaling *scaling, uint64_t *table);
+
+/* Rotary positions ([HiSA issue] "The pooled stream and positions", qk_rope_head_dim): for the
+ * i-th pair (a, b) of dims [rope_first, rope_first + rope_dims) of every head of token n, with
+ * the angle A = pos[n] * f_i (its sign changed if inverse):
+ *   (a, b) -> mscale * (a cos A - b sin A, a sin A + b cos A)
+ * in f32, rounded once to dst_dtype; the other dims are copied (converted).
+ *   table [rope_dims / 2] uint64 (device, from hisa_rope_table);  pos [tokens] int32 (any sign)
+ *   x, y  [tokens, heads, D] and x2, y2 [tokens, heads2, D] with the strides of the descriptor
+ * y == x (same strides and dtype) rotates in place and touches the rotated dims alone; the
+ * same for y2 == x2, and both are in place or neither is. Otherwise no output may overlap an
+ * input. Pointers are aligned to their element. No workspace. */
+HISA_API hisa_status hisa_rope(const hisa_rope_desc *desc, const uint64_t *table, const int32_t *pos,
+                      const void *x, void *y, const void *x2, void *y2, hisa_stream_t stream);
+
+/* Shared-prefix combine: the dense branch of hisa_sparse_attend (I = NULL) over the pooled
+ * stream made of the P shared rows followed by the sequence's own, the shared rows scored once
+ * for the whole batch. For query row j of sequence b at t = t0[b] + j the softmax runs over
+ * the visible local rows, all P shared rows, the own pooled rows i in [0, Np_b), Np_b =
+ * kv_off[b+1] - kv_off[b], and the per-head sink, which joins the normaliser and carries no
+ * value; K = V. With L > 1 own row i, at pooled position P + i, is visible iff P + i <
+ * floor((t+1)/r); with L = 1 all are, as in hisa_sparse_attend. The shared rows precede every
+ * sequence's own tokens and are always visible. A query row that sees nothing gives 0.
+ *   q          [B, L, H, Dh]  q_dtype (already roped)
+ *   local_kv   [B, W_max, Dh] kv_dtype (NULL if W_max is 0); local_len [B] int32 rows present
+ *              (<= W_max); local_pos0 [B] int32 absolute position of local row 0
+ *   prefix_kv  [P, Dh] kv_dtype (NULL if P is 0)
+ *   pooled_kv  [kv_rows, Dh] kv_dtype (NULL if Np_max is 0); kv_off [B+1] int64
+ *   sinks      [H] f32, or NULL for none (-inf is none for that head);  t0 [B] int32
+ *   out        [B, L, H, Dh] out_dtype, 16-byte aligned
+ * Rows that no query sees are not read. Offsets that do not fit set HISA_DEV_BAD_OFFSETS; that
+ * sequence's own rows are skipped. */
+HISA_API hisa_status hisa_prefix_attend(const hisa_prefix_desc *desc, const void *q, const void *local_kv,
+                               const int32_t *local_len, const int32_t *local_pos0,
+                               const void *prefix_kv, const void *pooled_kv, const int64_t *kv_off,
                                const float *sinks, const int32_t *t0, void *out, void *ws,
                                size_t ws_bytes, hisa_stream_t stream);
 
