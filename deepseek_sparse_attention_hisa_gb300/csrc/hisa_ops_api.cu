@@ -82,7 +82,27 @@ void prefix_plan(const hisa_prefix_desc *d, PrefixParams *p) {
     int64_t per = 0;
     p->tail_split = list > 0 ? split(queries, list, &per) : 0;
     p->tail_rows = (int)(per < kMaxRows ? per : kMaxRows);
-    p->pre_split = d->prefix_rows > 0 ? split((queries * d->H + 63) / 64, d->prefix_rows, &p->pre_rows) : 0;
+    if (d->prefix_rows == 0) return;
+    if (!prefix_tc_supported(d->H, d->Dh, d->kv_dtype == HISA_BF16)) {
+        p->pre_split = split((queries * d->H + 63) / 64, d->prefix_rows, &p->pre_rows);
+        return;
+    }
+    // Tensor cores: pairs of CTAs walk (two query rows, segment) items of `per` tiles of 64 rows.
+    // The split with the shortest longest walk, in tiles (about 0.7 us each): an item costs
+    // about 4 more (fill, epilogue), and each segment a write and a read of its sums (2 KB per
+    // query row and head, both ways at about 6 TB/s).
+    const int64_t tiles = (d->prefix_rows + 63) / 64, pairs = (queries + 1) / 2;
+    double best = 0.0;
+    for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {
+        const int64_t per_n = (tiles + n - 1) / n, segs = (tiles + per_n - 1) / per_n;
+        const int64_t walk = (pairs * segs + kSmTarget / 2 - 1) / (kSmTarget / 2);
+        const double cost = (double)walk * (double)(per_n + 4) + (double)segs * (double)queries * 64 * 4096 / 6e12 / 0.7e-6;
+        if (n == 1 || cost < best) {
+            best = cost;
+            p->pre_split = (int)segs;
+            p->pre_rows = per_n * 64;
+        }
+    }
 }
 
 }  // namespace
@@ -235,7 +255,8 @@ hisa_status hisa_prefix_attend(const hisa_prefix_desc *d, const void *q, const v
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (p.tail_split) e = launch_prefix_simt(p, 1, s);
-    if (e == cudaSuccess && p.pre_split) e = launch_prefix_simt(p, 0, s);
+    if (e == cudaSuccess && p.pre_split)
+        e = prefix_tc_supported(p.H, p.Dh, p.bf16) ? launch_prefix_tc(p, s) : launch_prefix_simt(p, 0, s);
     if (e == cudaSuccess) e = launch_prefix_merge(p, s);
     return from_cuda(e);
 }

@@ -1,0 +1,433 @@
+// Shared-prefix combine on the tensor cores: the shared rows' segments for 64 bf16 query heads
+// of 512 dims (one KV head, K = V).
+//
+// The shared rows are the same for every query row of the batch, so the query rows (64 heads
+// each) stack into tiles: S = Q K^T and O += P V are dense products of 4 * 512 operations per
+// (stacked row, shared row), bound by the tensor cores.
+//
+// A pair of CTAs (a cluster of two) takes two query rows (128 stacked rows) and one segment.
+// O is 128 x 512 f32: 64 KB of each CTA's 256 KB of TMEM per CTA only because the pair splits
+// the rows (cta_group::2, M = 128: CTA c holds rows 64 c .. + 63, at the full tensor rate, which a
+// single CTA with M = 64 rows halves). Per tile of kT = 64 shared rows:
+//   S [128 x 64]   = Q K^T    A = Q, each CTA its 64 rows; B = K, each CTA 32 of the 64 rows
+//   O [128 x 512] += P V      A = P, each CTA its 64 rows; B = V, each CTA 256 of the 512 dims
+// Both CTAs must give an operand at the same shared-memory offset, so a CTA stages the 32 rows
+// it gives as K and the 256 dims it gives as V separately (32 KB each), all by TMA from L2.
+// With kT = 64 the first product waits for its operands in shared memory (25 instead of 16
+// cycles per 16 dims: 2 KB of Q and 1 KB of K at 128 B per cycle); larger tiles leave no room
+// for two stages of each operand beside the 64 KB of Q. The ceiling is so about 78 % of the
+// tensor peak.
+//
+// The issue order S(0) S(1) PV(0) S(2) PV(1) ... leaves the softmax of a tile the time of one
+// product of each kind. TMEM layout of both accumulators: lanes 0-63 hold the CTA's 64 rows for
+// the first half of the columns, lanes 64-127 the same rows for the second half, so a row's
+// logits sit with two threads of one lane each, which exchange their maxima through shared
+// memory. The running maximum is lazy: O and the sums are rescaled only when a tile's maximum
+// exceeds it by more than 8 (log2 units), so p <= 256. P is rounded to bf16 for the second
+// product (a relative 2^-9 per weight, of random sign); sums are of the unrounded weights in f32.
+//
+// Warps of each CTA: 0-3 softmax and epilogue (thread = TMEM lane), 4 loads, 5 (of CTA 0) MMA
+// issue for the pair. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and the CTAs leave.
+#include "ops_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace hisa {
+namespace {
+
+using namespace tc;
+
+constexpr int kH = 64, kDH = 512, kT = 64;
+constexpr int kSoftWarps = 4, kLoadWarp = 4, kMmaWarp = 5, kThreads = 192;
+constexpr int kStages = 2;                              // of K, of V, of S and of P
+constexpr uint32_t kQBytes = kH * kDH * 2;              // 64 KB: 8 chunks [64 rows x 64 dims]
+constexpr uint32_t kKBytes = kT / 2 * kDH * 2;          // 32 KB: 8 chunks [32 rows x 64 dims]
+constexpr uint32_t kVBytes = kT * kDH;                  // 32 KB: 4 chunks [64 rows x 64 dims]
+constexpr uint32_t kPBytes = kH * kT * 2;               // 8 KB: one chunk [64 rows x 64 shared rows]
+constexpr uint32_t kKChunk = kT / 2 * 128, kVChunk = kT * 128, kQChunk = kH * 128;
+constexpr uint32_t kOffQ = 0, kOffK = kQBytes, kOffV = kOffK + kStages * kKBytes, kOffP = kOffV + kStages * kVBytes,
+                   kOffMisc = kOffP + kStages * kPBytes;
+constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f, kLazy = 8.0f;
+
+struct Misc {
+    // pair barriers, used in CTA 0: operands have landed in both CTAs; S read and P written by both
+    uint64_t kfull[kStages], vfull[kStages], qfull, sfree[kStages], pfull[kStages], ofree;
+    // each CTA's own, signalled by the MMAs of the pair
+    uint64_t kempty[kStages], vempty[kStages], qfree, sfull[kStages], pfree[kStages], ofull;
+    uint32_t tmem;
+    int abort;
+    float mx[2][2][kH];                                 // [tile parity][column half][row]: a tile's maxima
+};
+constexpr uint32_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// The shared::cluster address of `p`'s counterpart in CTA `cta` of the cluster.
+__device__ __forceinline__ uint32_t map_to(const void *p, uint32_t cta) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(cta));
+    return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const long long t0 = clock64();
+    for (uint32_t i = 0; i < (1u << 26); ++i) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+        if (ok) return true;
+        if ((i & 255u) == 255u && (*abort || clock64() - t0 > kWaitCycles)) return false;
+    }
+    return false;
+}
+__device__ __forceinline__ bool wait_pair_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, wait_pair(bar, parity, abort));
+}
+// Loads a box of the chunked map; the bytes count on `bar`, which may be the other CTA's.
+__device__ __forceinline__ void load_chunks(uint32_t dst, const CUtensorMap *map, int row, int chunk, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// One arrival on `bar` in both CTAs once every MMA issued so far has completed.
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+                 :: "r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+                 "%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+                   "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(addr));
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ float ex2(float x) {         // 2^x, relative error <= 2^-22; -inf -> +0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void store32(float *dst, const float *v) {   // one whole sector
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
+// True on the 64 threads of a named barrier iff v is true on all of them (a barrier itself).
+__device__ __forceinline__ bool pair_all(uint32_t id, bool v) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 64, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((uint32_t)v), "r"(id) : "memory");
+    return r != 0u;
+}
+
+struct Item {
+    int row, seg;             // this CTA's query row; segment
+    int first, rows, tiles;   // its shared rows
+};
+__device__ __forceinline__ Item item_of(const PrefixParams &p, int id, int rank) {
+    Item x;
+    const int pairs = (p.B * p.L + 1) / 2;
+    x.seg = id / pairs;
+    x.row = 2 * (id - x.seg * pairs) + rank;
+    const int64_t a = (int64_t)x.seg * p.pre_rows, e = a + p.pre_rows;
+    x.first = (int)a;
+    x.rows = (int)((e < p.P ? e : p.P) - a);
+    x.tiles = (x.rows + kT - 1) / kT;
+    return x;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+            const __grid_constant__ CUtensorMap vmap) {
+    extern __shared__ __align__(1024) uint8_t raw[];
+    const uint32_t r0 = smem_u32(raw);
+    uint8_t *smem = raw + (((r0 + 1023u) & ~1023u) - r0);
+    const uint32_t sbase = smem_u32(smem);
+    Misc *ms = reinterpret_cast<Misc *>(smem + kOffMisc);
+    volatile int *abort = &ms->abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank();
+    const int first_item = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ms->kfull[s], 1); mbar_init(&ms->vfull[s], 1);
+            mbar_init(&ms->sfree[s], 2 * kSoftWarps); mbar_init(&ms->pfull[s], 2 * kSoftWarps);
+            mbar_init(&ms->kempty[s], 1); mbar_init(&ms->vempty[s], 1);
+            mbar_init(&ms->sfull[s], 1); mbar_init(&ms->pfree[s], 1);
+        }
+        mbar_init(&ms->qfull, 1); mbar_init(&ms->qfree, 1);
+        mbar_init(&ms->ofree, 2 * kSoftWarps); mbar_init(&ms->ofull, 1);
+        mbar_fence_init();
+        ms->abort = 0;
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(&ms->tmem)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    fence_before_sync();
+    __syncthreads();
+    cluster_sync();                                     // both CTAs' barriers and TMEM are there
+    fence_after_sync();
+    const uint32_t tmem = ms->tmem;
+    grid_dep_wait();
+    bool ok = true;
+    auto fail = [&]() {
+        ok = false;
+        *abort = 1;
+    };
+
+    if (warp == kLoadWarp) {
+        // ---------------- loads of this CTA's share of Q, K and V ----------------
+        if (lane == 0) {
+            uint32_t g = 0;
+            int n = 0;
+            for (int id = first_item; id < items && ok; id += step, ++n) {
+                const Item x = item_of(p, id, rank);
+                if (n > 0 && !wait_pair(&ms->qfree, (n - 1) & 1, abort)) { fail(); break; }
+                if (rank == 0) mbar_arrive_expect_tx(&ms->qfull, 2 * kQBytes);
+                load_chunks(sbase + kOffQ, &qmap, x.row * kH, 0, map_to(&ms->qfull, 0));
+                for (int i = 0; i < x.tiles; ++i, ++g) {
+                    const uint32_t s = g % kStages, par = (g / kStages - 1) & 1;
+                    const int row = x.first + i * kT;
+                    if (g >= kStages && !wait_pair(&ms->kempty[s], par, abort)) { fail(); break; }
+                    if (rank == 0) mbar_arrive_expect_tx(&ms->kfull[s], 2 * kKBytes);
+                    load_chunks(sbase + kOffK + s * kKBytes, &kmap, row + rank * (kT / 2), 0, map_to(&ms->kfull[s], 0));
+                    if (g >= kStages && !wait_pair(&ms->vempty[s], par, abort)) { fail(); break; }
+                    if (rank == 0) mbar_arrive_expect_tx(&ms->vfull[s], 2 * kVBytes);
+                    load_chunks(sbase + kOffV + s * kVBytes, &vmap, row, rank * 4, map_to(&ms->vfull[s], 0));
+                }
+            }
+            if (!ok && rank == 0) {
+                // copies in flight land before the CTAs leave (bounded, whatever the abort flag says)
+                for (uint32_t b = g > kStages ? g - kStages : 0; b <= g; ++b) {
+                    mbar_wait(&ms->kfull[b % kStages], (b / kStages) & 1, 1u << 20);
+                    mbar_wait(&ms->vfull[b % kStages], (b / kStages) & 1, 1u << 20);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ---------------- MMA issue (CTA 0, for the pair) ----------------
+        if (rank == 0) {
+            const uint32_t id_s = idesc_bf16_f32(128, kT, 0, 0), id_o = idesc_bf16_f32(128, 256, 0, 1);
+            const uint64_t qd = smem_desc_sw128(sbase + kOffQ, 16, 1024);
+            uint32_t gs = 0, gp = 0;                    // tiles whose first / second product was issued
+            int n = 0;
+            auto first = [&]() -> bool {                // S = Q K^T of tile gs
+                const uint32_t s = gs % kStages;
+                if (!wait_pair_warp(&ms->kfull[s], (gs / kStages) & 1, abort)) return false;
+                if (gs >= kStages && !wait_pair_warp(&ms->sfree[s], (gs / kStages - 1) & 1, abort)) return false;
+                fence_after_sync();
+                const uint64_t kd = smem_desc_sw128(sbase + kOffK + s * kKBytes, 16, 1024);
+                const uint32_t d = tmem + kColS + s * (kT / 2);
+#pragma unroll
+                for (int ks = 0; ks < kDH / 16; ++ks)
+                    mma_pair(d, desc_add(qd, (ks >> 2) * kQChunk + (ks & 3) * 32),
+                             desc_add(kd, (ks >> 2) * kKChunk + (ks & 3) * 32), id_s, ks > 0);
+                commit_pair(&ms->sfull[s]);
+                commit_pair(&ms->kempty[s]);
+                ++gs;
+                return true;
+            };
+            auto second = [&](bool start) -> bool {     // O += P V of tile gp
+                const uint32_t s = gp % kStages;
+                if (!wait_pair_warp(&ms->vfull[s], (gp / kStages) & 1, abort)) return false;
+                if (!wait_pair_warp(&ms->pfull[s], (gp / kStages) & 1, abort)) return false;
+                fence_after_sync();
+                const uint64_t pd = smem_desc_sw128(sbase + kOffP + s * kPBytes, 16, 1024);
+                const uint64_t vd = smem_desc_sw128(sbase + kOffV + s * kVBytes, kVChunk, 1024);
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int ks = 0; ks < kT / 16; ++ks)
+                        mma_pair(tmem + kColO + m * 128, desc_add(pd, ks * 32), desc_add(vd, m * 2 * kVChunk + ks * 2048), id_o,
+                                 (ks > 0 || !start) ? 1u : 0u);
+                commit_pair(&ms->vempty[s]);
+                commit_pair(&ms->pfree[s]);
+                ++gp;
+                return true;
+            };
+            for (int id = first_item; id < items && ok; id += step, ++n) {
+                const Item x = item_of(p, id, 0);
+                if (!wait_pair_warp(&ms->qfull, n & 1, abort)) { fail(); break; }
+                fence_after_sync();
+                if (!first()) { fail(); break; }
+                for (int i = 0; i < x.tiles; ++i) {
+                    if (i + 1 < x.tiles && !first()) { fail(); break; }
+                    if (i + 1 == x.tiles) commit_pair(&ms->qfree);        // every S product of the item is issued
+                    // O starts over once the epilogues have read the item before
+                    if (i == 0 && n > 0 && !wait_pair_warp(&ms->ofree, (n - 1) & 1, abort)) { fail(); break; }
+                    if (!second(i == 0)) { fail(); break; }
+                }
+                if (!ok) break;
+                commit_pair(&ms->ofull);
+            }
+            if (!ok) {                                  // MMAs in flight end before TMEM is freed
+                commit_pair(&ms->qfree);
+                for (int k = 0; k < 2; ++k) mbar_wait(&ms->qfree, k, 1u << 20);
+            }
+        }
+    } else {
+        // ---------------- softmax and epilogue: thread = TMEM lane ----------------
+        const int r = (warp & 1) * 32 + lane, half = warp >> 1;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+        const float c2 = p.scale * kLog2e;
+        const uint32_t pairbar = 1 + (warp & 1);        // the two warps that share 32 rows
+        uint32_t g = 0;
+        int n = 0;
+        bool good = true;                               // no wait of this warp has run out; both warps of a
+                                                        // pair leave at the same barrier
+        for (int id = first_item; id < items && ok; id += step, ++n) {
+            const Item x = item_of(p, id, rank);
+            float m2 = -INFINITY, l = 0.f;
+            for (int i = 0; i < x.tiles; ++i, ++g) {
+                const uint32_t s = g % kStages, par = (g / kStages) & 1;
+                good = good && wait_pair_warp(&ms->sfull[s], par, abort);
+                fence_after_sync();
+                float v[32];
+                tmem_ld32(lanes + kColS + s * (kT / 2), v);
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(map_to(&ms->sfree[s], 0));
+                const int left = x.rows - i * kT - half * (kT / 2);      // of this thread's 32 shared rows
+                if (left < 32) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = k < left ? v[k] : -INFINITY;
+                }
+                float mx[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) mx[k] = fmaxf(v[k], v[k + 16]);
+#pragma unroll
+                for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+                    for (int k = 0; k < w; ++k) mx[k] = fmaxf(mx[k], mx[k + w]);
+                ms->mx[g & 1][half][r] = mx[0];
+                if (!pair_all(pairbar, good)) { fail(); break; }
+                const float tmax = fmaxf(mx[0], ms->mx[g & 1][half ^ 1][r]) * c2;   // c2 > 0
+                float alpha = 1.f;
+                if (tmax > m2 + kLazy) {
+                    alpha = ex2(m2 - tmax);             // first tile: 2^-inf = 0, and nothing to rescale
+                    m2 = tmax;
+                }
+                const float ref = m2 == -INFINITY ? 0.f : m2;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = ex2(fmaf(v[k], c2, -ref));
+                uint32_t u[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                    u[k] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+#pragma unroll
+                for (int w = 16; w >= 1; w >>= 1)
+#pragma unroll
+                    for (int k = 0; k < w; ++k) v[k] += v[k + w];
+                l = l * alpha + v[0];
+                // the P buffer's last reader, and for a rescale every product so far, has completed
+                if (g >= kStages) good = good && wait_pair_warp(&ms->pfree[s], par ^ 1, abort);
+                if (__any_sync(0xffffffffu, alpha != 1.f) && i > 0) {
+                    good = good && wait_pair_warp(&ms->pfree[(g - 1) % kStages], ((g - 1) / kStages) & 1, abort);
+                    fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < 256; c += 16) {
+                        float o[16];
+                        tmem_ld16(lanes + kColO + c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] *= alpha;
+                        tmem_st16(lanes + kColO + c, o);
+                    }
+                    tmem_st_wait();
+                }
+                uint8_t *pb = smem + kOffP + s * kPBytes;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    *reinterpret_cast<uint4 *>(pb + sw128_offset(r, half * 32 + k * 8)) =
+                        make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+                fence_async_smem();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(map_to(&ms->pfull[s], 0));
+            }
+            if (!ok) break;
+            good = good && wait_pair_warp(&ms->ofull, n & 1, abort);
+            fence_after_sync();
+            // the row's sum joins over its two threads
+            ms->mx[g & 1][half][r] = l;
+            if (!pair_all(pairbar, good)) { fail(); break; }
+            l += ms->mx[g & 1][half ^ 1][r];
+            asm volatile("bar.sync %0, 64;" ::"r"(pairbar) : "memory");
+            const bool there = x.row < p.B * p.L;
+            const int64_t rows = (int64_t)p.B * p.L * kH, at = (int64_t)(p.tail_split + x.seg) * rows + (int64_t)x.row * kH + r;
+            if (there && half == 0) *reinterpret_cast<float2 *>(p.part_ml + at * 2) = make_float2(m2 * kLn2, l);
+            float *dst = p.part_o + at * kDH + half * 256;
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 32) {
+                float o[32];
+                tmem_ld32(lanes + kColO + c, o);
+                if (there) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) store32(dst + c + k, o + k);
+                }
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(map_to(&ms->ofree, 0));
+        }
+    }
+    if (!ok) flag(p.status, HISA_DEV_TIMEOUT);
+    fence_before_sync();
+    __syncthreads();
+    cluster_sync();                                     // no CTA leaves while the other may signal it
+    if (warp == kMmaWarp) {
+        fence_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+}  // namespace
+
+bool prefix_tc_supported(int H, int Dh, int bf16) { return H == kH && Dh == kDH && bf16; }
+
+cudaError_t launch_prefix_tc(const PrefixParams &p, cudaStream_t s) {
+    const cudaError_t attr = smem_attr_once<k_prefix_tc>((int)kSmemBytes);
+    if (attr != cudaSuccess) return attr;
+    const int sms = device_sm_count();
+    if (sms < 2) return cudaErrorInvalidDevice;
+    CUtensorMap qmap, kmap, vmap;
+    const uint64_t qrows = (uint64_t)p.B * p.L * kH;
+    if (!encode_bf16_chunks(&qmap, p.q, qrows, kDH, kH, 8) ||
+        !encode_bf16_chunks(&kmap, p.prefix_kv, (uint64_t)p.P, kDH, kT / 2, 8) ||
+        !encode_bf16_chunks(&vmap, p.prefix_kv, (uint64_t)p.P, kDH, kT, 4))
+        return cudaErrorInvalidValue;
+    const int items = (p.B * p.L + 1) / 2 * p.pre_split;
+    const int pairs = items < sms / 2 ? items : sms / 2;
+    return launch_pdl(k_prefix_tc, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmemBytes, s, 1, p, items, qmap, kmap, vmap);
+}
+
+}  // namespace hisa

@@ -63,11 +63,20 @@ struct PrefixParams {
     uint32_t *status;
 };
 
+// Encodes a 3-D tensor map over bf16 [rows, cols]: chunks of 64 columns as the slowest
+// dimension, so one box of box_chunks x box_rows x 64 lands as box_chunks swizzled (128-byte)
+// K-major operand chunks. False if the driver has no encoder or rejects the map.
+bool encode_bf16_chunks(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                        uint32_t box_chunks);
+
 size_t prefix_workspace_bytes(const hisa_prefix_desc *d);
 
 cudaError_t launch_rms_norm(const NormParams &p, cudaStream_t s);
 cudaError_t launch_rope(const RopeParams &p, cudaStream_t s);
 cudaError_t launch_prefix_simt(const PrefixParams &p, int tail, cudaStream_t s);
+// The shared rows' segments on the tensor cores: bf16, 64 heads of 512 dims.
+bool prefix_tc_supported(int H, int Dh, int bf16);
+cudaError_t launch_prefix_tc(const PrefixParams &p, cudaStream_t s);
 cudaError_t launch_prefix_merge(const PrefixParams &p, cudaStream_t s);
 
 }  // namespace hisa

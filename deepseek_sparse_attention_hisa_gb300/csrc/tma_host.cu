@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include "hisa_internal.cuh"
+#include "ops_internal.cuh"
 
 namespace hisa {
 namespace {
@@ -43,6 +44,19 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType type, uint32_t esize, const
 bool encode_bf16_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                      uint32_t box_cols, uint32_t box_rows) {
     return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, cols, box_cols, box_rows);
+}
+
+bool encode_bf16_chunks(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                        uint32_t box_chunks) {
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
+    if (!fn || rows == 0 || cols % 64) return false;
+    const cuuint64_t dims[3] = {64, rows, cols / 64};
+    const cuuint64_t strides[2] = {cols * 2, 128};     // bytes from row to row, from chunk to chunk
+    const cuuint32_t box[3] = {64, box_rows, box_chunks};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_f32_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
