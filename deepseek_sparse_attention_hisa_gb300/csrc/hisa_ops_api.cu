@@ -70,9 +70,10 @@ void prefix_plan(const hisa_prefix_desc *d, PrefixParams *p) {
     const int64_t queries = (int64_t)d->B * d->L;
     const int64_t local = d->W_max < d->window ? d->W_max : d->window;
     const int64_t list = local + d->Np_max;
-    auto split = [](int64_t items, int64_t rows, int64_t *per) {
-        // about two CTAs per SM, at least 64 rows each
-        int64_t n = kTargetCtas / (items > 0 ? items : 1);
+    const bool tc = prefix_tc_supported(d->H, d->Dh, d->kv_dtype == HISA_BF16);
+    auto split = [tc](int64_t items, int64_t rows, int64_t *per) {
+        // about two CTAs per SM (the tensor-core kernels hold an SM: one), at least 64 rows each
+        int64_t n = (tc ? kSmTarget : kTargetCtas) / (items > 0 ? items : 1);
         const int64_t most = (rows + 63) / 64;
         n = n > most ? most : n;
         n = n < 1 ? 1 : (n > 64 ? 64 : n);
@@ -83,7 +84,7 @@ void prefix_plan(const hisa_prefix_desc *d, PrefixParams *p) {
     p->tail_split = list > 0 ? split(queries, list, &per) : 0;
     p->tail_rows = (int)(per < kMaxRows ? per : kMaxRows);
     if (d->prefix_rows == 0) return;
-    if (!prefix_tc_supported(d->H, d->Dh, d->kv_dtype == HISA_BF16)) {
+    if (!tc) {
         p->pre_split = split((queries * d->H + 63) / 64, d->prefix_rows, &p->pre_rows);
         return;
     }
@@ -103,6 +104,21 @@ void prefix_plan(const hisa_prefix_desc *d, PrefixParams *p) {
             p->pre_rows = per_n * 64;
         }
     }
+}
+
+// The local and own rows' segments on the tensor cores.
+cudaError_t launch_tail_tc(const PrefixParams &p, cudaStream_t s) {
+    AttnParams a{};
+    a.B = p.B; a.L = p.L; a.H = p.H; a.Dh = p.Dh; a.window = p.window; a.W_max = p.W_max; a.r = p.r;
+    a.causal = p.L > 1;
+    a.Np_max = p.Np_max; a.kv_rows = p.kv_rows;
+    a.scale = p.scale;
+    a.q = p.q; a.local_kv = p.local_kv; a.local_len = p.local_len; a.local_pos0 = p.local_pos0;
+    a.pooled_kv = p.pooled_kv; a.kv_off = p.kv_off; a.t0 = p.t0;
+    a.nsplit = p.tail_split; a.rows_per_split = p.tail_rows;
+    a.kv_bf16 = p.bf16;
+    a.status = p.status;
+    return launch_attend_tc_part(a, AttendPart{p.P, p.part_o, p.part_ml}, s);
 }
 
 }  // namespace
@@ -254,9 +270,9 @@ hisa_status hisa_prefix_attend(const hisa_prefix_desc *d, const void *q, const v
     p.status = static_cast<uint32_t *>(ws);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (p.tail_split) e = launch_prefix_simt(p, 1, s);
-    if (e == cudaSuccess && p.pre_split)
-        e = prefix_tc_supported(p.H, p.Dh, p.bf16) ? launch_prefix_tc(p, s) : launch_prefix_simt(p, 0, s);
+    const bool tc = prefix_tc_supported(p.H, p.Dh, p.bf16);
+    if (p.tail_split) e = tc ? launch_tail_tc(p, s) : launch_prefix_simt(p, 1, s);
+    if (e == cudaSuccess && p.pre_split) e = tc ? launch_prefix_tc(p, s) : launch_prefix_simt(p, 0, s);
     if (e == cudaSuccess) e = launch_prefix_merge(p, s);
     return from_cuda(e);
 }

@@ -63,6 +63,15 @@ struct PrefixParams {
     uint32_t *status;
 };
 
+// The tensor-core combine (k_attend_tc.cu) as segments of the shared-prefix combine: `base`
+// shared rows stand before the own rows; segment x goes to o[x, B * L * H, Dh], ml[x, B * L * H, 2].
+struct AttendPart {
+    int64_t base;
+    float *o;
+    float *ml;
+};
+cudaError_t launch_attend_tc_part(const AttnParams &p, const AttendPart &part, cudaStream_t s);
+
 // Encodes a 3-D tensor map over bf16 [rows, cols]: chunks of 64 columns as the slowest
 // dimension, so one box of box_chunks x box_rows x 64 lands as box_chunks swizzled (128-byte)
 // K-major operand chunks. False if the driver has no encoder or rejects the map.
