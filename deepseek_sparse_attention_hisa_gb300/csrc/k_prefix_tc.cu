@@ -18,16 +18,16 @@
 // for two stages of each operand beside the 64 KB of Q. The ceiling is so about 78 % of the
 // tensor peak.
 //
-// The issue order S(0) S(1) PV(0) S(2) PV(1) ... leaves the softmax of a tile the time of one
-// product of each kind. TMEM layout of both accumulators: lanes 0-63 hold the CTA's 64 rows for
+// S products run up to kSBufs tiles ahead of the PV products, so the tensor cores do not
+// wait for a tile's softmax and for the two crossings between the CTAs around it. TMEM layout of both accumulators: lanes 0-63 hold the CTA's 64 rows for
 // the first half of the columns, lanes 64-127 the same rows for the second half, so a row's
 // logits sit with two threads of one lane each, which exchange their maxima through shared
 // memory. The running maximum is lazy: O and the sums are rescaled only when a tile's maximum
 // exceeds it by more than 8 (log2 units), so p <= 256. P is rounded to bf16 for the second
 // product (a relative 2^-9 per weight, of random sign); sums are of the unrounded weights in f32.
 //
-// Warps of each CTA: 0-3 softmax and epilogue (thread = TMEM lane), 4 loads, 5 (of CTA 0) MMA
-// issue for the pair. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and the CTAs leave.
+// Warps of each CTA: 0-3 softmax and epilogue (thread = TMEM lane), 4 and 6 loads, 5 and 7
+// (of CTA 0) MMA issue for the pair. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and the CTAs leave.
 #include "ops_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -37,8 +37,9 @@ namespace {
 using namespace tc;
 
 constexpr int kH = 64, kDH = 512, kT = 64;
-constexpr int kSoftWarps = 4, kLoadWarp = 4, kMmaWarp = 5, kThreads = 192;
-constexpr int kStages = 2;                              // of K, of V, of S and of P
+constexpr int kSoftWarps = 4, kLoadWarp = 4, kMmaWarp = 5, kLoadVWarp = 6, kMmaPvWarp = 7, kThreads = 256;
+constexpr int kStages = 2;                              // of K, of V and of P
+constexpr int kSBufs = 4;                               // S tiles in TMEM
 constexpr uint32_t kQBytes = kH * kDH * 2;              // 64 KB: 8 chunks [64 rows x 64 dims]
 constexpr uint32_t kKBytes = kT / 2 * kDH * 2;          // 32 KB: 8 chunks [32 rows x 64 dims]
 constexpr uint32_t kVBytes = kT * kDH;                  // 32 KB: 4 chunks [64 rows x 64 dims]
@@ -46,14 +47,14 @@ constexpr uint32_t kPBytes = kH * kT * 2;               // 8 KB: one chunk [64 r
 constexpr uint32_t kKChunk = kT / 2 * 128, kVChunk = kT * 128, kQChunk = kH * 128;
 constexpr uint32_t kOffQ = 0, kOffK = kQBytes, kOffV = kOffK + kStages * kKBytes, kOffP = kOffV + kStages * kVBytes,
                    kOffMisc = kOffP + kStages * kPBytes;
-constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 512;
+constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;   // O: 256 columns, S: 32 each
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f, kLazy = 8.0f;
 
 struct Misc {
     // pair barriers, used in CTA 0: operands have landed in both CTAs; S read and P written by both
-    uint64_t kfull[kStages], vfull[kStages], qfull, sfree[kStages], pfull[kStages], ofree;
+    uint64_t kfull[kStages], vfull[kStages], qfull, sfree[kSBufs], pfull[kStages], ofree;
     // each CTA's own, signalled by the MMAs of the pair
-    uint64_t kempty[kStages], vempty[kStages], qfree, sfull[kStages], pfree[kStages], ofull;
+    uint64_t kempty[kStages], vempty[kStages], qfree, sfull[kSBufs], pfree[kStages], ofull, drain;
     uint32_t tmem;
     int abort;
     float mx[2][2][kH];                                 // [tile parity][column half][row]: a tile's maxima
@@ -75,23 +76,17 @@ __device__ __forceinline__ uint32_t map_to(const void *p, uint32_t cta) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(cta));
     return r;
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+// One arrival on a barrier of the pair. What the waiter goes on to use is its own CTA's TMEM and
+// shared memory, and the counterpart's through the pair's MMAs; each writer's fence (async proxy,
+// tcgen05) stands before its arrival, so no cluster-wide release is needed (it costs about 500
+// cycles, as an acquire does on the waiting side).
+__device__ __forceinline__ void arrive_pair(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
-__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    const long long t0 = clock64();
-    for (uint32_t i = 0; i < (1u << 26); ++i) {
-        uint32_t ok;
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-        if (ok) return true;
-        if ((i & 255u) == 255u && (*abort || clock64() - t0 > kWaitCycles)) return false;
-    }
-    return false;
-}
-__device__ __forceinline__ bool wait_pair_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, wait_pair(bar, parity, abort));
+// A bounded wait by a whole warp; the common case is a barrier that has completed.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const bool v = mbar_try_wait(bar, parity) || mbar_wait_abortable(bar, parity, abort);
+    return __all_sync(0xffffffffu, v);
 }
 // Loads a box of the chunked map; the bytes count on `bar`, which may be the other CTA's.
 __device__ __forceinline__ void load_chunks(uint32_t dst, const CUtensorMap *map, int row, int chunk, uint32_t bar) {
@@ -175,12 +170,16 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&ms->kfull[s], 1); mbar_init(&ms->vfull[s], 1);
-            mbar_init(&ms->sfree[s], 2 * kSoftWarps); mbar_init(&ms->pfull[s], 2 * kSoftWarps);
+            mbar_init(&ms->pfull[s], 2 * kSoftWarps);
             mbar_init(&ms->kempty[s], 1); mbar_init(&ms->vempty[s], 1);
-            mbar_init(&ms->sfull[s], 1); mbar_init(&ms->pfree[s], 1);
+            mbar_init(&ms->pfree[s], 1);
+        }
+        for (int s = 0; s < kSBufs; ++s) {
+            mbar_init(&ms->sfull[s], 1); mbar_init(&ms->sfree[s], 2 * kSoftWarps);
         }
         mbar_init(&ms->qfull, 1); mbar_init(&ms->qfree, 1);
         mbar_init(&ms->ofree, 2 * kSoftWarps); mbar_init(&ms->ofull, 1);
+        mbar_init(&ms->drain, 2);                       // one commit of each issuing warp
         mbar_fence_init();
         ms->abort = 0;
     }
@@ -201,96 +200,105 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
         *abort = 1;
     };
 
-    if (warp == kLoadWarp) {
-        // ---------------- loads of this CTA's share of Q, K and V ----------------
+    if (warp == kLoadWarp || warp == kLoadVWarp) {
+        // ---------------- loads of this CTA's share: Q and K, or V ----------------
+        // (two warps: K runs ahead of V by as many tiles as S runs ahead of PV)
         if (lane == 0) {
+            const bool v = warp == kLoadVWarp;
+            uint64_t *full = v ? ms->vfull : ms->kfull, *empty = v ? ms->vempty : ms->kempty;
+            const uint32_t bytes = v ? kVBytes : kKBytes, dst = sbase + (v ? kOffV : kOffK);
+            const CUtensorMap *map = v ? &vmap : &kmap;
             uint32_t g = 0;
             int n = 0;
             for (int id = first_item; id < items && ok; id += step, ++n) {
                 const Item x = item_of(p, id, rank);
-                if (n > 0 && !wait_pair(&ms->qfree, (n - 1) & 1, abort)) { fail(); break; }
-                if (rank == 0) mbar_arrive_expect_tx(&ms->qfull, 2 * kQBytes);
-                load_chunks(sbase + kOffQ, &qmap, x.row * kH, 0, map_to(&ms->qfull, 0));
+                if (!v) {
+                    if (n > 0 && !mbar_wait_abortable(&ms->qfree, (n - 1) & 1, abort)) { fail(); break; }
+                    if (rank == 0) mbar_arrive_expect_tx(&ms->qfull, 2 * kQBytes);
+                    load_chunks(sbase + kOffQ, &qmap, x.row * kH, 0, map_to(&ms->qfull, 0));
+                }
                 for (int i = 0; i < x.tiles; ++i, ++g) {
-                    const uint32_t s = g % kStages, par = (g / kStages - 1) & 1;
-                    const int row = x.first + i * kT;
-                    if (g >= kStages && !wait_pair(&ms->kempty[s], par, abort)) { fail(); break; }
-                    if (rank == 0) mbar_arrive_expect_tx(&ms->kfull[s], 2 * kKBytes);
-                    load_chunks(sbase + kOffK + s * kKBytes, &kmap, row + rank * (kT / 2), 0, map_to(&ms->kfull[s], 0));
-                    if (g >= kStages && !wait_pair(&ms->vempty[s], par, abort)) { fail(); break; }
-                    if (rank == 0) mbar_arrive_expect_tx(&ms->vfull[s], 2 * kVBytes);
-                    load_chunks(sbase + kOffV + s * kVBytes, &vmap, row, rank * 4, map_to(&ms->vfull[s], 0));
+                    const uint32_t s = g % kStages;
+                    if (g >= kStages && !mbar_wait_abortable(&empty[s], (g / kStages - 1) & 1, abort)) { fail(); break; }
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                    load_chunks(dst + s * bytes, map, x.first + i * kT + (v ? 0 : rank * (kT / 2)), v ? rank * 4 : 0,
+                                map_to(&full[s], 0));
                 }
             }
             if (!ok && rank == 0) {
                 // copies in flight land before the CTAs leave (bounded, whatever the abort flag says)
-                for (uint32_t b = g > kStages ? g - kStages : 0; b <= g; ++b) {
-                    mbar_wait(&ms->kfull[b % kStages], (b / kStages) & 1, 1u << 20);
-                    mbar_wait(&ms->vfull[b % kStages], (b / kStages) & 1, 1u << 20);
-                }
+                for (uint32_t b = g > kStages ? g - kStages : 0; b <= g; ++b)
+                    mbar_wait(&full[b % kStages], (b / kStages) & 1, 1u << 20);
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || warp == kMmaPvWarp) {
         // ---------------- MMA issue (CTA 0, for the pair) ----------------
-        if (rank == 0) {
-            const uint32_t id_s = idesc_bf16_f32(128, kT, 0, 0), id_o = idesc_bf16_f32(128, 256, 0, 1);
+        // One warp issues S = Q K^T, one O += P V: each pays for its own waits and commits, and
+        // S runs ahead of PV by as many tiles as it has buffers.
+        if (rank == 0 && warp == kMmaWarp) {
+            const uint32_t idesc = idesc_bf16_f32(128, kT, 0, 0);
             const uint64_t qd = smem_desc_sw128(sbase + kOffQ, 16, 1024);
-            uint32_t gs = 0, gp = 0;                    // tiles whose first / second product was issued
+            uint32_t g = 0;
             int n = 0;
-            auto first = [&]() -> bool {                // S = Q K^T of tile gs
-                const uint32_t s = gs % kStages;
-                if (!wait_pair_warp(&ms->kfull[s], (gs / kStages) & 1, abort)) return false;
-                if (gs >= kStages && !wait_pair_warp(&ms->sfree[s], (gs / kStages - 1) & 1, abort)) return false;
-                fence_after_sync();
-                const uint64_t kd = smem_desc_sw128(sbase + kOffK + s * kKBytes, 16, 1024);
-                const uint32_t d = tmem + kColS + s * (kT / 2);
-#pragma unroll
-                for (int ks = 0; ks < kDH / 16; ++ks)
-                    mma_pair(d, desc_add(qd, (ks >> 2) * kQChunk + (ks & 3) * 32),
-                             desc_add(kd, (ks >> 2) * kKChunk + (ks & 3) * 32), id_s, ks > 0);
-                commit_pair(&ms->sfull[s]);
-                commit_pair(&ms->kempty[s]);
-                ++gs;
-                return true;
-            };
-            auto second = [&](bool start) -> bool {     // O += P V of tile gp
-                const uint32_t s = gp % kStages;
-                if (!wait_pair_warp(&ms->vfull[s], (gp / kStages) & 1, abort)) return false;
-                if (!wait_pair_warp(&ms->pfull[s], (gp / kStages) & 1, abort)) return false;
-                fence_after_sync();
-                const uint64_t pd = smem_desc_sw128(sbase + kOffP + s * kPBytes, 16, 1024);
-                const uint64_t vd = smem_desc_sw128(sbase + kOffV + s * kVBytes, kVChunk, 1024);
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int ks = 0; ks < kT / 16; ++ks)
-                        mma_pair(tmem + kColO + m * 128, desc_add(pd, ks * 32), desc_add(vd, m * 2 * kVChunk + ks * 2048), id_o,
-                                 (ks > 0 || !start) ? 1u : 0u);
-                commit_pair(&ms->vempty[s]);
-                commit_pair(&ms->pfree[s]);
-                ++gp;
-                return true;
-            };
             for (int id = first_item; id < items && ok; id += step, ++n) {
                 const Item x = item_of(p, id, 0);
-                if (!wait_pair_warp(&ms->qfull, n & 1, abort)) { fail(); break; }
-                fence_after_sync();
-                if (!first()) { fail(); break; }
-                for (int i = 0; i < x.tiles; ++i) {
-                    if (i + 1 < x.tiles && !first()) { fail(); break; }
-                    if (i + 1 == x.tiles) commit_pair(&ms->qfree);        // every S product of the item is issued
-                    // O starts over once the epilogues have read the item before
-                    if (i == 0 && n > 0 && !wait_pair_warp(&ms->ofree, (n - 1) & 1, abort)) { fail(); break; }
-                    if (!second(i == 0)) { fail(); break; }
+                if (!wait_warp(&ms->qfull, n & 1, abort)) { fail(); break; }
+                for (int i = 0; i < x.tiles; ++i, ++g) {
+                    const uint32_t s = g % kStages, b = g % kSBufs;
+                    if (!wait_warp(&ms->kfull[s], (g / kStages) & 1, abort) ||
+                        (g >= kSBufs && !wait_warp(&ms->sfree[b], (g / kSBufs - 1) & 1, abort))) {
+                        fail();
+                        break;
+                    }
+                    fence_after_sync();
+                    const uint64_t kd = smem_desc_sw128(sbase + kOffK + s * kKBytes, 16, 1024);
+                    const uint32_t d = tmem + kColS + b * (kT / 2);
+#pragma unroll
+                    for (int ks = 0; ks < kDH / 16; ++ks)
+                        mma_pair(d, desc_add(qd, (ks >> 2) * kQChunk + (ks & 3) * 32),
+                                 desc_add(kd, (ks >> 2) * kKChunk + (ks & 3) * 32), idesc, ks > 0);
+                    commit_pair(&ms->sfull[b]);
+                    commit_pair(&ms->kempty[s]);
                 }
-                if (!ok) break;
-                commit_pair(&ms->ofull);
+                if (ok) commit_pair(&ms->qfree);
             }
-            if (!ok) {                                  // MMAs in flight end before TMEM is freed
-                commit_pair(&ms->qfree);
-                for (int k = 0; k < 2; ++k) mbar_wait(&ms->qfree, k, 1u << 20);
+        } else if (rank == 0) {
+            const uint32_t idesc = idesc_bf16_f32(128, 256, 0, 1);
+            uint32_t g = 0;
+            int n = 0;
+            for (int id = first_item; id < items && ok; id += step, ++n) {
+                const Item x = item_of(p, id, 0);
+                // O starts over once the epilogues have read the item before
+                if (n > 0 && !wait_warp(&ms->ofree, (n - 1) & 1, abort)) { fail(); break; }
+                for (int i = 0; i < x.tiles; ++i, ++g) {
+                    const uint32_t s = g % kStages;
+                    if (!wait_warp(&ms->vfull[s], (g / kStages) & 1, abort) ||
+                        !wait_warp(&ms->pfull[s], (g / kStages) & 1, abort)) {
+                        fail();
+                        break;
+                    }
+                    fence_after_sync();
+                    const uint64_t pd = smem_desc_sw128(sbase + kOffP + s * kPBytes, 16, 1024);
+                    const uint64_t vd = smem_desc_sw128(sbase + kOffV + s * kVBytes, kVChunk, 1024);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int ks = 0; ks < kT / 16; ++ks)
+                            mma_pair(tmem + kColO + m * 128, desc_add(pd, ks * 32), desc_add(vd, m * 2 * kVChunk + ks * 2048),
+                                     idesc, (ks > 0 || i > 0) ? 1u : 0u);
+                    commit_pair(&ms->vempty[s]);
+                    commit_pair(&ms->pfree[s]);
+                }
+                if (ok) commit_pair(&ms->ofull);
             }
+        }
+        if (rank == 0) {
+            // MMAs in flight end before TMEM is freed (bounded, whatever the abort flag says)
+            commit_pair(&ms->drain);
+            __syncwarp();
+            mbar_wait(&ms->drain, 0, 1u << 24);
+            __syncwarp();
         }
     } else {
         // ---------------- softmax and epilogue: thread = TMEM lane ----------------
@@ -306,14 +314,14 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
             const Item x = item_of(p, id, rank);
             float m2 = -INFINITY, l = 0.f;
             for (int i = 0; i < x.tiles; ++i, ++g) {
-                const uint32_t s = g % kStages, par = (g / kStages) & 1;
-                good = good && wait_pair_warp(&ms->sfull[s], par, abort);
+                const uint32_t s = g % kStages, par = (g / kStages) & 1, sb = g % kSBufs;
+                good = good && wait_warp(&ms->sfull[sb], (g / kSBufs) & 1, abort);
                 fence_after_sync();
                 float v[32];
-                tmem_ld32(lanes + kColS + s * (kT / 2), v);
+                tmem_ld32(lanes + kColS + sb * (kT / 2), v);
                 fence_before_sync();
                 __syncwarp();
-                if (lane == 0) arrive_cluster(map_to(&ms->sfree[s], 0));
+                if (lane == 0) arrive_pair(map_to(&ms->sfree[sb], 0));
                 const int left = x.rows - i * kT - half * (kT / 2);      // of this thread's 32 shared rows
                 if (left < 32) {
 #pragma unroll
@@ -349,9 +357,9 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                     for (int k = 0; k < w; ++k) v[k] += v[k + w];
                 l = l * alpha + v[0];
                 // the P buffer's last reader, and for a rescale every product so far, has completed
-                if (g >= kStages) good = good && wait_pair_warp(&ms->pfree[s], par ^ 1, abort);
+                if (g >= kStages) good = good && wait_warp(&ms->pfree[s], par ^ 1, abort);
                 if (__any_sync(0xffffffffu, alpha != 1.f) && i > 0) {
-                    good = good && wait_pair_warp(&ms->pfree[(g - 1) % kStages], ((g - 1) / kStages) & 1, abort);
+                    good = good && wait_warp(&ms->pfree[(g - 1) % kStages], ((g - 1) / kStages) & 1, abort);
                     fence_after_sync();
 #pragma unroll 1
                     for (int c = 0; c < 256; c += 16) {
@@ -372,10 +380,10 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                 fence_async_smem();
                 fence_before_sync();
                 __syncwarp();
-                if (lane == 0) arrive_cluster(map_to(&ms->pfull[s], 0));
+                if (lane == 0) arrive_pair(map_to(&ms->pfull[s], 0));
             }
             if (!ok) break;
-            good = good && wait_pair_warp(&ms->ofull, n & 1, abort);
+            good = good && wait_warp(&ms->ofull, n & 1, abort);
             fence_after_sync();
             // the row's sum joins over its two threads
             ms->mx[g & 1][half][r] = l;
@@ -397,7 +405,7 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
             }
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) arrive_cluster(map_to(&ms->ofree, 0));
+            if (lane == 0) arrive_pair(map_to(&ms->ofree, 0));
         }
     }
     if (!ok) flag(p.status, HISA_DEV_TIMEOUT);
