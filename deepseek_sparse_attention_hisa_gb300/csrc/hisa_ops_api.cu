@@ -115,7 +115,7 @@ cudaError_t launch_tail_tc(const PrefixParams &p, cudaStream_t s) {
     a.scale = p.scale;
     a.q = p.q; a.local_kv = p.local_kv; a.local_len = p.local_len; a.local_pos0 = p.local_pos0;
     a.pooled_kv = p.pooled_kv; a.kv_off = p.kv_off; a.t0 = p.t0;
-    a.nsplit = p.tail_split; a.rows_per_split = p.tail_rows;
+    a.nsplit = p.tail_split;
     a.kv_bf16 = p.bf16;
     a.status = p.status;
     return launch_attend_tc_part(a, AttendPart{p.P, p.part_o, p.part_ml}, s);

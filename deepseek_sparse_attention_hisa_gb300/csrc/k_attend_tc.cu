@@ -152,8 +152,10 @@ __device__ __forceinline__ Item item_of(const AttnParams &p, const AttendPart &p
     x.nloc = hi > lo ? hi - lo : 0;
     const int64_t npool = p.I ? (int64_t)p.k : x.Np;
     const int64_t ntot = x.nloc + npool;
-    x.e0 = (int64_t)x.split * p.rows_per_split;
-    x.e1 = x.e0 + p.rows_per_split;
+    int64_t per = p.rows_per_split;
+    if (kPart) per = ((ntot + p.nsplit - 1) / p.nsplit + kTR - 1) / kTR * kTR;   // even parts of this row's own list
+    x.e0 = (int64_t)x.split * per;
+    x.e1 = x.e0 + per;
     x.e1 = x.e1 > ntot ? ntot : x.e1;
     x.T = x.e1 > x.e0 ? (int)((x.e1 - x.e0 + kTR - 1) / kTR) : 0;
     x.V = !kPart && p.causal ? visible_len(x.t, p.r, x.Np) : x.Np;
@@ -210,7 +212,11 @@ __device__ __forceinline__ void attend_tc(const AttnParams &p, const AttendPart 
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = misc->tmem;
-    if (kPart) grid_dep_wait();
+    if (kPart) {
+        // the shared rows' kernel follows and depends on nothing of this one: it may take idle SMs
+        grid_dep_wait();
+        grid_dep_trigger();
+    }
     // else no grid_dep_wait() here: the producers wait before their first selected id and the
     // epilogue before its first output write; the first item's q and local rows go first
     bool ok = true;

@@ -26,7 +26,7 @@
 // exceeds it by more than 8 (log2 units), so p <= 256. P is rounded to bf16 for the second
 // product (a relative 2^-9 per weight, of random sign); sums are of the unrounded weights in f32.
 //
-// Warps of each CTA: 0-3 softmax and epilogue (thread = TMEM lane), 4 and 6 loads, 5 and 7
+// Warps of each CTA: 0-3 softmax and epilogue (thread = TMEM lane), 4 and 6 loads, 5, 7 and 8
 // (of CTA 0) MMA issue for the pair. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and the CTAs leave.
 #include "ops_internal.cuh"
 #include "tc_ptx.cuh"
@@ -37,7 +37,8 @@ namespace {
 using namespace tc;
 
 constexpr int kH = 64, kDH = 512, kT = 64;
-constexpr int kSoftWarps = 4, kLoadWarp = 4, kMmaWarp = 5, kLoadVWarp = 6, kMmaPvWarp = 7, kThreads = 256;
+constexpr int kSoftWarps = 4, kLoadWarp = 4, kMmaWarp = 5, kLoadVWarp = 6, kMmaPvWarp = 7, kMmaWarp2 = 8,
+              kThreads = 288;
 constexpr int kStages = 2;                              // of K, of V and of P
 constexpr int kSBufs = 4;                               // S tiles in TMEM
 constexpr uint32_t kQBytes = kH * kDH * 2;              // 64 KB: 8 chunks [64 rows x 64 dims]
@@ -177,9 +178,9 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
         for (int s = 0; s < kSBufs; ++s) {
             mbar_init(&ms->sfull[s], 1); mbar_init(&ms->sfree[s], 2 * kSoftWarps);
         }
-        mbar_init(&ms->qfull, 1); mbar_init(&ms->qfree, 1);
+        mbar_init(&ms->qfull, 1); mbar_init(&ms->qfree, 2);   // one commit of each S warp
         mbar_init(&ms->ofree, 2 * kSoftWarps); mbar_init(&ms->ofull, 1);
-        mbar_init(&ms->drain, 2);                       // one commit of each issuing warp
+        mbar_init(&ms->drain, 3);                       // one commit of each issuing warp
         mbar_fence_init();
         ms->abort = 0;
     }
@@ -193,7 +194,9 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
     cluster_sync();                                     // both CTAs' barriers and TMEM are there
     fence_after_sync();
     const uint32_t tmem = ms->tmem;
-    grid_dep_wait();
+    if (!p.tail_split) grid_dep_wait();
+    // else the grid before is the one of the call's own lists, which nothing here depends on and
+    // which let this one start once all work before it had completed; waited for at the end
     bool ok = true;
     auto fail = [&]() {
         ok = false;
@@ -232,11 +235,13 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp || warp == kMmaPvWarp) {
+    } else if (warp == kMmaWarp || warp == kMmaWarp2 || warp == kMmaPvWarp) {
         // ---------------- MMA issue (CTA 0, for the pair) ----------------
-        // One warp issues S = Q K^T, one O += P V: each pays for its own waits and commits, and
-        // S runs ahead of PV by as many tiles as it has buffers.
-        if (rank == 0 && warp == kMmaWarp) {
+        // Two warps issue S = Q K^T of the even and of the odd tiles, one O += P V: a warp's waits
+        // and commits (about 900 cycles a tile) hide behind the other's products. S runs ahead of
+        // PV by as many tiles as it has buffers.
+        if (rank == 0 && warp != kMmaPvWarp) {
+            const uint32_t mine = warp == kMmaWarp2;
             const uint32_t idesc = idesc_bf16_f32(128, kT, 0, 0);
             const uint64_t qd = smem_desc_sw128(sbase + kOffQ, 16, 1024);
             uint32_t g = 0;
@@ -245,6 +250,7 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                 const Item x = item_of(p, id, 0);
                 if (!wait_warp(&ms->qfull, n & 1, abort)) { fail(); break; }
                 for (int i = 0; i < x.tiles; ++i, ++g) {
+                    if ((g & 1) != mine) continue;
                     const uint32_t s = g % kStages, b = g % kSBufs;
                     if (!wait_warp(&ms->kfull[s], (g / kStages) & 1, abort) ||
                         (g >= kSBufs && !wait_warp(&ms->sfree[b], (g / kSBufs - 1) & 1, abort))) {
@@ -411,6 +417,7 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
     if (!ok) flag(p.status, HISA_DEV_TIMEOUT);
     fence_before_sync();
     __syncthreads();
+    grid_dep_wait();                                    // so that the merge, which waits for this grid, has both
     cluster_sync();                                     // no CTA leaves while the other may signal it
     if (warp == kMmaWarp) {
         fence_after_sync();
