@@ -144,16 +144,22 @@ def _check(status: int, where: str) -> None:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_current_raw_stream = None       # torch's current stream of the current device, as a handle
 
 
 def _stream(stream):
-    import torch
+    global _current_raw_stream
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        if _current_raw_stream is None:
+            import torch
+            torch.cuda.current_stream()                  # initialises CUDA, or says why it cannot
+            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _current_raw_stream = lambda: raw(device())  # noqa: E731
+        return _current_raw_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def dtype_code(t) -> int:

@@ -7,16 +7,19 @@
 // Bound by memory: about 6 operations per element against 4 to 16 bytes. A team of threads
 // holds a whole row in registers (a warp for rows of at most 1024 columns, else a CTA), so the
 // sum of squares, the scales and the output need no second read. Teams walk the rows with a
-// grid stride, and a team fetches its next row before it reduces the current one, so the
+// grid stride, and the next rows are on their way while a team reduces the current one, so the
 // barrier of the reduction does not leave the memory system idle. Sums are f32: each thread's
 // own columns in order, then a fixed tree over lanes and warps, so a row's result does not
 // depend on the other rows or on the launch.
 #include <cuda_fp8.h>
 
 #include "ops_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace hisa {
 namespace {
+
+constexpr int kMaxSmem = 224 * 1024;   // dynamic shared memory of a CTA
 
 struct None {};                       // no residual
 
@@ -72,19 +75,19 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-// Largest magnitude as bits: NaN orders above infinity, so a group that holds one gets a NaN scale.
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-__device__ __forceinline__ uint32_t lanes_max(uint32_t v, int lanes) {
-    for (int o = lanes >> 1; o >= 1; o >>= 1) {
-        const uint32_t u = __shfl_xor_sync(0xffffffffu, v, o);
-        v = u > v ? u : v;
-    }
+// The larger magnitude; NaN if either is one, so a group that holds a NaN gets a NaN scale.
+__device__ __forceinline__ float max_mag(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+__device__ __forceinline__ float lanes_max(float v, int lanes) {
+    for (int o = lanes >> 1; o >= 1; o >>= 1) v = max_mag(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
-// Scale of a group whose largest magnitude has these bits. The floor keeps the quotient normal.
-__device__ __forceinline__ float scale_of(uint32_t bits, int pow2) {
-    float a = __uint_as_float(bits);
+// Scale of a group of largest magnitude a. The floor keeps the quotient normal.
+__device__ __forceinline__ float scale_of(float a, int pow2) {
     a = a < 1e-10f ? 1e-10f : a;
     float s = a / 448.f;
     if (pow2 && s < INFINITY) {
@@ -94,53 +97,123 @@ __device__ __forceinline__ float scale_of(uint32_t bits, int pow2) {
     return s;
 }
 
-// Sum (or maximum) over the block's warps: one partial per warp, one barrier. Callers alternate
-// between two arrays, so the next call's writes meet no late reader.
-__device__ __forceinline__ float block_sum(float v, float *red, int warps) {
+// Joins one value per warp over the CTA: a partial each, one barrier, and the 32 slots (unused
+// ones hold 0) read as vectors. Callers alternate between two arrays, so the next call's writes
+// meet no late reader.
+__device__ __forceinline__ float block_sum(float v, float *red) {
     v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < warps; ++w) s += red[w];
-    return s;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < (int)(blockDim.x + 127) / 128; ++w) {
+        const float4 u = reinterpret_cast<const float4 *>(red)[w];
+        s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w;
+    }
+    return (s.x + s.y) + (s.z + s.w);
 }
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *red, int warps) {
+__device__ __forceinline__ float block_max(float v, float *red) {
     v = lanes_max(v, 32);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    uint32_t s = 0;
-    for (int w = 0; w < warps; ++w) s = red[w] > s ? red[w] : s;
+    float s = 0.f;
+    for (int w = 0; w < (int)(blockDim.x + 31) / 32; ++w) s = max_mag(s, red[w]);
     return s;
 }
 
-// Rows moved in units of 8 columns. WARP: a warp per row, else the CTA per row.
-template <typename XT, typename RT, int VPT, bool WARP>
-__global__ void __launch_bounds__(VPT <= 2 || WARP ? 512 : 1024, VPT <= 2 && !WARP ? 2 : 1) k_norm_wide(NormParams p) {
-    constexpr bool kRes = !std::is_same<RT, None>::value;
-    constexpr bool kPrefetch = VPT <= 2 || WARP;
-    __shared__ float red[2][32];
-    __shared__ uint32_t redm[2][32];
-    const int T = WARP ? 32 : blockDim.x;
-    const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-    const int warps = blockDim.x >> 5;
-    const int nvec = p.cols >> 3;
-    const int64_t step = WARP ? (int64_t)gridDim.x * warps : gridDim.x;
-    const float inv = 1.f / (float)p.cols;
-    int64_t row = WARP ? (int64_t)blockIdx.x * warps + (threadIdx.x >> 5) : blockIdx.x;
+// What both kernels of 8-column units do with a row. With t = h w, f = 1 / sqrt(mean(h^2) + eps) > 0
+// and y = t f, a group's largest |y| is f times its largest |t| (rounding is monotone), so the
+// scales need no pass after the reduction.
+template <typename RT, int VPT>
+struct Row {
+    float h[VPT][8];                                  // the row, then t
+    float top[VPT];                                   // largest |t| of the unit's group
+    float ss;
 
-    float w[VPT][8];                                  // this thread's columns, the same for every row
+    // Unit i: h = x (+ residual, rounded as stored), its squares, t = h w.
+    template <typename XT>
+    __device__ __forceinline__ void take(const NormParams &p, int i, int v, bool in, int64_t row, const Raw8<XT> &x,
+                                         const Raw8<RT> &r, const float (&w)[8]) {
+        if (!in) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = i * T + t;
+            for (int e = 0; e < 8; ++e) h[i][e] = 0.f;
+            return;
+        }
+        unpack(x, h[i]);
+        if constexpr (!std::is_same<RT, None>::value) {
+            float q[8];
+            unpack(r, q);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[i][e] = 0.f;
-        if (v < nvec) {
-            const float4 *wp = reinterpret_cast<const float4 *>(p.w + (int64_t)v * 8);
-            const float4 a = __ldg(wp), b = __ldg(wp + 1);
-            w[i][0] = a.x; w[i][1] = a.y; w[i][2] = a.z; w[i][3] = a.w;
-            w[i][4] = b.x; w[i][5] = b.y; w[i][6] = b.z; w[i][7] = b.w;
+            for (int e = 0; e < 8; ++e) h[i][e] += q[e];
+            if constexpr (std::is_same<RT, __nv_bfloat16>::value) {
+                Raw8<__nv_bfloat16> back;
+                back.v[0] = pack_bf16(h[i]);
+                unpack(back, h[i]);                    // the norm is over the sum as stored
+            }
+            if (p.res_out) store8(p.res_out, row * p.ld_res + (int64_t)v * 8, std::is_same<RT, __nv_bfloat16>::value, h[i]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            ss += h[i][e] * h[i][e];
+            h[i][e] *= w[e];
         }
     }
+    // Largest |t| per unit, joined over a group's lanes (or, for one scale per row, this thread's units).
+    __device__ __forceinline__ void tops(const NormParams &p) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float m[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m[e] = max_mag(h[i][e], h[i][e + 4]);
+            top[i] = max_mag(max_mag(m[0], m[1]), max_mag(m[2], m[3]));
+        }
+        if (p.group) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) top[i] = lanes_max(top[i], p.group >> 3);
+        } else {
+#pragma unroll
+            for (int i = 1; i < VPT; ++i) top[0] = max_mag(top[0], top[i]);
+        }
+    }
+    __device__ __forceinline__ void put(const NormParams &p, int i, int v, int64_t row, float f) {
+        const int64_t at = row * p.ld_out + (int64_t)v * 8;
+        if (p.out_dtype != HISA_E4M3) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[i][e] *= f;
+            store8(p.out, at, p.out_dtype == HISA_BF16, h[i]);
+            return;
+        }
+        const float s = scale_of(top[p.group ? i : 0] * f, p.pow2);
+        const float q = f / s;                         // t q is within a few f32 steps of y / s
+        if ((p.group ? v & ((p.group >> 3) - 1) : v) == 0)
+            p.scales[p.group ? row * (p.cols / p.group) + v / (p.group >> 3) : row] = s;
+        uint32_t c[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(h[i][4 * k] * q, h[i][4 * k + 1] * q), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h[i][4 * k + 2] * q, h[i][4 * k + 3] * q), __NV_SATFINITE, __NV_E4M3);
+            c[k] = lo | (hi << 16);
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + at) = make_uint2(c[0], c[1]);
+    }
+};
+
+__device__ __forceinline__ void load_w(const float *base, int v, int nvec, float (&w)[8]) {
+    const float4 *wp = reinterpret_cast<const float4 *>(base + (int64_t)(v < nvec ? v : 0) * 8);
+    const float4 a = __ldg(wp), b = __ldg(wp + 1);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+}
+
+// Rows of at most 1024 columns: a warp per row, the next row's loads in flight in registers.
+template <typename XT, typename RT, int VPT>
+__global__ void __launch_bounds__(256, 2) k_norm_warp(NormParams p) {
+    const int t = threadIdx.x & 31, nvec = p.cols >> 3;
+    const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+    int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const float inv = 1.f / (float)p.cols;
+    float w[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) load_w(p.w, i * 32 + t, nvec, w[i]);
     grid_dep_wait();
     Raw8<XT> x[VPT];
     Raw8<RT> r[VPT];
@@ -148,7 +221,7 @@ __global__ void __launch_bounds__(VPT <= 2 || WARP ? 512 : 1024, VPT <= 2 && !WA
         if (at >= p.rows) return;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = i * T + t;
+            const int v = i * 32 + t;
             if (v < nvec) {
                 load_raw(x[i], p.x, at * p.ld_x + (int64_t)v * 8);
                 load_raw(r[i], p.res, at * p.ld_res + (int64_t)v * 8);
@@ -156,87 +229,99 @@ __global__ void __launch_bounds__(VPT <= 2 || WARP ? 512 : 1024, VPT <= 2 && !WA
         }
     };
     fetch(row);
-    for (int par = 0; row < p.rows; row += step, par ^= 1) {
-        float h[VPT][8];
-        float ss = 0.f;
+    for (; row < p.rows; row += step) {
+        Row<RT, VPT> m;
+        m.ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = i * T + t;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] = 0.f;
-            if (v >= nvec) continue;
-            unpack(x[i], h[i]);
-            if constexpr (kRes) {
-                float q[8];
-                unpack(r[i], q);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[i][e] += q[e];
-                if constexpr (std::is_same<RT, __nv_bfloat16>::value) {
-                    Raw8<__nv_bfloat16> back;
-                    back.v[0] = pack_bf16(h[i]);
-                    unpack(back, h[i]);                // the norm is over the sum as stored
-                }
-                if (p.res_out) store8(p.res_out, row * p.ld_res + (int64_t)v * 8, std::is_same<RT, __nv_bfloat16>::value, h[i]);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss += h[i][e] * h[i][e];
+        for (int i = 0; i < VPT; ++i) m.take(p, i, i * 32 + t, i * 32 + t < nvec, row, x[i], r[i], w[i]);
+        fetch(row + step);
+        if (p.out_dtype == HISA_E4M3) {
+            m.tops(p);
+            if (!p.group) m.top[0] = lanes_max(m.top[0], 32);
         }
-        if (kPrefetch) fetch(row + step);
-        ss = WARP ? warp_sum(ss) : block_sum(ss, red[par], warps);
-        const float f = 1.f / sqrtf(ss * inv + p.eps);
+        const float f = 1.f / sqrtf(warp_sum(m.ss) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
+            if (i * 32 + t < nvec) m.put(p, i, i * 32 + t, row, f);
+    }
+}
+
+// Longer rows: a CTA per row. Rows to come are copied to shared memory asynchronously, STAGES - 1
+// of them in flight; a thread copies exactly the units that it reads itself, so it waits for its
+// own copies and needs no barrier for them.
+template <typename XT, typename RT, int VPT, int STAGES>
+__global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) k_norm_cta(NormParams p) {
+    constexpr int kX = sizeof(XT) / 2, kR = std::is_same<RT, None>::value ? 0 : sizeof(RT) / 2;   // 16-byte pieces per unit
+    extern __shared__ __align__(16) uint4 ring[];     // [stage][piece][unit]
+    __shared__ __align__(16) float red[2][32], redm[2][32];
+    const int T = blockDim.x, t = threadIdx.x, nvec = p.cols >> 3;
+    const float inv = 1.f / (float)p.cols;
+    if (t < 32) red[0][t] = red[1][t] = 0.f;
+    __syncthreads();
+    constexpr bool kHoldW = VPT <= 2;                 // this thread's weights stay in registers
+    float w[kHoldW ? VPT : 1][8];
+    if constexpr (kHoldW) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * f * w[i][e];
-        if (p.out_dtype != HISA_E4M3) {
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int v = i * T + t;
-                if (v < nvec) store8(p.out, row * p.ld_out + (int64_t)v * 8, p.out_dtype == HISA_BF16, h[i]);
-            }
-        } else {
-            uint32_t top[VPT];
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                top[i] = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t u = mag(h[i][e]);
-                    top[i] = u > top[i] ? u : top[i];
-                }
-            }
-            if (p.group == 0) {
-#pragma unroll
-                for (int i = 1; i < VPT; ++i) top[0] = top[i] > top[0] ? top[i] : top[0];
-                const uint32_t all = WARP ? lanes_max(top[0], 32) : block_max(top[0], redm[par], warps);
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) top[i] = all;
-            } else {
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) top[i] = lanes_max(top[i], p.group >> 3);
-            }
+        for (int i = 0; i < VPT; ++i) load_w(p.w, i * T + t, nvec, w[i]);
+    }
+    grid_dep_wait();
+    auto copy = [&](int64_t row, int stage) {
+        if (row < p.rows) {
+            uint4 *dst = ring + (int64_t)stage * (kX + kR) * nvec;
+            const uint4 *sx = reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + row * p.ld_x);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int v = i * T + t;
                 if (v >= nvec) continue;
-                const float s = scale_of(top[i], p.pow2);
-                const float q = 1.f / s;               // one division per unit; y * q is within an f32 step or two of y / s
-                const int lane0 = p.group ? (v & ((p.group >> 3) - 1)) : v;
-                if (lane0 == 0) p.scales[p.group ? row * (p.cols / p.group) + v / (p.group >> 3) : row] = s;
-                uint32_t c[2];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(h[i][4 * k] * q, h[i][4 * k + 1] * q),
-                                                                 __NV_SATFINITE, __NV_E4M3);
-                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h[i][4 * k + 2] * q, h[i][4 * k + 3] * q),
-                                                                 __NV_SATFINITE, __NV_E4M3);
-                    c[k] = lo | (hi << 16);
+                for (int k = 0; k < kX; ++k) tc::cp_async16(tc::smem_u32(dst + k * nvec + v), sx + kX * v + k);
+                if constexpr (kR > 0) {
+                    const uint4 *sr = reinterpret_cast<const uint4 *>(static_cast<const RT *>(p.res) + row * p.ld_res);
+#pragma unroll
+                    for (int k = 0; k < kR; ++k) tc::cp_async16(tc::smem_u32(dst + (kX + k) * nvec + v), sr + kR * v + k);
                 }
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + row * p.ld_out + (int64_t)v * 8) =
-                    make_uint2(c[0], c[1]);
             }
         }
-        if (!kPrefetch) fetch(row + step);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) copy(blockIdx.x + (int64_t)s * gridDim.x, s);
+    int stage = 0, par = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
+        if (STAGES == 1) copy(row, 0);
+        asm volatile("cp.async.wait_group %0;" :: "n"(STAGES > 1 ? STAGES - 2 : 0) : "memory");
+        const uint4 *src = ring + (int64_t)stage * (kX + kR) * nvec;
+        Row<RT, VPT> m;
+        m.ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * T + t;
+            Raw8<XT> x;
+            Raw8<RT> r;
+            if (v < nvec) {
+#pragma unroll
+                for (int k = 0; k < kX; ++k) x.v[k] = src[k * nvec + v];
+                if constexpr (kR > 0) {
+#pragma unroll
+                    for (int k = 0; k < kR; ++k) r.v[k] = src[(kX + k) * nvec + v];
+                }
+            }
+            if constexpr (!kHoldW) load_w(p.w, v, nvec, w[0]);
+            m.take(p, i, v, v < nvec, row, x, r, w[kHoldW ? i : 0]);
+        }
+        if (STAGES > 1) {
+            // into the stage read by the row before
+            copy(row + (int64_t)(STAGES - 1) * gridDim.x, stage == 0 ? STAGES - 1 : stage - 1);
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
+        }
+        if (p.out_dtype == HISA_E4M3) {
+            m.tops(p);
+            if (!p.group) m.top[0] = block_max(m.top[0], redm[par]);
+        }
+        const float f = 1.f / sqrtf(block_sum(m.ss, red[par]) * inv + p.eps);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (i * T + t < nvec) m.put(p, i, i * T + t, row, f);
     }
 }
 
@@ -250,13 +335,14 @@ __device__ __forceinline__ float load1(const void *base, int64_t at) {
 // row, single elements, neighbouring threads on neighbouring columns. A warp's 32 columns lie
 // in one scale group (groups are multiples of 32), whose maximum is joined in shared memory.
 template <typename XT, typename RT, int EPT>
-__global__ void __launch_bounds__(1024, 1) k_norm_narrow(NormParams p) {
+__global__ void __launch_bounds__(EPT == 16 ? 512 : 1024, EPT == 16 ? 2 : 1) k_norm_narrow(NormParams p) {
     constexpr bool kRes = !std::is_same<RT, None>::value;
-    __shared__ float red[2][32];
-    __shared__ uint32_t redm[2][32];
-    __shared__ uint32_t gmax[1024];
-    const int T = blockDim.x, t = threadIdx.x, warps = T >> 5;
+    __shared__ __align__(16) float red[2][32], redm[2][32];
+    __shared__ float gmax[1024];
+    const int T = blockDim.x, t = threadIdx.x;
     const float inv = 1.f / (float)p.cols;
+    if (t < 32) red[0][t] = red[1][t] = 0.f;
+    __syncthreads();
     grid_dep_wait();
     int par = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
@@ -289,9 +375,9 @@ __global__ void __launch_bounds__(1024, 1) k_norm_narrow(NormParams p) {
             }
             ss += h[i] * h[i];
         }
-        ss = block_sum(ss, red[par], warps);
+        ss = block_sum(ss, red[par]);
         const float f = 1.f / sqrtf(ss * inv + p.eps);
-        uint32_t all = 0;
+        float all = 0.f;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
             const int c = i * T + t;
@@ -311,12 +397,12 @@ __global__ void __launch_bounds__(1024, 1) k_norm_narrow(NormParams p) {
         }
         if (p.group == 0) {
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) all = mag(h[i]) > all ? mag(h[i]) : all;
-            all = block_max(all, redm[par], warps);
+            for (int i = 0; i < EPT; ++i) all = max_mag(all, h[i]);
+            all = block_max(all, redm[par]);
         } else {
 #pragma unroll
             for (int i = 0; i < EPT; ++i) {
-                const uint32_t m = lanes_max(mag(h[i]), 32);
+                const float m = lanes_max(fabsf(h[i]), 32);
                 const int c = i * T + t;
                 if ((t & 31) == 0 && c < p.cols) gmax[c >> 5] = m;
             }
@@ -326,10 +412,10 @@ __global__ void __launch_bounds__(1024, 1) k_norm_narrow(NormParams p) {
         for (int i = 0; i < EPT; ++i) {
             const int c = i * T + t;
             if (c >= p.cols) continue;
-            uint32_t top = all;
+            float top = all;
             if (p.group) {
                 const int g0 = c / p.group * (p.group >> 5);
-                for (int k = 0; k < (p.group >> 5); ++k) top = gmax[g0 + k] > top ? gmax[g0 + k] : top;
+                for (int k = 0; k < (p.group >> 5); ++k) top = max_mag(top, gmax[g0 + k]);
             }
             const float s = scale_of(top, p.pow2);
             if (p.group ? c % p.group == 0 : c == 0) p.scales[p.group ? row * (p.cols / p.group) + c / p.group : row] = s;
@@ -340,32 +426,43 @@ __global__ void __launch_bounds__(1024, 1) k_norm_narrow(NormParams p) {
 }
 
 template <auto Kernel>
-cudaError_t go(const NormParams &p, int threads, int64_t rows_per_cta, cudaStream_t s) {
+cudaError_t go(const NormParams &p, int threads, int64_t rows_per_cta, size_t smem, cudaStream_t s) {
+    if (smem) {
+        const cudaError_t e = smem_attr_once<Kernel>(kMaxSmem);
+        if (e != cudaSuccess) return e;
+    }
     // as many CTAs as the SMs hold at once; they walk the rows
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    int per = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, Kernel, threads, 0);
-    if (e != cudaSuccess) return e;
-    const int64_t want = (p.rows + rows_per_cta - 1) / rows_per_cta, most = (int64_t)sms * (per > 0 ? per : 1);
-    return launch_pdl(Kernel, dim3((unsigned)(want < most ? want : most)), dim3(threads), 0, s, p.chained, p);
+    const int64_t want = (p.rows + rows_per_cta - 1) / rows_per_cta;
+    int64_t most = sms;
+    if (want > sms) {
+        int per = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, Kernel, threads, smem);
+        if (e != cudaSuccess) return e;
+        most = (int64_t)sms * (per > 0 ? per : 1);
+    }
+    return launch_pdl(Kernel, dim3((unsigned)(want < most ? want : most)), dim3(threads), smem, s, p.chained, p);
 }
 
 template <typename XT, typename RT>
 cudaError_t pick(const NormParams &p, cudaStream_t s) {
-    if (p.wide) {
+    const size_t row = (size_t)p.cols * (sizeof(XT) + (std::is_same<RT, None>::value ? 0 : sizeof(RT)));
+    if (p.wide && row <= kMaxSmem) {
         const int nvec = p.cols / 8;
+        auto up = [](int n) { return (n + 31) / 32 * 32; };
         // up to 1024 columns a warp holds the row (no barrier); above, a CTA of up to 512 threads
         // with one or two units each, or of up to 1024 with four
-        if (nvec <= 32) return go<k_norm_wide<XT, RT, 1, true>>(p, 256, 8, s);
-        if (nvec <= 64) return go<k_norm_wide<XT, RT, 2, true>>(p, 256, 8, s);
-        if (nvec <= 128) return go<k_norm_wide<XT, RT, 4, true>>(p, 256, 8, s);
-        if (nvec <= 512) return go<k_norm_wide<XT, RT, 1, false>>(p, (nvec + 31) / 32 * 32, 1, s);
-        if (nvec <= 1024) return go<k_norm_wide<XT, RT, 2, false>>(p, ((nvec + 1) / 2 + 31) / 32 * 32, 1, s);
-        return go<k_norm_wide<XT, RT, 4, false>>(p, ((nvec + 3) / 4 + 31) / 32 * 32, 1, s);
+        if (nvec <= 32) return go<k_norm_warp<XT, RT, 1>>(p, 256, 8, 0, s);
+        if (nvec <= 64) return go<k_norm_warp<XT, RT, 2>>(p, 256, 8, 0, s);
+        if (nvec <= 128) return go<k_norm_warp<XT, RT, 4>>(p, 256, 8, 0, s);
+        if (nvec <= 512) return go<k_norm_cta<XT, RT, 1, 3>>(p, up(nvec), 1, 3 * row, s);
+        if (nvec <= 1024) return go<k_norm_cta<XT, RT, 2, 3>>(p, up((nvec + 1) / 2), 1, 3 * row, s);
+        if (3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 4, 3>>(p, up((nvec + 3) / 4), 1, 3 * row, s);
+        return go<k_norm_cta<XT, RT, 4, 1>>(p, up((nvec + 3) / 4), 1, row, s);
     }
-    if (p.cols <= 8192) return go<k_norm_narrow<XT, RT, 8>>(p, ((p.cols + 7) / 8 + 31) / 32 * 32, 1, s);
-    return go<k_norm_narrow<XT, RT, 32>>(p, ((p.cols + 31) / 32 + 31) / 32 * 32, 1, s);
+    if (p.cols <= 8192) return go<k_norm_narrow<XT, RT, 16>>(p, ((p.cols + 15) / 16 + 31) / 32 * 32, 1, 0, s);
+    return go<k_norm_narrow<XT, RT, 32>>(p, ((p.cols + 31) / 32 + 31) / 32 * 32, 1, 0, s);
 }
 
 }  // namespace

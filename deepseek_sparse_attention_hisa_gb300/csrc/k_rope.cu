@@ -9,59 +9,79 @@
 //
 // Bound by memory. The heads of all tokens are one list of rows (token, head); a thread owns one
 // unit of a row (8 neighbouring dims of one or of both halves, or a copied unit) and walks the
-// CTA's rows, four loads in flight, so the sine and cosine of its pairs are computed once per
-// token and not once per head. In place only the rotated dims move.
+// CTA's rows, four loads in flight. While they are, the CTA computes the sines and cosines of the
+// batch's few tokens into shared memory, once per token and pair and not once per head, on all
+// its threads (each thread computing its own pairs held the half layout at a sixth of this rate).
+// In place only the rotated dims move.
 #include "ops_internal.cuh"
 
 namespace hisa {
 namespace {
 
-constexpr int kUnroll = 4;
+// A unit as loaded: 8 dims in 16-byte pieces, or one.
+template <typename T, int N> struct Unit { uint4 v[sizeof(T) / 2]; };
+template <typename T> struct Unit<T, 1> { T v; };
 
-template <int N>
-__device__ __forceinline__ void load_unit(const void *base, int64_t at, int bf16, float (&f)[N]) {
+template <typename T, int N>
+__device__ __forceinline__ void load_unit(const void *base, int64_t at, Unit<T, N> &u) {
+    const T *p = static_cast<const T *>(base) + at;
     if constexpr (N == 1) {
-        f[0] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[at]) : static_cast<const float *>(base)[at];
-    } else if (bf16) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + at);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(u[i] << 16);
-            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
+        u.v = *p;
     } else {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
-        const float4 a = p[0], b = p[1];
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) u.v[i] = reinterpret_cast<const uint4 *>(p)[i];
     }
 }
-template <int N>
-__device__ __forceinline__ void store_unit(void *base, int64_t at, int bf16, const float (&f)[N]) {
+template <typename T, int N>
+__device__ __forceinline__ void to_floats(const Unit<T, N> &u, float (&f)[N]) {
     if constexpr (N == 1) {
-        if (bf16) static_cast<__nv_bfloat16 *>(base)[at] = __float2bfloat16_rn(f[0]);
-        else static_cast<float *>(base)[at] = f[0];
-    } else if (bf16) {
+        f[0] = to_f32(u.v);
+    } else if constexpr (sizeof(T) == 2) {
+        const uint32_t w[4] = {u.v[0].x, u.v[0].y, u.v[0].z, u.v[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f[4 * i] = __uint_as_float(u.v[i].x); f[4 * i + 1] = __uint_as_float(u.v[i].y);
+            f[4 * i + 2] = __uint_as_float(u.v[i].z); f[4 * i + 3] = __uint_as_float(u.v[i].w);
+        }
+    }
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_unit(void *base, int64_t at, const float (&f)[N]) {
+    T *p = static_cast<T *>(base) + at;
+    if constexpr (N == 1) {
+        if constexpr (sizeof(T) == 2) *p = __float2bfloat16_rn(f[0]);
+        else *p = f[0];
+    } else if constexpr (sizeof(T) == 2) {
         uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
             u[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(base) + at) = make_uint4(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
-        p[0] = make_float4(f[0], f[1], f[2], f[3]);
-        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
 }
 
 // N dims per unit (8, or 1 where a boundary is not a multiple of 8). A rotated unit is two
 // blocks of N dims, `lo` and `hi`: for the half layout the pairs (lo + e, hi + e); interleaved,
 // for N = 8 one block holding 4 pairs (hi unused), for N = 1 the pair (lo, hi).
-template <int N, bool HALF>
-__global__ void __launch_bounds__(N == 8 ? 256 : 1024) k_rope(RopeParams p) {
+// Rows per thread in flight: four, or two where a unit is 64 bytes (the registers of four would
+// halve the CTAs per SM).
+template <typename S, int N, bool HALF>
+constexpr int kUnroll = N == 8 && HALF && sizeof(S) == 4 ? 2 : 4;
+
+template <typename S, typename D, int N, bool HALF>
+__global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(RopeParams p) {
+    constexpr int kU = kUnroll<S, N, HALF>;
     constexpr bool kTwo = HALF || N == 1;                 // a rotated unit is two blocks
     constexpr int kPairs = kTwo ? N : N / 2;
     const int n_rot = p.dims / (kTwo ? 2 * N : N);
@@ -72,94 +92,101 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024) k_rope(RopeParams p) {
     int64_t r1 = r0 + p.rows_per_cta;
     r1 = r1 < p.rows ? r1 : p.rows;
     const bool rot = unit < n_rot;
+    const int pairs = p.dims / 2;
     int lo, hi = 0;
-    uint64_t freq[kPairs];
     if (rot) {
         if (HALF) { lo = p.first + unit * N; hi = lo + p.dims / 2; }
         else if (N == 1) { lo = p.first + 2 * unit; hi = lo + 1; }
         else lo = p.first + unit * N;
-#pragma unroll
-        for (int e = 0; e < kPairs; ++e) freq[e] = __ldg(p.table + unit * kPairs + e);
     } else {
         lo = (unit - n_rot) * N;                          // copied units: the dims before, then after, the rotated
         if (lo >= p.first) lo += p.dims;
     }
+    extern __shared__ __align__(16) float2 turn[];        // [token of the batch][pair]: mscale (cos, sin)
     grid_dep_wait();
-    float cs[kPairs], sn[kPairs];
-    int64_t have = -1;                                    // the token of cs and sn
-    for (int64_t base = r0 + sub; base < r1; base += (int64_t)per * kUnroll) {
-        float a[kUnroll][N], b[kTwo ? kUnroll : 1][N];
-        int64_t tok[kUnroll];
-        int head[kUnroll];
+    const int64_t batch = (int64_t)per * kU;
+    for (int64_t b0 = r0; b0 < r1; b0 += batch) {
+        const int64_t base = b0 + sub, last = (b0 + batch < r1 ? b0 + batch : r1) - 1;
+        const int64_t tok0 = b0 / p.heads_all;
+        const int at0 = (int)(base - tok0 * p.heads_all);
+        Unit<S, N> a[kU], b[kTwo ? kU : 1];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const int64_t row = base + (int64_t)k * per;
-            tok[k] = row / p.heads_all;
-            head[k] = (int)(row - tok[k] * p.heads_all);
-            if (row >= r1) continue;
-            const bool two = head[k] >= p.heads;
-            const void *src = two ? p.x2 : p.x;
-            const int64_t at = two ? tok[k] * p.x2_token + (head[k] - p.heads) * p.x2_head
-                                   : tok[k] * p.x_token + head[k] * p.x_head;
-            load_unit<N>(src, at + lo, p.src_bf16, a[k]);
-            if constexpr (kTwo)
-                if (rot) load_unit<N>(src, at + hi, p.src_bf16, b[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
+        for (int k = 0; k < kU; ++k) {
             if (base + (int64_t)k * per >= r1) break;
-            if (rot) {
-                if (tok[k] != have) {
-                    have = tok[k];
-                    const int64_t pos = p.pos[have];
+            const int tok = (at0 + k * per) / p.heads_all, head = at0 + k * per - tok * p.heads_all;
+            const bool two = head >= p.heads;
+            const void *src = two ? p.x2 : p.x;
+            const int64_t at = two ? (tok0 + tok) * p.x2_token + (head - p.heads) * p.x2_head
+                                   : (tok0 + tok) * p.x_token + head * p.x_head;
+            load_unit<S, N>(src, at + lo, a[k]);
+            if constexpr (kTwo)
+                if (rot) load_unit<S, N>(src, at + hi, b[k]);
+        }
+        const int angles = (int)(last / p.heads_all - tok0 + 1) * pairs;
+        for (int i = threadIdx.x; i < angles; i += blockDim.x) {
+            const int64_t pos = p.pos[tok0 + i / pairs];
+            const int64_t turns = (int64_t)((uint64_t)pos * __ldg(p.table + i % pairs));      // modulo one turn
+            float s, c;
+            sincospif(2.f * (__ll2float_rn(turns) * 0x1p-64f), &s, &c);
+            turn[i] = make_float2(c * p.mscale, s * p.mscale * p.sin_sign);
+        }
+        __syncthreads();
 #pragma unroll
-                    for (int e = 0; e < kPairs; ++e) {
-                        const int64_t turns = (int64_t)((uint64_t)pos * freq[e]);      // modulo one turn
-                        float s, c;
-                        sincospif(2.f * (__ll2float_rn(turns) * 0x1p-64f), &s, &c);
-                        cs[e] = c * p.mscale;
-                        sn[e] = s * p.mscale * p.sin_sign;
-                    }
-                }
+        for (int k = 0; k < kU; ++k) {
+            if (base + (int64_t)k * per >= r1) break;
+            const int tok = (at0 + k * per) / p.heads_all, head = at0 + k * per - tok * p.heads_all;
+            const bool two = head >= p.heads;
+            void *dst = two ? p.y2 : p.y;
+            const int64_t at = two ? (tok0 + tok) * p.y2_token + (head - p.heads) * p.y2_head
+                                   : (tok0 + tok) * p.y_token + head * p.y_head;
+            float u[N];
+            to_floats<S, N>(a[k], u);
+            if (rot) {
+                const float2 *cs = turn + tok * pairs + unit * kPairs;
                 if constexpr (kTwo) {
+                    float v[N];
+                    to_floats<S, N>(b[k], v);
 #pragma unroll
                     for (int e = 0; e < N; ++e) {
-                        const float u = a[k][e], v = b[k][e];
-                        a[k][e] = u * cs[e] - v * sn[e];
-                        b[k][e] = u * sn[e] + v * cs[e];
+                        const float x = u[e], y = v[e];
+                        u[e] = x * cs[e].x - y * cs[e].y;
+                        v[e] = x * cs[e].y + y * cs[e].x;
                     }
+                    store_unit<D, N>(dst, at + hi, v);
                 } else {
 #pragma unroll
                     for (int e = 0; e < kPairs; ++e) {
-                        const float u = a[k][2 * e], v = a[k][2 * e + 1];
-                        a[k][2 * e] = u * cs[e] - v * sn[e];
-                        a[k][2 * e + 1] = u * sn[e] + v * cs[e];
+                        const float x = u[2 * e], y = u[2 * e + 1];
+                        u[2 * e] = x * cs[e].x - y * cs[e].y;
+                        u[2 * e + 1] = x * cs[e].y + y * cs[e].x;
                     }
                 }
             }
-            const bool two = head[k] >= p.heads;
-            void *dst = two ? p.y2 : p.y;
-            const int64_t at = two ? tok[k] * p.y2_token + (head[k] - p.heads) * p.y2_head
-                                   : tok[k] * p.y_token + head[k] * p.y_head;
-            store_unit<N>(dst, at + lo, p.dst_bf16, a[k]);
-            if constexpr (kTwo)
-                if (rot) store_unit<N>(dst, at + hi, p.dst_bf16, b[k]);
+            store_unit<D, N>(dst, at + lo, u);
         }
+        if (b0 + batch < r1) __syncthreads();             // the angles are read before the next batch's are written
     }
 }
 
-template <int N>
-cudaError_t launch_n(RopeParams p, cudaStream_t s) {
-    const bool two = p.half || N == 1;
-    const int n = p.dims / (two ? 2 * N : N) + (p.inplace ? 0 : (p.D - p.dims) / N);
+template <typename S, typename D, int N, bool HALF>
+cudaError_t launch_as(RopeParams p, cudaStream_t s) {
+    constexpr bool kTwo = HALF || N == 1;
+    constexpr int kU = kUnroll<S, N, HALF>;
+    const int n = p.dims / (kTwo ? 2 * N : N) + (p.inplace ? 0 : (p.D - p.dims) / N);
     const int most = N == 8 ? 256 : 1024;                 // n <= 128 units of 8, n <= 1023 of 1
     int per = most / n;
     if (N == 1 && per > 1) per = (256 + n - 1) / n < per ? (256 + n - 1) / n : per;
     if (per > p.rows) per = (int)p.rows;
+    // the angles of a batch of rows, of as many tokens as it can touch (at most 16 KB for one row
+    // at a time, so the loop ends)
+    auto shared = [&](int per_) {
+        const int64_t tokens = ((int64_t)per_ * kU + p.heads_all - 2) / p.heads_all + 1;
+        return (size_t)tokens * (p.dims / 2) * sizeof(float2);
+    };
+    while (shared(per) > 40 * 1024) per = (per + 1) / 2;
     const int threads = per * n;
-    // rows per CTA: four loads per thread, more once every SM has several CTAs, so that a token's
-    // sines serve more of its heads
-    const int64_t few = (int64_t)per * kUnroll;
+    // rows per CTA: one batch, more once every SM has several CTAs
+    const int64_t few = (int64_t)per * kU;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     int64_t mul = p.rows / (few * sms * 8);
@@ -167,15 +194,22 @@ cudaError_t launch_n(RopeParams p, cudaStream_t s) {
     p.rows_per_cta = (int)(few * mul);
     const int64_t grid = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    auto kernel = p.half ? k_rope<N, true> : k_rope<N, false>;
-    return launch_pdl(kernel, dim3((unsigned)grid), dim3(threads), 0, s, p.chained, p);
+    return launch_pdl(k_rope<S, D, N, HALF>, dim3((unsigned)grid), dim3(threads), shared(per), s, p.chained, p);
+}
+
+template <typename S, typename D>
+cudaError_t launch_types(const RopeParams &p, cudaStream_t s) {
+    if (p.wide) return p.half ? launch_as<S, D, 8, true>(p, s) : launch_as<S, D, 8, false>(p, s);
+    return p.half ? launch_as<S, D, 1, true>(p, s) : launch_as<S, D, 1, false>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeParams &p, cudaStream_t s) {
     if (p.rows == 0) return cudaSuccess;
-    return p.wide ? launch_n<8>(p, s) : launch_n<1>(p, s);
+    if (p.src_bf16)
+        return p.dst_bf16 ? launch_types<__nv_bfloat16, __nv_bfloat16>(p, s) : launch_types<__nv_bfloat16, float>(p, s);
+    return p.dst_bf16 ? launch_types<float, __nv_bfloat16>(p, s) : launch_types<float, float>(p, s);
 }
 
 }  // namespace hisa
