@@ -154,13 +154,15 @@ hisa_status hisa_rms_norm(const hisa_norm_desc *d, const void *x, const void *re
     p.rows = d->rows; p.cols = d->cols;
     p.x_bf16 = d->x_dtype == HISA_BF16; p.res_bf16 = d->res_dtype == HISA_BF16;
     p.out_dtype = d->out_dtype; p.group = d->scale_group; p.pow2 = d->scale_pow2;
+    p.groups = p.group ? d->cols / p.group : 1;
+    p.unit_shift = 16;                                 // 32768 columns are 4096 units
+    for (int i = 2; i <= 5; ++i)
+        if (p.group == 8 << i) p.unit_shift = i;
     p.eps = d->eps;
     p.ld_x = d->ld_x; p.ld_res = residual ? d->ld_res : 0; p.ld_out = d->ld_out;
     p.x = x; p.res = residual; p.w = w; p.res_out = residual_out; p.out = out; p.scales = scales;
-    // units of 8 columns: 16 or 32 bytes of every tensor (8 of the 8-bit codes)
-    auto wide = [&](const void *a, int64_t ld, size_t es) {
-        return aligned(a, es == 1 ? 8 : 16) && (ld * (int64_t)es) % (es == 1 ? 8 : 16) == 0;
-    };
+    // units of 8 columns: 32, 16 or 8 bytes of every tensor
+    auto wide = [&](const void *a, int64_t ld, size_t es) { return aligned(a, 8 * es) && ld % 8 == 0; };
     p.wide = d->cols % 8 == 0 && aligned(w, 16) && wide(x, d->ld_x, sx) && wide(out, d->ld_out, so) &&
              (!residual || (wide(residual, d->ld_res, sr) && wide(residual_out, d->ld_res, sr)));
     p.chained = (d->flags & HISA_FLAG_CHAINED) != 0;
@@ -228,9 +230,9 @@ hisa_status hisa_rope(const hisa_rope_desc *d, const uint64_t *table, const int3
     p.x = x; p.x2 = x2; p.y = y; p.y2 = y2;
     p.x_token = d->x_token; p.x_head = d->x_head; p.y_token = d->y_token; p.y_head = d->y_head;
     p.x2_token = d->x2_token; p.x2_head = d->x2_head; p.y2_token = d->y2_token; p.y2_head = d->y2_head;
-    // units of 8 dims: 16 or 32 bytes at every boundary
+    // units of 8 dims: 32 or 16 bytes at every boundary
     auto wide = [](const void *a, int64_t token, int64_t head, size_t es) {
-        return aligned(a, 16) && (token * (int64_t)es) % 16 == 0 && (head * (int64_t)es) % 16 == 0;
+        return aligned(a, 8 * es) && token % 8 == 0 && head % 8 == 0;
     };
     p.wide = d->D % 8 == 0 && d->rope_first % 8 == 0 && d->rope_dims % (d->half ? 16 : 8) == 0 &&
              wide(x, d->x_token, d->x_head, ss) && wide(y, d->y_token, d->y_head, sd) &&

@@ -19,7 +19,7 @@
 namespace hisa {
 namespace {
 
-constexpr int kMaxSmem = 224 * 1024;   // dynamic shared memory of a CTA
+constexpr int kMaxSmem = 220 * 1024;   // dynamic shared memory of a CTA (beside up to 5 KB declared)
 
 struct None {};                       // no residual
 
@@ -64,9 +64,7 @@ __device__ __forceinline__ void store8(void *base, int64_t at, bool bf16, const 
     if (bf16) {
         *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(base) + at) = pack_bf16(f);
     } else {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
-        p[0] = make_float4(f[0], f[1], f[2], f[3]);
-        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        store_sector(static_cast<float *>(base) + at, f);
     }
 }
 
@@ -81,8 +79,11 @@ __device__ __forceinline__ float max_mag(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
     return r;
 }
+// Over aligned groups of `lanes` lanes (a power of two).
 __device__ __forceinline__ float lanes_max(float v, int lanes) {
-    for (int o = lanes >> 1; o >= 1; o >>= 1) v = max_mag(v, __shfl_xor_sync(0xffffffffu, v, o));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        if (lanes > o) v = max_mag(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
@@ -167,12 +168,17 @@ struct Row {
             top[i] = max_mag(max_mag(m[0], m[1]), max_mag(m[2], m[3]));
         }
         if (p.group) {
+            const int lanes = p.group >> 3;
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) top[i] = lanes_max(top[i], p.group >> 3);
+            for (int i = 0; i < VPT; ++i) top[i] = lanes_max(top[i], lanes);
         } else {
 #pragma unroll
             for (int i = 1; i < VPT; ++i) top[0] = max_mag(top[0], top[i]);
         }
+    }
+    __device__ __forceinline__ void same_top(float v) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) top[i] = v;
     }
     __device__ __forceinline__ void put(const NormParams &p, int i, int v, int64_t row, float f) {
         const int64_t at = row * p.ld_out + (int64_t)v * 8;
@@ -182,10 +188,10 @@ struct Row {
             store8(p.out, at, p.out_dtype == HISA_BF16, h[i]);
             return;
         }
-        const float s = scale_of(top[p.group ? i : 0] * f, p.pow2);
-        const float q = f / s;                         // t q is within a few f32 steps of y / s
-        if ((p.group ? v & ((p.group >> 3) - 1) : v) == 0)
-            p.scales[p.group ? row * (p.cols / p.group) + v / (p.group >> 3) : row] = s;
+        const float s = scale_of(top[i] * f, p.pow2);
+        const float q = __fdividef(f, s);              // t q is within a few f32 steps of y / s
+        const int g = v >> p.unit_shift;               // the unit's group (0 for one scale per row)
+        if (v == g << p.unit_shift) p.scales[row * p.groups + g] = s;
         uint32_t c[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -206,7 +212,7 @@ __device__ __forceinline__ void load_w(const float *base, int v, int nvec, float
 
 // Rows of at most 1024 columns: a warp per row, the next row's loads in flight in registers.
 template <typename XT, typename RT, int VPT>
-__global__ void __launch_bounds__(256, 2) k_norm_warp(NormParams p) {
+__global__ void __launch_bounds__(256, VPT == 1 ? 4 : (VPT == 2 ? 3 : 2)) k_norm_warp(NormParams p) {
     const int t = threadIdx.x & 31, nvec = p.cols >> 3;
     const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
     int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -237,9 +243,9 @@ __global__ void __launch_bounds__(256, 2) k_norm_warp(NormParams p) {
         fetch(row + step);
         if (p.out_dtype == HISA_E4M3) {
             m.tops(p);
-            if (!p.group) m.top[0] = lanes_max(m.top[0], 32);
+            if (!p.group) m.same_top(lanes_max(m.top[0], 32));
         }
-        const float f = 1.f / sqrtf(warp_sum(m.ss) * inv + p.eps);
+        const float f = rsqrtf(warp_sum(m.ss) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (i * 32 + t < nvec) m.put(p, i, i * 32 + t, row, f);
@@ -247,12 +253,12 @@ __global__ void __launch_bounds__(256, 2) k_norm_warp(NormParams p) {
 }
 
 // Longer rows: a CTA per row. Rows to come are copied to shared memory asynchronously, STAGES - 1
-// of them in flight; a thread copies exactly the units that it reads itself, so it waits for its
+// of them in flight; a warp copies exactly the units that it reads itself, so it waits for its
 // own copies and needs no barrier for them.
 template <typename XT, typename RT, int VPT, int STAGES>
-__global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) k_norm_cta(NormParams p) {
+__global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
     constexpr int kX = sizeof(XT) / 2, kR = std::is_same<RT, None>::value ? 0 : sizeof(RT) / 2;   // 16-byte pieces per unit
-    extern __shared__ __align__(16) uint4 ring[];     // [stage][piece][unit]
+    extern __shared__ __align__(16) uint4 ring[];     // [stage]: the row of x, the row of residual
     __shared__ __align__(16) float red[2][32], redm[2][32];
     const int T = blockDim.x, t = threadIdx.x, nvec = p.cols >> 3;
     const float inv = 1.f / (float)p.cols;
@@ -271,14 +277,19 @@ __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) k_nor
             const uint4 *sx = reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + row * p.ld_x);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int v = i * T + t;
-                if (v >= nvec) continue;
+                const int v0 = i * T + (t & ~31), lane = t & 31;      // the warp's units v0 .. v0 + 31
 #pragma unroll
-                for (int k = 0; k < kX; ++k) tc::cp_async16(tc::smem_u32(dst + k * nvec + v), sx + kX * v + k);
+                for (int k = 0; k < kX; ++k) {
+                    const int q = v0 * kX + k * 32 + lane;
+                    if (q < nvec * kX) tc::cp_async16(tc::smem_u32(dst + q), sx + q);
+                }
                 if constexpr (kR > 0) {
                     const uint4 *sr = reinterpret_cast<const uint4 *>(static_cast<const RT *>(p.res) + row * p.ld_res);
 #pragma unroll
-                    for (int k = 0; k < kR; ++k) tc::cp_async16(tc::smem_u32(dst + (kX + k) * nvec + v), sr + kR * v + k);
+                    for (int k = 0; k < kR; ++k) {
+                        const int q = v0 * kR + k * 32 + lane;
+                        if (q < nvec * kR) tc::cp_async16(tc::smem_u32(dst + kX * nvec + q), sr + q);
+                    }
                 }
             }
         }
@@ -290,6 +301,7 @@ __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) k_nor
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
         if (STAGES == 1) copy(row, 0);
         asm volatile("cp.async.wait_group %0;" :: "n"(STAGES > 1 ? STAGES - 2 : 0) : "memory");
+        __syncwarp();
         const uint4 *src = ring + (int64_t)stage * (kX + kR) * nvec;
         Row<RT, VPT> m;
         m.ss = 0.f;
@@ -300,15 +312,16 @@ __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) k_nor
             Raw8<RT> r;
             if (v < nvec) {
 #pragma unroll
-                for (int k = 0; k < kX; ++k) x.v[k] = src[k * nvec + v];
+                for (int k = 0; k < kX; ++k) x.v[k] = src[v * kX + k];
                 if constexpr (kR > 0) {
 #pragma unroll
-                    for (int k = 0; k < kR; ++k) r.v[k] = src[(kX + k) * nvec + v];
+                    for (int k = 0; k < kR; ++k) r.v[k] = src[kX * nvec + v * kR + k];
                 }
             }
             if constexpr (!kHoldW) load_w(p.w, v, nvec, w[0]);
             m.take(p, i, v, v < nvec, row, x, r, w[kHoldW ? i : 0]);
         }
+        __syncwarp();
         if (STAGES > 1) {
             // into the stage read by the row before
             copy(row + (int64_t)(STAGES - 1) * gridDim.x, stage == 0 ? STAGES - 1 : stage - 1);
@@ -316,9 +329,9 @@ __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) k_nor
         }
         if (p.out_dtype == HISA_E4M3) {
             m.tops(p);
-            if (!p.group) m.top[0] = block_max(m.top[0], redm[par]);
+            if (!p.group) m.same_top(block_max(m.top[0], redm[par]));
         }
-        const float f = 1.f / sqrtf(block_sum(m.ss, red[par]) * inv + p.eps);
+        const float f = rsqrtf(block_sum(m.ss, red[par]) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (i * T + t < nvec) m.put(p, i, i * T + t, row, f);
@@ -331,32 +344,107 @@ __device__ __forceinline__ float load1(const void *base, int64_t at) {
     else return to_f32(__ldcs(static_cast<const T *>(base) + at));
 }
 
-// Rows whose starts are not 16-byte aligned or whose length is not a multiple of 8: one CTA per
-// row, single elements, neighbouring threads on neighbouring columns. A warp's 32 columns lie
-// in one scale group (groups are multiples of 32), whose maximum is joined in shared memory.
-template <typename XT, typename RT, int EPT>
+// The 16-byte pieces that hold row `row` of a [rows, cols] array, whole: up to 15 bytes before
+// and after the row come along (they share a 16-byte block with an element of it).
+template <typename T>
+__device__ __forceinline__ void copy_row(uint8_t *dst, const void *base, int64_t at, int cols) {
+    if constexpr (!std::is_same<T, None>::value) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(static_cast<const T *>(base) + at), lo = a & ~(uintptr_t)15;
+        const int pieces = (int)((a - lo + (size_t)cols * sizeof(T) + 15) / 16);
+        for (int i = threadIdx.x; i < pieces; i += blockDim.x)
+            tc::cp_async16(tc::smem_u32(dst + 16 * i), reinterpret_cast<const void *>(lo + 16 * i));
+    }
+}
+template <typename T>
+__device__ __forceinline__ const uint8_t *row_in(const uint8_t *stage, const void *base, int64_t at) {
+    if constexpr (std::is_same<T, None>::value) return stage;
+    else return stage + (reinterpret_cast<uintptr_t>(static_cast<const T *>(base) + at) & 15);
+}
+// Writes n bytes (of `es`-byte elements) staged with the destination's own offset into a 16-byte
+// block: whole blocks at once, the row's ragged ends by elements. (Single elements from
+// neighbouring threads leave two partial sectors to every 128 bytes of a row that starts anywhere.)
+__device__ __forceinline__ void write_row(uint8_t *dst, const uint8_t *staged, int n, int es) {
+    const int a = (int)(reinterpret_cast<uintptr_t>(dst) & 15);
+    uint8_t *lo = dst - a;
+    for (int i = threadIdx.x; 16 * i < a + n; i += blockDim.x) {
+        if (16 * i >= a && 16 * i + 16 <= a + n) {
+            *reinterpret_cast<uint4 *>(lo + 16 * i) = *reinterpret_cast<const uint4 *>(staged + 16 * i);
+            continue;
+        }
+        const int b0 = 16 * i > a ? 16 * i : a, b1 = 16 * i + 16 < a + n ? 16 * i + 16 : a + n;
+        for (int b = b0; b < b1; b += es) {
+            if (es == 4) *reinterpret_cast<uint32_t *>(lo + b) = *reinterpret_cast<const uint32_t *>(staged + b);
+            else if (es == 2) *reinterpret_cast<uint16_t *>(lo + b) = *reinterpret_cast<const uint16_t *>(staged + b);
+            else lo[b] = staged[b];
+        }
+    }
+}
+template <typename T>
+constexpr size_t kElem = std::is_same<T, None>::value ? 0 : sizeof(T);
+// Bytes of a staged row.
+template <typename T>
+__host__ __device__ size_t stage_bytes(int cols) {
+    return kElem<T> ? ((size_t)cols * kElem<T> + 15 + 15) / 16 * 16 : 0;
+}
+
+// Rows whose starts are not aligned or whose length is not a multiple of 8: one CTA per row,
+// single elements, neighbouring threads on neighbouring columns. With STAGED, rows come in and go
+// out through shared memory in the aligned 16-byte blocks that cover them, the next row on its
+// way; else (rows too long for that) directly. A warp's 32 columns lie in one scale group (groups
+// are multiples of 32), whose maximum is joined in shared memory.
+template <typename XT, typename RT, int EPT, bool STAGED>
 __global__ void __launch_bounds__(EPT == 16 ? 512 : 1024, EPT == 16 ? 2 : 1) k_norm_narrow(NormParams p) {
     constexpr bool kRes = !std::is_same<RT, None>::value;
+    extern __shared__ __align__(16) uint4 ring[];     // two stages of x and residual; out; residual_out
     __shared__ __align__(16) float red[2][32], redm[2][32];
     __shared__ float gmax[1024];
     const int T = blockDim.x, t = threadIdx.x;
     const float inv = 1.f / (float)p.cols;
+    const size_t xb = stage_bytes<XT>(p.cols), rb = stage_bytes<RT>(p.cols), ob = stage_bytes<float>(p.cols);
+    uint8_t *in = reinterpret_cast<uint8_t *>(ring), *obuf = in + 2 * (xb + rb), *rbuf = obuf + ob;
+    const int es = p.out_dtype == HISA_F32 ? 4 : (p.out_dtype == HISA_BF16 ? 2 : 1);
     if (t < 32) red[0][t] = red[1][t] = 0.f;
     __syncthreads();
     grid_dep_wait();
+    auto copy = [&](int64_t row, int stage) {
+        if (row < p.rows) {
+            copy_row<XT>(in + stage * (xb + rb), p.x, row * p.ld_x, p.cols);
+            copy_row<RT>(in + stage * (xb + rb) + xb, p.res, row * p.ld_res, p.cols);
+        }
+    };
+    if constexpr (STAGED) copy(blockIdx.x, 0);
     int par = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
         float h[EPT];
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            const int c = i * T + t;
-            h[i] = c < p.cols ? load1<XT>(p.x, row * p.ld_x + c) : 0.f;
-        }
-        if constexpr (kRes) {
+        uint8_t *orow = static_cast<uint8_t *>(p.out) + row * p.ld_out * es, *rrow = nullptr;
+        if constexpr (kRes)
+            if (p.res_out) rrow = reinterpret_cast<uint8_t *>(static_cast<RT *>(p.res_out) + row * p.ld_res);
+        // where this row's elements are put: staged, with the destination's offset in its block
+        uint8_t *oput = STAGED ? obuf + (reinterpret_cast<uintptr_t>(orow) & 15) : orow;
+        uint8_t *rput = STAGED ? rbuf + (reinterpret_cast<uintptr_t>(rrow) & 15) : rrow;
+        if constexpr (STAGED) {
+            tc::cp_async_wait_all();
+            __syncthreads();                           // every thread's blocks of this row have landed,
+                                                       // and every thread is done with the row before
+            const uint8_t *src = in + par * (xb + rb);
+            const uint8_t *sx = row_in<XT>(src, p.x, row * p.ld_x), *sr = row_in<RT>(src + xb, p.res, row * p.ld_res);
+            copy(row + gridDim.x, par ^ 1);
 #pragma unroll
             for (int i = 0; i < EPT; ++i) {
                 const int c = i * T + t;
-                if (c < p.cols) h[i] += load1<RT>(p.res, row * p.ld_res + c);
+                h[i] = 0.f;
+                if (c < p.cols) {
+                    h[i] = to_f32(reinterpret_cast<const XT *>(sx)[c]);
+                    if constexpr (kRes) h[i] += to_f32(reinterpret_cast<const RT *>(sr)[c]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) {
+                const int c = i * T + t;
+                h[i] = c < p.cols ? load1<XT>(p.x, row * p.ld_x + c) : 0.f;
+                if constexpr (kRes)
+                    if (c < p.cols) h[i] += load1<RT>(p.res, row * p.ld_res + c);
             }
         }
         float ss = 0.f;
@@ -364,20 +452,18 @@ __global__ void __launch_bounds__(EPT == 16 ? 512 : 1024, EPT == 16 ? 2 : 1) k_n
         for (int i = 0; i < EPT; ++i) {
             const int c = i * T + t;
             if constexpr (kRes) {
-                const int64_t at = row * p.ld_res + c;
                 if constexpr (std::is_same<RT, __nv_bfloat16>::value) {
                     const __nv_bfloat16 b = __float2bfloat16_rn(h[i]);
                     h[i] = __bfloat162float(b);
-                    if (p.res_out && c < p.cols) static_cast<__nv_bfloat16 *>(p.res_out)[at] = b;
+                    if (rrow && c < p.cols) reinterpret_cast<__nv_bfloat16 *>(rput)[c] = b;
                 } else {
-                    if (p.res_out && c < p.cols) static_cast<float *>(p.res_out)[at] = h[i];
+                    if (rrow && c < p.cols) reinterpret_cast<float *>(rput)[c] = h[i];
                 }
             }
             ss += h[i] * h[i];
         }
         ss = block_sum(ss, red[par]);
-        const float f = 1.f / sqrtf(ss * inv + p.eps);
-        float all = 0.f;
+        const float f = rsqrtf(ss * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
             const int c = i * T + t;
@@ -388,40 +474,44 @@ __global__ void __launch_bounds__(EPT == 16 ? 512 : 1024, EPT == 16 ? 2 : 1) k_n
             for (int i = 0; i < EPT; ++i) {
                 const int c = i * T + t;
                 if (c >= p.cols) continue;
-                if (p.out_dtype == HISA_BF16)
-                    static_cast<__nv_bfloat16 *>(p.out)[row * p.ld_out + c] = __float2bfloat16_rn(h[i]);
-                else
-                    static_cast<float *>(p.out)[row * p.ld_out + c] = h[i];
+                if (p.out_dtype == HISA_BF16) reinterpret_cast<__nv_bfloat16 *>(oput)[c] = __float2bfloat16_rn(h[i]);
+                else reinterpret_cast<float *>(oput)[c] = h[i];
             }
-            continue;
-        }
-        if (p.group == 0) {
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) all = max_mag(all, h[i]);
-            all = block_max(all, redm[par]);
         } else {
+            float all = 0.f;
+            if (p.group == 0) {
+#pragma unroll
+                for (int i = 0; i < EPT; ++i) all = max_mag(all, h[i]);
+                all = block_max(all, redm[par]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPT; ++i) {
+                    const float m = lanes_max(h[i], 32);
+                    const int c = i * T + t;
+                    if ((t & 31) == 0 && c < p.cols) gmax[c >> 5] = m;
+                }
+                __syncthreads();
+            }
 #pragma unroll
             for (int i = 0; i < EPT; ++i) {
-                const float m = lanes_max(fabsf(h[i]), 32);
                 const int c = i * T + t;
-                if ((t & 31) == 0 && c < p.cols) gmax[c >> 5] = m;
+                if (c >= p.cols) continue;
+                const int g = c >> (p.unit_shift + 3); // the column's group (0 for one scale per row)
+                float top = all;
+                if (p.group)
+                    for (int k = 0; k < (p.group >> 5); ++k) top = max_mag(top, gmax[g * (p.group >> 5) + k]);
+                const float s = scale_of(top, p.pow2);
+                if (c == g << (p.unit_shift + 3)) p.scales[row * p.groups + g] = s;
+                oput[c] = __nv_cvt_float_to_fp8(h[i] * __fdividef(1.f, s), __NV_SATFINITE, __NV_E4M3);
             }
-            __syncthreads();
         }
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            const int c = i * T + t;
-            if (c >= p.cols) continue;
-            float top = all;
-            if (p.group) {
-                const int g0 = c / p.group * (p.group >> 5);
-                for (int k = 0; k < (p.group >> 5); ++k) top = max_mag(top, gmax[g0 + k]);
-            }
-            const float s = scale_of(top, p.pow2);
-            if (p.group ? c % p.group == 0 : c == 0) p.scales[p.group ? row * (p.cols / p.group) + c / p.group : row] = s;
-            static_cast<uint8_t *>(p.out)[row * p.ld_out + c] = __nv_cvt_float_to_fp8(h[i] * (1.f / s), __NV_SATFINITE, __NV_E4M3);
+        if constexpr (STAGED) {
+            __syncthreads();                           // the staged outputs are whole (and gmax has been read)
+            write_row(orow, obuf, p.cols * es, es);
+            if (rrow) write_row(rrow, rbuf, p.cols * (int)kElem<RT>, (int)kElem<RT>);
+        } else {
+            if (p.out_dtype == HISA_E4M3 && p.group) __syncthreads();   // gmax is read before the next row's is written
         }
-        if (p.group) __syncthreads();                  // gmax is read before the next row's is written
     }
 }
 
@@ -447,22 +537,25 @@ cudaError_t go(const NormParams &p, int threads, int64_t rows_per_cta, size_t sm
 
 template <typename XT, typename RT>
 cudaError_t pick(const NormParams &p, cudaStream_t s) {
-    const size_t row = (size_t)p.cols * (sizeof(XT) + (std::is_same<RT, None>::value ? 0 : sizeof(RT)));
+    const size_t row = (size_t)p.cols * (kElem<XT> + kElem<RT>);
     if (p.wide && row <= kMaxSmem) {
         const int nvec = p.cols / 8;
         auto up = [](int n) { return (n + 31) / 32 * 32; };
         // up to 1024 columns a warp holds the row (no barrier); above, a CTA of up to 512 threads
-        // with one or two units each, or of up to 1024 with four
+        // with a unit each, or of up to 1024 with two or four
         if (nvec <= 32) return go<k_norm_warp<XT, RT, 1>>(p, 256, 8, 0, s);
         if (nvec <= 64) return go<k_norm_warp<XT, RT, 2>>(p, 256, 8, 0, s);
         if (nvec <= 128) return go<k_norm_warp<XT, RT, 4>>(p, 256, 8, 0, s);
         if (nvec <= 512) return go<k_norm_cta<XT, RT, 1, 3>>(p, up(nvec), 1, 3 * row, s);
-        if (nvec <= 1024) return go<k_norm_cta<XT, RT, 2, 3>>(p, up((nvec + 1) / 2), 1, 3 * row, s);
+        if (nvec <= 2048 && 3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 2, 3>>(p, up((nvec + 1) / 2), 1, 3 * row, s);
         if (3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 4, 3>>(p, up((nvec + 3) / 4), 1, 3 * row, s);
         return go<k_norm_cta<XT, RT, 4, 1>>(p, up((nvec + 3) / 4), 1, row, s);
     }
-    if (p.cols <= 8192) return go<k_norm_narrow<XT, RT, 16>>(p, ((p.cols + 15) / 16 + 31) / 32 * 32, 1, 0, s);
-    return go<k_norm_narrow<XT, RT, 32>>(p, ((p.cols + 31) / 32 + 31) / 32 * 32, 1, 0, s);
+    if (p.cols <= 8192)                                // 192 KB at most
+        return go<k_norm_narrow<XT, RT, 16, true>>(p, ((p.cols + 15) / 16 + 31) / 32 * 32, 1,
+                                                   2 * (stage_bytes<XT>(p.cols) + stage_bytes<RT>(p.cols)) +
+                                                       stage_bytes<float>(p.cols) + stage_bytes<RT>(p.cols), s);
+    return go<k_norm_narrow<XT, RT, 32, false>>(p, ((p.cols + 31) / 32 + 31) / 32 * 32, 1, 0, s);
 }
 
 }  // namespace

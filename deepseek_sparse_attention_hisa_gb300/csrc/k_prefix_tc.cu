@@ -125,12 +125,6 @@ __device__ __forceinline__ float ex2(float x) {         // 2^x, relative error <
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void store32(float *dst, const float *v) {   // one whole sector
-    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                 :: "l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                 : "memory");
-}
-
 // True on the 64 threads of a named barrier iff v is true on all of them (a barrier itself).
 __device__ __forceinline__ bool pair_all(uint32_t id, bool v) {
     uint32_t r;
@@ -406,7 +400,7 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                 tmem_ld32(lanes + kColO + c, o);
                 if (there) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) store32(dst + c + k, o + k);
+                    for (int k = 0; k < 32; k += 8) store_sector(dst + c + k, o + k);
                 }
             }
             fence_before_sync();

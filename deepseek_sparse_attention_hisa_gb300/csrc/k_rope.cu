@@ -66,21 +66,20 @@ __device__ __forceinline__ void store_unit(void *base, int64_t at, const float (
         }
         *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        store_sector(p, f);
     }
 }
 
 // N dims per unit (8, or 1 where a boundary is not a multiple of 8). A rotated unit is two
 // blocks of N dims, `lo` and `hi`: for the half layout the pairs (lo + e, hi + e); interleaved,
 // for N = 8 one block holding 4 pairs (hi unused), for N = 1 the pair (lo, hi).
-// Rows per thread in flight: four, or two where a unit is 64 bytes (the registers of four would
-// halve the CTAs per SM).
+// Rows per thread in flight: four, or two where a unit is two blocks of 8 (the registers of four
+// would halve the CTAs per SM).
 template <typename S, int N, bool HALF>
-constexpr int kUnroll = N == 8 && HALF && sizeof(S) == 4 ? 2 : 4;
+constexpr int kUnroll = N == 8 && HALF ? 2 : 4;
 
 template <typename S, typename D, int N, bool HALF>
-__global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(RopeParams p) {
+__global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? (HALF && sizeof(S) == 2 ? 6 : 4) : 1) k_rope(RopeParams p) {
     constexpr int kU = kUnroll<S, N, HALF>;
     constexpr bool kTwo = HALF || N == 1;                 // a rotated unit is two blocks
     constexpr int kPairs = kTwo ? N : N / 2;

@@ -6,12 +6,22 @@
 
 namespace hisa {
 
+// Eight f32 to a 32-byte aligned address in one access: a whole sector per thread, where two
+// 16-byte stores each leave half of one.
+__device__ __forceinline__ void store_sector(float *dst, const float *v) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
 struct NormParams {
     int64_t rows;
     int cols;
     int x_bf16, res_bf16;
     int out_dtype;            // hisa_dtype
     int group;                // columns per scale (0: the row)
+    int groups;               // scales per row
+    int unit_shift;           // log2 of the 8-column units per scale (the row: past every unit)
     int pow2;
     float eps;
     int64_t ld_x, ld_res, ld_out;
@@ -21,7 +31,7 @@ struct NormParams {
     void *res_out;            // [rows, cols] or nullptr
     void *out;                // [rows, cols]
     float *scales;            // [rows, cols / group] (8-bit output)
-    int wide;                 // every row start is 16-byte aligned (8-byte for 8-bit codes), cols % 8 == 0
+    int wide;                 // every row start is aligned to 8 elements, cols % 8 == 0
     int chained;
 };
 

@@ -428,7 +428,8 @@ HISA_API hisa_status hisa_sparse_attend(const hisa_attn_desc *desc, const void *
  *   scales       [rows, cols / scale_group] f32 dense ([rows] if scale_group is 0): HISA_E4M3 only,
  *                else NULL
  * Apart from those two cases no output may overlap an input. Every pointer is aligned to its
- * element; rows whose starts are all 16-byte aligned are moved 16 bytes at a time. No workspace. */
+ * element; fastest where every row starts at a multiple of 8 elements and cols is one. Whole
+ * 16-byte blocks that hold an element of x or residual may be read. No workspace. */
 HISA_API hisa_status hisa_rms_norm(const hisa_norm_desc *desc, const void *x, const void *residual,
                           const float *w, void *residual_out, void *out, float *scales,
                           hisa_stream_t stream);
