@@ -60,11 +60,16 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&f)[8]) {
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ void store8(void *base, int64_t at, bool bf16, const float (&f)[8]) {
+// Unit v of a row that starts at `row`, in global memory or (SM) staged in shared memory.
+template <bool SM>
+__device__ __forceinline__ void store8(uint8_t *row, int v, bool bf16, const float (&f)[8]) {
     if (bf16) {
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(base) + at) = pack_bf16(f);
+        reinterpret_cast<uint4 *>(row)[v] = pack_bf16(f);
+    } else if (SM) {
+        reinterpret_cast<float4 *>(row)[2 * v] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4 *>(row)[2 * v + 1] = make_float4(f[4], f[5], f[6], f[7]);
     } else {
-        store_sector(static_cast<float *>(base) + at, f);
+        store_sector(reinterpret_cast<float *>(row) + 8 * v, f);
     }
 }
 
@@ -124,17 +129,18 @@ __device__ __forceinline__ float block_max(float v, float *red) {
 // What both kernels of 8-column units do with a row. With t = h w, f = 1 / sqrt(mean(h^2) + eps) > 0
 // and y = t f, a group's largest |y| is f times its largest |t| (rounding is monotone), so the
 // scales need no pass after the reduction.
-template <typename RT, int VPT>
+template <typename RT, int VPT, bool SM>
 struct Row {
     float h[VPT][8];                                  // the row, then t
     float top[VPT];                                   // largest |t| of the unit's group
     float ss;
 
-    // Unit i: h = x (+ residual, rounded as stored), its squares, t = h w.
+    // Unit i: h = x (+ residual, rounded as stored, and put to rrow), its squares, t = h w. `n` of its
+    // columns are there.
     template <typename XT>
-    __device__ __forceinline__ void take(const NormParams &p, int i, int v, bool in, int64_t row, const Raw8<XT> &x,
-                                         const Raw8<RT> &r, const float (&w)[8]) {
-        if (!in) {
+    __device__ __forceinline__ void take(int i, int v, int n, uint8_t *rrow, const Raw8<XT> &x, const Raw8<RT> &r,
+                                         const float (&w)[8]) {
+        if (n <= 0) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] = 0.f;
             return;
@@ -150,7 +156,11 @@ struct Row {
                 back.v[0] = pack_bf16(h[i]);
                 unpack(back, h[i]);                    // the norm is over the sum as stored
             }
-            if (p.res_out) store8(p.res_out, row * p.ld_res + (int64_t)v * 8, std::is_same<RT, __nv_bfloat16>::value, h[i]);
+            if (rrow) store8<SM>(rrow, v, std::is_same<RT, __nv_bfloat16>::value, h[i]);
+        }
+        if (SM && n < 8) {                             // the blocks that hold the row's end hold more
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[i][e] = e < n ? h[i][e] : 0.f;
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -180,12 +190,11 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) top[i] = v;
     }
-    __device__ __forceinline__ void put(const NormParams &p, int i, int v, int64_t row, float f) {
-        const int64_t at = row * p.ld_out + (int64_t)v * 8;
+    __device__ __forceinline__ void put(const NormParams &p, int i, int v, int64_t row, uint8_t *orow, float f) {
         if (p.out_dtype != HISA_E4M3) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] *= f;
-            store8(p.out, at, p.out_dtype == HISA_BF16, h[i]);
+            store8<SM>(orow, v, p.out_dtype == HISA_BF16, h[i]);
             return;
         }
         const float s = scale_of(top[i] * f, p.pow2);
@@ -199,9 +208,21 @@ struct Row {
             const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h[i][4 * k + 2] * q, h[i][4 * k + 3] * q), __NV_SATFINITE, __NV_E4M3);
             c[k] = lo | (hi << 16);
         }
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + at) = make_uint2(c[0], c[1]);
+        reinterpret_cast<uint2 *>(orow)[v] = make_uint2(c[0], c[1]);
     }
 };
+
+__device__ __forceinline__ int out_bytes(const NormParams &p) {
+    return p.out_dtype == HISA_F32 ? 4 : (p.out_dtype == HISA_BF16 ? 2 : 1);
+}
+__device__ __forceinline__ uint8_t *out_row(const NormParams &p, int64_t row) {
+    return static_cast<uint8_t *>(p.out) + row * p.ld_out * out_bytes(p);
+}
+template <typename RT>
+__device__ __forceinline__ uint8_t *res_row(const NormParams &p, int64_t row) {
+    if constexpr (std::is_same<RT, None>::value) return nullptr;
+    else return p.res_out ? reinterpret_cast<uint8_t *>(static_cast<RT *>(p.res_out) + row * p.ld_res) : nullptr;
+}
 
 __device__ __forceinline__ void load_w(const float *base, int v, int nvec, float (&w)[8]) {
     const float4 *wp = reinterpret_cast<const float4 *>(base + (int64_t)(v < nvec ? v : 0) * 8);
@@ -236,10 +257,11 @@ __global__ void __launch_bounds__(256, VPT == 1 ? 4 : (VPT == 2 ? 3 : 2)) k_norm
     };
     fetch(row);
     for (; row < p.rows; row += step) {
-        Row<RT, VPT> m;
+        Row<RT, VPT, false> m;
+        uint8_t *rrow = res_row<RT>(p, row), *orow = out_row(p, row);
         m.ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) m.take(p, i, i * 32 + t, i * 32 + t < nvec, row, x[i], r[i], w[i]);
+        for (int i = 0; i < VPT; ++i) m.take(i, i * 32 + t, i * 32 + t < nvec ? 8 : 0, rrow, x[i], r[i], w[i]);
         fetch(row + step);
         if (p.out_dtype == HISA_E4M3) {
             m.tops(p);
@@ -248,7 +270,7 @@ __global__ void __launch_bounds__(256, VPT == 1 ? 4 : (VPT == 2 ? 3 : 2)) k_norm
         const float f = rsqrtf(warp_sum(m.ss) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (i * 32 + t < nvec) m.put(p, i, i * 32 + t, row, f);
+            if (i * 32 + t < nvec) m.put(p, i, i * 32 + t, row, orow, f);
     }
 }
 
@@ -303,7 +325,8 @@ __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
         asm volatile("cp.async.wait_group %0;" :: "n"(STAGES > 1 ? STAGES - 2 : 0) : "memory");
         __syncwarp();
         const uint4 *src = ring + (int64_t)stage * (kX + kR) * nvec;
-        Row<RT, VPT> m;
+        Row<RT, VPT, false> m;
+        uint8_t *rrow = res_row<RT>(p, row), *orow = out_row(p, row);
         m.ss = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -319,7 +342,7 @@ __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
                 }
             }
             if constexpr (!kHoldW) load_w(p.w, v, nvec, w[0]);
-            m.take(p, i, v, v < nvec, row, x, r, w[kHoldW ? i : 0]);
+            m.take(i, v, v < nvec ? 8 : 0, rrow, x, r, w[kHoldW ? i : 0]);
         }
         __syncwarp();
         if (STAGES > 1) {
@@ -334,7 +357,7 @@ __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
         const float f = rsqrtf(block_sum(m.ss, red[par]) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (i * T + t < nvec) m.put(p, i, i * T + t, row, f);
+            if (i * T + t < nvec) m.put(p, i, i * T + t, row, orow, f);
     }
 }
 
@@ -343,9 +366,16 @@ __device__ __forceinline__ float load1(const void *base, int64_t at) {
     if constexpr (std::is_same<T, None>::value) return 0.f;
     else return to_f32(__ldcs(static_cast<const T *>(base) + at));
 }
+template <typename T>
+constexpr size_t kElem = std::is_same<T, None>::value ? 0 : sizeof(T);
+// Bytes of a staged row: the blocks that cover it, and those that shifted reads and the last unit
+// may touch past them.
+__host__ __device__ constexpr size_t stage_bytes(int cols, size_t es) {
+    return es ? ((size_t)cols * es + 15 + 15) / 16 * 16 + 64 : 0;
+}
 
-// The 16-byte pieces that hold row `row` of a [rows, cols] array, whole: up to 15 bytes before
-// and after the row come along (they share a 16-byte block with an element of it).
+// The 16-byte blocks that hold row `row` of an array, whole: up to 15 bytes before and after the
+// row come along (they share a block with an element of it).
 template <typename T>
 __device__ __forceinline__ void copy_row(uint8_t *dst, const void *base, int64_t at, int cols) {
     if constexpr (!std::is_same<T, None>::value) {
@@ -356,54 +386,66 @@ __device__ __forceinline__ void copy_row(uint8_t *dst, const void *base, int64_t
     }
 }
 template <typename T>
-__device__ __forceinline__ const uint8_t *row_in(const uint8_t *stage, const void *base, int64_t at) {
-    if constexpr (std::is_same<T, None>::value) return stage;
-    else return stage + (reinterpret_cast<uintptr_t>(static_cast<const T *>(base) + at) & 15);
+__device__ __forceinline__ int row_offset(const void *base, int64_t at) {
+    if constexpr (std::is_same<T, None>::value) return 0;
+    else return (int)(reinterpret_cast<uintptr_t>(static_cast<const T *>(base) + at) & 15);
 }
-// Writes n bytes (of `es`-byte elements) staged with the destination's own offset into a 16-byte
-// block: whole blocks at once, the row's ragged ends by elements. (Single elements from
-// neighbouring threads leave two partial sectors to every 128 bytes of a row that starts anywhere.)
+// 16 bytes from any byte offset of a 16-byte aligned shared-memory buffer: two aligned reads and
+// a shift that is the same for a whole row.
+__device__ __forceinline__ uint4 read_shifted(const uint8_t *buf, int off) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(buf + (off & ~15)), b = *reinterpret_cast<const uint4 *>(buf + (off & ~15) + 16);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = (off & 8) ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = (off & 4) ? w[i + 1] : w[i];
+    const int s = (off & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
+}
+// Writes n bytes (of `es`-byte elements) staged at a buffer's start: whole 16-byte blocks of the
+// destination at once, the row's ragged ends by elements.
 __device__ __forceinline__ void write_row(uint8_t *dst, const uint8_t *staged, int n, int es) {
     const int a = (int)(reinterpret_cast<uintptr_t>(dst) & 15);
     uint8_t *lo = dst - a;
     for (int i = threadIdx.x; 16 * i < a + n; i += blockDim.x) {
         if (16 * i >= a && 16 * i + 16 <= a + n) {
-            *reinterpret_cast<uint4 *>(lo + 16 * i) = *reinterpret_cast<const uint4 *>(staged + 16 * i);
+            *reinterpret_cast<uint4 *>(lo + 16 * i) = read_shifted(staged, 16 * i - a);
             continue;
         }
         const int b0 = 16 * i > a ? 16 * i : a, b1 = 16 * i + 16 < a + n ? 16 * i + 16 : a + n;
         for (int b = b0; b < b1; b += es) {
-            if (es == 4) *reinterpret_cast<uint32_t *>(lo + b) = *reinterpret_cast<const uint32_t *>(staged + b);
-            else if (es == 2) *reinterpret_cast<uint16_t *>(lo + b) = *reinterpret_cast<const uint16_t *>(staged + b);
-            else lo[b] = staged[b];
+            if (es == 4) *reinterpret_cast<uint32_t *>(lo + b) = *reinterpret_cast<const uint32_t *>(staged + b - a);
+            else if (es == 2) *reinterpret_cast<uint16_t *>(lo + b) = *reinterpret_cast<const uint16_t *>(staged + b - a);
+            else lo[b] = staged[b - a];
         }
     }
 }
-template <typename T>
-constexpr size_t kElem = std::is_same<T, None>::value ? 0 : sizeof(T);
-// Bytes of a staged row.
-template <typename T>
-__host__ __device__ size_t stage_bytes(int cols) {
-    return kElem<T> ? ((size_t)cols * kElem<T> + 15 + 15) / 16 * 16 : 0;
-}
 
-// Rows whose starts are not aligned or whose length is not a multiple of 8: one CTA per row,
-// single elements, neighbouring threads on neighbouring columns. With STAGED, rows come in and go
-// out through shared memory in the aligned 16-byte blocks that cover them, the next row on its
-// way; else (rows too long for that) directly. A warp's 32 columns lie in one scale group (groups
-// are multiples of 32), whose maximum is joined in shared memory.
-template <typename XT, typename RT, int EPT, bool STAGED>
-__global__ void __launch_bounds__(EPT == 16 ? 512 : 1024, EPT == 16 ? 2 : 1) k_norm_narrow(NormParams p) {
-    constexpr bool kRes = !std::is_same<RT, None>::value;
-    extern __shared__ __align__(16) uint4 ring[];     // two stages of x and residual; out; residual_out
+// Rows whose starts are not aligned or whose length is not a multiple of 8 columns: the same
+// units of 8 columns, a CTA per row. Rows come in and go out through shared memory in the aligned
+// 16-byte blocks that cover them, and the shift between blocks and units is made in registers.
+template <typename XT, typename RT, int VPT, int STAGES>
+__global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
+    extern __shared__ __align__(16) uint4 ring[];     // [stage]: x, residual; then out; residual_out
     __shared__ __align__(16) float red[2][32], redm[2][32];
-    __shared__ float gmax[1024];
-    const int T = blockDim.x, t = threadIdx.x;
+    const int T = blockDim.x, t = threadIdx.x, nvec = (p.cols + 7) >> 3;
     const float inv = 1.f / (float)p.cols;
-    const size_t xb = stage_bytes<XT>(p.cols), rb = stage_bytes<RT>(p.cols), ob = stage_bytes<float>(p.cols);
-    uint8_t *in = reinterpret_cast<uint8_t *>(ring), *obuf = in + 2 * (xb + rb), *rbuf = obuf + ob;
-    const int es = p.out_dtype == HISA_F32 ? 4 : (p.out_dtype == HISA_BF16 ? 2 : 1);
+    const int es = out_bytes(p);
+    const size_t xb = stage_bytes(p.cols, kElem<XT>), rb = stage_bytes(p.cols, kElem<RT>);
+    uint8_t *in = reinterpret_cast<uint8_t *>(ring), *obuf = in + STAGES * (xb + rb);
+    uint8_t *rbuf = obuf + stage_bytes(p.cols, es);
     if (t < 32) red[0][t] = red[1][t] = 0.f;
+    constexpr bool kHoldW = VPT <= 2;
+    float w[kHoldW ? VPT : 1][8];
+    auto load_some = [&](int v, float (&to)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) to[e] = v * 8 + e < p.cols ? __ldg(p.w + v * 8 + e) : 0.f;
+    };
+    if constexpr (kHoldW) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) load_some(i * T + t, w[i]);
+    }
     __syncthreads();
     grid_dep_wait();
     auto copy = [&](int64_t row, int stage) {
@@ -412,105 +454,111 @@ __global__ void __launch_bounds__(EPT == 16 ? 512 : 1024, EPT == 16 ? 2 : 1) k_n
             copy_row<RT>(in + stage * (xb + rb) + xb, p.res, row * p.ld_res, p.cols);
         }
     };
-    if constexpr (STAGED) copy(blockIdx.x, 0);
+    copy(blockIdx.x, 0);
     int par = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
-        float h[EPT];
-        uint8_t *orow = static_cast<uint8_t *>(p.out) + row * p.ld_out * es, *rrow = nullptr;
-        if constexpr (kRes)
-            if (p.res_out) rrow = reinterpret_cast<uint8_t *>(static_cast<RT *>(p.res_out) + row * p.ld_res);
-        // where this row's elements are put: staged, with the destination's offset in its block
-        uint8_t *oput = STAGED ? obuf + (reinterpret_cast<uintptr_t>(orow) & 15) : orow;
-        uint8_t *rput = STAGED ? rbuf + (reinterpret_cast<uintptr_t>(rrow) & 15) : rrow;
-        if constexpr (STAGED) {
-            tc::cp_async_wait_all();
-            __syncthreads();                           // every thread's blocks of this row have landed,
-                                                       // and every thread is done with the row before
-            const uint8_t *src = in + par * (xb + rb);
-            const uint8_t *sx = row_in<XT>(src, p.x, row * p.ld_x), *sr = row_in<RT>(src + xb, p.res, row * p.ld_res);
-            copy(row + gridDim.x, par ^ 1);
+        const uint8_t *src = in + (STAGES == 2 ? par : 0) * (xb + rb);
+        const int ax = row_offset<XT>(p.x, row * p.ld_x), ar = row_offset<RT>(p.res, row * p.ld_res);
+        uint8_t *rrow = res_row<RT>(p, row), *orow = out_row(p, row);
+        tc::cp_async_wait_all();
+        __syncthreads();                               // every thread's blocks of this row have landed, and
+                                                       // the row before has been written out
+        if (STAGES == 2) copy(row + gridDim.x, par ^ 1);
+        Row<RT, VPT, true> m;
+        m.ss = 0.f;
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                const int c = i * T + t;
-                h[i] = 0.f;
-                if (c < p.cols) {
-                    h[i] = to_f32(reinterpret_cast<const XT *>(sx)[c]);
-                    if constexpr (kRes) h[i] += to_f32(reinterpret_cast<const RT *>(sr)[c]);
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * T + t;
+            Raw8<XT> x;
+            Raw8<RT> r;
+            if (v < nvec) {
+#pragma unroll
+                for (int k = 0; k < (int)kElem<XT> / 2; ++k) x.v[k] = read_shifted(src, ax + 8 * (int)kElem<XT> * v + 16 * k);
+                if constexpr (kElem<RT> > 0) {
+#pragma unroll
+                    for (int k = 0; k < (int)kElem<RT> / 2; ++k)
+                        r.v[k] = read_shifted(src + xb, ar + 8 * (int)kElem<RT> * v + 16 * k);
                 }
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                const int c = i * T + t;
-                h[i] = c < p.cols ? load1<XT>(p.x, row * p.ld_x + c) : 0.f;
-                if constexpr (kRes)
-                    if (c < p.cols) h[i] += load1<RT>(p.res, row * p.ld_res + c);
-            }
+            if constexpr (!kHoldW) load_some(v, w[0]);
+            m.take(i, v, p.cols - 8 * v, rrow ? rbuf : nullptr, x, r, w[kHoldW ? i : 0]);
         }
-        float ss = 0.f;
+        if (p.out_dtype == HISA_E4M3) {
+            m.tops(p);
+            if (!p.group) m.same_top(block_max(m.top[0], redm[par]));
+        }
+        const float f = rsqrtf(block_sum(m.ss, red[par]) * inv + p.eps);
+        if (STAGES == 1) copy(row + gridDim.x, 0);     // every thread has read this row (the barrier of the sum)
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            const int c = i * T + t;
+        for (int i = 0; i < VPT; ++i)
+            if (i * T + t < nvec) m.put(p, i, i * T + t, row, obuf, f);
+        __syncthreads();                               // the staged outputs are whole
+        write_row(orow, obuf, p.cols * es, es);
+        if (rrow) write_row(rrow, rbuf, p.cols * (int)kElem<RT>, (int)kElem<RT>);
+    }
+}
+
+// Rows too long to be staged: one CTA per row, single elements, neighbouring threads on
+// neighbouring columns, the row read again (from L2) instead of held.
+template <typename XT, typename RT>
+__global__ void __launch_bounds__(1024, 1) k_norm_long(NormParams p) {
+    constexpr bool kRes = !std::is_same<RT, None>::value;
+    __shared__ __align__(16) float red[2][32], redm[2][32];
+    const int T = blockDim.x, t = threadIdx.x;
+    const float inv = 1.f / (float)p.cols;
+    if (t < 32) red[0][t] = red[1][t] = 0.f;
+    __syncthreads();
+    grid_dep_wait();
+    int par = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
+        auto value = [&](int c) {
+            float h = load1<XT>(p.x, row * p.ld_x + c);
+            if constexpr (kRes) h += load1<RT>(p.res, row * p.ld_res + c);
+            if constexpr (std::is_same<RT, __nv_bfloat16>::value) h = __bfloat162float(__float2bfloat16_rn(h));
+            return h;
+        };
+        float ss = 0.f, top = 0.f;
+        for (int c = t; c < p.cols; c += T) {
+            const float h = value(c);
+            ss += h * h;
+            top = max_mag(top, h * __ldg(p.w + c));
+        }
+        const float f = rsqrtf(block_sum(ss, red[par]) * inv + p.eps);
+        if (p.out_dtype == HISA_E4M3 && !p.group) top = block_max(top, redm[par]);
+        for (int c0 = 0; c0 < p.cols; c0 += T) {
+            const int c = c0 + t;
+            const bool in = c < p.cols;
+            const float h = in ? value(c) : 0.f;
+            const float y = in ? h * __ldg(p.w + c) : 0.f;
             if constexpr (kRes) {
-                if constexpr (std::is_same<RT, __nv_bfloat16>::value) {
-                    const __nv_bfloat16 b = __float2bfloat16_rn(h[i]);
-                    h[i] = __bfloat162float(b);
-                    if (rrow && c < p.cols) reinterpret_cast<__nv_bfloat16 *>(rput)[c] = b;
-                } else {
-                    if (rrow && c < p.cols) reinterpret_cast<float *>(rput)[c] = h[i];
+                if (in && p.res_out) {
+                    if constexpr (sizeof(RT) == 2) static_cast<RT *>(p.res_out)[row * p.ld_res + c] = __float2bfloat16_rn(h);
+                    else static_cast<RT *>(p.res_out)[row * p.ld_res + c] = h;
                 }
             }
-            ss += h[i] * h[i];
-        }
-        ss = block_sum(ss, red[par]);
-        const float f = rsqrtf(ss * inv + p.eps);
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            const int c = i * T + t;
-            h[i] = c < p.cols ? h[i] * f * __ldg(p.w + c) : 0.f;
-        }
-        if (p.out_dtype != HISA_E4M3) {
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                const int c = i * T + t;
-                if (c >= p.cols) continue;
-                if (p.out_dtype == HISA_BF16) reinterpret_cast<__nv_bfloat16 *>(oput)[c] = __float2bfloat16_rn(h[i]);
-                else reinterpret_cast<float *>(oput)[c] = h[i];
-            }
-        } else {
-            float all = 0.f;
-            if (p.group == 0) {
-#pragma unroll
-                for (int i = 0; i < EPT; ++i) all = max_mag(all, h[i]);
-                all = block_max(all, redm[par]);
+            const int64_t at = row * p.ld_out + c;
+            if (p.out_dtype == HISA_F32) {
+                if (in) static_cast<float *>(p.out)[at] = y * f;
+            } else if (p.out_dtype == HISA_BF16) {
+                if (in) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(y * f);
             } else {
-#pragma unroll
-                for (int i = 0; i < EPT; ++i) {
-                    const float m = lanes_max(h[i], 32);
-                    const int c = i * T + t;
-                    if ((t & 31) == 0 && c < p.cols) gmax[c >> 5] = m;
+                // a group of up to 256 columns spans 1, 2, 4 or 8 warps of this step (T is a multiple of 256)
+                float m = top;
+                if (p.group) {
+                    m = lanes_max(y, 32);
+                    if ((t & 31) == 0) redm[par][t >> 5] = m;
+                    __syncthreads();
+                    const int w0 = (t >> 5) & ~((p.group >> 5) - 1);
+                    for (int k = 0; k < (p.group >> 5); ++k) m = max_mag(m, redm[par][w0 + k]);
+                    __syncthreads();
                 }
-                __syncthreads();
+                if (in) {
+                    const float s = scale_of(m * f, p.pow2);
+                    const int g = c >> (p.unit_shift + 3);
+                    if (c == g << (p.unit_shift + 3)) p.scales[row * p.groups + g] = s;
+                    static_cast<uint8_t *>(p.out)[at] = __nv_cvt_float_to_fp8(y * __fdividef(f, s), __NV_SATFINITE, __NV_E4M3);
+                }
             }
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                const int c = i * T + t;
-                if (c >= p.cols) continue;
-                const int g = c >> (p.unit_shift + 3); // the column's group (0 for one scale per row)
-                float top = all;
-                if (p.group)
-                    for (int k = 0; k < (p.group >> 5); ++k) top = max_mag(top, gmax[g * (p.group >> 5) + k]);
-                const float s = scale_of(top, p.pow2);
-                if (c == g << (p.unit_shift + 3)) p.scales[row * p.groups + g] = s;
-                oput[c] = __nv_cvt_float_to_fp8(h[i] * __fdividef(1.f, s), __NV_SATFINITE, __NV_E4M3);
-            }
-        }
-        if constexpr (STAGED) {
-            __syncthreads();                           // the staged outputs are whole (and gmax has been read)
-            write_row(orow, obuf, p.cols * es, es);
-            if (rrow) write_row(rrow, rbuf, p.cols * (int)kElem<RT>, (int)kElem<RT>);
-        } else {
-            if (p.out_dtype == HISA_E4M3 && p.group) __syncthreads();   // gmax is read before the next row's is written
         }
     }
 }
@@ -538,9 +586,9 @@ cudaError_t go(const NormParams &p, int threads, int64_t rows_per_cta, size_t sm
 template <typename XT, typename RT>
 cudaError_t pick(const NormParams &p, cudaStream_t s) {
     const size_t row = (size_t)p.cols * (kElem<XT> + kElem<RT>);
+    const int nvec = (p.cols + 7) / 8;
+    auto up = [](int n) { return (n + 31) / 32 * 32; };
     if (p.wide && row <= kMaxSmem) {
-        const int nvec = p.cols / 8;
-        auto up = [](int n) { return (n + 31) / 32 * 32; };
         // up to 1024 columns a warp holds the row (no barrier); above, a CTA of up to 512 threads
         // with a unit each, or of up to 1024 with two or four
         if (nvec <= 32) return go<k_norm_warp<XT, RT, 1>>(p, 256, 8, 0, s);
@@ -551,11 +599,15 @@ cudaError_t pick(const NormParams &p, cudaStream_t s) {
         if (3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 4, 3>>(p, up((nvec + 3) / 4), 1, 3 * row, s);
         return go<k_norm_cta<XT, RT, 4, 1>>(p, up((nvec + 3) / 4), 1, row, s);
     }
-    if (p.cols <= 8192)                                // 192 KB at most
-        return go<k_norm_narrow<XT, RT, 16, true>>(p, ((p.cols + 15) / 16 + 31) / 32 * 32, 1,
-                                                   2 * (stage_bytes<XT>(p.cols) + stage_bytes<RT>(p.cols)) +
-                                                       stage_bytes<float>(p.cols) + stage_bytes<RT>(p.cols), s);
-    return go<k_norm_narrow<XT, RT, 32, false>>(p, ((p.cols + 31) / 32 + 31) / 32 * 32, 1, 0, s);
+    const size_t in = stage_bytes(p.cols, kElem<XT>) + stage_bytes(p.cols, kElem<RT>);
+    const size_t out = stage_bytes(p.cols, p.out_dtype == HISA_F32 ? 4 : (p.out_dtype == HISA_BF16 ? 2 : 1)) +
+                       (p.res_out ? stage_bytes(p.cols, kElem<RT>) : 0);
+    if (2 * in + out <= kMaxSmem) {
+        if (nvec <= 512) return go<k_norm_ragged<XT, RT, 1, 2>>(p, up(nvec), 1, 2 * in + out, s);
+        if (nvec <= 2048) return go<k_norm_ragged<XT, RT, 2, 2>>(p, up((nvec + 1) / 2), 1, 2 * in + out, s);
+    }
+    if (in + out <= kMaxSmem) return go<k_norm_ragged<XT, RT, 4, 1>>(p, up((nvec + 3) / 4), 1, in + out, s);
+    return go<k_norm_long<XT, RT>>(p, 1024, 1, 0, s);
 }
 
 }  // namespace
