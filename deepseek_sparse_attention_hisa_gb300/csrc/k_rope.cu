@@ -73,13 +73,13 @@ __device__ __forceinline__ void store_unit(void *base, int64_t at, const float (
 // N dims per unit (8, or 1 where a boundary is not a multiple of 8). A rotated unit is two
 // blocks of N dims, `lo` and `hi`: for the half layout the pairs (lo + e, hi + e); interleaved,
 // for N = 8 one block holding 4 pairs (hi unused), for N = 1 the pair (lo, hi).
-// Rows per thread in flight: four, or two where a unit is two blocks of 8 (the registers of four
-// would halve the CTAs per SM).
+// Rows per thread in flight: four, or two where a unit is 64 bytes (the registers of four would
+// halve the CTAs per SM).
 template <typename S, int N, bool HALF>
-constexpr int kUnroll = N == 8 && HALF ? 2 : 4;
+constexpr int kUnroll = N == 8 && HALF && sizeof(S) == 4 ? 2 : 4;
 
 template <typename S, typename D, int N, bool HALF>
-__global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? (HALF && sizeof(S) == 2 ? 6 : 4) : 1) k_rope(RopeParams p) {
+__global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(RopeParams p) {
     constexpr int kU = kUnroll<S, N, HALF>;
     constexpr bool kTwo = HALF || N == 1;                 // a rotated unit is two blocks
     constexpr int kPairs = kTwo ? N : N / 2;
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? (HALF && sizeof(
     const int n = n_rot + (p.inplace ? 0 : (p.D - p.dims) / N);
     const int per = blockDim.x / n;                       // rows the CTA takes at once
     const int unit = threadIdx.x % n, sub = threadIdx.x / n;
-    const int64_t r0 = (int64_t)blockIdx.x * p.rows_per_cta;
+    const int64_t r0 = blockIdx.x * p.rows_per_cta;
     int64_t r1 = r0 + p.rows_per_cta;
     r1 = r1 < p.rows ? r1 : p.rows;
     const bool rot = unit < n_rot;
@@ -104,22 +104,34 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? (HALF && sizeof(
     extern __shared__ __align__(16) float2 turn[];        // [token of the batch][pair]: mscale (cos, sin)
     grid_dep_wait();
     const int64_t batch = (int64_t)per * kU;
+    const int step_tok = per / p.heads_all, step_head = per - step_tok * p.heads_all;
     for (int64_t b0 = r0; b0 < r1; b0 += batch) {
         const int64_t base = b0 + sub, last = (b0 + batch < r1 ? b0 + batch : r1) - 1;
         const int64_t tok0 = b0 / p.heads_all;
-        const int at0 = (int)(base - tok0 * p.heads_all);
+        const S *x0 = static_cast<const S *>(p.x) + tok0 * p.x_token, *x20 = static_cast<const S *>(p.x2) + tok0 * p.x2_token;
+        const int left = (int)(r1 - base < batch ? r1 - base : batch);     // rows k per < left are there
         Unit<S, N> a[kU], b[kTwo ? kU : 1];
+        int tok[kU], head[kU];                            // token (from tok0 on) and head of row k
+        head[0] = (int)(base - tok0 * p.heads_all);
+        tok[0] = head[0] / p.heads_all;
+        head[0] -= tok[0] * p.heads_all;
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
-            if (base + (int64_t)k * per >= r1) break;
-            const int tok = (at0 + k * per) / p.heads_all, head = at0 + k * per - tok * p.heads_all;
-            const bool two = head >= p.heads;
-            const void *src = two ? p.x2 : p.x;
-            const int64_t at = two ? (tok0 + tok) * p.x2_token + (head - p.heads) * p.x2_head
-                                   : (tok0 + tok) * p.x_token + head * p.x_head;
-            load_unit<S, N>(src, at + lo, a[k]);
-            if constexpr (kTwo)
-                if (rot) load_unit<S, N>(src, at + hi, b[k]);
+            if (k > 0) {
+                tok[k] = tok[k - 1] + step_tok;
+                head[k] = head[k - 1] + step_head;
+                if (head[k] >= p.heads_all) {
+                    head[k] -= p.heads_all;
+                    ++tok[k];
+                }
+            }
+            if (k * per < left) {
+                const S *src = head[k] < p.heads ? x0 + tok[k] * p.x_token + head[k] * p.x_head
+                                                 : x20 + tok[k] * p.x2_token + (head[k] - p.heads) * p.x2_head;
+                load_unit<S, N>(src, lo, a[k]);
+                if constexpr (kTwo)
+                    if (rot) load_unit<S, N>(src, hi, b[k]);
+            }
         }
         const int angles = (int)(last / p.heads_all - tok0 + 1) * pairs;
         for (int i = threadIdx.x; i < angles; i += blockDim.x) {
@@ -130,18 +142,16 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? (HALF && sizeof(
             turn[i] = make_float2(c * p.mscale, s * p.mscale * p.sin_sign);
         }
         __syncthreads();
+        D *y0 = static_cast<D *>(p.y) + tok0 * p.y_token, *y20 = static_cast<D *>(p.y2) + tok0 * p.y2_token;
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
-            if (base + (int64_t)k * per >= r1) break;
-            const int tok = (at0 + k * per) / p.heads_all, head = at0 + k * per - tok * p.heads_all;
-            const bool two = head >= p.heads;
-            void *dst = two ? p.y2 : p.y;
-            const int64_t at = two ? (tok0 + tok) * p.y2_token + (head - p.heads) * p.y2_head
-                                   : (tok0 + tok) * p.y_token + head * p.y_head;
+            if (k * per >= left) break;
+            D *dst = head[k] < p.heads ? y0 + tok[k] * p.y_token + head[k] * p.y_head
+                                       : y20 + tok[k] * p.y2_token + (head[k] - p.heads) * p.y2_head;
             float u[N];
             to_floats<S, N>(a[k], u);
             if (rot) {
-                const float2 *cs = turn + tok * pairs + unit * kPairs;
+                const float2 *cs = turn + tok[k] * pairs + unit * kPairs;
                 if constexpr (kTwo) {
                     float v[N];
                     to_floats<S, N>(b[k], v);
@@ -151,7 +161,7 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? (HALF && sizeof(
                         u[e] = x * cs[e].x - y * cs[e].y;
                         v[e] = x * cs[e].y + y * cs[e].x;
                     }
-                    store_unit<D, N>(dst, at + hi, v);
+                    store_unit<D, N>(dst, hi, v);
                 } else {
 #pragma unroll
                     for (int e = 0; e < kPairs; ++e) {
@@ -161,7 +171,7 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? (HALF && sizeof(
                     }
                 }
             }
-            store_unit<D, N>(dst, at + lo, u);
+            store_unit<D, N>(dst, lo, u);
         }
         if (b0 + batch < r1) __syncthreads();             // the angles are read before the next batch's are written
     }
@@ -184,13 +194,12 @@ cudaError_t launch_as(RopeParams p, cudaStream_t s) {
     };
     while (shared(per) > 40 * 1024) per = (per + 1) / 2;
     const int threads = per * n;
-    // rows per CTA: one batch, more once every SM has several CTAs
+    // rows per CTA: whole batches, so that one round of CTAs (four per SM) takes all
     const int64_t few = (int64_t)per * kU;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    int64_t mul = p.rows / (few * sms * 8);
-    mul = mul < 1 ? 1 : (mul > 4 ? 4 : mul);
-    p.rows_per_cta = (int)(few * mul);
+    const int64_t batches = (p.rows + few - 1) / few, mul = (batches + 4 * sms - 1) / (4 * sms);
+    p.rows_per_cta = few * mul;
     const int64_t grid = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_pdl(k_rope<S, D, N, HALF>, dim3((unsigned)grid), dim3(threads), shared(per), s, p.chained, p);

@@ -47,7 +47,7 @@ struct RopeParams {
     const void *x, *x2;
     void *y, *y2;
     int64_t x_token, x_head, y_token, y_head, x2_token, x2_head, y2_token, y2_head;
-    int rows_per_cta;         // set by launch_rope
+    int64_t rows_per_cta;     // set by launch_rope
     int wide;                 // 8 elements per access fit every boundary
     int chained;
 };
