@@ -64,16 +64,35 @@ hisa_status check_prefix_desc(const hisa_prefix_desc *d) {
     return HISA_OK;
 }
 
-// Segments of the combine: ranges of a query row's own list and of the shared rows. Host
-// arithmetic only (it sizes the workspace).
+// Segments of the combine. Host arithmetic only (it sizes the workspace).
 void prefix_plan(const hisa_prefix_desc *d, PrefixParams *p) {
     const int64_t queries = (int64_t)d->B * d->L;
     const int64_t local = d->W_max < d->window ? d->W_max : d->window;
     const int64_t list = local + d->Np_max;
-    const bool tc = prefix_tc_supported(d->H, d->Dh, d->kv_dtype == HISA_BF16);
-    auto split = [tc](int64_t items, int64_t rows, int64_t *per) {
-        // about two CTAs per SM (the tensor-core kernels hold an SM: one), at least 64 rows each
-        int64_t n = (tc ? kSmTarget : kTargetCtas) / (items > 0 ? items : 1);
+    if (prefix_tc_supported(d->H, d->Dh, d->kv_dtype == HISA_BF16)) {
+        // Pairs of CTAs walk (two query rows, segment) items, a segment an even part of the pair's
+        // tiles: 32 own rows (of each query row) or 64 shared rows. The split with the shortest
+        // longest walk, in tiles (about 0.7 us each): an item costs about 4 more (fill, epilogue);
+        // with several segments each costs a write and a read of its sums (2 KB per query row and
+        // head, both ways at about 6 TB/s), and the merge a launch. Own lists are taken as half full.
+        const int64_t tiles = (d->prefix_rows + 63) / 64 + (local + 31) / 32 + (d->Np_max + 63) / 64;
+        const int64_t pairs = (queries + 1) / 2;
+        double best = 0.0;
+        p->pre_split = 1;
+        for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {
+            const int64_t walk = (pairs * n + kSmTarget / 2 - 1) / (kSmTarget / 2);
+            double cost = (double)walk * (double)((tiles + n - 1) / n + 4);
+            if (n > 1) cost += (double)n * (double)queries * 64 * 4096 / 6e12 / 0.7e-6 + 4;
+            if (n == 1 || cost < best) {
+                best = cost;
+                p->pre_split = (int)n;
+            }
+        }
+        return;
+    }
+    auto split = [](int64_t items, int64_t rows, int64_t *per) {
+        // about two CTAs per SM, at least 64 rows each
+        int64_t n = kTargetCtas / (items > 0 ? items : 1);
         const int64_t most = (rows + 63) / 64;
         n = n > most ? most : n;
         n = n < 1 ? 1 : (n > 64 ? 64 : n);
@@ -83,42 +102,13 @@ void prefix_plan(const hisa_prefix_desc *d, PrefixParams *p) {
     int64_t per = 0;
     p->tail_split = list > 0 ? split(queries, list, &per) : 0;
     p->tail_rows = (int)(per < kMaxRows ? per : kMaxRows);
-    if (d->prefix_rows == 0) return;
-    if (!tc) {
-        p->pre_split = split((queries * d->H + 63) / 64, d->prefix_rows, &p->pre_rows);
-        return;
-    }
-    // Tensor cores: pairs of CTAs walk (two query rows, segment) items of `per` tiles of 64 rows.
-    // The split with the shortest longest walk, in tiles (about 0.7 us each): an item costs
-    // about 4 more (fill, epilogue), and each segment a write and a read of its sums (2 KB per
-    // query row and head, both ways at about 6 TB/s).
-    const int64_t tiles = (d->prefix_rows + 63) / 64, pairs = (queries + 1) / 2;
-    double best = 0.0;
-    for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {
-        const int64_t per_n = (tiles + n - 1) / n, segs = (tiles + per_n - 1) / per_n;
-        const int64_t walk = (pairs * segs + kSmTarget / 2 - 1) / (kSmTarget / 2);
-        const double cost = (double)walk * (double)(per_n + 4) + (double)segs * (double)queries * 64 * 4096 / 6e12 / 0.7e-6;
-        if (n == 1 || cost < best) {
-            best = cost;
-            p->pre_split = (int)segs;
-            p->pre_rows = per_n * 64;
-        }
-    }
+    p->pre_split = d->prefix_rows > 0 ? split((queries * d->H + 63) / 64, d->prefix_rows, &p->pre_rows) : 0;
 }
 
-// The local and own rows' segments on the tensor cores.
-cudaError_t launch_tail_tc(const PrefixParams &p, cudaStream_t s) {
-    AttnParams a{};
-    a.B = p.B; a.L = p.L; a.H = p.H; a.Dh = p.Dh; a.window = p.window; a.W_max = p.W_max; a.r = p.r;
-    a.causal = p.L > 1;
-    a.Np_max = p.Np_max; a.kv_rows = p.kv_rows;
-    a.scale = p.scale;
-    a.q = p.q; a.local_kv = p.local_kv; a.local_len = p.local_len; a.local_pos0 = p.local_pos0;
-    a.pooled_kv = p.pooled_kv; a.kv_off = p.kv_off; a.t0 = p.t0;
-    a.nsplit = p.tail_split;
-    a.kv_bf16 = p.bf16;
-    a.status = p.status;
-    return launch_attend_tc_part(a, AttendPart{p.P, p.part_o, p.part_ml}, s);
+// Segments whose sums go through the workspace.
+size_t prefix_parts(const hisa_prefix_desc *d, const PrefixParams &p) {
+    if (prefix_tc_supported(d->H, d->Dh, d->kv_dtype == HISA_BF16) && p.pre_split == 1) return 0;
+    return (size_t)p.tail_split + p.pre_split;
 }
 
 }  // namespace
@@ -129,7 +119,7 @@ size_t prefix_workspace_bytes(const hisa_prefix_desc *d) {
     if (check_prefix_desc(d) != HISA_OK) return 0;
     PrefixParams p{};
     prefix_plan(d, &p);
-    const size_t rows = (size_t)d->B * d->L * d->H, seg = (size_t)p.tail_split + p.pre_split;
+    const size_t rows = (size_t)d->B * d->L * d->H, seg = prefix_parts(d, p);
     return kStatusBytes + round_up(seg * rows * d->Dh * sizeof(float)) + round_up(seg * rows * 2 * sizeof(float));
 }
 
@@ -265,16 +255,20 @@ hisa_status hisa_prefix_attend(const hisa_prefix_desc *d, const void *q, const v
     p.out = out;
     p.bf16 = d->kv_dtype == HISA_BF16; p.out_bf16 = d->out_dtype == HISA_BF16;
     prefix_plan(d, &p);
-    const size_t rows = (size_t)d->B * d->L * d->H, seg = (size_t)p.tail_split + p.pre_split;
+    const size_t rows = (size_t)d->B * d->L * d->H, seg = prefix_parts(d, p);
     char *base = static_cast<char *>(ws) + kStatusBytes;
     p.part_o = reinterpret_cast<float *>(base);
     p.part_ml = reinterpret_cast<float *>(base + round_up(seg * rows * d->Dh * sizeof(float)));
     p.status = static_cast<uint32_t *>(ws);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    const bool tc = prefix_tc_supported(p.H, p.Dh, p.bf16);
-    if (p.tail_split) e = tc ? launch_tail_tc(p, s) : launch_prefix_simt(p, 1, s);
-    if (e == cudaSuccess && p.pre_split) e = tc ? launch_prefix_tc(p, s) : launch_prefix_simt(p, 0, s);
+    if (prefix_tc_supported(p.H, p.Dh, p.bf16)) {
+        e = launch_prefix_tc(p, s);
+        if (p.pre_split == 1) return from_cuda(e);
+    } else {
+        if (p.tail_split) e = launch_prefix_simt(p, 1, s);
+        if (e == cudaSuccess && p.pre_split) e = launch_prefix_simt(p, 0, s);
+    }
     if (e == cudaSuccess) e = launch_prefix_merge(p, s);
     return from_cuda(e);
 }

@@ -22,12 +22,7 @@
 // start the next item). Every mbarrier
 // wait is bounded; a timeout sets HISA_DEV_TIMEOUT, raises a shared abort flag and the CTA
 // drains and exits.
-//
-// The kernel has a second form (kPart) for the shared-prefix combine (k_prefix.cu): the list is
-// the visible local rows and the own pooled rows, which stand behind `base` shared rows, and an
-// item's sums and statistics go out as one segment of that combine, with no sink.
 #include "hisa_internal.cuh"
-#include "ops_internal.cuh"
 #include "tc_ptx.cuh"
 
 namespace hisa {
@@ -120,31 +115,20 @@ struct Item {
     bool bad_off;
 };
 
-template <bool kPart>
-__device__ __forceinline__ Item item_of(const AttnParams &p, const AttendPart &pt, int id) {
+__device__ __forceinline__ Item item_of(const AttnParams &p, int id) {
     Item x;
     x.row = id / p.nsplit;
     x.split = id - x.row * p.nsplit;
     x.bq = x.row / p.L;
     const int j = x.row - x.bq * p.L;
     x.t = (int64_t)p.t0[x.bq] + j;
-    if (kPart && p.Np_max == 0) {                      // no offsets are given
-        x.k0 = x.Np = 0;
-        x.bad_off = false;
-    } else {
-        x.k0 = p.kv_off[x.bq];
-        x.Np = p.kv_off[x.bq + 1] - x.k0;
-        x.bad_off = !seq_ok(p.kv_off, x.bq, p.Np_max, p.kv_rows);
-        if (x.bad_off) x.Np = 0;
-    }
-    if (kPart && p.causal) {                           // the visible own rows are the first ones
-        const int64_t v = visible_len(x.t, p.r, pt.base + x.Np) - pt.base;
-        x.Np = v < 0 ? 0 : v;
-    }
-    const bool window = !kPart || p.W_max > 0;         // else no window buffer is given
-    int64_t nl = window ? p.local_len[x.bq] : 0;
+    x.k0 = p.kv_off[x.bq];
+    x.Np = p.kv_off[x.bq + 1] - x.k0;
+    x.bad_off = !seq_ok(p.kv_off, x.bq, p.Np_max, p.kv_rows);
+    if (x.bad_off) x.Np = 0;
+    int64_t nl = p.local_len[x.bq];
     nl = nl < 0 ? 0 : (nl > p.W_max ? p.W_max : nl);
-    const int64_t pos0 = window ? p.local_pos0[x.bq] : 0;
+    const int64_t pos0 = p.local_pos0[x.bq];
     int64_t lo = x.t - p.window + 1 - pos0, hi = x.t - pos0 + 1;
     lo = lo < 0 ? 0 : lo;
     hi = hi > nl ? nl : hi;
@@ -152,13 +136,11 @@ __device__ __forceinline__ Item item_of(const AttnParams &p, const AttendPart &p
     x.nloc = hi > lo ? hi - lo : 0;
     const int64_t npool = p.I ? (int64_t)p.k : x.Np;
     const int64_t ntot = x.nloc + npool;
-    int64_t per = p.rows_per_split;
-    if (kPart) per = ((ntot + p.nsplit - 1) / p.nsplit + kTR - 1) / kTR * kTR;   // even parts of this row's own list
-    x.e0 = (int64_t)x.split * per;
-    x.e1 = x.e0 + per;
+    x.e0 = (int64_t)x.split * p.rows_per_split;
+    x.e1 = x.e0 + p.rows_per_split;
     x.e1 = x.e1 > ntot ? ntot : x.e1;
     x.T = x.e1 > x.e0 ? (int)((x.e1 - x.e0 + kTR - 1) / kTR) : 0;
-    x.V = !kPart && p.causal ? visible_len(x.t, p.r, x.Np) : x.Np;
+    x.V = p.causal ? visible_len(x.t, p.r, x.Np) : x.Np;
     return x;
 }
 
@@ -176,8 +158,7 @@ __device__ __forceinline__ bool group_all(int id, int n, bool v) {
     return r != 0u;
 }
 
-template <bool kPart>
-__device__ __forceinline__ void attend_tc(const AttnParams &p, const AttendPart &part) {
+__global__ void __launch_bounds__(kThreads, 1) k_attend_tc(AttnParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -212,12 +193,7 @@ __device__ __forceinline__ void attend_tc(const AttnParams &p, const AttendPart 
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = misc->tmem;
-    if (kPart) {
-        // the shared rows' kernel follows and depends on nothing of this one: it may take idle SMs
-        grid_dep_wait();
-        grid_dep_trigger();
-    }
-    // else no grid_dep_wait() here: the producers wait before their first selected id and the
+    // no grid_dep_wait() here: the producers wait before their first selected id and the
     // epilogue before its first output write; the first item's q and local rows go first
     bool ok = true;
     auto fail = [&]() {
@@ -237,7 +213,7 @@ __device__ __forceinline__ void attend_tc(const AttnParams &p, const AttendPart 
         int n = 0;
         bool waited = false;                                  // grid_dep_wait() done
         for (int id = blockIdx.x; id < items; id += gridDim.x, ++n) {
-            const Item x = item_of<kPart>(p, part, id);
+            const Item x = item_of(p, id);
             const __nv_bfloat16 *qrow = reinterpret_cast<const __nv_bfloat16 *>(p.q) + (int64_t)x.row * kH * kDH;
             // the item's q: dims [0, kQT) into the next ring slot (its Full barrier, like a
             // tile's; the epilogue warps move them into TMEM and free the slot), dims [kQT, 512)
@@ -383,7 +359,7 @@ __device__ __forceinline__ void attend_tc(const AttnParams &p, const AttendPart 
         uint32_t gt = 0;                                  // list tiles (all items)
         int n = 0;
         for (int id = blockIdx.x; id < items && ok; id += gridDim.x, ++n) {
-            const Item x = item_of<kPart>(p, part, id);
+            const Item x = item_of(p, id);
             ++g;                                          // the ring entry that carried q
             if (warp == kMmaWarp) {
                 // S = Q . K^T of every tile of the item, then release q to the producers
@@ -462,7 +438,7 @@ __device__ __forceinline__ void attend_tc(const AttnParams &p, const AttendPart 
         const int h = warp * 16 + (lane & 15);
         const int half = lane >> 4;
         const float c2 = p.scale * kLog2e;
-        const float sink2 = kPart ? 0.f : p.sinks[h] * kLog2e;
+        const float sink2 = p.sinks[h] * kLog2e;
         uint32_t pfree_seen[kPBufs] = {};
         auto wait_pfree = [&](int buf, uint32_t phase) -> bool {   // PV of tile (kPBufs*phase + buf) done
             while (pfree_seen[buf] <= phase) {
@@ -476,7 +452,7 @@ __device__ __forceinline__ void attend_tc(const AttnParams &p, const AttendPart 
         uint32_t gt = 0;                                // list tiles (all items)
         int n = 0;
         for (int id = blockIdx.x; id < items; id += gridDim.x, ++n) {
-            const Item x = item_of<kPart>(p, part, id);
+            const Item x = item_of(p, id);
             float m2 = -INFINITY, l = 0.f;
             ++g;                                        // the ring entry that carried q (the epilogue's)
             for (int i = 0; i < x.T; ++i, ++g, ++gt) {
@@ -569,7 +545,7 @@ __device__ __forceinline__ void attend_tc(const AttnParams &p, const AttendPart 
             const bool wo = n < 1 || wait_bar(&bars[kBarOFree], (n - 1) & 1, abort);
             if (!group_all(kBarSoft, kSoftWarps * 32, wo)) { fail(); break; }
             if (lead) {
-                if (!kPart && p.nsplit == 1) {
+                if (p.nsplit == 1) {
                     const float M = fmaxf(m2, sink2);
                     const float wm = (m2 == -INFINITY) ? 0.f : exp2f(m2 - M);
                     misc->factor[h] = wm / (l * wm + exp2f(sink2 - M));
@@ -621,7 +597,7 @@ __device__ __forceinline__ void attend_tc(const AttnParams &p, const AttendPart 
         uint32_t gq = 0;                                // ring entry of this item's q
         int n = 0;
         for (int id = blockIdx.x; id < items; id += gridDim.x, ++n) {
-            const Item x = item_of<kPart>(p, part, id);
+            const Item x = item_of(p, id);
             if (n == 0 && !copy_q(0)) { fail(); break; }
             // the next item's q, as soon as this item's S products no longer read the old one
             if (id + (int)gridDim.x < items) {
@@ -638,28 +614,7 @@ __device__ __forceinline__ void attend_tc(const AttnParams &p, const AttendPart 
             fence_after_sync();
             if (n == 0) grid_dep_wait();                // before the first output write
             const bool have_o = x.T > 0;
-            if constexpr (kPart) {
-                const int64_t at = ((int64_t)x.split * p.B * p.L + x.row) * kH;
-                if (quad == 0) {
-                    for (int hh = lane; hh < kH; hh += 32)
-                        *reinterpret_cast<float2 *>(part.ml + (at + hh) * 2) = make_float2(misc->stat_m[hh], misc->stat_l[hh]);
-                }
-                for (int mt = 0; mt < 4; ++mt) {
-                    const int d = mt * 128 + quad * 32 + lane;
-                    for (int c = 0; c < 64; c += 16) {
-                        float o[16];
-                        if (have_o) {
-                            tmem_ld16(tmem + ((uint32_t)(32 * quad) << 16) + kColO + mt * 64 + c, o);
-                            tmem_ld_wait();
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 16; ++q) o[q] = 0.f;
-                        }
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) part.o[(at + c + q) * kDH + d] = o[q];
-                    }
-                }
-            } else if (p.nsplit == 1) {
+            if (p.nsplit == 1) {
                 const int64_t out0 = (int64_t)x.row * kH * kDH;
                 for (int mt = 0; mt < 4; ++mt) {
                     const int d = mt * 128 + quad * 32 + lane;
@@ -724,9 +679,6 @@ __device__ __forceinline__ void attend_tc(const AttnParams &p, const AttendPart 
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) k_attend_tc(AttnParams p) { attend_tc<false>(p, AttendPart{}); }
-__global__ void __launch_bounds__(kThreads, 1) k_attend_tc_part(AttnParams p, AttendPart part) { attend_tc<true>(p, part); }
-
 }  // namespace
 
 int attend_tc_supported(int H, int Dh, int kv_bf16) { return H == kH && Dh == kDH && kv_bf16; }
@@ -743,15 +695,6 @@ cudaError_t launch_attend_tc(const AttnParams &p, cudaStream_t s) {
     cudaError_t e = launch_pdl(k_attend_tc, grid, dim3(kThreads), kSmemBytes, s, p.chained, p);
     if (e != cudaSuccess || p.nsplit == 1) return e;
     return launch_attend_combine(p, s);
-}
-
-cudaError_t launch_attend_tc_part(const AttnParams &p, const AttendPart &part, cudaStream_t s) {
-    const cudaError_t attr = smem_attr_once<k_attend_tc_part>((int)kSmemBytes);
-    if (attr != cudaSuccess) return attr;
-    const int nsm = device_sm_count();
-    if (nsm <= 0) return cudaErrorInvalidDevice;
-    const int64_t items = (int64_t)p.B * p.L * p.nsplit;
-    return launch_pdl(k_attend_tc_part, dim3((unsigned)(items < nsm ? items : nsm)), dim3(kThreads), kSmemBytes, s, 1, p, part);
 }
 
 }  // namespace hisa

@@ -8,10 +8,10 @@
 // rows are stacked across sequences (one staged chunk of shared rows serves R stacked rows),
 // and the local and own rows become segments of one query row each.
 //
-// The kernel here: R query rows x 32 list rows per chunk, 16 threads per row group, scores and
+// The kernel here serves f32, and bf16 heads of 64 and 128 dims: R query rows x 32 list rows per chunk, 16 threads per row group, scores and
 // sums in f32 registers, the running maximum and sum per row (a rescale per chunk). Bound by the
 // FMA pipe and its shared-memory operands.
-#include "ops_internal.cuh"
+#include "prefix_common.cuh"
 
 namespace hisa {
 namespace {
@@ -33,40 +33,6 @@ __device__ __forceinline__ float4 load4(const T *p) {
         return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                            __uint_as_float(u.y & 0xffff0000u));
     }
-}
-
-// The visible part of query row q's own list: local rows [lo, lo + nloc) of its window buffer,
-// then own pooled rows [0, nown).
-struct Tail {
-    int64_t lo, nloc, k0, nown;
-};
-__device__ __forceinline__ Tail tail_of(const PrefixParams &p, int row, bool report) {
-    const int b = row / p.L, j = row - b * p.L;
-    const int64_t t = (int64_t)p.t0[b] + j;
-    Tail x{0, 0, 0, 0};
-    int64_t nl = p.W_max > 0 ? p.local_len[b] : 0;
-    nl = nl < 0 ? 0 : (nl > p.W_max ? p.W_max : nl);
-    if (nl > 0) {
-        const int64_t pos0 = p.local_pos0[b];
-        int64_t lo = t - p.window + 1 - pos0, hi = t - pos0 + 1;
-        lo = lo < 0 ? 0 : lo;
-        hi = hi > nl ? nl : hi;
-        x.lo = lo;
-        x.nloc = hi > lo ? hi - lo : 0;
-    }
-    if (p.Np_max > 0) {
-        if (seq_ok(p.kv_off, b, p.Np_max, p.kv_rows)) {
-            x.k0 = p.kv_off[b];
-            x.nown = p.kv_off[b + 1] - x.k0;
-            if (p.L > 1) {
-                const int64_t v = visible_len(t, p.r, p.P + x.nown) - p.P;
-                x.nown = v < 0 ? 0 : (v < x.nown ? v : x.nown);
-            }
-        } else if (report) {
-            flag(p.status, HISA_DEV_BAD_OFFSETS);
-        }
-    }
-    return x;
 }
 
 // One item: R stacked query rows (shared rows) or the R = H heads of one query row (its own
@@ -247,7 +213,8 @@ template <typename T>
 cudaError_t pick(const PrefixParams &p, int tail, cudaStream_t s) {
     if (p.Dh == 64) return tail ? go<8, 64, T>(p, 1, s) : go<64, 64, T>(p, 0, s);
     if (p.Dh == 128) return tail ? go<16, 128, T>(p, 1, s) : go<64, 128, T>(p, 0, s);
-    return go<64, 512, T>(p, tail, s);
+    if constexpr (sizeof(T) == 4) return go<64, 512, T>(p, tail, s);
+    return cudaErrorInvalidValue;                         // bf16 heads of 512 dims: k_prefix_tc.cu
 }
 
 }  // namespace

@@ -1,14 +1,13 @@
-// Shared-prefix combine on the tensor cores: the shared rows' segments for 64 bf16 query heads
-// of 512 dims (one KV head, K = V).
+// Shared-prefix combine on the tensor cores: 64 bf16 query heads of 512 dims (one KV head, K = V).
 //
 // The shared rows are the same for every query row of the batch, so the query rows (64 heads
 // each) stack into tiles: S = Q K^T and O += P V are dense products of 4 * 512 operations per
 // (stacked row, shared row), bound by the tensor cores.
 //
-// A pair of CTAs (a cluster of two) takes two query rows (128 stacked rows) and one segment.
-// O is 128 x 512 f32: 64 KB of each CTA's 256 KB of TMEM per CTA only because the pair splits
-// the rows (cta_group::2, M = 128: CTA c holds rows 64 c .. + 63, at the full tensor rate, which a
-// single CTA with M = 64 rows halves). Per tile of kT = 64 shared rows:
+// A pair of CTAs (a cluster of two) takes two query rows (128 stacked rows) and one segment of
+// their rows. O is 128 x 512 f32, and the pair splits its rows (cta_group::2, M = 128: CTA c holds
+// rows 64 c .. + 63 in 256 of its 512 TMEM columns, at the full tensor rate, which a single CTA
+// with M = 64 rows halves). Per tile of kT = 64 shared rows:
 //   S [128 x 64]   = Q K^T    A = Q, each CTA its 64 rows; B = K, each CTA 32 of the 64 rows
 //   O [128 x 512] += P V      A = P, each CTA its 64 rows; B = V, each CTA 256 of the 512 dims
 // Both CTAs must give an operand at the same shared-memory offset, so a CTA stages the 32 rows
@@ -18,17 +17,26 @@
 // for two stages of each operand beside the 64 KB of Q. The ceiling is so about 78 % of the
 // tensor peak.
 //
+// The local and own pooled rows of the two query rows come last, in tiles of the same shape:
+// 32 rows of each (TMA again, but for the ragged ends of the lists). S has then 64 columns of which each CTA's
+// rows use the 32 of their own query row, and the two CTAs' parts of P V are issued apart, with the
+// other CTA's TMEM lanes masked off, so that nothing of one sequence's rows (a NaN, say) reaches
+// the other. That does half the useful work per tile, but needs no second kernel, no second read
+// of Q and no sums through memory; with one segment the epilogue writes the output itself.
+//
 // S products run up to kSBufs tiles ahead of the PV products, so the tensor cores do not
-// wait for a tile's softmax and for the two crossings between the CTAs around it. TMEM layout of both accumulators: lanes 0-63 hold the CTA's 64 rows for
-// the first half of the columns, lanes 64-127 the same rows for the second half, so a row's
-// logits sit with two threads of one lane each, which exchange their maxima through shared
-// memory. The running maximum is lazy: O and the sums are rescaled only when a tile's maximum
-// exceeds it by more than 8 (log2 units), so p <= 256. P is rounded to bf16 for the second
-// product (a relative 2^-9 per weight, of random sign); sums are of the unrounded weights in f32.
+// wait for a tile's softmax and for the two crossings between the CTAs around it. TMEM layout of
+// both accumulators: lanes 0-63 hold the CTA's 64 rows for the first half of the columns, lanes
+// 64-127 the same rows for the second half, so a row's logits sit with two threads of one lane
+// each, which exchange their maxima through shared memory. The running maximum is lazy: O and the
+// sums are rescaled only when a tile's maximum exceeds it by more than 8 (log2 units), so p <= 256.
+// P is rounded to bf16 for the second product (a relative 2^-9 per weight, of random sign); sums
+// are of the unrounded weights in f32.
 //
 // Warps of each CTA: 0-3 softmax and epilogue (thread = TMEM lane), 4 and 6 loads, 5, 7 and 8
-// (of CTA 0) MMA issue for the pair. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and the CTAs leave.
-#include "ops_internal.cuh"
+// (of CTA 0) MMA issue for the pair. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and
+// the CTAs leave.
+#include "prefix_common.cuh"
 #include "tc_ptx.cuh"
 
 namespace hisa {
@@ -95,6 +103,10 @@ __device__ __forceinline__ void load_chunks(uint32_t dst, const CUtensorMap *map
                  "[%0], [%1, {%2, %3, %4}], [%5];"
                  :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void prefetch_chunks(const CUtensorMap *map, int row) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+                 :: "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0) : "memory");
+}
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
                  "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
@@ -125,6 +137,25 @@ __device__ __forceinline__ float ex2(float x) {         // 2^x, relative error <
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The same for one CTA's lanes: `other` (0 or 1) names the CTA whose TMEM lanes stay as they are.
+__device__ __forceinline__ void mma_pair_masked(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, int other) {
+    const uint32_t m0 = other == 0 ? 0xffffffffu : 0u, m1 = ~m0;
+    asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5, %6, %6, %6, %6}, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(m0), "r"(m1) : "memory");
+}
+// 32 bytes of output: one sector, or two halves where the output is only 16-byte aligned.
+__device__ __forceinline__ void store_out(void *dst, const uint32_t (&v)[8], bool sector) {
+    if (sector) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                     :: "l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
 // True on the 64 threads of a named barrier iff v is true on all of them (a barrier itself).
 __device__ __forceinline__ bool pair_all(uint32_t id, bool v) {
     uint32_t r;
@@ -133,25 +164,55 @@ __device__ __forceinline__ bool pair_all(uint32_t id, bool v) {
     return r != 0u;
 }
 
-struct Item {
-    int row, seg;             // this CTA's query row; segment
-    int first, rows, tiles;   // its shared rows
+// Tensor maps of own rows (window buffers, pooled rows): boxes of kTO rows, all or half the dims.
+struct Maps {
+    CUtensorMap k, v;
 };
-__device__ __forceinline__ Item item_of(const PrefixParams &p, int id, int rank) {
+
+// One item: a pair of query rows and an even part [a, a + tiles) of the pair's tiles, of which the
+// first `shared` hold the shared rows and the others the query rows' own lists.
+constexpr int kTO = kT / 2;   // own rows of each query row per tile
+struct Item {
+    int row[2], seg;          // query rows of CTA 0 and 1 (the second may be past the last)
+    Tail tail[2];
+    int shared, a, tiles;
+};
+__device__ __forceinline__ Item item_of(const PrefixParams &p, int id, bool report) {
     Item x;
     const int pairs = (p.B * p.L + 1) / 2;
     x.seg = id / pairs;
-    x.row = 2 * (id - x.seg * pairs) + rank;
-    const int64_t a = (int64_t)x.seg * p.pre_rows, e = a + p.pre_rows;
-    x.first = (int)a;
-    x.rows = (int)((e < p.P ? e : p.P) - a);
-    x.tiles = (x.rows + kT - 1) / kT;
+    int own = 0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        x.row[c] = 2 * (id - x.seg * pairs) + c;
+        x.tail[c] = Tail{0, 0, 0, 0};
+        if (x.row[c] < p.B * p.L) x.tail[c] = tail_of(p, x.row[c], report && x.seg == 0);
+        const int t = (int)((x.tail[c].nloc + kTO - 1) / kTO + (x.tail[c].nown + kTO - 1) / kTO);
+        own = t > own ? t : own;
+    }
+    x.shared = (int)((p.P + kT - 1) / kT);
+    const int64_t total = (int64_t)x.shared + own;
+    x.a = (int)(total * x.seg / p.pre_split);
+    x.tiles = (int)(total * (x.seg + 1) / p.pre_split) - x.a;
     return x;
+}
+// A query row's part of own tile i: up to kTO neighbouring rows of its window buffer, then of its
+// pooled rows.
+struct Part {
+    int64_t row;              // first row in local_kv or pooled_kv
+    int count;                // 0..kTO
+    bool local;
+};
+__device__ __forceinline__ Part part_of(const PrefixParams &p, int row, const Tail &l, int i) {
+    const int64_t nl = (l.nloc + kTO - 1) / kTO;
+    const bool local = i < nl;
+    const int64_t at = (local ? (int64_t)i : i - nl) * kTO, n = (local ? l.nloc : l.nown) - at;
+    return Part{local ? (int64_t)(row / p.L) * p.W_max + l.lo + at : l.k0 + at, (int)(n < 0 ? 0 : (n < kTO ? n : kTO)), local};
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-            const __grid_constant__ CUtensorMap vmap) {
+            const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Maps lmap, const __grid_constant__ Maps omap) {
     extern __shared__ __align__(1024) uint8_t raw[];
     const uint32_t r0 = smem_u32(raw);
     uint8_t *smem = raw + (((r0 + 1023u) & ~1023u) - r0);
@@ -164,7 +225,7 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&ms->kfull[s], 1); mbar_init(&ms->vfull[s], 1);
+            mbar_init(&ms->kfull[s], 2); mbar_init(&ms->vfull[s], 2);   // one arrival of each CTA's loader
             mbar_init(&ms->pfull[s], 2 * kSoftWarps);
             mbar_init(&ms->kempty[s], 1); mbar_init(&ms->vempty[s], 1);
             mbar_init(&ms->pfree[s], 1);
@@ -188,9 +249,7 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
     cluster_sync();                                     // both CTAs' barriers and TMEM are there
     fence_after_sync();
     const uint32_t tmem = ms->tmem;
-    if (!p.tail_split) grid_dep_wait();
-    // else the grid before is the one of the call's own lists, which nothing here depends on and
-    // which let this one start once all work before it had completed; waited for at the end
+    grid_dep_wait();
     bool ok = true;
     auto fail = [&]() {
         ok = false;
@@ -200,33 +259,109 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
     if (warp == kLoadWarp || warp == kLoadVWarp) {
         // ---------------- loads of this CTA's share: Q and K, or V ----------------
         // (two warps: K runs ahead of V by as many tiles as S runs ahead of PV)
-        if (lane == 0) {
-            const bool v = warp == kLoadVWarp;
-            uint64_t *full = v ? ms->vfull : ms->kfull, *empty = v ? ms->vempty : ms->kempty;
-            const uint32_t bytes = v ? kVBytes : kKBytes, dst = sbase + (v ? kOffV : kOffK);
-            const CUtensorMap *map = v ? &vmap : &kmap;
-            uint32_t g = 0;
-            int n = 0;
-            for (int id = first_item; id < items && ok; id += step, ++n) {
-                const Item x = item_of(p, id, rank);
-                if (!v) {
-                    if (n > 0 && !mbar_wait_abortable(&ms->qfree, (n - 1) & 1, abort)) { fail(); break; }
+        const bool v = warp == kLoadVWarp;
+        uint64_t *full = v ? ms->vfull : ms->kfull, *empty = v ? ms->vempty : ms->kempty;
+        const uint32_t bytes = v ? kVBytes : kKBytes, dst0 = sbase + (v ? kOffV : kOffK);
+        const CUtensorMap *map = v ? &vmap : &kmap;
+        uint32_t g = 0;
+        int n = 0, pending = -1;                        // stage whose copies are on their way
+        auto settle = [&](bool newer) {                 // its copies have landed; tell the MMA warps
+            if (pending < 0) return;
+            if (newer) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.wait_group 0;" ::: "memory");
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_pair(map_to(&full[pending], 0));
+            pending = -1;
+        };
+        for (int id = first_item; id < items && ok; id += step, ++n) {
+            const Item x = item_of(p, id, false);
+            if (!v) {
+                if (n > 0 && !wait_warp(&ms->qfree, (n - 1) & 1, abort)) { fail(); break; }
+                if (lane == 0) {
                     if (rank == 0) mbar_arrive_expect_tx(&ms->qfull, 2 * kQBytes);
-                    load_chunks(sbase + kOffQ, &qmap, x.row * kH, 0, map_to(&ms->qfull, 0));
-                }
-                for (int i = 0; i < x.tiles; ++i, ++g) {
-                    const uint32_t s = g % kStages;
-                    if (g >= kStages && !mbar_wait_abortable(&empty[s], (g / kStages - 1) & 1, abort)) { fail(); break; }
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
-                    load_chunks(dst + s * bytes, map, x.first + i * kT + (v ? 0 : rank * (kT / 2)), v ? rank * 4 : 0,
-                                map_to(&full[s], 0));
+                    load_chunks(sbase + kOffQ, &qmap, (rank ? x.row[1] : x.row[0]) * kH, 0, map_to(&ms->qfull, 0));
                 }
             }
-            if (!ok && rank == 0) {
-                // copies in flight land before the CTAs leave (bounded, whatever the abort flag says)
-                for (uint32_t b = g > kStages ? g - kStages : 0; b <= g; ++b)
-                    mbar_wait(&full[b % kStages], (b / kStages) & 1, 1u << 20);
+            if (!v) {
+                // own rows come from far: ask for them in L2 while the shared rows' tiles run
+                const int row = rank ? x.row[1] : x.row[0];
+                const Tail mine = rank ? x.tail[1] : x.tail[0];
+                for (int i = (x.a > x.shared ? x.a : x.shared) + lane; i < x.a + x.tiles; i += 32) {
+                    const Part part = part_of(p, row, mine, i - x.shared);
+                    if (part.count > 0) prefetch_chunks(part.local ? &lmap.k : &omap.k, (int)part.row);
+                }
             }
+            for (int i = x.a; i < x.a + x.tiles; ++i, ++g) {
+                const uint32_t s = g % kStages, par = (g / kStages - 1) & 1;
+                if (g >= kStages && !__all_sync(0xffffffffu, mbar_try_wait(&empty[s], par))) {
+                    settle(false);
+                    if (!wait_warp(&empty[s], par, abort)) { fail(); break; }
+                }
+                const uint32_t dst = dst0 + s * bytes;
+                if (i < x.shared) {                     // shared rows
+                    if (lane == 0) {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                        else arrive_pair(map_to(&full[s], 0));
+                        load_chunks(dst, map, i * kT + (v ? 0 : rank * (kT / 2)), v ? rank * 4 : 0,
+                                    map_to(&full[s], 0));
+                    }
+                    settle(false);
+                    continue;
+                }
+                // own rows: as K this CTA's 32, all dims; as V both CTAs' 32, this CTA's 256 dims. K comes
+                // whole (logits of rows past a list's end are masked), and so does V where the part is
+                // whole. A ragged V part is copied with zeros for the rest of its rows, since a weight
+                // of zero does not silence a NaN; an empty one is not used.
+                const Part part[2] = {part_of(p, x.row[0], x.tail[0], i - x.shared), part_of(p, x.row[1], x.tail[1], i - x.shared)};
+                const uint32_t block = kTO * (v ? 256 : kDH) * 2;
+                uint32_t tx = 0;                        // TMA bytes of both CTAs
+                bool ragged = false;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const bool tma = v ? part[c].count == kTO : part[c].count > 0;
+                    tx += tma ? (v ? 2 * block : block) : 0;
+                    ragged |= v && part[c].count > 0 && !tma;
+                    if (tma && lane == 0 && (v || c == rank)) {
+                        const Maps &m = part[c].local ? lmap : omap;
+                        load_chunks(dst + (v ? c * block : 0), v ? &m.v : &m.k, (int)part[c].row, v ? rank * 4 : 0,
+                                    map_to(&full[s], 0));
+                    }
+                }
+                if (rank == 0 && lane == 0) {
+                    if (ragged) asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;"
+                                             :: "r"(smem_u32(&full[s])), "r"(tx) : "memory");
+                    else mbar_arrive_expect_tx(&full[s], tx);
+                }
+                if (rank == 1 && lane == 0 && !ragged) arrive_pair(map_to(&full[s], 0));
+                if (!ragged) {
+                    settle(false);
+                    continue;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (part[c].count == 0 || part[c].count == kTO) continue;
+                    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(part[c].local ? p.local_kv : p.pooled_kv) +
+                                               part[c].row * kDH + rank * 256 + lane * 8;
+                    const uint32_t to = dst + c * block + (lane >> 3) * (kTO * 128);
+#pragma unroll 8
+                    for (int r = 0; r < kTO; ++r) {
+                        const bool in = r < part[c].count;
+                        cp_async16_zfill(to + sw128_offset(r, (lane & 7) * 8), in ? static_cast<const void *>(src + r * kDH) : p.q, in);
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                settle(true);
+                pending = (int)s;
+            }
+            // an item's last tile is not held back by what the next item waits for
+            settle(false);
+        }
+        cp_async_wait_all();
+        if (!ok && rank == 0 && lane == 0) {
+            // copies in flight land before the CTAs leave (bounded, whatever the abort flag says)
+            for (uint32_t b = g > kStages ? g - kStages : 0; b <= g; ++b)
+                mbar_wait(&full[b % kStages], (b / kStages) & 1, 1u << 20);
         }
         __syncwarp();
     } else if (warp == kMmaWarp || warp == kMmaWarp2 || warp == kMmaPvWarp) {
@@ -241,7 +376,7 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
             uint32_t g = 0;
             int n = 0;
             for (int id = first_item; id < items && ok; id += step, ++n) {
-                const Item x = item_of(p, id, 0);
+                const Item x = item_of(p, id, false);
                 if (!wait_warp(&ms->qfull, n & 1, abort)) { fail(); break; }
                 for (int i = 0; i < x.tiles; ++i, ++g) {
                     if ((g & 1) != mine) continue;
@@ -268,7 +403,8 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
             uint32_t g = 0;
             int n = 0;
             for (int id = first_item; id < items && ok; id += step, ++n) {
-                const Item x = item_of(p, id, 0);
+                const Item x = item_of(p, id, false);
+                bool started[2] = {false, false};       // whether the CTA's lanes of O hold sums yet
                 // O starts over once the epilogues have read the item before
                 if (n > 0 && !wait_warp(&ms->ofree, (n - 1) & 1, abort)) { fail(); break; }
                 for (int i = 0; i < x.tiles; ++i, ++g) {
@@ -281,12 +417,31 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                     fence_after_sync();
                     const uint64_t pd = smem_desc_sw128(sbase + kOffP + s * kPBytes, 16, 1024);
                     const uint64_t vd = smem_desc_sw128(sbase + kOffV + s * kVBytes, kVChunk, 1024);
+                    if (x.a + i < x.shared) {
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                        for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int ks = 0; ks < kT / 16; ++ks)
-                            mma_pair(tmem + kColO + m * 128, desc_add(pd, ks * 32), desc_add(vd, m * 2 * kVChunk + ks * 2048),
-                                     idesc, (ks > 0 || i > 0) ? 1u : 0u);
+                            for (int ks = 0; ks < kT / 16; ++ks)
+                                mma_pair(tmem + kColO + m * 128, desc_add(pd, ks * 32),
+                                         desc_add(vd, m * 2 * kVChunk + ks * 2048), idesc, (ks > 0 || i > 0) ? 1u : 0u);
+                        started[0] = started[1] = true;   // (these tiles come first)
+                    } else {
+                        // a block of 32 rows for each CTA, each onto that CTA's own lanes alone
+                        const uint64_t od = smem_desc_sw128(sbase + kOffV + s * kVBytes, kTO * 128, 1024);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int count = part_of(p, x.row[c], x.tail[c], x.a + i - x.shared).count;
+                            if (count == 0) continue;
+#pragma unroll
+                            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                for (int ks = 0; ks < kTO / 16; ++ks)
+                                    mma_pair_masked(tmem + kColO + m * 128, desc_add(pd, (c * 2 + ks) * 32),
+                                                    desc_add(od, c * (kVBytes / 2) + m * 2 * (kTO * 128) + ks * 2048), idesc,
+                                                    (ks > 0 || started[c]) ? 1u : 0u, 1 - c);
+                            started[c] = true;
+                        }
+                    }
                     commit_pair(&ms->vempty[s]);
                     commit_pair(&ms->pfree[s]);
                 }
@@ -305,13 +460,16 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
         const int r = (warp & 1) * 32 + lane, half = warp >> 1;
         const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
         const float c2 = p.scale * kLog2e;
+        const bool sector = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
         const uint32_t pairbar = 1 + (warp & 1);        // the two warps that share 32 rows
         uint32_t g = 0;
         int n = 0;
         bool good = true;                               // no wait of this warp has run out; both warps of a
                                                         // pair leave at the same barrier
         for (int id = first_item; id < items && ok; id += step, ++n) {
-            const Item x = item_of(p, id, rank);
+            const Item x = item_of(p, id, tid == 0 && rank == 0);
+            const int row = rank ? x.row[1] : x.row[0];
+            const Tail mine = rank ? x.tail[1] : x.tail[0];
             float m2 = -INFINITY, l = 0.f;
             for (int i = 0; i < x.tiles; ++i, ++g) {
                 const uint32_t s = g % kStages, par = (g / kStages) & 1, sb = g % kSBufs;
@@ -322,7 +480,11 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) arrive_pair(map_to(&ms->sfree[sb], 0));
-                const int left = x.rows - i * kT - half * (kT / 2);      // of this thread's 32 shared rows
+                // how many of this thread's 32 columns are rows that it sees
+                const int ti = x.a + i;
+                const int64_t seen = ti < x.shared ? p.P - (int64_t)ti * kT - half * kTO
+                                     : half == rank ? part_of(p, row, mine, ti - x.shared).count : 0;
+                const int left = seen < 32 ? (int)seen : 32;
                 if (left < 32) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = k < left ? v[k] : -INFINITY;
@@ -390,17 +552,48 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
             if (!pair_all(pairbar, good)) { fail(); break; }
             l += ms->mx[g & 1][half ^ 1][r];
             asm volatile("bar.sync %0, 64;" ::"r"(pairbar) : "memory");
-            const bool there = x.row < p.B * p.L;
-            const int64_t rows = (int64_t)p.B * p.L * kH, at = (int64_t)(p.tail_split + x.seg) * rows + (int64_t)x.row * kH + r;
-            if (there && half == 0) *reinterpret_cast<float2 *>(p.part_ml + at * 2) = make_float2(m2 * kLn2, l);
-            float *dst = p.part_o + at * kDH + half * 256;
+            const bool there = row < p.B * p.L, some = !(m2 == -INFINITY && l == 0.f);   // a row was seen
+            const int64_t rows = (int64_t)p.B * p.L * kH, g0 = (int64_t)row * kH + r;
+            float f = 1.f;                              // with one segment: the output's scale
+            if (p.pre_split == 1) {
+                const float sink2 = p.sinks ? p.sinks[r] * kLog2e : -INFINITY;
+                const float top = fmaxf(m2, sink2), ref = top == -INFINITY ? 0.f : top;
+                const float w = exp2f(m2 - ref), den = l * w + exp2f(sink2 - ref);
+                f = den == 0.f ? 0.f : w / den;         // nothing visible, no sink: 0
+            }
+            const int64_t at = (int64_t)x.seg * rows + g0;
+            if (there && half == 0 && p.pre_split > 1)
+                *reinterpret_cast<float2 *>(p.part_ml + at * 2) = make_float2(m2 * kLn2, l);
 #pragma unroll 1
             for (int c = 0; c < 256; c += 32) {
                 float o[32];
                 tmem_ld32(lanes + kColO + c, o);
-                if (there) {
+                if (!there) continue;
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) store_sector(dst + c + k, o + k);
+                for (int k = 0; k < 32; ++k) o[k] = some ? o[k] * f : 0.f;
+                const int d = half * 256 + c;
+                if (p.pre_split > 1) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) store_sector(p.part_o + at * kDH + d + k, o + k);
+                } else if (p.out_bf16) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 16) {
+                        uint32_t u[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(o[k + 2 * e], o[k + 2 * e + 1]);
+                            u[e] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                        store_out(static_cast<__nv_bfloat16 *>(p.out) + g0 * kDH + d + k, u, sector);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        uint32_t u[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(o[k + e]);
+                        store_out(static_cast<float *>(p.out) + g0 * kDH + d + k, u, sector);
+                    }
                 }
             }
             fence_before_sync();
@@ -411,7 +604,6 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
     if (!ok) flag(p.status, HISA_DEV_TIMEOUT);
     fence_before_sync();
     __syncthreads();
-    grid_dep_wait();                                    // so that the merge, which waits for this grid, has both
     cluster_sync();                                     // no CTA leaves while the other may signal it
     if (warp == kMmaWarp) {
         fence_after_sync();
@@ -430,13 +622,22 @@ cudaError_t launch_prefix_tc(const PrefixParams &p, cudaStream_t s) {
     if (sms < 2) return cudaErrorInvalidDevice;
     CUtensorMap qmap, kmap, vmap;
     const uint64_t qrows = (uint64_t)p.B * p.L * kH;
+    const void *pre = p.P > 0 ? p.prefix_kv : p.q;
+    const uint64_t pre_rows = p.P > 0 ? (uint64_t)p.P : qrows;
     if (!encode_bf16_chunks(&qmap, p.q, qrows, kDH, kH, 8) ||
-        !encode_bf16_chunks(&kmap, p.prefix_kv, (uint64_t)p.P, kDH, kT / 2, 8) ||
-        !encode_bf16_chunks(&vmap, p.prefix_kv, (uint64_t)p.P, kDH, kT, 4))
+        !encode_bf16_chunks(&kmap, pre, pre_rows, kDH, kT / 2, 8) || !encode_bf16_chunks(&vmap, pre, pre_rows, kDH, kT, 4))
+        return cudaErrorInvalidValue;
+    // a map has rows: an array that is not there is never loaded from
+    Maps lmap, omap;
+    const void *loc = p.W_max > 0 ? p.local_kv : p.q, *own = p.kv_rows > 0 && p.pooled_kv ? p.pooled_kv : p.q;
+    const uint64_t loc_rows = p.W_max > 0 ? (uint64_t)p.B * p.W_max : qrows;
+    const uint64_t own_rows = p.kv_rows > 0 && p.pooled_kv ? (uint64_t)p.kv_rows : qrows;
+    if (!encode_bf16_chunks(&lmap.k, loc, loc_rows, kDH, kTO, 8) || !encode_bf16_chunks(&lmap.v, loc, loc_rows, kDH, kTO, 4) ||
+        !encode_bf16_chunks(&omap.k, own, own_rows, kDH, kTO, 8) || !encode_bf16_chunks(&omap.v, own, own_rows, kDH, kTO, 4))
         return cudaErrorInvalidValue;
     const int items = (p.B * p.L + 1) / 2 * p.pre_split;
     const int pairs = items < sms / 2 ? items : sms / 2;
-    return launch_pdl(k_prefix_tc, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmemBytes, s, 1, p, items, qmap, kmap, vmap);
+    return launch_pdl(k_prefix_tc, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmemBytes, s, 1, p, items, qmap, kmap, vmap, lmap, omap);
 }
 
 }  // namespace hisa

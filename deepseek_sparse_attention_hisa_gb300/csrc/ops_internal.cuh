@@ -66,21 +66,13 @@ struct PrefixParams {
     int bf16, out_bf16;
     int tail_split;           // segments [0, tail_split): a query row's local and own rows
     int tail_rows;            // list rows of one of them
-    int pre_split;            // segments [tail_split, tail_split + pre_split): shared rows
-    int64_t pre_rows;         // shared rows of one of them
+    int pre_split;            // segments [tail_split, tail_split + pre_split): shared rows (on the
+                              // tensor cores all rows, and no tail segments)
+    int64_t pre_rows;         // shared rows of one of them (CUDA cores)
     float *part_o;            // [segments, B * L * H, Dh]
     float *part_ml;           // [segments, B * L * H, 2]: maximum (of the logits), sum
     uint32_t *status;
 };
-
-// The tensor-core combine (k_attend_tc.cu) as segments of the shared-prefix combine: `base`
-// shared rows stand before the own rows; segment x goes to o[x, B * L * H, Dh], ml[x, B * L * H, 2].
-struct AttendPart {
-    int64_t base;
-    float *o;
-    float *ml;
-};
-cudaError_t launch_attend_tc_part(const AttnParams &p, const AttendPart &part, cudaStream_t s);
 
 // Encodes a 3-D tensor map over bf16 [rows, cols]: chunks of 64 columns as the slowest
 // dimension, so one box of box_chunks x box_rows x 64 lands as box_chunks swizzled (128-byte)
@@ -93,7 +85,8 @@ size_t prefix_workspace_bytes(const hisa_prefix_desc *d);
 cudaError_t launch_rms_norm(const NormParams &p, cudaStream_t s);
 cudaError_t launch_rope(const RopeParams &p, cudaStream_t s);
 cudaError_t launch_prefix_simt(const PrefixParams &p, int tail, cudaStream_t s);
-// The shared rows' segments on the tensor cores: bf16, 64 heads of 512 dims.
+// The whole combine on the tensor cores for 64 bf16 heads of 512 dims: pre_split segments of each
+// query row's rows (own and shared), or with one segment the output itself.
 bool prefix_tc_supported(int H, int Dh, int bf16);
 cudaError_t launch_prefix_tc(const PrefixParams &p, cudaStream_t s);
 cudaError_t launch_prefix_merge(const PrefixParams &p, cudaStream_t s);

@@ -467,7 +467,7 @@ HISA_API hisa_status hisa_rope(const hisa_rope_desc *desc, const uint64_t *table
  *   pooled_kv  [kv_rows, Dh] kv_dtype (NULL if Np_max is 0); kv_off [B+1] int64
  *   sinks      [H] f32, or NULL for none (-inf is none for that head);  t0 [B] int32
  *   out        [B, L, H, Dh] out_dtype, 16-byte aligned
- * Rows that no query sees are not read. Offsets that do not fit set HISA_DEV_BAD_OFFSETS; that
+ * What rows hold that a query row does not see has no effect on it. Offsets that do not fit set HISA_DEV_BAD_OFFSETS; that
  * sequence's own rows are skipped. */
 HISA_API hisa_status hisa_prefix_attend(const hisa_prefix_desc *desc, const void *q, const void *local_kv,
                                const int32_t *local_len, const int32_t *local_pos0,
