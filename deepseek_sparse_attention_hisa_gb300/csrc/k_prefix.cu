@@ -52,7 +52,7 @@ __global__ void __launch_bounds__((R < 16 ? R : 16) * 16) k_prefix_simt(PrefixPa
     Tail x{0, 0, 0, 0};
     int64_t e0, e1;
     if (tail) {
-        x = tail_of(p, blockIdx.x, seg == 0 && tid == 0);
+        x = tail_of(p, blockIdx.x, tail_fetch(p, blockIdx.x), seg == 0 && tid == 0);
         e0 = (int64_t)seg * p.tail_rows;
         e1 = e0 + p.tail_rows;
         const int64_t n = x.nloc + x.nown;

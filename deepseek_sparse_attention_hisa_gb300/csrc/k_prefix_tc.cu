@@ -144,18 +144,6 @@ __device__ __forceinline__ void mma_pair_masked(uint32_t d, uint64_t a, uint64_t
                  "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5, %6, %6, %6, %6}, p;\n\t}"
                  :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(m0), "r"(m1) : "memory");
 }
-// 32 bytes of output: one sector, or two halves where the output is only 16-byte aligned.
-__device__ __forceinline__ void store_out(void *dst, const uint32_t (&v)[8], bool sector) {
-    if (sector) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                     :: "l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    }
-}
-
 // True on the 64 threads of a named barrier iff v is true on all of them (a barrier itself).
 __device__ __forceinline__ bool pair_all(uint32_t id, bool v) {
     uint32_t r;
@@ -182,18 +170,24 @@ __device__ __forceinline__ Item item_of(const PrefixParams &p, int id, bool repo
     const int pairs = (p.B * p.L + 1) / 2;
     x.seg = id / pairs;
     int own = 0;
+    TailIn in[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         x.row[c] = 2 * (id - x.seg * pairs) + c;
-        x.tail[c] = Tail{0, 0, 0, 0};
-        if (x.row[c] < p.B * p.L) x.tail[c] = tail_of(p, x.row[c], report && x.seg == 0);
+        in[c] = tail_fetch(p, x.row[c] < p.B * p.L ? x.row[c] : x.row[0]);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const bool there = x.row[c] < p.B * p.L;
+        x.tail[c] = tail_of(p, there ? x.row[c] : x.row[0], in[c], report && x.seg == 0 && there);
+        if (!there) x.tail[c] = Tail{0, 0, 0, 0};
         const int t = (int)((x.tail[c].nloc + kTO - 1) / kTO + (x.tail[c].nown + kTO - 1) / kTO);
         own = t > own ? t : own;
     }
     x.shared = (int)((p.P + kT - 1) / kT);
-    const int64_t total = (int64_t)x.shared + own;
-    x.a = (int)(total * x.seg / p.pre_split);
-    x.tiles = (int)(total * (x.seg + 1) / p.pre_split) - x.a;
+    const int total = x.shared + own, q = total / p.pre_split, r = total - q * p.pre_split;
+    x.a = q * x.seg + r * x.seg / p.pre_split;         // floor(total * seg / pre_split)
+    x.tiles = q * (x.seg + 1) + r * (x.seg + 1) / p.pre_split - x.a;
     return x;
 }
 // A query row's part of own tile i: up to kTO neighbouring rows of its window buffer, then of its
@@ -274,15 +268,24 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
             if (lane == 0) arrive_pair(map_to(&full[pending], 0));
             pending = -1;
         };
+        const int pairs = (p.B * p.L + 1) / 2;
         for (int id = first_item; id < items && ok; id += step, ++n) {
-            const Item x = item_of(p, id, false);
             if (!v) {
                 if (n > 0 && !wait_warp(&ms->qfree, (n - 1) & 1, abort)) { fail(); break; }
                 if (lane == 0) {
                     if (rank == 0) mbar_arrive_expect_tx(&ms->qfull, 2 * kQBytes);
-                    load_chunks(sbase + kOffQ, &qmap, (rank ? x.row[1] : x.row[0]) * kH, 0, map_to(&ms->qfull, 0));
+                    load_chunks(sbase + kOffQ, &qmap, (2 * (id % pairs) + rank) * kH, 0, map_to(&ms->qfull, 0));
                 }
             }
+            // the cluster's first tile, where it is the first shared one whatever the lists hold: on
+            // its way before the sequences' numbers are there
+            const bool early = n == 0 && id < pairs && p.P >= (int64_t)kT * p.pre_split;
+            if (early && lane == 0) {
+                if (rank == 0) mbar_arrive_expect_tx(&full[0], 2 * bytes);
+                else arrive_pair(map_to(&full[0], 0));
+                load_chunks(dst0, map, v ? 0 : rank * (kT / 2), v ? rank * 4 : 0, map_to(&full[0], 0));
+            }
+            const Item x = item_of(p, id, false);
             if (!v) {
                 // own rows come from far: ask for them in L2 while the shared rows' tiles run
                 const int row = rank ? x.row[1] : x.row[0];
@@ -292,7 +295,8 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                     if (part.count > 0) prefetch_chunks(part.local ? &lmap.k : &omap.k, (int)part.row);
                 }
             }
-            for (int i = x.a; i < x.a + x.tiles; ++i, ++g) {
+            if (early) g = 1;
+            for (int i = x.a + (early ? 1 : 0); i < x.a + x.tiles; ++i, ++g) {
                 const uint32_t s = g % kStages, par = (g / kStages - 1) & 1;
                 if (g >= kStages && !__all_sync(0xffffffffu, mbar_try_wait(&empty[s], par))) {
                     settle(false);
@@ -460,14 +464,13 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
         const int r = (warp & 1) * 32 + lane, half = warp >> 1;
         const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
         const float c2 = p.scale * kLog2e;
-        const bool sector = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
         const uint32_t pairbar = 1 + (warp & 1);        // the two warps that share 32 rows
         uint32_t g = 0;
         int n = 0;
         bool good = true;                               // no wait of this warp has run out; both warps of a
                                                         // pair leave at the same barrier
-        for (int id = first_item; id < items && ok; id += step, ++n) {
-            const Item x = item_of(p, id, tid == 0 && rank == 0);
+        Item x = item_of(p, first_item, tid == 0 && rank == 0), next = x;
+        for (int id = first_item; id < items && ok; id += step, ++n, x = next) {
             const int row = rank ? x.row[1] : x.row[0];
             const Tail mine = rank ? x.tail[1] : x.tail[0];
             float m2 = -INFINITY, l = 0.f;
@@ -545,6 +548,7 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                 if (lane == 0) arrive_pair(map_to(&ms->pfull[s], 0));
             }
             if (!ok) break;
+            if (id + step < items) next = item_of(p, id + step, tid == 0 && rank == 0);   // while the last products run
             good = good && wait_warp(&ms->ofull, n & 1, abort);
             fence_after_sync();
             // the row's sum joins over its two threads
@@ -564,37 +568,55 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
             const int64_t at = (int64_t)x.seg * rows + g0;
             if (there && half == 0 && p.pre_split > 1)
                 *reinterpret_cast<float2 *>(p.part_ml + at * 2) = make_float2(m2 * kLn2, l);
+            // O goes out 128 bytes of each row at a time through shared memory (P's buffers are free):
+            // the two warps of 32 rows put their 64 (row, half) pieces there and write them to memory
+            // with eight neighbouring lanes per piece
+            const bool to_bf16 = p.pre_split == 1 && p.out_bf16;
+            uint8_t *out = p.pre_split > 1 ? reinterpret_cast<uint8_t *>(p.part_o + (int64_t)x.seg * rows * kDH)
+                                           : static_cast<uint8_t *>(p.out);
+            const int es = to_bf16 ? 2 : 4, dims = 128 / es;
+            uint8_t *stage = smem + kOffP + (warp & 1) * kPBytes;
+            const int piece = half * 32 + lane, t64 = half * 32 + lane;
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
+            for (int c = 0; c < 256; c += dims) {
                 float o[32];
                 tmem_ld32(lanes + kColO + c, o);
-                if (!there) continue;
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = some ? o[k] * f : 0.f;
-                const int d = half * 256 + c;
-                if (p.pre_split > 1) {
+                if (to_bf16) {
+                    float o2[32];
+                    tmem_ld32(lanes + kColO + c + 32, o2);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) store_sector(p.part_o + at * kDH + d + k, o + k);
-                } else if (p.out_bf16) {
+                    for (int k = 0; k < 32; ++k) o2[k] = some ? o2[k] * f : 0.f;
+                    uint32_t u[32];
 #pragma unroll
-                    for (int k = 0; k < 32; k += 16) {
-                        uint32_t u[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(o[k + 2 * e], o[k + 2 * e + 1]);
-                            u[e] = *reinterpret_cast<const uint32_t *>(&b);
-                        }
-                        store_out(static_cast<__nv_bfloat16 *>(p.out) + g0 * kDH + d + k, u, sector);
+                    for (int k = 0; k < 16; ++k) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]),
+                                             b2 = __floats2bfloat162_rn(o2[2 * k], o2[2 * k + 1]);
+                        u[k] = *reinterpret_cast<const uint32_t *>(&b);
+                        u[16 + k] = *reinterpret_cast<const uint32_t *>(&b2);
                     }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4 *>(stage + piece * 128 + ((k ^ (piece & 7)) << 4)) =
+                            make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        uint32_t u[8];
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<float4 *>(stage + piece * 128 + ((k ^ (piece & 7)) << 4)) =
+                            make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+                asm volatile("bar.sync %0, 64;" ::"r"(pairbar) : "memory");
+                if (there) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(o[k + e]);
-                        store_out(static_cast<float *>(p.out) + g0 * kDH + d + k, u, sector);
+                    for (int j = 0; j < 8; ++j) {
+                        const int e = (t64 >> 3) + 8 * j, u = t64 & 7;            // piece, 16-byte unit
+                        const int64_t g = (int64_t)row * kH + (warp & 1) * 32 + (e & 31);
+                        *reinterpret_cast<uint4 *>(out + (g * kDH + (e >> 5) * 256 + c) * es + u * 16) =
+                            *reinterpret_cast<const uint4 *>(stage + e * 128 + ((u ^ (e & 7)) << 4));
                     }
                 }
+                asm volatile("bar.sync %0, 64;" ::"r"(pairbar) : "memory");
             }
             fence_before_sync();
             __syncwarp();
