@@ -48,7 +48,11 @@ __global__ void __launch_bounds__((R < 16 ? R : 16) * 16) k_prefix_simt(PrefixPa
     const int seg = blockIdx.y;
     const int64_t rows = (int64_t)p.B * p.L * p.H;
     const int64_t g0 = (int64_t)blockIdx.x * R;
-    grid_dep_wait();
+    // The own lists' kernel comes first and lets the shared rows' start beside it, once all work
+    // before it has completed; that one depends on nothing of it and waits for it at its end, so
+    // that the merge, which waits for the last grid, has both.
+    if (tail || !p.tail_split) grid_dep_wait();
+    if (tail) grid_dep_trigger();
     Tail x{0, 0, 0, 0};
     int64_t e0, e1;
     if (tail) {
@@ -160,6 +164,7 @@ __global__ void __launch_bounds__((R < 16 ? R : 16) * 16) k_prefix_simt(PrefixPa
         for (int j = 0; j < DJ; ++j)
             *reinterpret_cast<float4 *>(p.part_o + (at + g) * DH + 4 * tc + 64 * j) = acc[i][j];
     }
+    if (!tail) grid_dep_wait();
 }
 
 // Joins the segments of one (query row, head) and the sink: DH / 4 threads, four dims each.

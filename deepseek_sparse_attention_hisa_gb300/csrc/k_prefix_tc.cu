@@ -165,7 +165,9 @@ struct Item {
     Tail tail[2];
     int shared, a, tiles;
 };
-__device__ __forceinline__ Item item_of(const PrefixParams &p, int id, bool report) {
+// Not inlined: one copy of the code for the five warp roles that ask for it at the kernel's start, each
+// of which waited about a microsecond for instructions of its own.
+__device__ __noinline__ Item item_of(const PrefixParams &p, int id, bool report) {
     Item x;
     const int pairs = (p.B * p.L + 1) / 2;
     x.seg = id / pairs;
