@@ -90,9 +90,9 @@ void prefix_plan(const hisa_prefix_desc *d, PrefixParams *p) {
         }
         return;
     }
-    auto split = [](int64_t items, int64_t rows, int64_t *per) {
-        // about two CTAs per SM, at least 64 rows each
-        int64_t n = kTargetCtas / (items > 0 ? items : 1);
+    auto split = [](int64_t items, int64_t rows, int64_t ctas, int64_t *per) {
+        // about `ctas` CTAs, at least 64 rows each
+        int64_t n = ctas / (items > 0 ? items : 1);
         const int64_t most = (rows + 63) / 64;
         n = n > most ? most : n;
         n = n < 1 ? 1 : (n > 64 ? 64 : n);
@@ -100,9 +100,27 @@ void prefix_plan(const hisa_prefix_desc *d, PrefixParams *p) {
         return (int)((rows + *per - 1) / *per);
     };
     int64_t per = 0;
-    p->tail_split = list > 0 ? split(queries, list, &per) : 0;
+    // five CTAs of the own lists' kernel fit an SM (two, or one with 512 dims, of the shared rows')
+    p->tail_split = list > 0 ? split(queries, list, d->Dh == 512 ? kSmTarget : 5 * kSmTarget, &per) : 0;
     p->tail_rows = (int)(per < kMaxRows ? per : kMaxRows);
-    p->pre_split = d->prefix_rows > 0 ? split((queries * d->H + 63) / 64, d->prefix_rows, &p->pre_rows) : 0;
+    if (d->prefix_rows == 0) return;
+    if (d->kv_dtype == HISA_BF16) {
+        // tiles of 128 stacked rows x ranges of whole 128-row tiles, one CTA per SM: the split with
+        // the shortest longest walk, an item costing about 4 tiles more (fill, epilogue)
+        const int64_t items = (queries * d->H + 127) / 128, tiles = (d->prefix_rows + 127) / 128;
+        int64_t best = 0;
+        for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {
+            const int64_t per_n = (tiles + n - 1) / n, segs = (tiles + per_n - 1) / per_n;
+            const int64_t cost = (items * segs + kSmTarget - 1) / kSmTarget * (per_n + 4);
+            if (n == 1 || cost < best) {
+                best = cost;
+                p->pre_split = (int)segs;
+                p->pre_rows = per_n * 128;
+            }
+        }
+        return;
+    }
+    p->pre_split = split((queries * d->H + 63) / 64, d->prefix_rows, d->Dh == 512 ? kSmTarget : kTargetCtas, &p->pre_rows);
 }
 
 // Segments whose sums go through the workspace.
@@ -267,7 +285,7 @@ hisa_status hisa_prefix_attend(const hisa_prefix_desc *d, const void *q, const v
         if (p.pre_split == 1) return from_cuda(e);
     } else {
         if (p.tail_split) e = launch_prefix_simt(p, 1, s);
-        if (e == cudaSuccess && p.pre_split) e = launch_prefix_simt(p, 0, s);
+        if (e == cudaSuccess && p.pre_split) e = p.bf16 ? launch_prefix_tc1(p, s) : launch_prefix_simt(p, 0, s);
     }
     if (e == cudaSuccess) e = launch_prefix_merge(p, s);
     return from_cuda(e);

@@ -8,7 +8,7 @@
 // rows are stacked across sequences (one staged chunk of shared rows serves R stacked rows),
 // and the local and own rows become segments of one query row each.
 //
-// The kernel here serves f32, and bf16 heads of 64 and 128 dims: R query rows x 32 list rows per chunk, 16 threads per row group, scores and
+// The kernel here serves f32, and the own lists of bf16 heads of 64 and 128 dims: R query rows x 32 list rows per chunk, 16 threads per row group, scores and
 // sums in f32 registers, the running maximum and sum per row (a rescale per chunk). Bound by the
 // FMA pipe and its shared-memory operands.
 #include "prefix_common.cuh"
@@ -216,10 +216,14 @@ cudaError_t go(const PrefixParams &p, int tail, cudaStream_t s) {
 
 template <typename T>
 cudaError_t pick(const PrefixParams &p, int tail, cudaStream_t s) {
-    if (p.Dh == 64) return tail ? go<8, 64, T>(p, 1, s) : go<64, 64, T>(p, 0, s);
-    if (p.Dh == 128) return tail ? go<16, 128, T>(p, 1, s) : go<64, 128, T>(p, 0, s);
-    if constexpr (sizeof(T) == 4) return go<64, 512, T>(p, tail, s);
-    return cudaErrorInvalidValue;                         // bf16 heads of 512 dims: k_prefix_tc.cu
+    if (tail && p.Dh == 64) return go<8, 64, T>(p, 1, s);
+    if (tail && p.Dh == 128) return go<16, 128, T>(p, 1, s);
+    if constexpr (sizeof(T) == 4) {                       // in bf16: k_prefix_tc.cu and k_prefix_tc1.cu
+        if (p.Dh == 64) return go<64, 64, T>(p, 0, s);
+        if (p.Dh == 128) return go<64, 128, T>(p, 0, s);
+        return go<64, 512, T>(p, tail, s);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace

@@ -92,11 +92,6 @@ __device__ __forceinline__ uint32_t map_to(const void *p, uint32_t cta) {
 __device__ __forceinline__ void arrive_pair(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
-// A bounded wait by a whole warp; the common case is a barrier that has completed.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    const bool v = mbar_try_wait(bar, parity) || mbar_wait_abortable(bar, parity, abort);
-    return __all_sync(0xffffffffu, v);
-}
 // Loads a box of the chunked map; the bytes count on `bar`, which may be the other CTA's.
 __device__ __forceinline__ void load_chunks(uint32_t dst, const CUtensorMap *map, int row, int chunk, uint32_t bar) {
     asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
@@ -118,25 +113,6 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
                  "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
                  :: "r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
-                 "%29,%30,%31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-                   "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(addr));
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ float ex2(float x) {         // 2^x, relative error <= 2^-22; -inf -> +0
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // The same for one CTA's lanes: `other` (0 or 1) names the CTA whose TMEM lanes stay as they are.
 __device__ __forceinline__ void mma_pair_masked(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, int other) {
     const uint32_t m0 = other == 0 ? 0xffffffffu : 0u, m1 = ~m0;
@@ -144,14 +120,6 @@ __device__ __forceinline__ void mma_pair_masked(uint32_t d, uint64_t a, uint64_t
                  "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5, %6, %6, %6, %6}, p;\n\t}"
                  :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(m0), "r"(m1) : "memory");
 }
-// True on the 64 threads of a named barrier iff v is true on all of them (a barrier itself).
-__device__ __forceinline__ bool pair_all(uint32_t id, bool v) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 64, p;\n\t"
-                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((uint32_t)v), "r"(id) : "memory");
-    return r != 0u;
-}
-
 // Tensor maps of own rows (window buffers, pooled rows): boxes of kTO rows, all or half the dims.
 struct Maps {
     CUtensorMap k, v;

@@ -89,6 +89,8 @@ cudaError_t launch_prefix_simt(const PrefixParams &p, int tail, cudaStream_t s);
 // query row's rows (own and shared), or with one segment the output itself.
 bool prefix_tc_supported(int H, int Dh, int bf16);
 cudaError_t launch_prefix_tc(const PrefixParams &p, cudaStream_t s);
+// The shared rows' segments on the tensor cores for bf16 heads of 64 and 128 dims.
+cudaError_t launch_prefix_tc1(const PrefixParams &p, cudaStream_t s);
 cudaError_t launch_prefix_merge(const PrefixParams &p, cudaStream_t s);
 
 }  // namespace hisa
