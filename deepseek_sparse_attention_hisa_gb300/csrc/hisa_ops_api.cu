@@ -100,8 +100,8 @@ void prefix_plan(const hisa_prefix_desc *d, PrefixParams *p) {
         return (int)((rows + *per - 1) / *per);
     };
     int64_t per = 0;
-    // five CTAs of the own lists' kernel fit an SM (two, or one with 512 dims, of the shared rows')
-    p->tail_split = list > 0 ? split(queries, list, d->Dh == 512 ? kSmTarget : 5 * kSmTarget, &per) : 0;
+    // eight or more CTAs of the own lists' kernel fit an SM (one of 512 dims)
+    p->tail_split = list > 0 ? split(queries, list, d->Dh == 512 ? kSmTarget : 8 * kSmTarget, &per) : 0;
     p->tail_rows = (int)(per < kMaxRows ? per : kMaxRows);
     if (d->prefix_rows == 0) return;
     if (d->kv_dtype == HISA_BF16) {

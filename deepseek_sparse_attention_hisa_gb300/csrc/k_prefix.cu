@@ -8,7 +8,7 @@
 // rows are stacked across sequences (one staged chunk of shared rows serves R stacked rows),
 // and the local and own rows become segments of one query row each.
 //
-// The kernel here serves f32, and the own lists of bf16 heads of 64 and 128 dims: R query rows x 32 list rows per chunk, 16 threads per row group, scores and
+// The kernel here serves f32, and the own lists of bf16 heads of 64 and 128 dims: R query rows x 32 list rows per chunk, 16 threads per two or four rows, scores and
 // sums in f32 registers, the running maximum and sum per row (a rescale per chunk). Bound by the
 // FMA pipe and its shared-memory operands.
 #include "prefix_common.cuh"
@@ -36,12 +36,15 @@ __device__ __forceinline__ float4 load4(const T *p) {
 }
 
 // One item: R stacked query rows (shared rows) or the R = H heads of one query row (its own
-// list), and one segment of the list. TR x 16 threads; thread (tr, tc) owns rows tr + TR i,
-// scores of chunk rows tc + 16 j, and dims 4 tc + 64 j of the sums.
+// list), and one segment of the list. Thread (tr, tc) of TR x 16 owns kPer rows tr + TR i,
+// their scores of chunk rows tc + 16 j, and dims 4 tc + 64 j of their sums.
+template <int R>
+constexpr int kPer = R == 64 ? 4 : 2;
 template <int R, int DH, typename T>
-__global__ void __launch_bounds__((R < 16 ? R : 16) * 16) k_prefix_simt(PrefixParams p, int tail) {
+__global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_prefix_simt(PrefixParams p, int tail) {
     using S = Smem<R, DH>;
-    constexpr int TR = R < 16 ? R : 16, RP = R / TR, NT = TR * 16, DJ = DH / 64;
+    constexpr int RP = kPer<R>, TR = R / RP, NT = TR * 16, DJ = DH / 64;
+    constexpr int LD = kChunk * (DH / 4) / NT;            // units of four dims per thread and chunk
     extern __shared__ __align__(16) float sm[];
     float *sq = sm, *skv = sq + R * S::kStride, *sp = skv + kChunk * S::kStride;
     const int tid = threadIdx.x, tr = tid / 16, tc = tid % 16;
@@ -86,16 +89,40 @@ __global__ void __launch_bounds__((R < 16 ? R : 16) * 16) k_prefix_simt(PrefixPa
 #pragma unroll
         for (int j = 0; j < DJ; ++j) acc[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    // a chunk waits in registers while the one before is worked on (but for 512 dims, too many)
+    constexpr bool kAhead = LD <= 16;
+    using Raw = typename std::conditional<sizeof(T) == 4, float4, uint2>::type;
+    Raw raw[kAhead ? LD : 1];
+    auto at = [&](int64_t c0, int i) -> const T * {
+        const int64_t e = c0 + i / (DH / 4);
+        if (e >= e1) return nullptr;
+        return (tail ? (e < x.nloc ? loc + e * DH : own + (e - x.nloc) * DH) : pre + e * DH) + (i % (DH / 4)) * 4;
+    };
+    auto fetch = [&](int64_t c0) {
+#pragma unroll
+        for (int k = 0; k < LD; ++k) {
+            const T *src = at(c0, tid + k * NT);
+            raw[k] = Raw{};
+            if (src) raw[k] = *reinterpret_cast<const Raw *>(src);
+        }
+    };
+    auto put = [&](int i, const float4 &v) {
+        *reinterpret_cast<float4 *>(skv + i / (DH / 4) * S::kStride + (i % (DH / 4)) * 4) = v;
+    };
+    if constexpr (kAhead) fetch(e0);
     for (int64_t c0 = e0; c0 < e1; c0 += kChunk) {
         __syncthreads();                                  // the previous chunk has been read
-        for (int i = tid; i < kChunk * (DH / 4); i += NT) {
-            const int r = i / (DH / 4), d = (i % (DH / 4)) * 4;
-            const int64_t e = c0 + r;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (e < e1) v = load4((tail ? (e < x.nloc ? loc + e * DH : own + (e - x.nloc) * DH) : pre + e * DH) + d);
-            *reinterpret_cast<float4 *>(skv + r * S::kStride + d) = v;
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < LD; ++k) put(tid + k * NT, load4(reinterpret_cast<const T *>(&raw[k])));
+        } else {
+            for (int i = tid; i < kChunk * (DH / 4); i += NT) {
+                const T *src = at(c0, i);
+                put(i, src ? load4(src) : make_float4(0.f, 0.f, 0.f, 0.f));
+            }
         }
         __syncthreads();
+        if constexpr (kAhead) fetch(c0 + kChunk);
         float s[RP][2];
 #pragma unroll
         for (int i = 0; i < RP; ++i) s[i][0] = s[i][1] = 0.f;
@@ -154,15 +181,15 @@ __global__ void __launch_bounds__((R < 16 ? R : 16) * 16) k_prefix_simt(PrefixPa
         }
         __syncwarp();                                     // sp is read before the next chunk's is written
     }
-    const int64_t at = (int64_t)((tail ? 0 : p.tail_split) + seg) * rows;
+    const int64_t seg0 = (int64_t)((tail ? 0 : p.tail_split) + seg) * rows;
 #pragma unroll
     for (int i = 0; i < RP; ++i) {
         const int64_t g = g0 + tr + TR * i;
         if (g >= rows) continue;
-        if (tc == 0) *reinterpret_cast<float2 *>(p.part_ml + (at + g) * 2) = make_float2(m[i], l[i]);
+        if (tc == 0) *reinterpret_cast<float2 *>(p.part_ml + (seg0 + g) * 2) = make_float2(m[i], l[i]);
 #pragma unroll
         for (int j = 0; j < DJ; ++j)
-            *reinterpret_cast<float4 *>(p.part_o + (at + g) * DH + 4 * tc + 64 * j) = acc[i][j];
+            *reinterpret_cast<float4 *>(p.part_o + (seg0 + g) * DH + 4 * tc + 64 * j) = acc[i][j];
     }
     if (!tail) grid_dep_wait();
 }
@@ -211,7 +238,7 @@ cudaError_t go(const PrefixParams &p, int tail, cudaStream_t s) {
     const int64_t rows = (int64_t)p.B * p.L * p.H;
     const int64_t tiles = (rows + R - 1) / R;
     return launch_pdl(k_prefix_simt<R, DH, T>, dim3((unsigned)tiles, (unsigned)(tail ? p.tail_split : p.pre_split)),
-                      dim3((R < 16 ? R : 16) * 16), bytes, s, 1, p, tail);
+                      dim3(R / kPer<R> * 16), bytes, s, 1, p, tail);
 }
 
 template <typename T>
