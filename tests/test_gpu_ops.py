@@ -480,6 +480,92 @@ def test_prefix_same_bits_every_time(H, dt):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("H,dt", [(16, "bf16"), (64, "bf16"), (16, "f32")])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prefix_sequences_do_not_meet(H, dt, bad):
+    # a sequence whose own or local rows hold a NaN or an infinity spoils no other
+    c = prefix_case(5, 1, H, 130, [70, 33, 64, 5, 0], dt)
+    clean, _ = run_prefix(c, "f32")
+    c["pooled"][int(c["off"][1]) + 7] = bad
+    c["pooled"][int(c["off"][2]) + 63] = bad
+    c["local"][4, 3] = bad
+    out, _ = run_prefix(c, "f32")
+    for b in range(5):
+        if b in (0, 3):
+            assert torch.equal(out[b], clean[b])
+        else:
+            assert not torch.isfinite(out[b]).all()
+
+
+@pytest.mark.parametrize("H,dt,P,own", [(64, "bf16", 1500, [5, 0, 40]), (64, "bf16", 10, [0, 31, 32, 33]), (16, "bf16", 1500, [5, 0])])
+def test_prefix_chained(H, dt, P, own):
+    c = prefix_case(len(own), 1, H, P, own, dt)
+    out, ws = run_prefix(c, "bf16", flags=hb.FLAG_CHAINED)
+    for _ in range(3):                                           # a call directly behind another, same workspace
+        out, ws = run_prefix(c, "bf16", ws=ws, out=out.zero_(), flags=hb.FLAG_CHAINED)
+    assert hb.device_status(ws) == 0
+    check_prefix(c, out, "bf16")
+
+
+@pytest.mark.parametrize("offset", [8, 16])
+def test_prefix_output_aligned_to_16_bytes_alone(offset):
+    c = prefix_case(2, 1, 64, 100, [3, 40], "bf16")
+    buf = torch.zeros(2 * 64 * 512 + 64, device="cuda", dtype=torch.bfloat16)
+    out = buf[offset:offset + 2 * 64 * 512].view(2, 1, 64, 512)
+    run_prefix(c, "bf16", out=out)
+    check_prefix(c, out, "bf16")
+    assert (buf[:offset] == 0).all() and (buf[offset + 2 * 64 * 512:] == 0).all()
+
+
+@pytest.mark.parametrize("window,L", [(16, 1), (33, 5), (128, 9)])
+def test_prefix_windows(window, L):
+    # windows that start and end inside the buffer
+    c = prefix_case(3, L, 64, 70, [9, 0, 40], "bf16", window=window, W=window + 40, t0=4 * 70 + 60)
+    for b in range(3):
+        c["len"][b] = window + 30 - 11 * b
+        c["pos0"][b] = c["t0"][b] - window - 5 + b
+        n = int(c["len"][b])
+        c["local"][b] = randn(tuple(c["local"][b].shape), "bf16", 40 + b)
+        c["local"][b, n:] = NAN
+    out, _ = run_prefix(c, "f32")
+    check_prefix(c, out, "f32")
+
+
+# ------------------------------------------------------------------------------------
+# offsets past 32 bits
+# ------------------------------------------------------------------------------------
+def test_norm_past_32_bits():
+    rows, cols = 300001, 8192                                    # 2.46e9 elements
+    x, w = torch.zeros((rows, cols), device="cuda", dtype=torch.bfloat16), torch.ones(cols, device="cuda")
+    pick = [0, 131072, 262144, rows - 1]
+    x[pick] = randn((4, cols), "bf16", 60)
+    out, _, _ = run_norm(x, None, w, "bf16", out=x)
+    assert torch.equal(x[1], torch.zeros_like(x[1]))
+    check_norm(randn((4, cols), "bf16", 60), None, w, "bf16", x[pick], None, None)
+
+
+def test_rope_past_32_bits():
+    tokens, heads, D = 66000, 64, 512                            # 2.16e9 elements, in place
+    x = torch.zeros((tokens, heads, D), device="cuda", dtype=torch.bfloat16)
+    pick = torch.tensor([0, 65535, 65536, tokens - 1], device="cuda")
+    x[pick] = randn((4, heads, D), "bf16", 61)
+    was, pos = x[pick].clone(), torch.arange(tokens, device="cuda", dtype=torch.int32)
+    run_rope(x, x, pos, 64, 448)
+    check_rope(x[pick], *rope_exact(was, pos[pick], 64, 448, 0, 0, 0.0, 1.0), "bf16")
+
+
+def test_prefix_own_rows_past_32_bits():
+    c = prefix_case(3, 1, 64, 100, [40, 7, 33], "bf16")
+    far = 4_300_000                                              # rows of 1 KiB: past 2^32 bytes and 2^31 elements
+    pool = torch.empty((far + 100, 512), device="cuda", dtype=torch.bfloat16)
+    pool[far:far + 80] = c["pooled"][:80]
+    pool[far + 80:] = NAN
+    c["pooled"], c["off"] = pool, c["off"] + far
+    out, ws = run_prefix(c, "f32")
+    assert hb.device_status(ws) == 0
+    check_prefix(c, out, "f32")
+
+
 # ------------------------------------------------------------------------------------
 # streams and graphs
 # ------------------------------------------------------------------------------------
