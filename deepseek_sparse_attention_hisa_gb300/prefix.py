@@ -1,0 +1,95 @@
+"""Device-resident state of one attention layer's decode for a batch that shares a long prefix,
+and the calls of a step, in order.
+
+Marshalling only: torch allocates the tensors, owns the stream and multiplies by the projection
+weights; everything else is one libhisa entry point each (include/hisa.h):
+
+  hisa_rms_norm       residual addition, norm, 8-bit activations with scales
+  (projections)       queries and the token's KV row, torch matmul
+  hisa_rope           queries, and the KV row straight into its slot of the window buffer
+  hisa_prefix_attend  the dense combine over window, shared pooled rows, own pooled rows and sinks
+  hisa_rope           the output turned back (K = V: its rotated dims carry positions), in place
+"""
+from __future__ import annotations
+
+from . import binding as hb
+
+H, DH, ROPE_DIMS = 64, 512, 64
+
+
+class PrefixDecode:
+    """B sequences that decode in step behind one shared prefix of P pooled rows.
+
+    weights: norm [hidden] f32, q [hidden, H * DH] bf16, kv [hidden, DH] bf16, sinks [H] f32.
+    prefix_kv: [P, DH] bf16. start: the position of the first token decoded. steps: how many tokens
+    the window buffer takes. own_rows: pooled rows each sequence may add (append_pooled)."""
+
+    def __init__(self, B, weights, prefix_kv, start, steps, own_rows=0, window=128, r=4, eps=1e-6, theta=160000.0,
+                 device="cuda"):
+        import torch
+        self.B, self.w, self.prefix_kv, self.n = B, weights, prefix_kv, 0
+        self.start, self.steps, self.hidden = start, steps, weights["norm"].numel()
+        bf16 = dict(device=device, dtype=torch.bfloat16)
+        i32 = dict(device=device, dtype=torch.int32)
+        group = 128 if self.hidden % 128 == 0 else 0
+        self.norm_desc = hb.NormDesc(rows=B, cols=self.hidden, x_dtype=hb.HISA_BF16, res_dtype=hb.HISA_BF16,
+                                     out_dtype=hb.HISA_E4M3, scale_group=group, eps=eps, ld_x=self.hidden,
+                                     ld_res=self.hidden, ld_out=self.hidden)
+        self.codes = torch.empty((B, self.hidden), device=device, dtype=torch.float8_e4m3fn)
+        self.scales = torch.empty((B, self.hidden // (group or self.hidden)), device=device)
+        self.table = hb.rope_table(hb.RopeScaling(rope_dims=ROPE_DIMS, kind=hb.ROPE_PLAIN, theta=theta), device)
+        self.local = torch.zeros((B, steps, DH), **bf16)
+        self.q = torch.empty((B, H, DH), **bf16)
+        rope = dict(tokens=B, heads=H, D=DH, rope_dims=ROPE_DIMS, rope_first=DH - ROPE_DIMS, mscale=1.0,
+                    x_token=H * DH, x_head=DH, y_token=H * DH, y_head=DH)
+        self.rope_desc = hb.RopeDesc(heads2=1, src_dtype=hb.HISA_BF16, dst_dtype=hb.HISA_BF16, x2_token=DH, x2_head=DH,
+                                     y2_token=steps * DH, y2_head=DH, **rope)
+        self.back_desc = hb.RopeDesc(heads2=0, inverse=1, src_dtype=hb.HISA_BF16, dst_dtype=hb.HISA_BF16, **rope)
+        self.pooled = torch.zeros((max(B * own_rows, 1), DH), **bf16)
+        self.own_rows, self.own = own_rows, [0] * B
+        self.kv_off = torch.zeros(B + 1, device=device, dtype=torch.int64)
+        self.pos = torch.full((B,), start, **i32)
+        self.local_pos0 = torch.full((B,), start, **i32)
+        self.local_len = torch.zeros(B, **i32)
+        self.desc = hb.PrefixDesc(B=B, L=1, H=H, Dh=DH, window=window, W_max=steps, r=r, prefix_rows=prefix_kv.shape[0],
+                                  Np_max=own_rows, kv_rows=self.pooled.shape[0], scale=0.0, q_dtype=hb.HISA_BF16,
+                                  kv_dtype=hb.HISA_BF16, out_dtype=hb.HISA_BF16)
+        self.ws = hb.alloc_workspace(hb.workspace_bytes(hb.OP_PREFIX_ATTEND, self.desc), device)
+        self.out = torch.empty((B, H, DH), **bf16)
+
+    def append_pooled(self, rows):
+        """Replaces the sequences' own pooled rows: a list of [n_b, DH] bf16 tensors."""
+        import torch
+        if len(rows) != self.B or any(x.shape[0] > self.own_rows for x in rows):
+            raise ValueError("one tensor of at most own_rows rows per sequence")
+        off = [0]
+        for x in rows:
+            self.pooled[off[-1]:off[-1] + x.shape[0]] = x
+            off.append(off[-1] + x.shape[0])
+        self.kv_off.copy_(torch.tensor(off, dtype=torch.int64))
+
+    def activations(self):
+        """The norm's 8-bit output as bf16, for projections whose weights are bf16."""
+        import torch
+        groups = self.scales.shape[1]
+        return (self.codes.float().view(self.B, groups, -1) * self.scales[..., None]).view(self.B, -1).to(torch.bfloat16)
+
+    def step(self, x, residual):
+        """One token per sequence: x, residual [B, hidden] bf16 (residual is updated in place).
+        Returns the combine's output [B, H, DH] bf16, turned back to position-free dims."""
+        if self.n == self.steps:
+            raise ValueError("the window buffer is full")
+        hb.rms_norm(self.norm_desc, x, residual, self.w["norm"], residual, self.codes, self.scales)
+        a = self.activations()
+        q, kv = a @ self.w["q"], a @ self.w["kv"]
+        hb.rope(self.rope_desc, self.table, self.pos, q, self.q, kv, self.local[:, self.n])
+        self.n += 1
+        self.local_len.fill_(self.n)
+        hb.prefix_attend(self.desc, self.q, self.local, self.local_len, self.local_pos0, self.prefix_kv, self.pooled,
+                         self.kv_off, self.w["sinks"], self.pos, self.out, self.ws)
+        hb.rope(self.back_desc, self.table, self.pos, self.out, self.out)
+        self.pos += 1
+        return self.out
+
+    def status(self) -> int:
+        return hb.device_status(self.ws)

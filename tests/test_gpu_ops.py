@@ -607,3 +607,22 @@ def test_another_stream_and_a_graph():
         g.replay()
         torch.cuda.synchronize()
         check()
+
+
+# ------------------------------------------------------------------------------------
+# together: a layer's decode step
+# ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("batch,prefix,hidden,steps", [(5, 300, 1024, 6), (2, 64, 1000, 3)])
+def test_shared_prefix_decode(batch, prefix, hidden, steps):
+    # Roped queries and rows, the weights of the softmax, and the output are each rounded to bf16
+    # (half a step, 2^-8 of a value at most); logits of about 4 standard deviations turn the queries'
+    # and rows' share into 2 * 2^-8 * 8 of the weights. The last rotation rounds once more. All of it
+    # stays below a tenth of the largest output.
+    import sys
+
+    import deepseek_sparse_attention_hisa_gb300 as pkg
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(pkg.__file__)))
+    sys.path.insert(0, os.path.join(root, "examples"))
+    import shared_prefix_decode
+    assert shared_prefix_decode.run(batch, prefix, hidden, steps, own_rows=40, say=lambda *_: None) < 0.1
