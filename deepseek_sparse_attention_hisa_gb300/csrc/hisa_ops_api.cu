@@ -245,7 +245,6 @@ hisa_status hisa_rope(const hisa_rope_desc *d, const uint64_t *table, const int3
     p.wide = d->D % 8 == 0 && d->rope_first % 8 == 0 && d->rope_dims % (d->half ? 16 : 8) == 0 &&
              wide(x, d->x_token, d->x_head, ss) && wide(y, d->y_token, d->y_head, sd) &&
              (!d->heads2 || (wide(x2, d->x2_token, d->x2_head, ss) && wide(y2, d->y2_token, d->y2_head, sd)));
-    p.chained = (d->flags & HISA_FLAG_CHAINED) != 0;
     return from_cuda(launch_rope(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -239,9 +239,11 @@ __global__ void __launch_bounds__(256, VPT == 1 ? 4 : (VPT == 2 ? 3 : 2)) k_norm
     int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const float inv = 1.f / (float)p.cols;
     float w[VPT][8];
+    if (!p.chained) grid_dep_wait();
 #pragma unroll
     for (int i = 0; i < VPT; ++i) load_w(p.w, i * 32 + t, nvec, w[i]);
-    grid_dep_wait();
+    if (p.chained) grid_dep_wait();
+    grid_dep_trigger();
     Raw8<XT> x[VPT];
     Raw8<RT> r[VPT];
     auto fetch = [&](int64_t at) {
@@ -288,11 +290,13 @@ __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
     __syncthreads();
     constexpr bool kHoldW = VPT <= 2;                 // this thread's weights stay in registers
     float w[kHoldW ? VPT : 1][8];
+    if (!p.chained) grid_dep_wait();
     if constexpr (kHoldW) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) load_w(p.w, i * T + t, nvec, w[i]);
     }
-    grid_dep_wait();
+    if (p.chained) grid_dep_wait();
+    grid_dep_trigger();
     auto copy = [&](int64_t row, int stage) {
         if (row < p.rows) {
             uint4 *dst = ring + (int64_t)stage * (kX + kR) * nvec;
@@ -442,12 +446,14 @@ __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) to[e] = v * 8 + e < p.cols ? __ldg(p.w + v * 8 + e) : 0.f;
     };
+    if (!p.chained) grid_dep_wait();
     if constexpr (kHoldW) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) load_some(i * T + t, w[i]);
     }
     __syncthreads();
-    grid_dep_wait();
+    if (p.chained) grid_dep_wait();
+    grid_dep_trigger();
     auto copy = [&](int64_t row, int stage) {
         if (row < p.rows) {
             copy_row<XT>(in + stage * (xb + rb), p.x, row * p.ld_x, p.cols);
@@ -509,6 +515,7 @@ __global__ void __launch_bounds__(1024, 1) k_norm_long(NormParams p) {
     if (t < 32) red[0][t] = red[1][t] = 0.f;
     __syncthreads();
     grid_dep_wait();
+    grid_dep_trigger();
     int par = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
         auto value = [&](int c) {
@@ -580,7 +587,7 @@ cudaError_t go(const NormParams &p, int threads, int64_t rows_per_cta, size_t sm
         if (e != cudaSuccess) return e;
         most = (int64_t)sms * (per > 0 ? per : 1);
     }
-    return launch_pdl(Kernel, dim3((unsigned)(want < most ? want : most)), dim3(threads), smem, s, p.chained, p);
+    return launch_pdl(Kernel, dim3((unsigned)(want < most ? want : most)), dim3(threads), smem, s, 1, p);
 }
 
 template <typename XT, typename RT>

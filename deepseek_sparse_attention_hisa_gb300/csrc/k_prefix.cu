@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_pref
     // before it has completed; that one depends on nothing of it and waits for it at its end, so
     // that the merge, which waits for the last grid, has both.
     if (tail || !p.tail_split) grid_dep_wait();
-    if (tail) grid_dep_trigger();
+    grid_dep_trigger();
     Tail x{0, 0, 0, 0};
     int64_t e0, e1;
     if (tail) {
@@ -200,6 +200,7 @@ template <int DH>
 __global__ void k_prefix_merge(PrefixParams p) {
     constexpr int kPer = 128 / (DH / 4);                  // (query row, head) pairs per CTA
     grid_dep_wait();
+    grid_dep_trigger();
     const int64_t rows = (int64_t)p.B * p.L * p.H;
     const int sub = threadIdx.x / (DH / 4), d = (threadIdx.x % (DH / 4)) * 4;
     const int64_t g = (int64_t)blockIdx.x * kPer + sub;

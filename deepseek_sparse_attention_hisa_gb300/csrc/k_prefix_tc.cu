@@ -47,7 +47,9 @@ using namespace tc;
 constexpr int kH = 64, kDH = 512, kT = 64;
 constexpr int kSoftWarps = 4, kLoadWarp = 4, kMmaWarp = 5, kLoadVWarp = 6, kMmaPvWarp = 7, kMmaWarp2 = 8,
               kThreads = 288;
-constexpr int kStages = 2;                              // of K, of V and of P
+constexpr int kStages = 2;                              // of K, of V and of P (two: a K stage and an S buffer then
+                                                        // belong to the even or the odd tiles' S warp alone, which
+                                                        // sees every phase of its barriers)
 constexpr int kSBufs = 4;                               // S tiles in TMEM
 constexpr uint32_t kQBytes = kH * kDH * 2;              // 64 KB: 8 chunks [64 rows x 64 dims]
 constexpr uint32_t kKBytes = kT / 2 * kDH * 2;          // 32 KB: 8 chunks [32 rows x 64 dims]
@@ -214,6 +216,7 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
     fence_after_sync();
     const uint32_t tmem = ms->tmem;
     grid_dep_wait();
+    grid_dep_trigger();
     bool ok = true;
     auto fail = [&]() {
         ok = false;
@@ -422,13 +425,12 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                 if (ok) commit_pair(&ms->ofull);
             }
         }
-        if (rank == 0) {
-            // MMAs in flight end before TMEM is freed (bounded, whatever the abort flag says)
-            commit_pair(&ms->drain);
-            __syncwarp();
-            mbar_wait(&ms->drain, 0, 1u << 24);
-            __syncwarp();
-        }
+        // MMAs in flight end, and their arrivals reach both CTAs, before TMEM is freed and a CTA leaves
+        // (bounded, whatever the abort flag says)
+        if (rank == 0) commit_pair(&ms->drain);
+        __syncwarp();
+        mbar_wait(&ms->drain, 0, 1u << 24);
+        __syncwarp();
     } else {
         // ---------------- softmax and epilogue: thread = TMEM lane ----------------
         const int r = (warp & 1) * 32 + lane, half = warp >> 1;

@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_tc1(PrefixParams p, cons
     fence_after_sync();
     const uint32_t tmem = ms->tmem;
     if (!p.tail_split) grid_dep_wait();                 // else see the end
+    grid_dep_trigger();
     bool ok = true;
     auto fail = [&]() {
         ok = false;

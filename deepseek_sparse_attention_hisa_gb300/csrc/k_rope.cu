@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(Ro
     }
     extern __shared__ __align__(16) float2 turn[];        // [token of the batch][pair]: mscale (cos, sin)
     grid_dep_wait();
+    grid_dep_trigger();
     const int64_t batch = (int64_t)per * kU;
     const int step_tok = per / p.heads_all, step_head = per - step_tok * p.heads_all;
     for (int64_t b0 = r0; b0 < r1; b0 += batch) {
@@ -202,7 +203,7 @@ cudaError_t launch_as(RopeParams p, cudaStream_t s) {
     p.rows_per_cta = few * mul;
     const int64_t grid = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return launch_pdl(k_rope<S, D, N, HALF>, dim3((unsigned)grid), dim3(threads), shared(per), s, p.chained, p);
+    return launch_pdl(k_rope<S, D, N, HALF>, dim3((unsigned)grid), dim3(threads), shared(per), s, 1, p);
 }
 
 template <typename S, typename D>

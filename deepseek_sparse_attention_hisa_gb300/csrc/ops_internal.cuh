@@ -6,6 +6,11 @@
 
 namespace hisa {
 
+// The kernels here are launched as programmatic dependents, always: each waits for the grid before
+// it (grid_dep_wait) before it touches memory that grid may write, and lets the next one be
+// scheduled (grid_dep_trigger) right after, so that launches overlap and no grid runs beside the
+// one two back.
+
 // Eight f32 to a 32-byte aligned address in one access: a whole sector per thread, where two
 // 16-byte stores each leave half of one.
 __device__ __forceinline__ void store_sector(float *dst, const float *v) {
@@ -32,7 +37,7 @@ struct NormParams {
     void *out;                // [rows, cols]
     float *scales;            // [rows, cols / group] (8-bit output)
     int wide;                 // every row start is aligned to 8 elements, cols % 8 == 0
-    int chained;
+    int chained;              // w may be read before the previous grid has completed
 };
 
 struct RopeParams {
@@ -49,7 +54,6 @@ struct RopeParams {
     int64_t x_token, x_head, y_token, y_head, x2_token, x2_head, y2_token, y2_head;
     int64_t rows_per_cta;     // set by launch_rope
     int wide;                 // 8 elements per access fit every boundary
-    int chained;
 };
 
 // One shared-prefix combine. Partials of a segment (a range of the shared rows, or of a query

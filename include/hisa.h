@@ -29,8 +29,7 @@
  *    stream has completed, as with any ordinary launch, except kernels that read nothing
  *    before the previous grid has completed (the coarse stage's pipeline, the selects and
  *    merges that follow a call's scoring or combine kernel, and the kernels of
- *    hisa_prefix_attend), which may always overlap
- *    its end.
+ *    hisa_rms_norm, hisa_rope and hisa_prefix_attend), which may always overlap its end.
  *  - Ragged batches: sequence b owns pooled rows [key_off[b], key_off[b+1]) of the
  *    packed key / KV arrays, so Np_b = key_off[b+1] - key_off[b] (int64, device).
  *  - Positions: t0[b] (int32, device) is the absolute token position of query
