@@ -72,7 +72,7 @@ struct PrefixParams {
     int tail_rows;            // list rows of one of them
     int pre_split;            // segments [tail_split, tail_split + pre_split): shared rows (on the
                               // tensor cores all rows, and no tail segments)
-    int64_t pre_rows;         // shared rows of one of them (CUDA cores)
+    int64_t pre_rows;         // shared rows of one of them (not for 512 bf16 dims)
     float *part_o;            // [segments, B * L * H, Dh]
     float *part_ml;           // [segments, B * L * H, 2]: maximum (of the logits), sum
     uint32_t *status;
