@@ -211,5 +211,10 @@ def test_rope_table_refusals(lib, kw):
 
 def test_largest_descriptors_size(lib):
     # sizes that pass 32 bits are computed in 64
-    d = prefix_desc(B=304, L=64, prefix_rows=1 << 20, Np_max=1 << 20, kv_rows=1 << 30)
-    assert hb.workspace_bytes(hb.OP_PREFIX_ATTEND, d) > 304 * 64 * 64 * 512 * 4 * 2
+    kw = dict(B=304, L=64, prefix_rows=1 << 20, Np_max=1 << 20, kv_rows=1 << 30)
+    # f32: own and shared rows are summed apart, 512 sums, a maximum and a sum per row and segment
+    sums = 304 * 64 * 64 * (512 + 2) * 4
+    d = prefix_desc(**kw, q_dtype=hb.HISA_F32, kv_dtype=hb.HISA_F32)
+    assert hb.workspace_bytes(hb.OP_PREFIX_ATTEND, d) >= 2 * sums
+    # bf16: this many query rows fill the GPU with one segment each, which needs no sums in memory
+    assert hb.workspace_bytes(hb.OP_PREFIX_ATTEND, prefix_desc(**kw)) == 256
