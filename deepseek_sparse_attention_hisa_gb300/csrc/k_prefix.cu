@@ -8,9 +8,12 @@
 // rows are stacked across sequences (one staged chunk of shared rows serves R stacked rows),
 // and the local and own rows become segments of one query row each.
 //
-// The kernel here serves f32, and the own lists of bf16 heads of 64 and 128 dims: R query rows x 32 list rows per chunk, 16 threads per two or four rows, scores and
-// sums in f32 registers, the running maximum and sum per row (a rescale per chunk). Bound by the
-// FMA pipe and its shared-memory operands.
+// The kernel here serves f32, and the own lists of bf16 heads of 64 and 128 dims: R query rows x
+// 32 list rows per chunk, 16 threads per two or four rows, scores and sums in f32 registers, the
+// running maximum and sum per row (a rescale per chunk). Bound by the FMA pipe and its
+// shared-memory operands. Measured: the own lists (up to 512 rows) of 304 query rows of 16 x 128
+// bf16 67 us; a call of 7 x 3 query rows of 16 x 128 f32 over 1003 shared rows 25 us, the latency of
+// three dependent kernels (its products would take 2.6).
 #include "prefix_common.cuh"
 
 namespace hisa {

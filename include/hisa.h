@@ -466,8 +466,10 @@ HISA_API hisa_status hisa_rope(const hisa_rope_desc *desc, const uint64_t *table
  *   pooled_kv  [kv_rows, Dh] kv_dtype (NULL if Np_max is 0); kv_off [B+1] int64
  *   sinks      [H] f32, or NULL for none (-inf is none for that head);  t0 [B] int32
  *   out        [B, L, H, Dh] out_dtype, 16-byte aligned
- * What rows hold that a query row does not see has no effect on it. Offsets that do not fit set HISA_DEV_BAD_OFFSETS; that
- * sequence's own rows are skipped. */
+ * What rows hold that a query row does not see has no effect on it. Offsets that do not fit set
+ * HISA_DEV_BAD_OFFSETS; that sequence's own rows are skipped. Few query rows are split along
+ * the rows they see and need the more workspace for it: a workspace that serves several batch
+ * sizes takes the maximum of hisa_workspace_bytes over them. */
 HISA_API hisa_status hisa_prefix_attend(const hisa_prefix_desc *desc, const void *q, const void *local_kv,
                                const int32_t *local_len, const int32_t *local_pos0,
                                const void *prefix_kv, const void *pooled_kv, const int64_t *kv_off,
