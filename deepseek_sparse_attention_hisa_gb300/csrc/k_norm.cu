@@ -78,6 +78,28 @@ __device__ __forceinline__ void store8(uint8_t *row, int v, bool bf16, const flo
     }
 }
 
+// Two f32 operations by one instruction (each rounded as alone): many rows are bound by the
+// number of instructions before they are by memory.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rn.f32x2 x, x, y, z; "
+        "mov.b64 {%0, %1}, x;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -88,6 +110,19 @@ __device__ __forceinline__ float max_mag(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
     return r;
+}
+__device__ __forceinline__ float max_mag(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ uint4 add_bf16(uint4 a, uint4 b) {
+    auto add = [](uint32_t x, uint32_t y) {
+        uint32_t r;
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+        return r;
+    };
+    return make_uint4(add(a.x, b.x), add(a.y, b.y), add(a.z, b.z), add(a.w, b.w));
 }
 // Over aligned groups of `lanes` lanes (a power of two).
 __device__ __forceinline__ float lanes_max(float v, int lanes) {
@@ -100,7 +135,10 @@ __device__ __forceinline__ float lanes_max(float v, int lanes) {
 // Scale of a group of largest magnitude a. The floor keeps the quotient normal.
 __device__ __forceinline__ float scale_of(float a, int pow2) {
     a = a < 1e-10f ? 1e-10f : a;
-    float s = a / 448.f;
+    // a / 448, correctly rounded: Markstein's step on the product with the rounded reciprocal
+    // (an infinity or NaN stays one)
+    const float s0 = a * (1.f / 448.f);
+    float s = a < INFINITY ? fmaf(fmaf(-448.f, s0, a), 1.f / 448.f, s0) : a;
     if (pow2 && s < INFINITY) {
         const uint32_t u = __float_as_uint(s);
         s = __uint_as_float((u & 0x7f800000u) + ((u & 0x007fffffu) ? 0x00800000u : 0u));
@@ -115,12 +153,19 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = 0; w < (int)(blockDim.x + 127) / 128; ++w) {
-        const float4 u = reinterpret_cast<const float4 *>(red)[w];
-        s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w;
+    float2 a = make_float2(0.f, 0.f), b = a;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h == 1 && blockDim.x <= 512) break;
+#pragma unroll
+        for (int w = 4 * h; w < 4 * h + 4; ++w) {
+            const float4 u = reinterpret_cast<const float4 *>(red)[w];
+            a = add2(a, make_float2(u.x, u.y));
+            b = add2(b, make_float2(u.z, u.w));
+        }
     }
-    return (s.x + s.y) + (s.z + s.w);
+    a = add2(a, b);
+    return a.x + a.y;
 }
 __device__ __forceinline__ float block_max(float v, float *red) {
     v = lanes_max(v, 32);
@@ -138,7 +183,9 @@ template <typename RT, int VPT, bool SM>
 struct Row {
     float h[VPT][8];                                  // the row, then t
     float top[VPT];                                   // largest |t| of the unit's group
-    float ss;
+    float2 ss2 = {0.f, 0.f};
+
+    __device__ __forceinline__ float ss() const { return ss2.x + ss2.y; }
 
     // Unit i: h = x (+ residual, rounded as stored, and put to rrow), its squares, t = h w. `n` of its
     // columns are there.
@@ -150,37 +197,46 @@ struct Row {
             for (int e = 0; e < 8; ++e) h[i][e] = 0.f;
             return;
         }
-        unpack(x, h[i]);
-        if constexpr (!std::is_same<RT, None>::value) {
-            float q[8];
-            unpack(r, q);
+        if constexpr (std::is_same<XT, __nv_bfloat16>::value && std::is_same<RT, __nv_bfloat16>::value) {
+            // the sum in bf16 is the f32 sum rounded: one that f32 cannot hold is no tie of bf16
+            Raw8<__nv_bfloat16> sum;
+            sum.v[0] = add_bf16(x.v[0], r.v[0]);
+            unpack(sum, h[i]);
+            if (rrow) reinterpret_cast<uint4 *>(rrow)[v] = sum.v[0];
+        } else {
+            unpack(x, h[i]);
+            if constexpr (!std::is_same<RT, None>::value) {
+                float q[8];
+                unpack(r, q);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] += q[e];
-            if constexpr (std::is_same<RT, __nv_bfloat16>::value) {
-                Raw8<__nv_bfloat16> back;
-                back.v[0] = pack_bf16(h[i]);
-                unpack(back, h[i]);                    // the norm is over the sum as stored
+                for (int e = 0; e < 8; ++e) h[i][e] += q[e];
+                if constexpr (std::is_same<RT, __nv_bfloat16>::value) {
+                    Raw8<__nv_bfloat16> back;
+                    back.v[0] = pack_bf16(h[i]);
+                    unpack(back, h[i]);                // the norm is over the sum as stored
+                }
+                if (rrow) store8<SM>(rrow, v, std::is_same<RT, __nv_bfloat16>::value, h[i]);
             }
-            if (rrow) store8<SM>(rrow, v, std::is_same<RT, __nv_bfloat16>::value, h[i]);
         }
         if (SM && n < 8) {                             // the blocks that hold the row's end hold more
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] = e < n ? h[i][e] : 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            ss += h[i][e] * h[i][e];
-            h[i][e] *= w[e];
+        for (int e = 0; e < 8; e += 2) {
+            float2 u = make_float2(h[i][e], h[i][e + 1]);
+            ss2 = fma2(u, u, ss2);
+            u = mul2(u, make_float2(w[e], w[e + 1]));
+            h[i][e] = u.x;
+            h[i][e + 1] = u.y;
         }
     }
     // Largest |t| per unit, joined over a group's lanes (or, for one scale per row, this thread's units).
     __device__ __forceinline__ void tops(const NormParams &p) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            float m[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m[e] = max_mag(h[i][e], h[i][e + 4]);
-            top[i] = max_mag(max_mag(m[0], m[1]), max_mag(m[2], m[3]));
+            const float a = max_mag(h[i][0], h[i][1], h[i][2]), b = max_mag(h[i][3], h[i][4], h[i][5]);
+            top[i] = max_mag(max_mag(a, h[i][6], h[i][7]), b);
         }
         if (p.group) {
             const int lanes = p.group >> 3;
@@ -195,22 +251,30 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) top[i] = v;
     }
-    __device__ __forceinline__ void put(const NormParams &p, int i, int v, int64_t row, uint8_t *orow, float f) {
-        if (p.out_dtype != HISA_E4M3) {
+    __device__ __forceinline__ void times(int i, float f) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] *= f;
+        for (int e = 0; e < 8; e += 2) {
+            const float2 u = mul2(make_float2(h[i][e], h[i][e + 1]), make_float2(f, f));
+            h[i][e] = u.x;
+            h[i][e + 1] = u.y;
+        }
+    }
+    __device__ __forceinline__ void put(const NormParams &p, int i, int v, float *scales, uint8_t *orow, float f) {
+        if (p.out_dtype != HISA_E4M3) {
+            times(i, f);
             store8<SM>(orow, v, p.out_dtype == HISA_BF16, h[i]);
             return;
         }
         const float s = scale_of(top[i] * f, p.pow2);
         const float q = __fdividef(f, s);              // t q is within a few f32 steps of y / s
         const int g = v >> p.unit_shift;               // the unit's group (0 for one scale per row)
-        if (v == g << p.unit_shift) p.scales[row * p.groups + g] = s;
+        if (v == g << p.unit_shift) scales[g] = s;
+        times(i, q);
         uint32_t c[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(h[i][4 * k] * q, h[i][4 * k + 1] * q), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h[i][4 * k + 2] * q, h[i][4 * k + 3] * q), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(h[i][4 * k], h[i][4 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h[i][4 * k + 2], h[i][4 * k + 3]), __NV_SATFINITE, __NV_E4M3);
             c[k] = lo | (hi << 16);
         }
         reinterpret_cast<uint2 *>(orow)[v] = make_uint2(c[0], c[1]);
@@ -266,7 +330,6 @@ __global__ void __launch_bounds__(256, VPT == 1 ? 4 : (VPT == 2 ? 3 : 2)) k_norm
     for (; row < p.rows; row += step) {
         Row<RT, VPT, false> m;
         uint8_t *rrow = res_row<RT>(p, row), *orow = out_row(p, row);
-        m.ss = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) m.take(i, i * 32 + t, i * 32 + t < nvec ? 8 : 0, rrow, x[i], r[i], w[i]);
         fetch(row + step);
@@ -274,10 +337,10 @@ __global__ void __launch_bounds__(256, VPT == 1 ? 4 : (VPT == 2 ? 3 : 2)) k_norm
             m.tops(p);
             if (!p.group) m.same_top(lanes_max(m.top[0], 32));
         }
-        const float f = rsqrtf(warp_sum(m.ss) * inv + p.eps);
+        const float f = rsqrtf(warp_sum(m.ss()) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (i * 32 + t < nvec) m.put(p, i, i * 32 + t, row, orow, f);
+            if (i * 32 + t < nvec) m.put(p, i, i * 32 + t, p.scales + row * p.groups, orow, f);
     }
 }
 
@@ -302,41 +365,65 @@ __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
     }
     if (p.chained) grid_dep_wait();
     grid_dep_trigger();
-    auto copy = [&](int64_t row, int stage) {
-        if (row < p.rows) {
-            uint4 *dst = ring + (int64_t)stage * (kX + kR) * nvec;
-            const uint4 *sx = reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + row * p.ld_x);
+    // Everything that a row needs of its number moves on by a constant where registers allow: rows
+    // are short enough for the multiplications to count.
+    constexpr bool kStep = VPT <= 2;
+    const int q0x = (t & ~31) * kX + (t & 31), q0r = (t & ~31) * kR + (t & 31);      // this thread's first pieces
+    const uint8_t *nx = reinterpret_cast<const uint8_t *>(static_cast<const XT *>(p.x) + blockIdx.x * p.ld_x) + 16 * q0x;
+    const int64_t step_x = gridDim.x * p.ld_x * (int64_t)sizeof(XT);
+    const uint8_t *nr = nullptr;
+    int64_t step_r = 0;
+    if constexpr (kR > 0) {
+        nr = reinterpret_cast<const uint8_t *>(static_cast<const RT *>(p.res) + blockIdx.x * p.ld_res) + 16 * q0r;
+        step_r = gridDim.x * p.ld_res * (int64_t)sizeof(RT);
+    }
+    const uint32_t stage_b = (uint32_t)(kX + kR) * nvec * 16, ring0 = tc::smem_u32(ring);
+    int64_t next = blockIdx.x;                        // the row to copy next
+    auto copy = [&](int stage) {
+        if (next < p.rows) {
+            if constexpr (!kStep) {
+                nx = reinterpret_cast<const uint8_t *>(static_cast<const XT *>(p.x) + next * p.ld_x) + 16 * q0x;
+                if constexpr (kR > 0) nr = reinterpret_cast<const uint8_t *>(static_cast<const RT *>(p.res) + next * p.ld_res) + 16 * q0r;
+            }
+            const uint32_t dst = ring0 + stage * stage_b;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int v0 = i * T + (t & ~31), lane = t & 31;      // the warp's units v0 .. v0 + 31
 #pragma unroll
-                for (int k = 0; k < kX; ++k) {
-                    const int q = v0 * kX + k * 32 + lane;
-                    if (q < nvec * kX) tc::cp_async16(tc::smem_u32(dst + q), sx + q);
+                for (int k = 0; k < kX; ++k) {        // the warp's units i T + t & ~31 .. + 31
+                    const int q = i * T * kX + 32 * k;
+                    if (q0x + q < nvec * kX) tc::cp_async16(dst + 16 * (q0x + q), nx + 16 * q);
                 }
-                if constexpr (kR > 0) {
-                    const uint4 *sr = reinterpret_cast<const uint4 *>(static_cast<const RT *>(p.res) + row * p.ld_res);
 #pragma unroll
-                    for (int k = 0; k < kR; ++k) {
-                        const int q = v0 * kR + k * 32 + lane;
-                        if (q < nvec * kR) tc::cp_async16(tc::smem_u32(dst + kX * nvec + q), sr + q);
-                    }
+                for (int k = 0; k < kR; ++k) {
+                    const int q = i * T * kR + 32 * k;
+                    if (q0r + q < nvec * kR) tc::cp_async16(dst + 16 * (kX * nvec + q0r + q), nr + 16 * q);
                 }
             }
+            if constexpr (kStep) {
+                nx += step_x;
+                nr += step_r;
+            }
         }
+        next += gridDim.x;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) copy(blockIdx.x + (int64_t)s * gridDim.x, s);
+    for (int s = 0; s < STAGES - 1; ++s) copy(s);
+    uint8_t *orow = out_row(p, blockIdx.x), *rrow = res_row<RT>(p, blockIdx.x);
+    const int64_t step_o = gridDim.x * p.ld_out * out_bytes(p);
+    float *srow = p.scales + (int64_t)blockIdx.x * p.groups;
     int stage = 0, par = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
-        if (STAGES == 1) copy(row, 0);
+        if (STAGES == 1) copy(0);
         asm volatile("cp.async.wait_group %0;" :: "n"(STAGES > 1 ? STAGES - 2 : 0) : "memory");
         __syncwarp();
-        const uint4 *src = ring + (int64_t)stage * (kX + kR) * nvec;
+        const uint4 *src = ring + stage * (kX + kR) * nvec;
+        if constexpr (!kStep) {
+            orow = out_row(p, row);
+            rrow = res_row<RT>(p, row);
+            srow = p.scales + row * p.groups;
+        }
         Row<RT, VPT, false> m;
-        uint8_t *rrow = res_row<RT>(p, row), *orow = out_row(p, row);
-        m.ss = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = i * T + t;
@@ -356,17 +443,22 @@ __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
         __syncwarp();
         if (STAGES > 1) {
             // into the stage read by the row before
-            copy(row + (int64_t)(STAGES - 1) * gridDim.x, stage == 0 ? STAGES - 1 : stage - 1);
+            copy(stage == 0 ? STAGES - 1 : stage - 1);
             stage = stage + 1 == STAGES ? 0 : stage + 1;
         }
         if (p.out_dtype == HISA_E4M3) {
             m.tops(p);
             if (!p.group) m.same_top(block_max(m.top[0], redm[par]));
         }
-        const float f = rsqrtf(block_sum(m.ss, red[par]) * inv + p.eps);
+        const float f = rsqrtf(block_sum(m.ss(), red[par]) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (i * T + t < nvec) m.put(p, i, i * T + t, row, orow, f);
+            if (i * T + t < nvec) m.put(p, i, i * T + t, srow, orow, f);
+        if constexpr (kStep) {
+            orow += step_o;
+            if (rrow) rrow += step_r;
+            srow += (int64_t)gridDim.x * p.groups;
+        }
     }
 }
 
@@ -447,7 +539,12 @@ __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
     if (t < 32) red[0][t] = red[1][t] = 0.f;
     constexpr bool kHoldW = VPT <= 2;
     float w[kHoldW ? VPT : 1][8];
+    const bool whole_w = (reinterpret_cast<uintptr_t>(p.w) & 15) == 0;
     auto load_some = [&](int v, float (&to)[8]) {
+        if (whole_w && v * 8 + 8 <= p.cols) {          // single elements, 32 bytes apart, cost four times the wavefronts
+            load_w(p.w, v, nvec, to);
+            return;
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) to[e] = v * 8 + e < p.cols ? __ldg(p.w + v * 8 + e) : 0.f;
     };
@@ -464,19 +561,19 @@ __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
             copy_row<XT>(in + stage * (xb + rb), p.x, row * p.ld_x, p.cols);
             copy_row<RT>(in + stage * (xb + rb) + xb, p.res, row * p.ld_res, p.cols);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    copy(blockIdx.x, 0);
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) copy(blockIdx.x + (int64_t)s * gridDim.x, s);
     int par = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
         const uint8_t *src = in + (STAGES == 2 ? par : 0) * (xb + rb);
         const int ax = row_offset<XT>(p.x, row * p.ld_x), ar = row_offset<RT>(p.res, row * p.ld_res);
         uint8_t *rrow = res_row<RT>(p, row), *orow = out_row(p, row);
-        tc::cp_async_wait_all();
+        asm volatile("cp.async.wait_group %0;" :: "n"(STAGES - 1) : "memory");
         __syncthreads();                               // every thread's blocks of this row have landed, and
                                                        // the row before has been written out
-        if (STAGES == 2) copy(row + gridDim.x, par ^ 1);
         Row<RT, VPT, true> m;
-        m.ss = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = i * T + t;
@@ -498,11 +595,11 @@ __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
             m.tops(p);
             if (!p.group) m.same_top(block_max(m.top[0], redm[par]));
         }
-        const float f = rsqrtf(block_sum(m.ss, red[par]) * inv + p.eps);
-        if (STAGES == 1) copy(row + gridDim.x, 0);     // every thread has read this row (the barrier of the sum)
+        const float f = rsqrtf(block_sum(m.ss(), red[par]) * inv + p.eps);
+        copy(row + (int64_t)STAGES * gridDim.x, STAGES == 2 ? par : 0);   // every thread has read this row (the sum's barrier)
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (i * T + t < nvec) m.put(p, i, i * T + t, row, obuf, f);
+            if (i * T + t < nvec) m.put(p, i, i * T + t, p.scales + row * p.groups, obuf, f);
         __syncthreads();                               // the staged outputs are whole
         write_row(orow, obuf, p.cols * es, es);
         if (rrow) write_row(rrow, rbuf, p.cols * (int)kElem<RT>, (int)kElem<RT>);

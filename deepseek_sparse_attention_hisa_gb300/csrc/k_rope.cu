@@ -106,7 +106,15 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(Ro
         lo = (unit - n_rot) * N;                          // copied units: the dims before, then after, the rotated
         if (lo >= p.first) lo += p.dims;
     }
-    extern __shared__ __align__(16) float2 turn[];        // [token of the batch][pair]: mscale (cos, sin)
+    // [token of the batch][pair]: mscale (cos, sin). A unit of 8 dims reads its pairs two at a time, and
+    // the units' first two come first, then their next two: neighbouring lanes read neighbouring
+    // 16 bytes (unit by unit they would meet in a quarter of the banks).
+    extern __shared__ __align__(16) float2 turn[];
+    auto slot = [&](int pair) {
+        if (N == 1) return pair;
+        const int of = pair / kPairs, at = pair % kPairs;
+        return ((at >> 1) * n_rot + of) * 2 + (at & 1);
+    };
     grid_dep_wait();
     grid_dep_trigger();
     const int64_t batch = (int64_t)per * kU;
@@ -145,7 +153,7 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(Ro
             const int64_t turns = (int64_t)((uint64_t)pos * __ldg(p.table + i % pairs));      // modulo one turn
             float s, c;
             sincospif(2.f * (__ll2float_rn(turns) * 0x1p-64f), &s, &c);
-            turn[i] = make_float2(c * p.mscale, s * p.mscale * p.sin_sign);
+            turn[i / pairs * pairs + slot(i % pairs)] = make_float2(c * p.mscale, s * p.mscale * p.sin_sign);
         }
         __syncthreads();
         D *y0 = static_cast<D *>(p.y) + tok0 * p.y_token, *y20 = static_cast<D *>(p.y2) + tok0 * p.y2_token;
@@ -157,7 +165,18 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(Ro
             float u[N];
             to_floats<S, N>(a[k], u);
             if (rot) {
-                const float2 *cs = turn + tok[k] * pairs + unit * kPairs;
+                float2 cs[kPairs];
+                if constexpr (N == 1) {
+                    cs[0] = turn[tok[k] * pairs + unit];
+                } else {
+                    const float4 *at = reinterpret_cast<const float4 *>(turn + tok[k] * pairs) + unit;
+#pragma unroll
+                    for (int e = 0; e < kPairs / 2; ++e) {
+                        const float4 two = at[e * n_rot];
+                        cs[2 * e] = make_float2(two.x, two.y);
+                        cs[2 * e + 1] = make_float2(two.z, two.w);
+                    }
+                }
                 if constexpr (kTwo) {
                     float v[N];
                     to_floats<S, N>(b[k], v);
