@@ -173,6 +173,12 @@ hisa_status hisa_rms_norm(const hisa_norm_desc *d, const void *x, const void *re
     auto wide = [&](const void *a, int64_t ld, size_t es) { return aligned(a, 8 * es) && ld % 8 == 0; };
     p.wide = d->cols % 8 == 0 && aligned(w, 16) && wide(x, d->ld_x, sx) && wide(out, d->ld_out, so) &&
              (!residual || (wide(residual, d->ld_res, sr) && wide(residual_out, d->ld_res, sr)));
+    auto phase = [](const void *a, size_t es) { return (int)(reinterpret_cast<uintptr_t>(a) / es % 8); };
+    p.phase = phase(x, sx);
+    if (p.group || phase(out, so) != p.phase || (d->ld_x - d->ld_out) % 8 ||
+        (residual && (phase(residual, sr) != p.phase || (d->ld_x - d->ld_res) % 8)) ||
+        (residual_out && phase(residual_out, sr) != p.phase))
+        p.phase = -1;
     p.chained = (d->flags & HISA_FLAG_CHAINED) != 0;
     return from_cuda(launch_rms_norm(p, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -12,10 +12,11 @@
 // own columns in order, then a fixed tree over lanes and warps, so a row's result does not
 // depend on the other rows or on the launch.
 //
-// Measured: 16384 x 7168 bf16 with a bf16 residual to e4m3 by 128: 130 us, 6.34 TB/s, 93 % of a
-// plain copy's rate; 304 x 7168 of the same: 5.4 us, one launch and one round trip to memory;
-// 1001 x 5003 f32: 12.7 us, of which 5.9 are its bytes (two to three rows per CTA, one after
-// another, do not hide the latency); 16384 x 5003 f32: 5.0 TB/s.
+// Measured: 16384 x 7168 bf16 with a bf16 residual to e4m3 by 128: 121 us, 6.8 TB/s, what a plain
+// copy reaches; without a residual 83 us, bound by its instructions (about 20 per element); 304 x
+// 7168: 4.6 us, one launch and one round trip to memory; 1001 x 5003 f32: 9.2 us, of which 5.9 are
+// its bytes (two to three rows per CTA, one after another, do not hide the latency); 16384 x 5003
+// bf16 60 us, 5.5 TB/s.
 #include <cuda_fp8.h>
 
 #include "ops_internal.cuh"
@@ -75,6 +76,19 @@ __device__ __forceinline__ void store8(uint8_t *row, int v, bool bf16, const flo
         reinterpret_cast<float4 *>(row)[2 * v + 1] = make_float4(f[4], f[5], f[6], f[7]);
     } else {
         store_sector(reinterpret_cast<float *>(row) + 8 * v, f);
+    }
+}
+
+// Elements [lo, hi) of unit v.
+template <typename T>
+__device__ __forceinline__ void store_part(uint8_t *row, int v, int lo, int hi, const float (&f)[8]) {
+    T *at = reinterpret_cast<T *>(row) + 8 * v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (e < lo || e >= hi) continue;
+        if constexpr (sizeof(T) == 4) at[e] = f[e];
+        else if constexpr (sizeof(T) == 2) at[e] = __float2bfloat16_rn(f[e]);
+        else at[e] = __nv_cvt_float_to_fp8(f[e], __NV_SATFINITE, __NV_E4M3);
     }
 }
 
@@ -149,10 +163,7 @@ __device__ __forceinline__ float scale_of(float a, int pow2) {
 // Joins one value per warp over the CTA: a partial each, one barrier, and the 32 slots (unused
 // ones hold 0) read as vectors. Callers alternate between two arrays, so the next call's writes
 // meet no late reader.
-__device__ __forceinline__ float block_sum(float v, float *red) {
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
+__device__ __forceinline__ float sum_of(const float *red) {
     float2 a = make_float2(0.f, 0.f), b = a;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -167,19 +178,48 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     a = add2(a, b);
     return a.x + a.y;
 }
+__device__ __forceinline__ float max_of(const float *red) {
+    float s = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h == 1 && blockDim.x <= 512) break;
+#pragma unroll
+        for (int w = 4 * h; w < 4 * h + 4; ++w) {
+            const float4 u = reinterpret_cast<const float4 *>(red)[w];
+            s = max_mag(max_mag(s, u.x, u.y), u.z, u.w);
+        }
+    }
+    return s;
+}
+__device__ __forceinline__ float block_sum(float v, float *red) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return sum_of(red);
+}
+__device__ __forceinline__ void block_sum_max(float &v, float &top, float *red, float *redm) {
+    v = warp_sum(v);
+    top = lanes_max(top, 32);
+    if ((threadIdx.x & 31) == 0) {
+        red[threadIdx.x >> 5] = v;
+        redm[threadIdx.x >> 5] = top;
+    }
+    __syncthreads();
+    v = sum_of(red);
+    top = max_of(redm);
+}
 __device__ __forceinline__ float block_max(float v, float *red) {
     v = lanes_max(v, 32);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < (int)(blockDim.x + 31) / 32; ++w) s = max_mag(s, red[w]);
-    return s;
+    return max_of(red);
 }
 
 // What both kernels of 8-column units do with a row. With t = h w, f = 1 / sqrt(mean(h^2) + eps) > 0
 // and y = t f, a group's largest |y| is f times its largest |t| (rounding is monotone), so the
 // scales need no pass after the reduction.
-template <typename RT, int VPT, bool SM>
+// SM: through shared memory; RAG: the row's first and last unit may be cut.
+template <typename RT, int VPT, bool SM, bool RAG>
 struct Row {
     float h[VPT][8];                                  // the row, then t
     float top[VPT];                                   // largest |t| of the unit's group
@@ -187,11 +227,12 @@ struct Row {
 
     __device__ __forceinline__ float ss() const { return ss2.x + ss2.y; }
 
-    // Unit i: h = x (+ residual, rounded as stored, and put to rrow), its squares, t = h w. `n` of its
-    // columns are there.
+    // Unit i: h = x (+ residual, rounded as stored, and put to rrow), its squares, t = h w. Its columns
+    // [lo, n) are there.
     template <typename XT>
-    __device__ __forceinline__ void take(int i, int v, int n, uint8_t *rrow, const Raw8<XT> &x, const Raw8<RT> &r,
+    __device__ __forceinline__ void take(int i, int v, int lo, int n, uint8_t *rrow, const Raw8<XT> &x, const Raw8<RT> &r,
                                          const float (&w)[8]) {
+        const bool cut = RAG && (lo > 0 || n < 8);
         if (n <= 0) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] = 0.f;
@@ -202,7 +243,8 @@ struct Row {
             Raw8<__nv_bfloat16> sum;
             sum.v[0] = add_bf16(x.v[0], r.v[0]);
             unpack(sum, h[i]);
-            if (rrow) reinterpret_cast<uint4 *>(rrow)[v] = sum.v[0];
+            if (rrow && cut) store_part<RT>(rrow, v, lo, n, h[i]);
+            else if (rrow) reinterpret_cast<uint4 *>(rrow)[v] = sum.v[0];
         } else {
             unpack(x, h[i]);
             if constexpr (!std::is_same<RT, None>::value) {
@@ -215,12 +257,13 @@ struct Row {
                     back.v[0] = pack_bf16(h[i]);
                     unpack(back, h[i]);                // the norm is over the sum as stored
                 }
-                if (rrow) store8<SM>(rrow, v, std::is_same<RT, __nv_bfloat16>::value, h[i]);
+                if (rrow && cut) store_part<RT>(rrow, v, lo, n, h[i]);
+                else if (rrow) store8<SM>(rrow, v, std::is_same<RT, __nv_bfloat16>::value, h[i]);
             }
         }
-        if (SM && n < 8) {                             // the blocks that hold the row's end hold more
+        if (cut || (SM && n < 8)) {                    // the blocks that hold the row's ends hold more
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] = e < n ? h[i][e] : 0.f;
+            for (int e = 0; e < 8; ++e) h[i][e] = e >= lo && e < n ? h[i][e] : 0.f;
         }
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
@@ -259,9 +302,15 @@ struct Row {
             h[i][e + 1] = u.y;
         }
     }
-    __device__ __forceinline__ void put(const NormParams &p, int i, int v, float *scales, uint8_t *orow, float f) {
+    __device__ __forceinline__ void put(const NormParams &p, int i, int v, int lo, int n, float *scales, uint8_t *orow, float f) {
+        const bool cut = RAG && (lo > 0 || n < 8);
         if (p.out_dtype != HISA_E4M3) {
             times(i, f);
+            if (cut) {
+                if (p.out_dtype == HISA_BF16) store_part<__nv_bfloat16>(orow, v, lo, n, h[i]);
+                else store_part<float>(orow, v, lo, n, h[i]);
+                return;
+            }
             store8<SM>(orow, v, p.out_dtype == HISA_BF16, h[i]);
             return;
         }
@@ -270,6 +319,10 @@ struct Row {
         const int g = v >> p.unit_shift;               // the unit's group (0 for one scale per row)
         if (v == g << p.unit_shift) scales[g] = s;
         times(i, q);
+        if (cut) {
+            store_part<uint8_t>(orow, v, lo, n, h[i]);
+            return;
+        }
         uint32_t c[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -284,13 +337,14 @@ struct Row {
 __device__ __forceinline__ int out_bytes(const NormParams &p) {
     return p.out_dtype == HISA_F32 ? 4 : (p.out_dtype == HISA_BF16 ? 2 : 1);
 }
-__device__ __forceinline__ uint8_t *out_row(const NormParams &p, int64_t row) {
-    return static_cast<uint8_t *>(p.out) + row * p.ld_out * out_bytes(p);
+// Where unit 0 of a row lies, s elements before the row.
+__device__ __forceinline__ uint8_t *out_row(const NormParams &p, int64_t row, int s = 0) {
+    return static_cast<uint8_t *>(p.out) + (row * p.ld_out - s) * out_bytes(p);
 }
 template <typename RT>
-__device__ __forceinline__ uint8_t *res_row(const NormParams &p, int64_t row) {
+__device__ __forceinline__ uint8_t *res_row(const NormParams &p, int64_t row, int s = 0) {
     if constexpr (std::is_same<RT, None>::value) return nullptr;
-    else return p.res_out ? reinterpret_cast<uint8_t *>(static_cast<RT *>(p.res_out) + row * p.ld_res) : nullptr;
+    else return p.res_out ? reinterpret_cast<uint8_t *>(static_cast<RT *>(p.res_out) + row * p.ld_res - s) : nullptr;
 }
 
 __device__ __forceinline__ void load_w(const float *base, int v, int nvec, float (&w)[8]) {
@@ -300,17 +354,65 @@ __device__ __forceinline__ void load_w(const float *base, int v, int nvec, float
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
+// Rows that do not start at a multiple of 8 elements, but at the same remainder s in every array
+// (contiguous arrays of any width): the units are the aligned ones, unit v columns 8 v - s .. + 7,
+// the first and the last cut. A team's rows lie a multiple of 8 rows apart, so s is the team's
+// constant and the weights are shifted once. (The shift of every row through shared memory, which
+// k_norm_ragged makes, took 12.8 instead of 9.9 us for 1001 x 5003 f32.)
+__device__ __forceinline__ int shift_of(const NormParams &p, int64_t row) { return (int)((p.phase + row * p.ld_x) & 7); }
+__device__ __forceinline__ void load_w_cut(const NormParams &p, int v, int s, float (&w)[8]) {
+    float a[16];                                       // columns 8 v - 8 .. 8 v + 7
+    const bool whole = (reinterpret_cast<uintptr_t>(p.w) & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = 8 * v - 8 + 4 * j;
+        if (whole && c >= 0 && c + 4 <= p.cols) {
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(p.w + c));
+            a[4 * j] = u.x; a[4 * j + 1] = u.y; a[4 * j + 2] = u.z; a[4 * j + 3] = u.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[4 * j + e] = c + e >= 0 && c + e < p.cols ? __ldg(p.w + c + e) : 0.f;
+        }
+    }
+    const int d = 8 - s;                               // 1 .. 8
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = d & 8 ? a[i + 8] : a[i];
+#pragma unroll
+    for (int i = 0; i < 11; ++i) a[i] = d & 4 ? a[i + 4] : a[i];
+#pragma unroll
+    for (int i = 0; i < 9; ++i) a[i] = d & 2 ? a[i + 2] : a[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = d & 1 ? a[i + 1] : a[i];
+}
+// The pieces of a cut unit that hold one of its columns [lo, n).
+template <typename T>
+__device__ __forceinline__ void load_raw_cut(Raw8<T> &r, const uint8_t *row, int v, int lo, int n) {
+    if constexpr (!std::is_same<T, None>::value) {
+        constexpr int kP = sizeof(T) / 2, kE = 8 / kP; // pieces per unit, elements per piece
+        const uint4 *p = reinterpret_cast<const uint4 *>(row) + v * kP;
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+            if (kE * i < n && kE * i + kE > lo) r.v[i] = __ldcs(p + i);
+    }
+}
+
 // Rows of at most 1024 columns: a warp per row, the next row's loads in flight in registers.
-template <typename XT, typename RT, int VPT>
+template <typename XT, typename RT, int VPT, bool RAG>
 __global__ void __launch_bounds__(256, VPT == 1 ? 4 : (VPT == 2 ? 3 : 2)) k_norm_warp(NormParams p) {
-    const int t = threadIdx.x & 31, nvec = p.cols >> 3;
-    const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+    const int t = threadIdx.x & 31;
+    const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);       // a multiple of 8
     int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int s = RAG ? shift_of(p, row) : 0, nvec = (p.cols + s + 7) >> 3;
+    auto lo = [&](int v) { return RAG && v == 0 ? s : 0; };
+    auto hi = [&](int v) { const int n = p.cols + s - 8 * v; return v >= nvec ? 0 : RAG && n < 8 ? n : 8; };
     const float inv = 1.f / (float)p.cols;
     float w[VPT][8];
     if (!p.chained) grid_dep_wait();
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) load_w(p.w, i * 32 + t, nvec, w[i]);
+    for (int i = 0; i < VPT; ++i) {
+        if constexpr (RAG) load_w_cut(p, i * 32 + t, s, w[i]);
+        else load_w(p.w, i * 32 + t, nvec, w[i]);
+    }
     if (p.chained) grid_dep_wait();
     grid_dep_trigger();
     Raw8<XT> x[VPT];
@@ -320,7 +422,11 @@ __global__ void __launch_bounds__(256, VPT == 1 ? 4 : (VPT == 2 ? 3 : 2)) k_norm
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = i * 32 + t;
-            if (v < nvec) {
+            if constexpr (RAG) {
+                load_raw_cut<XT>(x[i], reinterpret_cast<const uint8_t *>(static_cast<const XT *>(p.x) + at * p.ld_x - s), v, lo(v), hi(v));
+                if constexpr (!std::is_same<RT, None>::value)
+                    load_raw_cut<RT>(r[i], reinterpret_cast<const uint8_t *>(static_cast<const RT *>(p.res) + at * p.ld_res - s), v, lo(v), hi(v));
+            } else if (v < nvec) {
                 load_raw(x[i], p.x, at * p.ld_x + (int64_t)v * 8);
                 load_raw(r[i], p.res, at * p.ld_res + (int64_t)v * 8);
             }
@@ -328,10 +434,10 @@ __global__ void __launch_bounds__(256, VPT == 1 ? 4 : (VPT == 2 ? 3 : 2)) k_norm
     };
     fetch(row);
     for (; row < p.rows; row += step) {
-        Row<RT, VPT, false> m;
-        uint8_t *rrow = res_row<RT>(p, row), *orow = out_row(p, row);
+        Row<RT, VPT, false, RAG> m;
+        uint8_t *rrow = res_row<RT>(p, row, s), *orow = out_row(p, row, s);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) m.take(i, i * 32 + t, i * 32 + t < nvec ? 8 : 0, rrow, x[i], r[i], w[i]);
+        for (int i = 0; i < VPT; ++i) m.take(i, i * 32 + t, lo(i * 32 + t), hi(i * 32 + t), rrow, x[i], r[i], w[i]);
         fetch(row + step);
         if (p.out_dtype == HISA_E4M3) {
             m.tops(p);
@@ -340,50 +446,59 @@ __global__ void __launch_bounds__(256, VPT == 1 ? 4 : (VPT == 2 ? 3 : 2)) k_norm
         const float f = rsqrtf(warp_sum(m.ss()) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (i * 32 + t < nvec) m.put(p, i, i * 32 + t, p.scales + row * p.groups, orow, f);
+            if (i * 32 + t < nvec) m.put(p, i, i * 32 + t, lo(i * 32 + t), hi(i * 32 + t), p.scales + row * p.groups, orow, f);
     }
 }
 
 // Longer rows: a CTA per row. Rows to come are copied to shared memory asynchronously, STAGES - 1
 // of them in flight; a warp copies exactly the units that it reads itself, so it waits for its
 // own copies and needs no barrier for them.
-template <typename XT, typename RT, int VPT, int STAGES>
+template <typename XT, typename RT, int VPT, int STAGES, bool RAG>
 __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
     constexpr int kX = sizeof(XT) / 2, kR = std::is_same<RT, None>::value ? 0 : sizeof(RT) / 2;   // 16-byte pieces per unit
     extern __shared__ __align__(16) uint4 ring[];     // [stage]: the row of x, the row of residual
     __shared__ __align__(16) float red[2][32], redm[2][32];
-    const int T = blockDim.x, t = threadIdx.x, nvec = p.cols >> 3;
+    const int T = blockDim.x, t = threadIdx.x;
+    const int s = RAG ? shift_of(p, blockIdx.x) : 0, nvec = (p.cols + s + 7) >> 3;
+    const int held = RAG ? (p.cols + 14) >> 3 : nvec; // units of a stage
+    auto lo = [&](int v) { return RAG && v == 0 ? s : 0; };
+    auto hi = [&](int v) { const int n = p.cols + s - 8 * v; return v >= nvec ? 0 : RAG && n < 8 ? n : 8; };
     const float inv = 1.f / (float)p.cols;
-    if (t < 32) red[0][t] = red[1][t] = 0.f;
+    if (t < 32) red[0][t] = red[1][t] = redm[0][t] = redm[1][t] = 0.f;
     __syncthreads();
     constexpr bool kHoldW = VPT <= 2;                 // this thread's weights stay in registers
     float w[kHoldW ? VPT : 1][8];
-    if (!p.chained) grid_dep_wait();
-    if constexpr (kHoldW) {
+    auto weights = [&](int v, float (&to)[8]) {
+        if constexpr (RAG) load_w_cut(p, v, s, to);
+        else load_w(p.w, v, nvec, to);
+    };
+    if (kHoldW && p.chained) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) load_w(p.w, i * T + t, nvec, w[i]);
+        for (int i = 0; i < VPT; ++i) weights(i * T + t, w[kHoldW ? i : 0]);
     }
-    if (p.chained) grid_dep_wait();
+    grid_dep_wait();
     grid_dep_trigger();
     // Everything that a row needs of its number moves on by a constant where registers allow: rows
     // are short enough for the multiplications to count.
     constexpr bool kStep = VPT <= 2;
     const int q0x = (t & ~31) * kX + (t & 31), q0r = (t & ~31) * kR + (t & 31);      // this thread's first pieces
-    const uint8_t *nx = reinterpret_cast<const uint8_t *>(static_cast<const XT *>(p.x) + blockIdx.x * p.ld_x) + 16 * q0x;
+    const uint8_t *nx = reinterpret_cast<const uint8_t *>(static_cast<const XT *>(p.x) + blockIdx.x * p.ld_x - s) + 16 * q0x;
     const int64_t step_x = gridDim.x * p.ld_x * (int64_t)sizeof(XT);
     const uint8_t *nr = nullptr;
     int64_t step_r = 0;
     if constexpr (kR > 0) {
-        nr = reinterpret_cast<const uint8_t *>(static_cast<const RT *>(p.res) + blockIdx.x * p.ld_res) + 16 * q0r;
+        nr = reinterpret_cast<const uint8_t *>(static_cast<const RT *>(p.res) + blockIdx.x * p.ld_res - s) + 16 * q0r;
         step_r = gridDim.x * p.ld_res * (int64_t)sizeof(RT);
     }
-    const uint32_t stage_b = (uint32_t)(kX + kR) * nvec * 16, ring0 = tc::smem_u32(ring);
+    const uint32_t stage_b = (uint32_t)(kX + kR) * held * 16, ring0 = tc::smem_u32(ring);
     int64_t next = blockIdx.x;                        // the row to copy next
+    // the pieces that hold an element of the row
+    auto piece = [&](int q, int per) { return (!RAG || (q + 1) * 8 > s * per) && q * 8 < (RAG ? p.cols + s : nvec * 8) * per; };
     auto copy = [&](int stage) {
         if (next < p.rows) {
             if constexpr (!kStep) {
-                nx = reinterpret_cast<const uint8_t *>(static_cast<const XT *>(p.x) + next * p.ld_x) + 16 * q0x;
-                if constexpr (kR > 0) nr = reinterpret_cast<const uint8_t *>(static_cast<const RT *>(p.res) + next * p.ld_res) + 16 * q0r;
+                nx = reinterpret_cast<const uint8_t *>(static_cast<const XT *>(p.x) + next * p.ld_x - s) + 16 * q0x;
+                if constexpr (kR > 0) nr = reinterpret_cast<const uint8_t *>(static_cast<const RT *>(p.res) + next * p.ld_res - s) + 16 * q0r;
             }
             const uint32_t dst = ring0 + stage * stage_b;
 #pragma unroll
@@ -391,12 +506,12 @@ __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
 #pragma unroll
                 for (int k = 0; k < kX; ++k) {        // the warp's units i T + t & ~31 .. + 31
                     const int q = i * T * kX + 32 * k;
-                    if (q0x + q < nvec * kX) tc::cp_async16(dst + 16 * (q0x + q), nx + 16 * q);
+                    if (piece(q0x + q, kX)) tc::cp_async16(dst + 16 * (q0x + q), nx + 16 * q);
                 }
 #pragma unroll
                 for (int k = 0; k < kR; ++k) {
                     const int q = i * T * kR + 32 * k;
-                    if (q0r + q < nvec * kR) tc::cp_async16(dst + 16 * (kX * nvec + q0r + q), nr + 16 * q);
+                    if (piece(q0r + q, kR)) tc::cp_async16(dst + 16 * (kX * held + q0r + q), nr + 16 * q);
                 }
             }
             if constexpr (kStep) {
@@ -408,8 +523,12 @@ __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) copy(s);
-    uint8_t *orow = out_row(p, blockIdx.x), *rrow = res_row<RT>(p, blockIdx.x);
+    for (int k = 0; k < STAGES - 1; ++k) copy(k);
+    if (kHoldW && !p.chained) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) weights(i * T + t, w[kHoldW ? i : 0]);
+    }
+    uint8_t *orow = out_row(p, blockIdx.x, s), *rrow = res_row<RT>(p, blockIdx.x, s);
     const int64_t step_o = gridDim.x * p.ld_out * out_bytes(p);
     float *srow = p.scales + (int64_t)blockIdx.x * p.groups;
     int stage = 0, par = 0;
@@ -417,13 +536,13 @@ __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
         if (STAGES == 1) copy(0);
         asm volatile("cp.async.wait_group %0;" :: "n"(STAGES > 1 ? STAGES - 2 : 0) : "memory");
         __syncwarp();
-        const uint4 *src = ring + stage * (kX + kR) * nvec;
+        const uint4 *src = ring + stage * (kX + kR) * held;
         if constexpr (!kStep) {
-            orow = out_row(p, row);
-            rrow = res_row<RT>(p, row);
+            orow = out_row(p, row, s);
+            rrow = res_row<RT>(p, row, s);
             srow = p.scales + row * p.groups;
         }
-        Row<RT, VPT, false> m;
+        Row<RT, VPT, false, RAG> m;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = i * T + t;
@@ -434,11 +553,11 @@ __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
                 for (int k = 0; k < kX; ++k) x.v[k] = src[v * kX + k];
                 if constexpr (kR > 0) {
 #pragma unroll
-                    for (int k = 0; k < kR; ++k) r.v[k] = src[kX * nvec + v * kR + k];
+                    for (int k = 0; k < kR; ++k) r.v[k] = src[kX * held + v * kR + k];
                 }
             }
-            if constexpr (!kHoldW) load_w(p.w, v, nvec, w[0]);
-            m.take(i, v, v < nvec ? 8 : 0, rrow, x, r, w[kHoldW ? i : 0]);
+            if constexpr (!kHoldW) weights(v, w[0]);
+            m.take(i, v, lo(v), hi(v), rrow, x, r, w[kHoldW ? i : 0]);
         }
         __syncwarp();
         if (STAGES > 1) {
@@ -446,14 +565,19 @@ __global__ void __launch_bounds__(1024, 1) k_norm_cta(NormParams p) {
             copy(stage == 0 ? STAGES - 1 : stage - 1);
             stage = stage + 1 == STAGES ? 0 : stage + 1;
         }
-        if (p.out_dtype == HISA_E4M3) {
-            m.tops(p);
-            if (!p.group) m.same_top(block_max(m.top[0], redm[par]));
+        if (p.out_dtype == HISA_E4M3) m.tops(p);
+        float sum = m.ss();
+        if (p.out_dtype == HISA_E4M3 && !p.group) {
+            float top = m.top[0];
+            block_sum_max(sum, top, red[par], redm[par]);
+            m.same_top(top);
+        } else {
+            sum = block_sum(sum, red[par]);
         }
-        const float f = rsqrtf(block_sum(m.ss(), red[par]) * inv + p.eps);
+        const float f = rsqrtf(sum * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (i * T + t < nvec) m.put(p, i, i * T + t, srow, orow, f);
+            if (i * T + t < nvec) m.put(p, i, i * T + t, lo(i * T + t), hi(i * T + t), srow, orow, f);
         if constexpr (kStep) {
             orow += step_o;
             if (rrow) rrow += step_r;
@@ -523,8 +647,8 @@ __device__ __forceinline__ void write_row(uint8_t *dst, const uint8_t *staged, i
     }
 }
 
-// Rows whose starts are not aligned or whose length is not a multiple of 8 columns: the same
-// units of 8 columns, a CTA per row. Rows come in and go out through shared memory in the aligned
+// Rows that start at different remainders in different arrays, or with groups that the aligned units
+// would straddle: the same units of 8 columns, a CTA per row. Rows come in and go out through shared memory in the aligned
 // 16-byte blocks that cover them, and the shift between blocks and units is made in registers.
 template <typename XT, typename RT, int VPT, int STAGES>
 __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
@@ -536,7 +660,7 @@ __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
     const size_t xb = stage_bytes(p.cols, kElem<XT>), rb = stage_bytes(p.cols, kElem<RT>);
     uint8_t *in = reinterpret_cast<uint8_t *>(ring), *obuf = in + STAGES * (xb + rb);
     uint8_t *rbuf = obuf + stage_bytes(p.cols, es);
-    if (t < 32) red[0][t] = red[1][t] = 0.f;
+    if (t < 32) red[0][t] = red[1][t] = redm[0][t] = redm[1][t] = 0.f;
     constexpr bool kHoldW = VPT <= 2;
     float w[kHoldW ? VPT : 1][8];
     const bool whole_w = (reinterpret_cast<uintptr_t>(p.w) & 15) == 0;
@@ -573,7 +697,7 @@ __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
         asm volatile("cp.async.wait_group %0;" :: "n"(STAGES - 1) : "memory");
         __syncthreads();                               // every thread's blocks of this row have landed, and
                                                        // the row before has been written out
-        Row<RT, VPT, true> m;
+        Row<RT, VPT, true, false> m;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = i * T + t;
@@ -589,17 +713,22 @@ __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
                 }
             }
             if constexpr (!kHoldW) load_some(v, w[0]);
-            m.take(i, v, p.cols - 8 * v, rrow ? rbuf : nullptr, x, r, w[kHoldW ? i : 0]);
+            m.take(i, v, 0, p.cols - 8 * v, rrow ? rbuf : nullptr, x, r, w[kHoldW ? i : 0]);
         }
-        if (p.out_dtype == HISA_E4M3) {
-            m.tops(p);
-            if (!p.group) m.same_top(block_max(m.top[0], redm[par]));
+        if (p.out_dtype == HISA_E4M3) m.tops(p);
+        float sum = m.ss();
+        if (p.out_dtype == HISA_E4M3 && !p.group) {
+            float top = m.top[0];
+            block_sum_max(sum, top, red[par], redm[par]);
+            m.same_top(top);
+        } else {
+            sum = block_sum(sum, red[par]);
         }
-        const float f = rsqrtf(block_sum(m.ss(), red[par]) * inv + p.eps);
+        const float f = rsqrtf(sum * inv + p.eps);
         copy(row + (int64_t)STAGES * gridDim.x, STAGES == 2 ? par : 0);   // every thread has read this row (the sum's barrier)
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (i * T + t < nvec) m.put(p, i, i * T + t, p.scales + row * p.groups, obuf, f);
+            if (i * T + t < nvec) m.put(p, i, i * T + t, 0, 8, p.scales + row * p.groups, obuf, f);
         __syncthreads();                               // the staged outputs are whole
         write_row(orow, obuf, p.cols * es, es);
         if (rrow) write_row(rrow, rbuf, p.cols * (int)kElem<RT>, (int)kElem<RT>);
@@ -614,7 +743,7 @@ __global__ void __launch_bounds__(1024, 1) k_norm_long(NormParams p) {
     __shared__ __align__(16) float red[2][32], redm[2][32];
     const int T = blockDim.x, t = threadIdx.x;
     const float inv = 1.f / (float)p.cols;
-    if (t < 32) red[0][t] = red[1][t] = 0.f;
+    if (t < 32) red[0][t] = red[1][t] = redm[0][t] = redm[1][t] = 0.f;
     __syncthreads();
     grid_dep_wait();
     grid_dep_trigger();
@@ -672,8 +801,9 @@ __global__ void __launch_bounds__(1024, 1) k_norm_long(NormParams p) {
     }
 }
 
+// A team's rows are `apart` rows apart, or a multiple of that.
 template <auto Kernel>
-cudaError_t go(const NormParams &p, int threads, int64_t rows_per_cta, size_t smem, cudaStream_t s) {
+cudaError_t go(const NormParams &p, int threads, int64_t rows_per_cta, size_t smem, cudaStream_t s, int64_t apart = 1) {
     if (smem) {
         const cudaError_t e = smem_attr_once<Kernel>(kMaxSmem);
         if (e != cudaSuccess) return e;
@@ -688,26 +818,41 @@ cudaError_t go(const NormParams &p, int threads, int64_t rows_per_cta, size_t sm
         const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, Kernel, threads, smem);
         if (e != cudaSuccess) return e;
         most = (int64_t)sms * (per > 0 ? per : 1);
+        most = most > apart ? most / apart * apart : apart;
+    } else if (want > 1) {
+        most = want;
     }
     return launch_pdl(Kernel, dim3((unsigned)(want < most ? want : most)), dim3(threads), smem, s, 1, p);
 }
 
+// Units of 8 columns, aligned in memory.
+template <typename XT, typename RT, bool RAG>
+cudaError_t pick_units(const NormParams &p, int nvec, cudaStream_t s) {
+    auto up = [](int n) { return (n + 31) / 32 * 32; };
+    const size_t row = (size_t)nvec * 8 * (kElem<XT> + kElem<RT>);
+    // up to 1024 columns a warp holds the row (no barrier); above, a CTA of up to 512 threads
+    // with a unit each, or of up to 1024 with two or four. Three stages are two rows in flight per
+    // CTA. Where two CTAs of two units per thread share an SM, one row each in flight is enough and
+    // keeps what DRAM serves at once closer together (16384 x 7168 bf16 with residual to e4m3: 122
+    // against 142 us; 5003 f32 with f32 residual, where three stages leave room for one CTA, 199
+    // against 238). Alone on its SM a CTA needs both (8192 x 16384 bf16: 81 against 89 us).
+    if (nvec <= 32) return go<k_norm_warp<XT, RT, 1, RAG>>(p, 256, 8, 0, s);
+    if (nvec <= 64) return go<k_norm_warp<XT, RT, 2, RAG>>(p, 256, 8, 0, s);
+    if (nvec <= 128) return go<k_norm_warp<XT, RT, 4, RAG>>(p, 256, 8, 0, s);
+    if (nvec <= 512) return go<k_norm_cta<XT, RT, 1, 3, RAG>>(p, up(nvec), 1, 3 * row, s, RAG ? 8 : 1);
+    if (nvec <= 1024 && 4 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 2, 2, RAG>>(p, up((nvec + 1) / 2), 1, 2 * row, s, RAG ? 8 : 1);
+    if (nvec <= 2048 && 3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 2, 3, RAG>>(p, up((nvec + 1) / 2), 1, 3 * row, s, RAG ? 8 : 1);
+    if (3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 4, 3, RAG>>(p, up((nvec + 3) / 4), 1, 3 * row, s, RAG ? 8 : 1);
+    return go<k_norm_cta<XT, RT, 4, 1, RAG>>(p, up((nvec + 3) / 4), 1, row, s, RAG ? 8 : 1);
+}
+
 template <typename XT, typename RT>
 cudaError_t pick(const NormParams &p, cudaStream_t s) {
-    const size_t row = (size_t)p.cols * (kElem<XT> + kElem<RT>);
-    const int nvec = (p.cols + 7) / 8;
+    const int nvec = (p.cols + 7) / 8, cut = (p.cols + 14) / 8;
+    const size_t unit = 8 * (kElem<XT> + kElem<RT>);
     auto up = [](int n) { return (n + 31) / 32 * 32; };
-    if (p.wide && row <= kMaxSmem) {
-        // up to 1024 columns a warp holds the row (no barrier); above, a CTA of up to 512 threads
-        // with a unit each, or of up to 1024 with two or four
-        if (nvec <= 32) return go<k_norm_warp<XT, RT, 1>>(p, 256, 8, 0, s);
-        if (nvec <= 64) return go<k_norm_warp<XT, RT, 2>>(p, 256, 8, 0, s);
-        if (nvec <= 128) return go<k_norm_warp<XT, RT, 4>>(p, 256, 8, 0, s);
-        if (nvec <= 512) return go<k_norm_cta<XT, RT, 1, 3>>(p, up(nvec), 1, 3 * row, s);
-        if (nvec <= 2048 && 3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 2, 3>>(p, up((nvec + 1) / 2), 1, 3 * row, s);
-        if (3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 4, 3>>(p, up((nvec + 3) / 4), 1, 3 * row, s);
-        return go<k_norm_cta<XT, RT, 4, 1>>(p, up((nvec + 3) / 4), 1, row, s);
-    }
+    if (p.wide && nvec * unit <= kMaxSmem) return pick_units<XT, RT, false>(p, nvec, s);
+    if (p.phase >= 0 && cut <= 4096 && cut * unit <= kMaxSmem) return pick_units<XT, RT, true>(p, cut, s);
     const size_t in = stage_bytes(p.cols, kElem<XT>) + stage_bytes(p.cols, kElem<RT>);
     const size_t out = stage_bytes(p.cols, p.out_dtype == HISA_F32 ? 4 : (p.out_dtype == HISA_BF16 ? 2 : 1)) +
                        (p.res_out ? stage_bytes(p.cols, kElem<RT>) : 0);

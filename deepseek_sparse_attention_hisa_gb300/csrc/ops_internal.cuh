@@ -37,6 +37,8 @@ struct NormParams {
     void *out;                // [rows, cols]
     float *scales;            // [rows, cols / group] (8-bit output)
     int wide;                 // every row start is aligned to 8 elements, cols % 8 == 0
+    int phase;                // row 0's start modulo 8 elements if every row's is the same in all arrays, and
+                              // scales are per row; else -1
     int chained;              // w may be read before the previous grid has completed
 };
 

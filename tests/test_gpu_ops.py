@@ -141,6 +141,36 @@ def test_norm_strides_leave_the_rest(ld, off, ot):
         assert (buf == fill).all()                               # nothing outside the rows was written
 
 
+@pytest.mark.parametrize("rows,cols", [(13, 1), (20, 3), (2500, 333), (1300, 1003), (1300, 5003), (900, 9001), (700, 20011)])
+@pytest.mark.parametrize("off", [0, 5])
+@pytest.mark.parametrize("xt,rt,ot", [("bf16", "bf16", "bf16"), ("f32", None, "f32"), ("bf16", "f32", "e4m3"),
+                                      ("f32", "bf16", "bf16")])
+def test_norm_rows_start_anywhere(rows, cols, off, xt, rt, ot):
+    # rows one after another: they start at every remainder, the same in all arrays
+    bx, x = strided(rows, cols, xt, cols, off, 3.0)
+    bo, out = strided(rows, cols, ot, cols, off, 9.0)
+    x.copy_(randn((rows, cols), xt, 16))
+    br = res = keep = None
+    if rt is not None:
+        br, res = strided(rows, cols, rt, cols, off, 5.0)
+        res.copy_(randn((rows, cols), rt, 17, 2.0))
+        keep = res.clone()
+    w = 1 + randn((cols,), "f32", 18, 0.1)
+    _, _, scales = run_norm(x, res, w, ot, out=out, res_out=res)
+    check_norm(x, keep, w, ot, out, res, scales)
+    for buf, view, fill in ((bx, x, 3.0), (br, res, 5.0), (bo, out, 9.0)):
+        if buf is not None:
+            view.fill_(fill)
+            assert (buf.float() == fill).all()                   # nothing outside the rows was written
+
+
+def test_norm_ragged_in_place():
+    x, w = randn((1500, 5003), "f32", 19), 1 + randn((5003,), "f32", 20, 0.1)
+    old = x.clone()
+    run_norm(x, None, w, "f32", out=x)
+    check_norm(old, None, w, "f32", x, None, None)
+
+
 def test_norm_in_place_and_sum_not_kept():
     x, res, w = randn((50, 4096), "bf16", 11), randn((50, 4096), "bf16", 12), torch.ones(4096, device="cuda")
     old, before = x.clone(), res.clone()
