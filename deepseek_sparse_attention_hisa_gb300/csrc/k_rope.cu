@@ -9,15 +9,15 @@
 //
 // Bound by memory. The heads of all tokens are one list of rows (token, head); a thread owns one
 // unit of a row (8 neighbouring dims of one or of both halves, or a copied unit) and walks the
-// CTA's rows, four loads in flight. While they are, the CTA computes the sines and cosines of the
-// batch's few tokens into shared memory, once per token and pair and not once per head, on all
-// its threads (each thread computing its own pairs held the half layout at a sixth of this rate).
-// In place only the rotated dims move.
+// CTA's rows, 64 bytes in flight (128 for f32 halves). While they are, the CTA computes the sines
+// and cosines of the batch's few tokens into shared memory, once per token and pair and not once
+// per head, on all its threads (each thread computing its own pairs held the half layout at a
+// sixth of this rate). In place only the rotated dims move.
 //
-// Measured: 4096 tokens of 64 + 1 heads of 512, f32 to bf16: 125 us, 6.54 TB/s, 96 % of a plain
-// copy's rate; 2047 tokens of 64 x 128 bf16 in the half layout: 17.8 us (9.9 are its bytes; the
-// instructions of two 16-byte blocks per thread and the CTA's start bound it); the last 64 dims of
-// 304 tokens of 64 + 1 heads in place: 5.3 us per call, 4.6 us of it on the device.
+// Measured: 4096 tokens of 64 + 1 heads of 512, f32 to bf16: 124 us, 6.6 TB/s, 97 % of a plain
+// copy's rate; 2047 tokens of 64 x 128 bf16, 64 dims rotated in the half layout: 15.6 us (9.9 are
+// its bytes; instructions, the angles' latency and the CTAs' start bound it); the last 64 dims of
+// 304 tokens of 64 + 1 heads in place: 4.3 us per call, which its launch bounds.
 #include "ops_internal.cuh"
 
 namespace hisa {
@@ -78,10 +78,12 @@ __device__ __forceinline__ void store_unit(void *base, int64_t at, const float (
 // N dims per unit (8, or 1 where a boundary is not a multiple of 8). A rotated unit is two
 // blocks of N dims, `lo` and `hi`: for the half layout the pairs (lo + e, hi + e); interleaved,
 // for N = 8 one block holding 4 pairs (hi unused), for N = 1 the pair (lo, hi).
-// Rows per thread in flight: four, or two where a unit is 64 bytes (the registers of four would
-// halve the CTAs per SM).
+// Rows per thread in flight: four of 16 bytes, two of more. More in flight spreads what DRAM serves
+// at once (4096 x 65 x 512 f32 to bf16: 125 us with two, 132 with four) and costs the half layout
+// its registers (2047 x 64 x 128 bf16, all dims: 13.1 us with two, 13.9 with four); fewer leave DRAM
+// idle (interleaved bf16, 4096 x 65 x 512: 90 us with four, 94 with three, 104 with two).
 template <typename S, int N, bool HALF>
-constexpr int kUnroll = N == 8 && HALF && sizeof(S) == 4 ? 2 : 4;
+constexpr int kUnroll = N == 8 && (HALF || sizeof(S) == 4) ? 2 : 4;
 
 template <typename S, typename D, int N, bool HALF>
 __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(RopeParams p) {
@@ -90,11 +92,9 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(Ro
     constexpr int kPairs = kTwo ? N : N / 2;
     const int n_rot = p.dims / (kTwo ? 2 * N : N);
     const int n = n_rot + (p.inplace ? 0 : (p.D - p.dims) / N);
-    const int per = blockDim.x / n;                       // rows the CTA takes at once
-    const int unit = threadIdx.x % n, sub = threadIdx.x / n;
+    const int sub = threadIdx.x / n, unit = threadIdx.x - sub * n, per = p.per;
     const int64_t r0 = blockIdx.x * p.rows_per_cta;
-    int64_t r1 = r0 + p.rows_per_cta;
-    r1 = r1 < p.rows ? r1 : p.rows;
+    const int mine = (int)(p.rows - r0 < p.rows_per_cta ? p.rows - r0 : p.rows_per_cta);
     const bool rot = unit < n_rot;
     const int pairs = p.dims / 2;
     int lo, hi = 0;
@@ -106,34 +106,34 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(Ro
         lo = (unit - n_rot) * N;                          // copied units: the dims before, then after, the rotated
         if (lo >= p.first) lo += p.dims;
     }
-    // [token of the batch][pair]: mscale (cos, sin). A unit of 8 dims reads its pairs two at a time, and
-    // the units' first two come first, then their next two: neighbouring lanes read neighbouring
-    // 16 bytes (unit by unit they would meet in a quarter of the banks).
-    extern __shared__ __align__(16) float2 turn[];
-    auto slot = [&](int pair) {
-        if (N == 1) return pair;
-        const int of = pair / kPairs, at = pair % kPairs;
-        return ((at >> 1) * n_rot + of) * 2 + (at & 1);
-    };
+    // [token of the batch][pair]: mscale (cos, sin). For a unit of 8 dims two pairs' cosines, then
+    // their sines, and the units' first two pairs come first, then their next two: neighbouring
+    // lanes read neighbouring 16 bytes (unit by unit they would meet in a quarter of the banks).
+    extern __shared__ __align__(16) float turn[];
     grid_dep_wait();
     grid_dep_trigger();
-    const int64_t batch = (int64_t)per * kU;
-    const int step_tok = per / p.heads_all, step_head = per - step_tok * p.heads_all;
-    for (int64_t b0 = r0; b0 < r1; b0 += batch) {
-        const int64_t base = b0 + sub, last = (b0 + batch < r1 ? b0 + batch : r1) - 1;
-        const int64_t tok0 = b0 / p.heads_all;
+    // the first row's token and head (grid * heads_all fits 32 bits), and this thread's from there on
+    const uint32_t past = blockIdx.x * (uint32_t)p.cta_head;
+    int64_t tok0 = (int64_t)blockIdx.x * p.cta_tok + past / (uint32_t)p.heads_all;
+    int head0 = (int)(past % (uint32_t)p.heads_all);
+    const int sub_tok = sub / p.heads_all, sub_head = sub - sub_tok * p.heads_all;
+    for (int done = 0; done < mine; done += p.batch) {
+        const int here = mine - done < p.batch ? mine - done : p.batch;
+        const int left = here - sub;                      // rows k per < left are there
         const S *x0 = static_cast<const S *>(p.x) + tok0 * p.x_token, *x20 = static_cast<const S *>(p.x2) + tok0 * p.x2_token;
-        const int left = (int)(r1 - base < batch ? r1 - base : batch);     // rows k per < left are there
         Unit<S, N> a[kU], b[kTwo ? kU : 1];
         int tok[kU], head[kU];                            // token (from tok0 on) and head of row k
-        head[0] = (int)(base - tok0 * p.heads_all);
-        tok[0] = head[0] / p.heads_all;
-        head[0] -= tok[0] * p.heads_all;
+        head[0] = head0 + sub_head;
+        tok[0] = sub_tok;
+        if (head[0] >= p.heads_all) {
+            head[0] -= p.heads_all;
+            ++tok[0];
+        }
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
             if (k > 0) {
-                tok[k] = tok[k - 1] + step_tok;
-                head[k] = head[k - 1] + step_head;
+                tok[k] = tok[k - 1] + p.step_tok;
+                head[k] = head[k - 1] + p.step_head;
                 if (head[k] >= p.heads_all) {
                     head[k] -= p.heads_all;
                     ++tok[k];
@@ -147,13 +147,24 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(Ro
                     if (rot) load_unit<S, N>(src, hi, b[k]);
             }
         }
-        const int angles = (int)(last / p.heads_all - tok0 + 1) * pairs;
-        for (int i = threadIdx.x; i < angles; i += blockDim.x) {
-            const int64_t pos = p.pos[tok0 + i / pairs];
-            const int64_t turns = (int64_t)((uint64_t)pos * __ldg(p.table + i % pairs));      // modulo one turn
+        const uint32_t angles = ((uint32_t)(head0 + here - 1) / (uint32_t)p.heads_all + 1) * pairs;
+        for (uint32_t i = threadIdx.x; i < angles; i += blockDim.x) {
+            const uint32_t tk = i / (uint32_t)pairs, pair = i - tk * pairs;
+            const int64_t pos = p.pos[tok0 + tk];
+            const int64_t turns = (int64_t)((uint64_t)pos * __ldg(p.table + pair));           // modulo one turn
             float s, c;
             sincospif(2.f * (__ll2float_rn(turns) * 0x1p-64f), &s, &c);
-            turn[i / pairs * pairs + slot(i % pairs)] = make_float2(c * p.mscale, s * p.mscale * p.sin_sign);
+            c *= p.mscale;
+            s *= p.mscale * p.sin_sign;
+            if constexpr (N == 1) {
+                turn[2 * i] = c;
+                turn[2 * i + 1] = s;
+            } else {
+                const uint32_t of = pair / kPairs, at = pair % kPairs;
+                float *to = turn + 2 * tk * pairs + ((at >> 1) * n_rot + of) * 4 + (at & 1);
+                to[0] = c;
+                to[2] = s;
+            }
         }
         __syncthreads();
         D *y0 = static_cast<D *>(p.y) + tok0 * p.y_token, *y20 = static_cast<D *>(p.y2) + tok0 * p.y2_token;
@@ -165,40 +176,41 @@ __global__ void __launch_bounds__(N == 8 ? 256 : 1024, N == 8 ? 4 : 1) k_rope(Ro
             float u[N];
             to_floats<S, N>(a[k], u);
             if (rot) {
-                float2 cs[kPairs];
+                const float *cs = turn + 2 * tok[k] * pairs;
                 if constexpr (N == 1) {
-                    cs[0] = turn[tok[k] * pairs + unit];
-                } else {
-                    const float4 *at = reinterpret_cast<const float4 *>(turn + tok[k] * pairs) + unit;
-#pragma unroll
-                    for (int e = 0; e < kPairs / 2; ++e) {
-                        const float4 two = at[e * n_rot];
-                        cs[2 * e] = make_float2(two.x, two.y);
-                        cs[2 * e + 1] = make_float2(two.z, two.w);
-                    }
-                }
-                if constexpr (kTwo) {
-                    float v[N];
+                    float v[1];
                     to_floats<S, N>(b[k], v);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        const float x = u[e], y = v[e];
-                        u[e] = x * cs[e].x - y * cs[e].y;
-                        v[e] = x * cs[e].y + y * cs[e].x;
-                    }
+                    const float x = u[0], y = v[0], c = cs[2 * unit], s = cs[2 * unit + 1];
+                    u[0] = x * c - y * s;
+                    v[0] = x * s + y * c;
                     store_unit<D, N>(dst, hi, v);
                 } else {
+                    float v[kTwo ? N : 1];
+                    if constexpr (kTwo) to_floats<S, N>(b[k], v);
 #pragma unroll
-                    for (int e = 0; e < kPairs; ++e) {
-                        const float x = u[2 * e], y = u[2 * e + 1];
-                        u[2 * e] = x * cs[e].x - y * cs[e].y;
-                        u[2 * e + 1] = x * cs[e].y + y * cs[e].x;
+                    for (int e = 0; e < kPairs; e += 2) {     // two pairs at once
+                        const float4 t4 = reinterpret_cast<const float4 *>(cs)[(e / 2) * n_rot + unit];
+                        const float2 c = make_float2(t4.x, t4.y), s = make_float2(t4.z, t4.w), ns = make_float2(-t4.z, -t4.w);
+                        float &x0r = u[kTwo ? e : 2 * e], &x1r = u[kTwo ? e + 1 : 2 * e + 2];
+                        float &y0r = kTwo ? v[kTwo ? e : 0] : u[kTwo ? e : 2 * e + 1];
+                        float &y1r = kTwo ? v[kTwo ? e + 1 : 0] : u[kTwo ? e : 2 * e + 3];
+                        const float2 x = make_float2(x0r, x1r), y = make_float2(y0r, y1r);
+                        const float2 xt = fma2(y, ns, mul2(x, c)), yt = fma2(x, s, mul2(y, c));
+                        x0r = xt.x; x1r = xt.y;
+                        y0r = yt.x; y1r = yt.y;
                     }
+                    if constexpr (kTwo) store_unit<D, N>(dst, hi, v);
                 }
             }
             store_unit<D, N>(dst, lo, u);
         }
-        if (b0 + batch < r1) __syncthreads();             // the angles are read before the next batch's are written
+        if (done + p.batch < mine) __syncthreads();       // the angles are read before the next batch's are written
+        tok0 += p.batch_tok;
+        head0 += p.batch_head;
+        if (head0 >= p.heads_all) {
+            head0 -= p.heads_all;
+            ++tok0;
+        }
     }
 }
 
@@ -225,6 +237,11 @@ cudaError_t launch_as(RopeParams p, cudaStream_t s) {
     if (sms <= 0) return cudaErrorInvalidDevice;
     const int64_t batches = (p.rows + few - 1) / few, mul = (batches + 4 * sms - 1) / (4 * sms);
     p.rows_per_cta = few * mul;
+    p.per = per;
+    p.batch = (int)few;
+    p.cta_tok = (int)(p.rows_per_cta / p.heads_all); p.cta_head = (int)(p.rows_per_cta % p.heads_all);
+    p.batch_tok = (int)(few / p.heads_all); p.batch_head = (int)(few % p.heads_all);
+    p.step_tok = per / p.heads_all; p.step_head = per % p.heads_all;
     const int64_t grid = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_pdl(k_rope<S, D, N, HALF>, dim3((unsigned)grid), dim3(threads), shared(per), s, 1, p);

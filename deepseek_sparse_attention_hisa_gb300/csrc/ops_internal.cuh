@@ -11,6 +11,28 @@ namespace hisa {
 // scheduled (grid_dep_trigger) right after, so that launches overlap and no grid runs beside the
 // one two back.
 
+// Two f32 operations by one instruction (each rounded as alone): many rows are bound by the
+// number of instructions before they are by memory.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rn.f32x2 x, x, y, z; "
+        "mov.b64 {%0, %1}, x;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
 // Eight f32 to a 32-byte aligned address in one access: a whole sector per thread, where two
 // 16-byte stores each leave half of one.
 __device__ __forceinline__ void store_sector(float *dst, const float *v) {
@@ -54,7 +76,11 @@ struct RopeParams {
     const void *x, *x2;
     void *y, *y2;
     int64_t x_token, x_head, y_token, y_head, x2_token, x2_head, y2_token, y2_head;
-    int64_t rows_per_cta;     // set by launch_rope
+    // set by launch_rope: rows of a CTA, of a batch, and that a CTA takes at once, and the tokens and
+    // heads that each of them is (the kernel then divides nothing of 64 bits)
+    int64_t rows_per_cta;
+    int batch, per;
+    int cta_tok, cta_head, batch_tok, batch_head, step_tok, step_head;
     int wide;                 // 8 elements per access fit every boundary
 };
 
