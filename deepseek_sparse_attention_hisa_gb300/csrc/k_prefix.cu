@@ -197,32 +197,15 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_pref
     if (!tail) grid_dep_wait();
 }
 
-// Joins the segments of one (query row, head) and the sink: DH / 4 threads, four dims each.
-// Bound by memory: every segment's sums are read once.
+// Joins the segments of a (query row, head) and the sink: DH / 4 threads, four dims each. Bound by
+// memory: every segment's sums are read once. With few rows there are many segments to each (up to
+// 128), whose loads one after another would take longer than the segments themselves (1 x 8 x 64
+// f32 over 8000 shared rows: 36 us for the call, 18 so): then (ALL) a CTA's threads share one row,
+// the statistics are loaded at once, and groups of DH / 4 threads take every k-th segment.
+constexpr int kMergeThreads = 256, kMaxSegs = 128;
+
 template <int DH>
-__global__ void k_prefix_merge(PrefixParams p) {
-    constexpr int kPer = 128 / (DH / 4);                  // (query row, head) pairs per CTA
-    grid_dep_wait();
-    grid_dep_trigger();
-    const int64_t rows = (int64_t)p.B * p.L * p.H;
-    const int sub = threadIdx.x / (DH / 4), d = (threadIdx.x % (DH / 4)) * 4;
-    const int64_t g = (int64_t)blockIdx.x * kPer + sub;
-    if (g >= rows) return;
-    const int nseg = p.tail_split + p.pre_split;
-    const float sink = p.sinks ? p.sinks[g % p.H] : -INFINITY;
-    float M = sink;
-    for (int s = 0; s < nseg; ++s) M = fmaxf(M, p.part_ml[(s * rows + g) * 2]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float den = expf(sink - ref);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < nseg; ++s) {
-        const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + (s * rows + g) * 2);
-        if (ml.x == -INFINITY && ml.y == 0.f) continue;   // a segment that holds nothing
-        const float a = expf(ml.x - ref);
-        den += ml.y * a;
-        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p.part_o + (s * rows + g) * DH + d));
-        o.x += v.x * a; o.y += v.y * a; o.z += v.z * a; o.w += v.w * a;
-    }
+__device__ __forceinline__ void put_merged(const PrefixParams &p, int64_t g, int d, float4 o, float den) {
     const float f = den == 0.f ? 0.f : 1.f / den;         // nothing visible, no sink: 0
     o.x *= f; o.y *= f; o.z *= f; o.w *= f;
     if (p.out_bf16) {
@@ -231,6 +214,74 @@ __global__ void k_prefix_merge(PrefixParams p) {
             make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
     } else {
         *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + g * DH + d) = o;
+    }
+}
+
+template <int DH, bool ALL>
+__global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(PrefixParams p) {
+    constexpr int kT = DH / 4, kGroups = kMergeThreads / kT;
+    grid_dep_wait();
+    grid_dep_trigger();
+    const int64_t rows = (int64_t)p.B * p.L * p.H;
+    const int grp = threadIdx.x / kT, d = (threadIdx.x % kT) * 4;
+    const int nseg = p.tail_split + p.pre_split;
+    auto stats = [&](int s, int64_t g) { return *reinterpret_cast<const float2 *>(p.part_ml + (s * rows + g) * 2); };
+    // a segment that holds nothing has no sums to read
+    auto empty = [](float2 ml) { return ml.x == -INFINITY && ml.y == 0.f; };
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (!ALL) {
+        const int64_t g = (int64_t)blockIdx.x * kGroups + grp;
+        if (g >= rows) return;
+        const float sink = p.sinks ? p.sinks[g % p.H] : -INFINITY;
+        float M = sink;
+#pragma unroll 4
+        for (int s = 0; s < nseg; ++s) M = fmaxf(M, stats(s, g).x);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float den = expf(sink - ref);
+#pragma unroll 4
+        for (int s = 0; s < nseg; ++s) {
+            const float2 ml = stats(s, g);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!empty(ml)) v = __ldcs(reinterpret_cast<const float4 *>(p.part_o + (s * rows + g) * DH + d));
+            const float a = empty(ml) ? 0.f : expf(ml.x - ref);
+            den += ml.y * a;
+            o.x += v.x * a; o.y += v.y * a; o.z += v.z * a; o.w += v.w * a;
+        }
+        put_merged<DH>(p, g, d, o, den);
+    } else {
+        __shared__ float weight[kMaxSegs];                // e^{m - M}; -1: nothing there
+        __shared__ float2 ml[kMaxSegs];
+        __shared__ float4 part[kGroups][kT];
+        const int64_t g = blockIdx.x;
+        for (int s = threadIdx.x; s < nseg; s += kMergeThreads) ml[s] = stats(s, g);
+        __syncthreads();
+        const float sink = p.sinks ? p.sinks[g % p.H] : -INFINITY;
+        float M = sink;
+        for (int s = 0; s < nseg; ++s) M = fmaxf(M, ml[s].x);
+        const float ref = M == -INFINITY ? 0.f : M;
+        for (int s = threadIdx.x; s < nseg; s += kMergeThreads) weight[s] = empty(ml[s]) ? -1.f : expf(ml[s].x - ref);
+        __syncthreads();
+#pragma unroll 4
+        for (int s = grp; s < nseg; s += kGroups) {
+            const float a = weight[s];
+            const bool none = a < 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!none) v = __ldcs(reinterpret_cast<const float4 *>(p.part_o + (s * rows + g) * DH + d));
+            const float b = none ? 0.f : a;
+            o.x += v.x * b; o.y += v.y * b; o.z += v.z * b; o.w += v.w * b;
+        }
+        part[grp][d / 4] = o;
+        __syncthreads();
+        if (grp) return;
+        float den = expf(sink - ref);
+        for (int s = 0; s < nseg; ++s)
+            if (!(weight[s] < 0.f)) den += ml[s].y * weight[s];
+#pragma unroll
+        for (int k = 1; k < kGroups; ++k) {
+            const float4 v = part[k][d / 4];
+            o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+        }
+        put_merged<DH>(p, g, d, o, den);
     }
 }
 
@@ -257,6 +308,19 @@ cudaError_t pick(const PrefixParams &p, int tail, cudaStream_t s) {
     return cudaErrorInvalidValue;
 }
 
+template <int DH>
+cudaError_t merge(const PrefixParams &p, cudaStream_t s) {
+    const int64_t rows = (int64_t)p.B * p.L * p.H;
+    constexpr int kGroups = kMergeThreads / (DH / 4);
+    // a CTA per row while all rows are on the GPU at once, and more segments than a thread's loads in
+    // flight (at 1120 rows of 128 and 5 segments it costs 2 us)
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    if (rows <= 4 * sms && p.tail_split + p.pre_split > 4)
+        return launch_pdl(k_prefix_merge<DH, true>, dim3((unsigned)rows), dim3(kMergeThreads), 0, s, 1, p);
+    return launch_pdl(k_prefix_merge<DH, false>, dim3((unsigned)((rows + kGroups - 1) / kGroups)), dim3(kMergeThreads), 0, s, 1, p);
+}
+
 }  // namespace
 
 cudaError_t launch_prefix_simt(const PrefixParams &p, int tail, cudaStream_t s) {
@@ -264,12 +328,10 @@ cudaError_t launch_prefix_simt(const PrefixParams &p, int tail, cudaStream_t s) 
 }
 
 cudaError_t launch_prefix_merge(const PrefixParams &p, cudaStream_t s) {
-    const int64_t rows = (int64_t)p.B * p.L * p.H;
-    const int per = 128 / (p.Dh / 4);
-    const dim3 grid((unsigned)((rows + per - 1) / per));
-    if (p.Dh == 64) return launch_pdl(k_prefix_merge<64>, grid, dim3(128), 0, s, 1, p);
-    if (p.Dh == 128) return launch_pdl(k_prefix_merge<128>, grid, dim3(128), 0, s, 1, p);
-    return launch_pdl(k_prefix_merge<512>, grid, dim3(128), 0, s, 1, p);
+    if (p.tail_split + p.pre_split > kMaxSegs) return cudaErrorInvalidValue;
+    if (p.Dh == 64) return merge<64>(p, s);
+    if (p.Dh == 128) return merge<128>(p, s);
+    return merge<512>(p, s);
 }
 
 }  // namespace hisa
