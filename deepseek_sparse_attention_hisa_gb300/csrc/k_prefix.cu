@@ -83,14 +83,14 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_pref
     const T *own = static_cast<const T *>(p.pooled_kv) + x.k0 * DH;
     const T *pre = static_cast<const T *>(p.prefix_kv);
 
-    float4 acc[RP][DJ];
+    float2 acc[RP][DJ][2];
     float m[RP], l[RP];
 #pragma unroll
     for (int i = 0; i < RP; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < DJ; ++j) acc[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < DJ; ++j) acc[i][j][0] = acc[i][j][1] = make_float2(0.f, 0.f);
     }
     // a chunk waits in registers while the one before is worked on (but for 512 dims, too many)
     constexpr bool kAhead = LD <= 16;
@@ -126,9 +126,9 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_pref
         }
         __syncthreads();
         if constexpr (kAhead) fetch(c0 + kChunk);
-        float s[RP][2];
+        float2 s[RP][2];                                  // even and odd dims' sums
 #pragma unroll
-        for (int i = 0; i < RP; ++i) s[i][0] = s[i][1] = 0.f;
+        for (int i = 0; i < RP; ++i) s[i][0] = s[i][1] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int d = 0; d < DH; d += 4) {
             const float4 k0 = *reinterpret_cast<const float4 *>(skv + tc * S::kStride + d);
@@ -136,15 +136,16 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_pref
 #pragma unroll
             for (int i = 0; i < RP; ++i) {
                 const float4 a = *reinterpret_cast<const float4 *>(sq + (tr + TR * i) * S::kStride + d);
-                s[i][0] += a.x * k0.x + a.y * k0.y + a.z * k0.z + a.w * k0.w;
-                s[i][1] += a.x * k1.x + a.y * k1.y + a.z * k1.z + a.w * k1.w;
+                const float2 lo = make_float2(a.x, a.y), hi = make_float2(a.z, a.w);
+                s[i][0] = fma2(hi, make_float2(k0.z, k0.w), fma2(lo, make_float2(k0.x, k0.y), s[i][0]));
+                s[i][1] = fma2(hi, make_float2(k1.z, k1.w), fma2(lo, make_float2(k1.x, k1.y), s[i][1]));
             }
         }
         float al[RP];
 #pragma unroll
         for (int i = 0; i < RP; ++i) {
-            const float z0 = c0 + tc < e1 ? s[i][0] * p.scale : -INFINITY;
-            const float z1 = c0 + tc + 16 < e1 ? s[i][1] * p.scale : -INFINITY;
+            const float z0 = c0 + tc < e1 ? (s[i][0].x + s[i][0].y) * p.scale : -INFINITY;
+            const float z1 = c0 + tc + 16 < e1 ? (s[i][1].x + s[i][1].y) * p.scale : -INFINITY;
             float mx = fmaxf(z0, z1);
 #pragma unroll
             for (int o = 8; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -165,9 +166,12 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_pref
         for (int i = 0; i < RP; ++i)
 #pragma unroll
             for (int j = 0; j < DJ; ++j) {
-                acc[i][j].x *= al[i]; acc[i][j].y *= al[i]; acc[i][j].z *= al[i]; acc[i][j].w *= al[i];
+                acc[i][j][0] = mul2(acc[i][j][0], make_float2(al[i], al[i]));
+                acc[i][j][1] = mul2(acc[i][j][1], make_float2(al[i], al[i]));
             }
-        const int nk = e1 - c0 < kChunk ? (int)(e1 - c0) : kChunk;
+        // by fours: rows past the end are staged as zeros and weigh 0
+        const int nk = e1 - c0 < kChunk ? ((int)(e1 - c0) + 3) & ~3 : kChunk;
+#pragma unroll 4
         for (int k = 0; k < nk; ++k) {
             float w[RP];
 #pragma unroll
@@ -177,8 +181,8 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_pref
                 const float4 v = *reinterpret_cast<const float4 *>(skv + k * S::kStride + 4 * tc + 64 * j);
 #pragma unroll
                 for (int i = 0; i < RP; ++i) {
-                    acc[i][j].x += w[i] * v.x; acc[i][j].y += w[i] * v.y;
-                    acc[i][j].z += w[i] * v.z; acc[i][j].w += w[i] * v.w;
+                    acc[i][j][0] = fma2(make_float2(w[i], w[i]), make_float2(v.x, v.y), acc[i][j][0]);
+                    acc[i][j][1] = fma2(make_float2(w[i], w[i]), make_float2(v.z, v.w), acc[i][j][1]);
                 }
             }
         }
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_pref
         if (tc == 0) *reinterpret_cast<float2 *>(p.part_ml + (seg0 + g) * 2) = make_float2(m[i], l[i]);
 #pragma unroll
         for (int j = 0; j < DJ; ++j)
-            *reinterpret_cast<float4 *>(p.part_o + (seg0 + g) * DH + 4 * tc + 64 * j) = acc[i][j];
+            *reinterpret_cast<float4 *>(p.part_o + (seg0 + g) * DH + 4 * tc + 64 * j) = make_float4(acc[i][j][0].x, acc[i][j][0].y, acc[i][j][1].x, acc[i][j][1].y);
     }
     if (!tail) grid_dep_wait();
 }
