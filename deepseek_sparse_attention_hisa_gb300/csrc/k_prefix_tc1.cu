@@ -10,7 +10,7 @@
 // row exchange their maxima through shared memory. Lazy rescaling, rounding of P and sums as in
 // k_prefix_tc.cu.
 //
-// Measured: 304 query rows of 16 x 128 over 16384 shared rows 105 us with their own lists (67 us
+// Measured: 304 query rows of 16 x 128 over 16384 shared rows 105 us with their own lists (62 us
 // before or beside them on CUDA cores) and the merge.
 //
 // Warps: 0-7 softmax and epilogue, 8 loads, 9 S issue, 10 PV issue. Every wait is bounded; a
