@@ -164,6 +164,20 @@ def test_norm_rows_start_anywhere(rows, cols, off, xt, rt, ot):
             assert (buf.float() == fill).all()                   # nothing outside the rows was written
 
 
+@pytest.mark.parametrize("cols", [512, 4096, 1001])
+def test_norm_residual_sum_of_any_bits(cols):
+    # every exponent, subnormals, infinities and NaN: the sum kept is the f32 sum, rounded
+    g = torch.Generator(device="cuda").manual_seed(21)
+    x, res = (torch.randint(-32768, 32768, (300, cols), generator=g, device="cuda", dtype=torch.int32).to(torch.int16)
+              .view(torch.bfloat16) for _ in range(2))
+    near = torch.arange(300 * cols, device="cuda").view(300, cols) % 2 == 0
+    res = torch.where(near, (x.view(torch.int16) ^ -32768 ^ (res.view(torch.int16) & 1023)).view(torch.bfloat16), res)
+    want = (x.float() + res.float()).to(torch.bfloat16)
+    _, got, _ = run_norm(x, res, torch.ones(cols, device="cuda"), "bf16")
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
+
+
 def test_norm_ragged_in_place():
     x, w = randn((1500, 5003), "f32", 19), 1 + randn((5003,), "f32", 20, 0.1)
     old = x.clone()
