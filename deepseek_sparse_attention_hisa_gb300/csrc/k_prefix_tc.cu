@@ -547,12 +547,14 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                 *reinterpret_cast<float2 *>(p.part_ml + at * 2) = make_float2(m2 * kLn2, l);
             // O goes out 128 bytes of each row at a time through shared memory (P's buffers are free):
             // the two warps of 32 rows put their 64 (row, half) pieces there and write them to memory
-            // with eight neighbouring lanes per piece
+            // with eight neighbouring lanes per piece. They use the 4 KB of each P buffer that holds
+            // their own 32 rows: the CTA's other two warps may be at the next item's P already.
             const bool to_bf16 = p.pre_split == 1 && p.out_bf16;
             uint8_t *out = p.pre_split > 1 ? reinterpret_cast<uint8_t *>(p.part_o + (int64_t)x.seg * rows * kDH)
                                            : static_cast<uint8_t *>(p.out);
             const int es = to_bf16 ? 2 : 4, dims = 128 / es;
-            uint8_t *stage = smem + kOffP + (warp & 1) * kPBytes;
+            uint8_t *stage = smem + kOffP + (warp & 1) * (kPBytes / 2);
+            auto piece_at = [&](int e) { return stage + (e >> 5) * kPBytes + (e & 31) * 128; };
             const int piece = half * 32 + lane, t64 = half * 32 + lane;
 #pragma unroll 1
             for (int c = 0; c < 256; c += dims) {
@@ -575,12 +577,12 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                     }
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<uint4 *>(stage + piece * 128 + ((k ^ (piece & 7)) << 4)) =
+                        *reinterpret_cast<uint4 *>(piece_at(piece) + ((k ^ (piece & 7)) << 4)) =
                             make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<float4 *>(stage + piece * 128 + ((k ^ (piece & 7)) << 4)) =
+                        *reinterpret_cast<float4 *>(piece_at(piece) + ((k ^ (piece & 7)) << 4)) =
                             make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 }
                 asm volatile("bar.sync %0, 64;" ::"r"(pairbar) : "memory");
@@ -590,7 +592,7 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                         const int e = (t64 >> 3) + 8 * j, u = t64 & 7;            // piece, 16-byte unit
                         const int64_t g = (int64_t)row * kH + (warp & 1) * 32 + (e & 31);
                         *reinterpret_cast<uint4 *>(out + (g * kDH + (e >> 5) * 256 + c) * es + u * 16) =
-                            *reinterpret_cast<const uint4 *>(stage + e * 128 + ((u ^ (e & 7)) << 4));
+                            *reinterpret_cast<const uint4 *>(piece_at(e) + ((u ^ (e & 7)) << 4));
                     }
                 }
                 asm volatile("bar.sync %0, 64;" ::"r"(pairbar) : "memory");

@@ -551,6 +551,17 @@ def test_prefix_chained(H, dt, P, own):
     check_prefix(c, out, "bf16")
 
 
+@pytest.mark.parametrize("B,L,P,own", [(58, 4, 18796, 0), (107, 2, 22071, 3), (185, 1, 21246, 40), (43, 4, 24075, 300)])
+def test_prefix_many_items_per_pair(B, L, P, own):
+    # query rows that keep every pair of CTAs at several segments: the same bits every time
+    c = prefix_case(B, L, 64, P, [own] * B, "bf16")
+    first = run_prefix(c, "bf16")[0].clone()
+    assert torch.isfinite(first.float()).all()
+    for _ in range(8):
+        out, ws = run_prefix(c, "bf16")
+        assert torch.equal(out, first) and hb.device_status(ws) == 0
+
+
 @pytest.mark.parametrize("offset", [8, 16])
 def test_prefix_output_aligned_to_16_bytes_alone(offset):
     c = prefix_case(2, 1, 64, 100, [3, 40], "bf16")
