@@ -17,18 +17,42 @@ from . import binding as hb
 H, DH, ROPE_DIMS = 64, 512, 64
 
 
+def _expect(t, name, shape, dtype, device, layout="dense"):
+    """The kernels get pointers: whatever a tensor is not, they would read or write past its end.
+    layout: "rows" may lie further apart than they are wide (a slice of a wider tensor); "any" is
+    for what torch multiplies by."""
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: {list(shape)} {dtype} on {device} expected, "
+                         f"got {list(t.shape)} {t.dtype} on {t.device}")
+    fits = {"dense": t.is_contiguous(), "any": True,
+            "rows": t.stride(-1) == 1 and (t.shape[0] == 1 or t.stride(0) >= shape[-1])}
+    if not fits[layout]:
+        raise ValueError(f"{name}: strides {t.stride()} are not dense")
+
+
 class PrefixDecode:
     """B sequences that decode in step behind one shared prefix of P pooled rows.
 
-    weights: norm [hidden] f32, q [hidden, H * DH] bf16, kv [hidden, DH] bf16, sinks [H] f32.
+    weights: norm [hidden] f32, q [hidden, H * DH] bf16, kv [hidden, DH] bf16, sinks [H] f32 (or None).
     prefix_kv: [P, DH] bf16. start: the position of the first token decoded. steps: how many tokens
-    the window buffer takes. own_rows: pooled rows each sequence may add (append_pooled)."""
+    the window buffer takes. own_rows: pooled rows each sequence may add (append_pooled).
+    Tensors of another shape, type, device or layout raise ValueError."""
 
     def __init__(self, B, weights, prefix_kv, start, steps, own_rows=0, window=128, r=4, eps=1e-6, theta=160000.0,
                  device="cuda"):
         import torch
         self.B, self.w, self.prefix_kv, self.n = B, weights, prefix_kv, 0
         self.start, self.steps, self.hidden = start, steps, weights["norm"].numel()
+        if B < 1 or steps < 1 or own_rows < 0 or start < 0 or start + steps > 2**31:
+            raise ValueError("B and steps of 1 at least, own_rows and positions from 0 to 2^31 - 1 expected")
+        self.device = torch.empty(0, device=device).device
+        at = self.device
+        _expect(weights["norm"], "weights['norm']", (self.hidden,), torch.float32, at)
+        _expect(weights["q"], "weights['q']", (self.hidden, H * DH), torch.bfloat16, at, "any")
+        _expect(weights["kv"], "weights['kv']", (self.hidden, DH), torch.bfloat16, at, "any")
+        if weights["sinks"] is not None:
+            _expect(weights["sinks"], "weights['sinks']", (H,), torch.float32, at)
+        _expect(prefix_kv, "prefix_kv", (prefix_kv.shape[0], DH), torch.bfloat16, at)
         bf16 = dict(device=device, dtype=torch.bfloat16)
         i32 = dict(device=device, dtype=torch.int32)
         group = 128 if self.hidden % 128 == 0 else 0
@@ -60,8 +84,8 @@ class PrefixDecode:
     def append_pooled(self, rows):
         """Replaces the sequences' own pooled rows: a list of [n_b, DH] bf16 tensors."""
         import torch
-        if len(rows) != self.B or any(x.shape[0] > self.own_rows for x in rows):
-            raise ValueError("one tensor of at most own_rows rows per sequence")
+        if len(rows) != self.B or any(x.dim() != 2 or x.shape[0] > self.own_rows or x.shape[1] != DH for x in rows):
+            raise ValueError(f"one tensor of at most own_rows rows of {DH} per sequence")
         off = [0]
         for x in rows:
             self.pooled[off[-1]:off[-1] + x.shape[0]] = x
@@ -75,10 +99,16 @@ class PrefixDecode:
         return (self.codes.float().view(self.B, groups, -1) * self.scales[..., None]).view(self.B, -1).to(torch.bfloat16)
 
     def step(self, x, residual):
-        """One token per sequence: x, residual [B, hidden] bf16 (residual is updated in place).
-        Returns the combine's output [B, H, DH] bf16, turned back to position-free dims."""
+        """One token per sequence: x, residual [B, hidden] bf16, rows dense (residual is updated in place).
+        Returns the combine's output [B, H, DH] bf16, turned back to position-free dims; the next step
+        writes it anew."""
+        import torch
         if self.n == self.steps:
             raise ValueError("the window buffer is full")
+        for t, name in ((x, "x"), (residual, "residual")):
+            _expect(t, name, (self.B, self.hidden), torch.bfloat16, self.device, "rows")
+        self.norm_desc.ld_x = x.stride(0) if self.B > 1 else self.hidden
+        self.norm_desc.ld_res = residual.stride(0) if self.B > 1 else self.hidden
         hb.rms_norm(self.norm_desc, x, residual, self.w["norm"], residual, self.codes, self.scales)
         a = self.activations()
         q, kv = a @ self.w["q"], a @ self.w["kv"]
