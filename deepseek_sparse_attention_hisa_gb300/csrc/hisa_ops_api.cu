@@ -233,6 +233,15 @@ hisa_status hisa_rope(const hisa_rope_desc *d, const uint64_t *table, const int3
     if (d->heads2 && ((x2 == y2) != inplace ||
                       (inplace && (d->x2_token != d->y2_token || d->x2_head != d->y2_head))))
         return HISA_EINVAL;
+    // neighbouring rows of an output that overlap (a broadcast view rotated in place, say) would be
+    // written by several threads, in no order
+    const int64_t written = inplace ? d->rope_dims : d->D;
+    auto apart = [&](int64_t heads, int64_t token, int64_t head) {
+        return (d->tokens == 1 || token >= written) && (heads <= 1 || head >= written) &&
+               (d->tokens == 1 || heads <= 1 || token != head);
+    };
+    if (!apart(d->heads, d->y_token, d->y_head) || (d->heads2 && !apart(d->heads2, d->y2_token, d->y2_head)))
+        return HISA_EINVAL;
     RopeParams p{};
     p.heads = d->heads; p.heads_all = d->heads + d->heads2;
     p.rows = d->tokens * p.heads_all;

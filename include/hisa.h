@@ -447,7 +447,9 @@ HISA_API hisa_status hisa_rope_table(const hisa_rope_scaling *scaling, uint64_t 
  *   x, y  [tokens, heads, D] and x2, y2 [tokens, heads2, D] with the strides of the descriptor
  * y == x (same strides and dtype) rotates in place and touches the rotated dims alone; the
  * same for y2 == x2, and both are in place or neither is. Otherwise no output may overlap an
- * input. Pointers are aligned to their element. No workspace. */
+ * input. The heads of an output do not overlap one another (strides of neighbours below D, or in
+ * place below rope_dims, are refused); those of an input may (a stride of 0 repeats a row).
+ * Pointers are aligned to their element. No workspace. */
 HISA_API hisa_status hisa_rope(const hisa_rope_desc *desc, const uint64_t *table, const int32_t *pos,
                       const void *x, void *y, const void *x2, void *y2, hisa_stream_t stream);
 

@@ -129,6 +129,18 @@ def test_rope_refuses_pointers(lib):
     assert lib.hisa_rope(ctypes.byref(z), None, None, None, None, None, None, None) == hb.HISA_OK
 
 
+@pytest.mark.parametrize("inplace,kw", [
+    (True, dict(x_head=0, y_head=0)), (True, dict(x_head=63, y_head=63)), (True, dict(x_token=0, y_token=0)),
+    (True, dict(x_token=512, y_token=512)), (True, dict(x2_token=0, y2_token=0)), (False, dict(y_head=0)), (False, dict(y_head=511)),
+    (False, dict(y_token=511)), (False, dict(y_token=512)), (False, dict(heads2=2, y2_head=256, y2_token=1024)),
+    (False, dict(heads2=2, y2_head=512, y2_token=512))])
+def test_rope_refuses_rows_that_overlap(lib, inplace, kw):
+    # a broadcast view rotated in place would turn as often as it repeats, in no order
+    d = rope_desc(**kw)
+    y = FAKE if inplace else P(1 << 21)
+    assert lib.hisa_rope(ctypes.byref(d), FAKE, FAKE, FAKE, y, FAKE, y, None) == hb.HISA_EINVAL
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(B=0), hb.HISA_EINVAL), (dict(L=0), hb.HISA_EINVAL), (dict(window=-1), hb.HISA_EINVAL),
     (dict(W_max=-1), hb.HISA_EINVAL), (dict(r=0), hb.HISA_EINVAL), (dict(flags=2), hb.HISA_EINVAL),
