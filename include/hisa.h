@@ -24,7 +24,8 @@
  *    output. Set the flag only when the kernel just before the call on the stream is
  *    another libhisa call and none of those early-read inputs is written by it (the
  *    usual chain: hisa_block_filter(_append) -> hisa_select_topk -> hisa_sparse_attend).
- *    With it hisa_rms_norm reads w, and hisa_rope its table, before that kernel has completed.
+ *    With it hisa_rms_norm may read w before that kernel has completed; hisa_rope and
+ *    hisa_prefix_attend take the flag and read nothing early.
  *    Without the flag (flags = 0) a call's kernels start after the previous work on the
  *    stream has completed, as with any ordinary launch, except kernels that read nothing
  *    before the previous grid has completed (the coarse stage's pipeline, the selects and

@@ -1,11 +1,11 @@
-"""More of the operators around the step against their definitions in f64 (GB300): full batches of
-the shared-prefix combine, whose pairs of CTAs each take several items."""
+"""More of the operators around the step (GB300): full batches of the shared-prefix combine against
+f64, whose pairs of CTAs each take several items; calls made with HISA_FLAG_CHAINED."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
 from deepseek_sparse_attention_hisa_gb300 import binding as hb  # noqa: E402
-from test_gpu_ops import U, _built, half_step, prefix_case, prefix_rows, run_prefix  # noqa: E402, F401
+from test_gpu_ops import CODE, DT, U, _built, half_step, prefix_case, prefix_rows, randn, run_norm, run_prefix  # noqa: E402, F401
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -71,3 +71,46 @@ def test_prefix_one_row_outweighs_all(dt, lead):
     c["pooled"][:-3, 0] = 0.0
     out, _ = run_prefix(c, "f32")
     check_rows(c, out, "f32", [(0, 0), (1, 0), (2, 0)])
+
+
+# ------------------------------------------------------------------------------------
+# chained calls
+# ------------------------------------------------------------------------------------
+# every form of the norm: a warp per row, a CTA with one, two and four units per thread, cut units,
+# rows at different remainders, rows too long to be staged
+@pytest.mark.parametrize("cols,ld,xt,rt,ot", [(512, 512, "bf16", "bf16", "bf16"), (1001, 1001, "f32", None, "f32"),
+                                              (1000, 1003, "bf16", "f32", "bf16"), (4096, 4096, "bf16", "bf16", "e4m3"),
+                                              (7168, 7168, "bf16", "bf16", "e4m3"), (5003, 5003, "f32", "f32", "f32"),
+                                              (20000, 20000, "bf16", None, "bf16"), (9000, 9003, "bf16", None, "bf16"),
+                                              (20000, 20003, "bf16", "bf16", "bf16"), (32768, 32768, "f32", "f32", "f32")])
+def test_norm_chained(cols, ld, xt, rt, ot):
+    # a chain in which each norm reads what the one before wrote, and weights that no kernel writes
+    rows, n = 700, 3
+    w = [1 + randn((cols,), "f32", 70 + i, 0.1) for i in range(n)]
+    x0 = torch.zeros((rows, ld), device="cuda", dtype=DT[xt])
+    x0[:, :cols] = randn((rows, cols), xt, 80)
+    res = None if rt is None else randn((rows, cols), rt, 81, 2.0)
+
+    def chain(flags):
+        x, got = x0[:, :cols], []
+        for i in range(n):
+            last = i == n - 1
+            out_dt = ot if last else xt
+            out = torch.empty((rows, cols if last else ld), device="cuda", dtype=DT[out_dt])[:, :cols]
+            res_out = None if res is None else torch.empty_like(res)
+            scales = torch.empty((rows, 1), device="cuda") if out_dt == "e4m3" else None
+            got.append((x, out, res_out, scales, hb.NormDesc(
+                rows=rows, cols=cols, x_dtype=CODE[xt], res_dtype=CODE[rt or "f32"], out_dtype=CODE[out_dt], eps=1e-6,
+                ld_x=x.stride(0), ld_res=cols, ld_out=out.stride(0), flags=flags)))
+            x = out
+        torch.cuda.synchronize()                      # nothing but the chain runs from here on
+        for (a, out, res_out, scales, d), wi in zip(got, w):
+            hb.rms_norm(d, a, res, wi, res_out, out, scales)
+        torch.cuda.synchronize()
+        return [t.float() for g in got for t in g[1:4] if t is not None]
+
+    want = chain(0)
+    assert all(torch.isfinite(t).all() for t in want)
+    for _ in range(5):
+        for a, b in zip(chain(hb.FLAG_CHAINED), want):
+            assert torch.equal(a, b)
