@@ -3,7 +3,8 @@
   python examples/shared_prefix_decode.py [--batch 64] [--prefix 8192] [--hidden 4096] [--steps 16]
 
 Weights and states are random. Every step's output is compared with the same step in f64 on the
-activations that the norm produced, and the time of a step is printed.
+activations that the norm produced and the queries and KV rows rounded as the layer stores them, and
+the time of a step is printed.
 """
 import argparse
 import math
@@ -25,7 +26,7 @@ def turn(x, pos, sign):
     return torch.cat([x[..., :-ROPE_DIMS], z], -1)
 
 
-def run(batch=64, prefix=8192, hidden=4096, steps=16, own_rows=96, seed=0, say=print):
+def run(batch=64, prefix=8192, hidden=4096, steps=16, own_rows=96, seed=0, window=128, say=print):
     """Returns the largest error of any step relative to the largest output."""
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
@@ -37,7 +38,7 @@ def run(batch=64, prefix=8192, hidden=4096, steps=16, own_rows=96, seed=0, say=p
     w = {"norm": 1 + normal(hidden, std=0.1), "q": normal(hidden, H * DH, std=2 * hidden**-0.5).to(bf16),
          "kv": normal(hidden, DH, std=hidden**-0.5).to(bf16), "sinks": normal(H) + 4}
     start = 4 * prefix + 3
-    layer = PrefixDecode(batch, w, normal(prefix, DH).to(bf16), start, steps, own_rows)
+    layer = PrefixDecode(batch, w, normal(prefix, DH).to(bf16), start, steps, own_rows, window)
     own = [normal(int(torch.randint(0, own_rows + 1, (1,), generator=g, device="cuda")), DH).to(bf16) for _ in range(batch)]
     layer.append_pooled(own)
     worst, spent = 0.0, []
@@ -55,9 +56,9 @@ def run(batch=64, prefix=8192, hidden=4096, steps=16, own_rows=96, seed=0, say=p
         q = (act @ w["q"]).view(batch, H, DH).double()
         kv = (act @ w["kv"]).double()
         for s in check:
-            rows[s].append(turn(kv[s], start + n, 1))
-            v = torch.cat([torch.stack(rows[s]), layer.prefix_kv.double(), own[s].double()])
-            z = turn(q[s], start + n, 1) @ v.t() / math.sqrt(DH)
+            rows[s].append(turn(kv[s], start + n, 1).to(bf16).double())
+            v = torch.cat([torch.stack(rows[s][-window:]), layer.prefix_kv.double(), own[s].double()])
+            z = turn(q[s], start + n, 1).to(bf16).double() @ v.t() / math.sqrt(DH)
             p = torch.softmax(torch.cat([z, w["sinks"].double()[:, None]], -1), -1)[:, :-1]
             want = turn(p @ v, start + n, -1)
             worst = max(worst, ((out[s].double() - want).abs().max() / want.abs().max()).item())

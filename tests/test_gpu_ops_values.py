@@ -114,3 +114,23 @@ def test_norm_chained(cols, ld, xt, rt, ot):
     for _ in range(5):
         for a, b in zip(chain(hb.FLAG_CHAINED), want):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------------------------
+# together: a layer's decode step
+# ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("batch,prefix,hidden,steps,window", [(3, 40, 512, 12, 5), (2, 9, 1000, 140, 128)])
+def test_shared_prefix_decode_past_the_window(batch, prefix, hidden, steps, window):
+    # More tokens than the window holds. With queries and rows rounded alike, what is left are a weight's
+    # rounding and the two of the output, before and after it is turned back (a pair's two values mix:
+    # sqrt(2) of each): (1 + 2 sqrt(2)) 2^-8 of the weighted rows' magnitudes. Those of N(0, 1) rows are at
+    # most a few times the largest output, by at most the weights' effective number: below
+    # 4 (1 + 2 sqrt(2)) 2^-8 = 0.06. Dropping or keeping one row of the window too many moves a step of few
+    # rows by more.
+    import os
+    import sys
+
+    import deepseek_sparse_attention_hisa_gb300 as pkg
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(pkg.__file__))), "examples"))
+    import shared_prefix_decode
+    assert shared_prefix_decode.run(batch, prefix, hidden, steps, own_rows=3, window=window, say=lambda *_: None) < 0.06
