@@ -14,7 +14,7 @@
 // shared-memory operands; two products go into one instruction. Measured: the own lists (up to
 // 512 rows) of 300 query rows of 16 x 128 bf16 62 us; a call of 7 x 3 query rows of 16 x 128 f32 over
 // 1003 shared rows 21 us, the latency of three dependent kernels (its products would take 2.6); 76
-// query rows of 64 x 512 f32 over 1000 shared rows 386 us, 30 TFLOP/s.
+// query rows of 64 x 512 f32 over 1000 shared rows 330 us, 34 TFLOP/s.
 #include "prefix_common.cuh"
 
 namespace hisa {
@@ -93,8 +93,10 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_pref
 #pragma unroll
         for (int j = 0; j < DJ; ++j) acc[i][j][0] = acc[i][j][1] = make_float2(0.f, 0.f);
     }
-    // a chunk waits in registers while the one before is worked on (but for 512 dims, too many)
-    constexpr bool kAhead = LD <= 16;
+    // a chunk waits in registers while the one before is worked on, but for 512 dims: 64 more registers
+    // beside 128 of sums spill (76 x 64 x 512 f32 over 1000 rows 330 us without, 373 with; 304 rows over
+    // 4096 and up to 512 own 4.81 against 5.23 ms; 1 row over 8000 77 against 86 us)
+    constexpr bool kAhead = LD < 16;
     using Raw = typename std::conditional<sizeof(T) == 4, float4, uint2>::type;
     Raw raw[kAhead ? LD : 1];
     auto at = [&](int64_t c0, int i) -> const T * {
