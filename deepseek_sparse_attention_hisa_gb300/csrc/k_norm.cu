@@ -10,7 +10,10 @@
 // grid stride, and the next rows are on their way while a team reduces the current one, so the
 // barrier of the reduction does not leave the memory system idle. Sums are f32: each thread's
 // own columns in order, then a fixed tree over lanes and warps, so a row's result does not
-// depend on the other rows or on the launch.
+// depend on the other rows or on how many there are. Which columns a thread owns follows the
+// alignment of the row's start where that differs from row to row (cut units, below): the same
+// row at another remainder modulo 8 elements, or taken by another kernel for its strides, is
+// summed in another order.
 //
 // Measured: 16384 x 7168 bf16 with a bf16 residual to e4m3 by 128: 121 us, 6.8 TB/s, what a plain
 // copy reaches; without a residual 83 us, bound by its instructions (about 20 per element); 304 x

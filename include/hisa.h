@@ -417,7 +417,9 @@ HISA_API hisa_status hisa_sparse_attend(const hisa_attn_desc *desc, const void *
  *   largest magnitude a, scale = max(a, 1e-10) / 448, with scale_pow2 the next power of two at
  *   or above it, and out = y / scale rounded to nearest even (|y / scale| <= 448 but for f32
  *   rounding, which saturates). A row that holds a NaN or an infinity gives NaN where the
- *   formula does; the other rows are not affected.
+ *   formula does; the other rows are not affected. A row's bits depend on its values and
+ *   on the layout (the strides, and where the row starts modulo 8 elements in each array), not on
+ *   the other rows or their number.
  *   x            [rows, cols] x_dtype, rows ld_x apart
  *   residual     [rows, cols] res_dtype, rows ld_res apart, or NULL (h = x)
  *   w            [cols] f32

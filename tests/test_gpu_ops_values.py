@@ -116,6 +116,23 @@ def test_norm_chained(cols, ld, xt, rt, ot):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("rows,cols", [(900, 1001), (700, 5003), (500, 9001)])
+@pytest.mark.parametrize("xt,rt,ot", [("f32", None, "f32"), ("bf16", "bf16", "bf16"), ("bf16", "f32", "e4m3")])
+def test_norm_rows_of_odd_widths_do_not_depend_on_the_batch(rows, cols, xt, rt, ot):
+    # rows that start at every remainder: the same row in place, by itself and among a few
+    x, w = randn((rows, cols), xt, 90), 1 + randn((cols,), "f32", 91, 0.1)
+    res = None if rt is None else randn((rows, cols), rt, 92, 2.0)
+    whole, kept, s = run_norm(x, res, w, ot)
+    for a, n in ((0, 1), (1, 1), (rows // 2 + 3, 1), (rows - 1, 1), (5, 9), (rows - 30, 30)):
+        part = slice(a, a + n)
+        out, res_out = torch.empty_like(whole), None if res is None else torch.empty_like(res)
+        _, _, s1 = run_norm(x[part], None if res is None else res[part], w, ot, out=out[part],
+                            res_out=None if res is None else res_out[part])
+        assert torch.equal(out[part].float(), whole[part].float())
+        assert res is None or torch.equal(res_out[part], kept[part])
+        assert s is None or torch.equal(s1, s[part])
+
+
 # ------------------------------------------------------------------------------------
 # together: a layer's decode step
 # ------------------------------------------------------------------------------------
