@@ -30,8 +30,9 @@
 // 64-127 the same rows for the second half, so a row's logits sit with two threads of one lane
 // each, which exchange their maxima through shared memory. The running maximum is lazy: O and the
 // sums are rescaled only when a tile's maximum exceeds it by more than 8 (log2 units), so p <= 256.
-// P is rounded to bf16 for the second product (a relative 2^-9 per weight, of random sign); sums
-// are of the unrounded weights in f32.
+// P is rounded to bf16 for the second product, which takes bf16 operands (2^-8 of a weight at most,
+// of random sign; a second plane of the remainders would cost half the products again); sums are
+// of the unrounded weights in f32.
 //
 // Warps of each CTA: 0-3 softmax and epilogue (thread = TMEM lane), 4 and 6 loads, 5, 7 and 8
 // (of CTA 0) MMA issue for the pair. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and

@@ -13,8 +13,9 @@
  *  - Tensor pointers are DEVICE pointers owned by the caller; tensors are dense,
  *    row-major, with the shapes written beside each argument. The library never
  *    allocates, never frees, never synchronises the stream and keeps no state
- *    between calls; it is safe to call from several host threads on different
- *    streams with different workspaces.
+ *    between calls (but what the runtime said of the device and of a kernel's occupancy);
+ *    it is safe to call from several host threads on different streams with different
+ *    workspaces.
  *  - Consecutive calls may overlap, on request: a call whose descriptor sets
  *    HISA_FLAG_CHAINED launches its kernels as programmatic dependents of the
  *    kernel before it on the stream, so it may start while that kernel finishes.
@@ -416,7 +417,9 @@ HISA_API hisa_status hisa_sparse_attend(const hisa_attn_desc *desc, const void *
  *   out = y rounded once, or in 8 bits: per group of scale_group columns (the row if 0) of
  *   largest magnitude a, scale = max(a, 1e-10) / 448, with scale_pow2 the next power of two at
  *   or above it, and out = y / scale rounded to nearest even (|y / scale| <= 448 but for f32
- *   rounding, which saturates). A row that holds a NaN or an infinity gives NaN where the
+ *   rounding, which saturates). The quotient carries a few f32 roundings, so one that lies within
+ *   them of the middle between two codes may take either. Squares and products are f32 too: a row
+ *   whose squares overflow gives 0 (NaN where h w overflows as well). A row that holds a NaN or an infinity gives NaN where the
  *   formula does; the other rows are not affected. A row's bits depend on its values and
  *   on the layout (the strides, and where the row starts modulo 8 elements in each array), not on
  *   the other rows or their number.
@@ -464,6 +467,9 @@ HISA_API hisa_status hisa_rope(const hisa_rope_desc *desc, const uint64_t *table
  * value; K = V. With L > 1 own row i, at pooled position P + i, is visible iff P + i <
  * floor((t+1)/r); with L = 1 all are, as in hisa_sparse_attend. The shared rows precede every
  * sequence's own tokens and are always visible. A query row that sees nothing gives 0.
+ * Logits, maxima, sums and outputs are f32. With bf16 inputs each softmax weight is rounded to
+ * bf16 (by 2^-8 of it at most) for its product with the values, as in hisa_sparse_attend, also where
+ * out is f32; with f32 inputs it is not.
  *   q          [B, L, H, Dh]  q_dtype (already roped)
  *   local_kv   [B, W_max, Dh] kv_dtype (NULL if W_max is 0); local_len [B] int32 rows present
  *              (<= W_max); local_pos0 [B] int32 absolute position of local row 0
