@@ -30,6 +30,7 @@
 namespace hisa {
 namespace {
 
+constexpr int kMaxCols = 32768;        // what the entry point accepts
 constexpr int kMaxSmem = 220 * 1024;   // dynamic shared memory of a CTA (beside up to 5 KB declared)
 
 struct None {};                       // no residual
@@ -837,8 +838,14 @@ cudaError_t pick_units(const NormParams &p, int nvec, cudaStream_t s) {
     if (nvec <= 512) return go<k_norm_cta<XT, RT, 1, 3, RAG>>(p, up(nvec), 1, 3 * row, s, RAG ? 8 : 1);
     if (nvec <= 1024 && 4 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 2, 2, RAG>>(p, up((nvec + 1) / 2), 1, 2 * row, s, RAG ? 8 : 1);
     if (nvec <= 2048 && 3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 2, 3, RAG>>(p, up((nvec + 1) / 2), 1, 3 * row, s, RAG ? 8 : 1);
-    if (3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 4, 3, RAG>>(p, up((nvec + 3) / 4), 1, 3 * row, s, RAG ? 8 : 1);
-    return go<k_norm_cta<XT, RT, 4, 1, RAG>>(p, up((nvec + 3) / 4), 1, row, s, RAG ? 8 : 1);
+    // more than 2048 units take four per thread; what no row of these types reaches is not built
+    constexpr size_t kUnit = 8 * (kElem<XT> + kElem<RT>);
+    if constexpr (3 * 2049 * kUnit <= kMaxSmem) {
+        if (3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 4, 3, RAG>>(p, up((nvec + 3) / 4), 1, 3 * row, s, RAG ? 8 : 1);
+    }
+    if constexpr (3 * 4096 * kUnit > kMaxSmem)
+        return go<k_norm_cta<XT, RT, 4, 1, RAG>>(p, up((nvec + 3) / 4), 1, row, s, RAG ? 8 : 1);
+    return cudaErrorInvalidValue;
 }
 
 template <typename XT, typename RT>
@@ -856,7 +863,9 @@ cudaError_t pick(const NormParams &p, cudaStream_t s) {
         if (nvec <= 2048) return go<k_norm_ragged<XT, RT, 2, 2>>(p, up((nvec + 1) / 2), 1, 2 * in + out, s);
     }
     if (in + out <= kMaxSmem) return go<k_norm_ragged<XT, RT, 4, 1>>(p, up((nvec + 3) / 4), 1, in + out, s);
-    return go<k_norm_long<XT, RT>>(p, 1024, 1, 0, s);
+    // (f32 output and the kept sum at most; the bf16 rows without a residual all fit)
+    if constexpr (kMaxCols * (kElem<XT> + 2 * kElem<RT> + 4) > kMaxSmem) return go<k_norm_long<XT, RT>>(p, 1024, 1, 0, s);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
