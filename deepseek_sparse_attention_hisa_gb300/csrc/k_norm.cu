@@ -342,7 +342,7 @@ __device__ __forceinline__ void load_w(const float *base, int v, int nvec, float
 // (contiguous arrays of any width): the units are the aligned ones, unit v columns 8 v - s .. + 7,
 // the first and the last cut. A team's rows lie a multiple of 8 rows apart, so s is the team's
 // constant and the weights are shifted once. (The shift of every row through shared memory, which
-// k_norm_ragged makes, took 12.8 instead of 9.9 us for 1001 x 5003 f32.)
+// k_norm_ragged makes, takes 12.4 instead of 9.2 us for 1001 x 5003 f32.)
 __device__ __forceinline__ int shift_of(const NormParams &p, int64_t row) { return (int)((p.phase + row * p.ld_x) & 7); }
 __device__ __forceinline__ void load_w_cut(const NormParams &p, int v, int s, float (&w)[8]) {
     float a[16];                                       // columns 8 v - 8 .. 8 v + 7
@@ -633,16 +633,19 @@ __device__ __forceinline__ void write_row(uint8_t *dst, const uint8_t *staged, i
 
 // Rows that start at different remainders in different arrays, or with groups that the aligned units
 // would straddle: the same units of 8 columns, a CTA per row. Rows come in and go out through shared memory in the aligned
-// 16-byte blocks that cover them, and the shift between blocks and units is made in registers.
-template <typename XT, typename RT, int VPT, int STAGES>
+// 16-byte blocks that cover them, and the shift between blocks and units is made in registers. One
+// row is staged and the next one asked for as soon as it has been read; two (which cost CTAs per SM)
+// were no faster: 16384 x 5003 bf16 with residual 136 against 135 us, 4096 x 6001 f32 with f32 residual
+// 109 against 83, 8192 x 12001 bf16 116 against 120.
+template <typename XT, typename RT, int VPT>
 __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
-    extern __shared__ __align__(16) uint4 ring[];     // [stage]: x, residual; then out; residual_out
+    extern __shared__ __align__(16) uint4 ring[];     // x, residual, out, residual_out
     __shared__ __align__(16) float red[2][32], redm[2][32];
     const int T = blockDim.x, t = threadIdx.x, nvec = (p.cols + 7) >> 3;
     const float inv = 1.f / (float)p.cols;
     const int es = out_bytes(p);
     const size_t xb = stage_bytes(p.cols, kElem<XT>), rb = stage_bytes(p.cols, kElem<RT>);
-    uint8_t *in = reinterpret_cast<uint8_t *>(ring), *obuf = in + STAGES * (xb + rb);
+    uint8_t *in = reinterpret_cast<uint8_t *>(ring), *obuf = in + xb + rb;
     uint8_t *rbuf = obuf + stage_bytes(p.cols, es);
     if (t < 32) red[0][t] = red[1][t] = redm[0][t] = redm[1][t] = 0.f;
     constexpr bool kHoldW = VPT <= 2;
@@ -664,21 +667,19 @@ __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
     __syncthreads();
     if (p.chained) grid_dep_wait();
     grid_dep_trigger();
-    auto copy = [&](int64_t row, int stage) {
+    auto copy = [&](int64_t row) {
         if (row < p.rows) {
-            copy_row<XT>(in + stage * (xb + rb), p.x, row * p.ld_x, p.cols);
-            copy_row<RT>(in + stage * (xb + rb) + xb, p.res, row * p.ld_res, p.cols);
+            copy_row<XT>(in, p.x, row * p.ld_x, p.cols);
+            copy_row<RT>(in + xb, p.res, row * p.ld_res, p.cols);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll
-    for (int s = 0; s < STAGES; ++s) copy(blockIdx.x + (int64_t)s * gridDim.x, s);
+    copy(blockIdx.x);
     int par = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
-        const uint8_t *src = in + (STAGES == 2 ? par : 0) * (xb + rb);
         const int ax = row_offset<XT>(p.x, row * p.ld_x), ar = row_offset<RT>(p.res, row * p.ld_res);
         uint8_t *rrow = res_row<RT>(p, row), *orow = out_row(p, row);
-        asm volatile("cp.async.wait_group %0;" :: "n"(STAGES - 1) : "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();                               // every thread's blocks of this row have landed, and
                                                        // the row before has been written out
         Row<RT, VPT, true, false> m;
@@ -689,11 +690,11 @@ __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
             Raw8<RT> r;
             if (v < nvec) {
 #pragma unroll
-                for (int k = 0; k < (int)kElem<XT> / 2; ++k) x.v[k] = read_shifted(src, ax + 8 * (int)kElem<XT> * v + 16 * k);
+                for (int k = 0; k < (int)kElem<XT> / 2; ++k) x.v[k] = read_shifted(in, ax + 8 * (int)kElem<XT> * v + 16 * k);
                 if constexpr (kElem<RT> > 0) {
 #pragma unroll
                     for (int k = 0; k < (int)kElem<RT> / 2; ++k)
-                        r.v[k] = read_shifted(src + xb, ar + 8 * (int)kElem<RT> * v + 16 * k);
+                        r.v[k] = read_shifted(in + xb, ar + 8 * (int)kElem<RT> * v + 16 * k);
                 }
             }
             if constexpr (!kHoldW) load_some(v, w[0]);
@@ -709,7 +710,7 @@ __global__ void __launch_bounds__(1024, 1) k_norm_ragged(NormParams p) {
             sum = block_sum(sum, red[par]);
         }
         const float f = rsqrtf(sum * inv + p.eps);
-        copy(row + (int64_t)STAGES * gridDim.x, STAGES == 2 ? par : 0);   // every thread has read this row (the sum's barrier)
+        copy(row + gridDim.x);                         // every thread has read this row (the sum's barrier)
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (i * T + t < nvec) m.put(p, i, i * T + t, 0, 8, p.scales + row * p.groups, obuf, f);
@@ -826,8 +827,12 @@ template <typename XT, typename RT, bool RAG>
 cudaError_t pick_units(const NormParams &p, int nvec, cudaStream_t s) {
     auto up = [](int n) { return (n + 31) / 32 * 32; };
     const size_t row = (size_t)nvec * 8 * (kElem<XT> + kElem<RT>);
-    // up to 1024 columns a warp holds the row (no barrier); above, a CTA of up to 512 threads
-    // with a unit each, or of up to 1024 with two or four. Three stages are two rows in flight per
+    // up to 1024 columns a warp holds the row, with no barrier (16384 x 256 bf16 3.7 against 5.9 us by a
+    // CTA per row, 512 6.0 against 6.7; at 1024 1001 rows 3.4 against 3.6, 16384 rows 12.7 against 12.5, to
+    // 8 bits with a residual 22.0 against 20.0); above, a CTA of up to 512 threads with a unit each, or of
+    // up to 1024 with two; with four only where two do not hold the row, or its bytes leave no room for
+    // three of it (16384 x 7168 bf16 with residual to e4m3 by four 169 against 122 us, 8192 x 16384 bf16 95
+    // against 81). Three stages are two rows in flight per
     // CTA. Where two CTAs of two units per thread share an SM, one row each in flight is enough and
     // keeps what DRAM serves at once closer together (16384 x 7168 bf16 with residual to e4m3: 122
     // against 142 us; 5003 f32 with f32 residual, where three stages leave room for one CTA, 199
@@ -838,7 +843,7 @@ cudaError_t pick_units(const NormParams &p, int nvec, cudaStream_t s) {
     if (nvec <= 512) return go<k_norm_cta<XT, RT, 1, 3, RAG>>(p, up(nvec), 1, 3 * row, s, RAG ? 8 : 1);
     if (nvec <= 1024 && 4 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 2, 2, RAG>>(p, up((nvec + 1) / 2), 1, 2 * row, s, RAG ? 8 : 1);
     if (nvec <= 2048 && 3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 2, 3, RAG>>(p, up((nvec + 1) / 2), 1, 3 * row, s, RAG ? 8 : 1);
-    // more than 2048 units take four per thread; what no row of these types reaches is not built
+    // (what no row of these types reaches is not built)
     constexpr size_t kUnit = 8 * (kElem<XT> + kElem<RT>);
     if constexpr (3 * 2049 * kUnit <= kMaxSmem) {
         if (3 * row <= kMaxSmem) return go<k_norm_cta<XT, RT, 4, 3, RAG>>(p, up((nvec + 3) / 4), 1, 3 * row, s, RAG ? 8 : 1);
@@ -858,12 +863,14 @@ cudaError_t pick(const NormParams &p, cudaStream_t s) {
     const size_t in = stage_bytes(p.cols, kElem<XT>) + stage_bytes(p.cols, kElem<RT>);
     const size_t out = stage_bytes(p.cols, p.out_dtype == HISA_F32 ? 4 : (p.out_dtype == HISA_BF16 ? 2 : 1)) +
                        (p.res_out ? stage_bytes(p.cols, kElem<RT>) : 0);
-    if (2 * in + out <= kMaxSmem) {
-        if (nvec <= 512) return go<k_norm_ragged<XT, RT, 1, 2>>(p, up(nvec), 1, 2 * in + out, s);
-        if (nvec <= 2048) return go<k_norm_ragged<XT, RT, 2, 2>>(p, up((nvec + 1) / 2), 1, 2 * in + out, s);
+    if (in + out <= kMaxSmem) {
+        if (nvec <= 512) return go<k_norm_ragged<XT, RT, 1>>(p, up(nvec), 1, in + out, s);
+        if (nvec <= 2048) return go<k_norm_ragged<XT, RT, 2>>(p, up((nvec + 1) / 2), 1, in + out, s);
+        return go<k_norm_ragged<XT, RT, 4>>(p, up((nvec + 3) / 4), 1, in + out, s);
     }
-    if (in + out <= kMaxSmem) return go<k_norm_ragged<XT, RT, 4, 1>>(p, up((nvec + 3) / 4), 1, in + out, s);
-    // (f32 output and the kept sum at most; the bf16 rows without a residual all fit)
+    // (f32 output and the kept sum at most; the bf16 rows without a residual all fit.) Staged rows are
+    // taken wherever they fit: 4096 x 20011 bf16 100 us so, 312 read twice; 4096 x 13001 f32 with f32
+    // residual 189 against 372. 4096 x 32768 f32 with f32 residual, which do not: 904 us.
     if constexpr (kMaxCols * (kElem<XT> + 2 * kElem<RT> + 4) > kMaxSmem) return go<k_norm_long<XT, RT>>(p, 1024, 1, 0, s);
     return cudaErrorInvalidValue;
 }
