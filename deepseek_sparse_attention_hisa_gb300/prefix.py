@@ -35,7 +35,7 @@ class PrefixDecode:
 
     weights: norm [hidden] f32, q [hidden, H * DH] bf16, kv [hidden, DH] bf16, sinks [H] f32 (or None).
     prefix_kv: [P, DH] bf16. start: the position of the first token decoded. steps: how many tokens
-    the window buffer takes. own_rows: pooled rows each sequence may add (append_pooled).
+    the window buffer takes. own_rows: pooled rows each sequence may add (set_pooled).
     Tensors of another shape, type, device or layout raise ValueError."""
 
     def __init__(self, B, weights, prefix_kv, start, steps, own_rows=0, window=128, r=4, eps=1e-6, theta=160000.0,
@@ -70,7 +70,7 @@ class PrefixDecode:
                                      y2_token=steps * DH, y2_head=DH, **rope)
         self.back_desc = hb.RopeDesc(heads2=0, inverse=1, src_dtype=hb.HISA_BF16, dst_dtype=hb.HISA_BF16, **rope)
         self.pooled = torch.zeros((max(B * own_rows, 1), DH), **bf16)
-        self.own_rows, self.own = own_rows, [0] * B
+        self.own_rows = own_rows
         self.kv_off = torch.zeros(B + 1, device=device, dtype=torch.int64)
         self.pos = torch.full((B,), start, **i32)
         self.local_pos0 = torch.full((B,), start, **i32)
@@ -81,8 +81,8 @@ class PrefixDecode:
         self.ws = hb.alloc_workspace(hb.workspace_bytes(hb.OP_PREFIX_ATTEND, self.desc), device)
         self.out = torch.empty((B, H, DH), **bf16)
 
-    def append_pooled(self, rows):
-        """Replaces the sequences' own pooled rows: a list of [n_b, DH] bf16 tensors."""
+    def set_pooled(self, rows):
+        """The sequences' own pooled rows, in place of those they had: a list of [n_b, DH] bf16 tensors."""
         import torch
         if len(rows) != self.B or any(x.dim() != 2 or x.shape[0] > self.own_rows or x.shape[1] != DH for x in rows):
             raise ValueError(f"one tensor of at most own_rows rows of {DH} per sequence")
@@ -92,8 +92,11 @@ class PrefixDecode:
             off.append(off[-1] + x.shape[0])
         self.kv_off.copy_(torch.tensor(off, dtype=torch.int64))
 
+    append_pooled = set_pooled        # the name it had, though it never appended
+
     def activations(self):
-        """The norm's 8-bit output as bf16, for projections whose weights are bf16."""
+        """The norm's 8-bit output as bf16: what projections of 8-bit activations are given, for weights
+        in bf16."""
         import torch
         groups = self.scales.shape[1]
         return (self.codes.float().view(self.B, groups, -1) * self.scales[..., None]).view(self.B, -1).to(torch.bfloat16)

@@ -40,7 +40,7 @@ def run(batch=64, prefix=8192, hidden=4096, steps=16, own_rows=96, seed=0, windo
     start = 4 * prefix + 3
     layer = PrefixDecode(batch, w, normal(prefix, DH).to(bf16), start, steps, own_rows, window)
     own = [normal(int(torch.randint(0, own_rows + 1, (1,), generator=g, device="cuda")), DH).to(bf16) for _ in range(batch)]
-    layer.append_pooled(own)
+    layer.set_pooled(own)
     worst, spent = 0.0, []
     check = sorted({0, batch // 2, batch - 1})
     rows = {b: [] for b in check}

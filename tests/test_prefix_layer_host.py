@@ -107,3 +107,12 @@ def test_weights_may_be_transposed(calls):
     p = layer(w=weights(q=torch.zeros(H * DH, HIDDEN, dtype=BF16).t(), kv=torch.zeros(DH, HIDDEN, dtype=BF16).t()))
     p.step(rows(), rows())
     assert len(calls) == 4
+
+
+def test_pooled_rows_are_replaced(calls):
+    p = layer()
+    p.set_pooled([torch.full((2, DH), 1.0, dtype=BF16)] * 3)
+    p.set_pooled([torch.full((n, DH), 2.0, dtype=BF16) for n in (0, 1, 2)])
+    assert p.kv_off.tolist() == [0, 0, 1, 3] and (p.pooled[:3] == 2).all()
+    p.append_pooled([torch.full((1, DH), 3.0, dtype=BF16)] * 3)
+    assert p.kv_off.tolist() == [0, 1, 2, 3] and (p.pooled[:3] == 3).all()
