@@ -36,10 +36,13 @@ class PrefixDecode:
     weights: norm [hidden] f32, q [hidden, H * DH] bf16, kv [hidden, DH] bf16, sinks [H] f32 (or None).
     prefix_kv: [P, DH] bf16. start: the position of the first token decoded. steps: how many tokens
     the window buffer takes. own_rows: pooled rows each sequence may add (set_pooled).
+    recent: [n, DH] or, one's own for each sequence, [B, n, DH] bf16: the KV rows of the n positions
+    before start, rotated, as far back as the window reaches (n up to window - 1 matter); without
+    them the first tokens see nothing of the prompt but its pooled rows.
     Tensors of another shape, type, device or layout raise ValueError."""
 
     def __init__(self, B, weights, prefix_kv, start, steps, own_rows=0, window=128, r=4, eps=1e-6, theta=160000.0,
-                 device="cuda"):
+                 device="cuda", recent=None):
         import torch
         self.B, self.w, self.prefix_kv, self.n = B, weights, prefix_kv, 0
         self.start, self.steps, self.hidden = start, steps, weights["norm"].numel()
@@ -53,6 +56,11 @@ class PrefixDecode:
         if weights["sinks"] is not None:
             _expect(weights["sinks"], "weights['sinks']", (H,), torch.float32, at)
         _expect(prefix_kv, "prefix_kv", (prefix_kv.shape[0], DH), torch.bfloat16, at)
+        self.held = 0 if recent is None else recent.shape[-2]          # rows of the window buffer before start
+        if recent is not None:
+            _expect(recent, "recent", (*((B,) if recent.dim() == 3 else ()), self.held, DH), torch.bfloat16, at, "any")
+            if self.held > start:
+                raise ValueError(f"recent: {self.held} rows before position {start}")
         bf16 = dict(device=device, dtype=torch.bfloat16)
         i32 = dict(device=device, dtype=torch.int32)
         group = 128 if self.hidden % 128 == 0 else 0
@@ -62,20 +70,22 @@ class PrefixDecode:
         self.codes = torch.empty((B, self.hidden), device=device, dtype=torch.float8_e4m3fn)
         self.scales = torch.empty((B, self.hidden // (group or self.hidden)), device=device)
         self.table = hb.rope_table(hb.RopeScaling(rope_dims=ROPE_DIMS, kind=hb.ROPE_PLAIN, theta=theta), device)
-        self.local = torch.zeros((B, steps, DH), **bf16)
+        self.local = torch.zeros((B, self.held + steps, DH), **bf16)
+        if recent is not None:
+            self.local[:, :self.held] = recent
         self.q = torch.empty((B, H, DH), **bf16)
         rope = dict(tokens=B, heads=H, D=DH, rope_dims=ROPE_DIMS, rope_first=DH - ROPE_DIMS, mscale=1.0,
                     x_token=H * DH, x_head=DH, y_token=H * DH, y_head=DH)
         self.rope_desc = hb.RopeDesc(heads2=1, src_dtype=hb.HISA_BF16, dst_dtype=hb.HISA_BF16, x2_token=DH, x2_head=DH,
-                                     y2_token=steps * DH, y2_head=DH, **rope)
+                                     y2_token=self.local.stride(0), y2_head=DH, **rope)
         self.back_desc = hb.RopeDesc(heads2=0, inverse=1, src_dtype=hb.HISA_BF16, dst_dtype=hb.HISA_BF16, **rope)
         self.pooled = torch.zeros((max(B * own_rows, 1), DH), **bf16)
         self.own_rows = own_rows
         self.kv_off = torch.zeros(B + 1, device=device, dtype=torch.int64)
         self.pos = torch.full((B,), start, **i32)
-        self.local_pos0 = torch.full((B,), start, **i32)
+        self.local_pos0 = torch.full((B,), start - self.held, **i32)
         self.local_len = torch.zeros(B, **i32)
-        self.desc = hb.PrefixDesc(B=B, L=1, H=H, Dh=DH, window=window, W_max=steps, r=r, prefix_rows=prefix_kv.shape[0],
+        self.desc = hb.PrefixDesc(B=B, L=1, H=H, Dh=DH, window=window, W_max=self.local.shape[1], r=r, prefix_rows=prefix_kv.shape[0],
                                   Np_max=own_rows, kv_rows=self.pooled.shape[0], scale=0.0, q_dtype=hb.HISA_BF16,
                                   kv_dtype=hb.HISA_BF16, out_dtype=hb.HISA_BF16)
         self.ws = hb.alloc_workspace(hb.workspace_bytes(hb.OP_PREFIX_ATTEND, self.desc), device)
@@ -115,9 +125,9 @@ class PrefixDecode:
         hb.rms_norm(self.norm_desc, x, residual, self.w["norm"], residual, self.codes, self.scales)
         a = self.activations()
         q, kv = a @ self.w["q"], a @ self.w["kv"]
-        hb.rope(self.rope_desc, self.table, self.pos, q, self.q, kv, self.local[:, self.n])
+        hb.rope(self.rope_desc, self.table, self.pos, q, self.q, kv, self.local[:, self.held + self.n])
         self.n += 1
-        self.local_len.fill_(self.n)
+        self.local_len.fill_(self.held + self.n)
         hb.prefix_attend(self.desc, self.q, self.local, self.local_len, self.local_pos0, self.prefix_kv, self.pooled,
                          self.kv_off, self.w["sinks"], self.pos, self.out, self.ws)
         hb.rope(self.back_desc, self.table, self.pos, self.out, self.out)

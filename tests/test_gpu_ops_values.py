@@ -151,3 +151,30 @@ def test_shared_prefix_decode_past_the_window(batch, prefix, hidden, steps, wind
     sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(pkg.__file__))), "examples"))
     import shared_prefix_decode
     assert shared_prefix_decode.run(batch, prefix, hidden, steps, own_rows=3, window=window, say=lambda *_: None) < 0.06
+
+
+@pytest.mark.parametrize("own_each", [False, True])
+def test_decode_sees_the_prompts_last_rows(own_each):
+    # The window's rows of before the first token count as the tokens' own do; those out of the window
+    # (NaN here) do not. Queries and rows rounded alike, the bound as above.
+    from deepseek_sparse_attention_hisa_gb300.prefix import PrefixDecode
+    B, P, hidden, steps, window, held, start = 3, 20, 512, 5, 8, 11, 90
+    w = {"norm": 1 + randn((hidden,), "f32", 1, 0.1), "q": randn((hidden, 64 * 512), "bf16", 2, 2 * hidden**-0.5),
+         "kv": randn((hidden, 512), "bf16", 3, hidden**-0.5), "sinks": randn((64,), "f32", 4)}
+    recent = randn((B, held, 512) if own_each else (held, 512), "bf16", 5)
+    recent[..., :held - window + 1, :] = float("nan")
+    layer = PrefixDecode(B, w, randn((P, 512), "bf16", 6), start, steps, 0, window, recent=recent)
+    for n in range(steps):
+        out = layer.step(randn((B, hidden), "bf16", 10 + n), randn((B, hidden), "bf16", 20 + n)).double()
+        assert layer.status() == 0
+        q = layer.q.double()
+        for b in range(B):
+            lo = max(0, held + n + 1 - window)
+            v = torch.cat([layer.local[b, lo:held + n + 1].double(), layer.prefix_kv.double()])
+            p = torch.softmax(torch.cat([q[b] @ v.t() * 512**-0.5, w["sinks"].double()[:, None]], -1), -1)[:, :-1]
+            want = p @ v
+            f = 160000.0 ** (-torch.arange(32, device="cuda", dtype=torch.float64) / 32) * (start + n)
+            c, s = f.cos(), f.sin()
+            a, d = want[:, 448::2].clone(), want[:, 449::2].clone()
+            want[:, 448::2], want[:, 449::2] = a * c + d * s, d * c - a * s
+            assert ((out[b] - want).abs().max() / want.abs().max()).item() < 0.06

@@ -116,3 +116,20 @@ def test_pooled_rows_are_replaced(calls):
     assert p.kv_off.tolist() == [0, 0, 1, 3] and (p.pooled[:3] == 2).all()
     p.append_pooled([torch.full((1, DH), 3.0, dtype=BF16)] * 3)
     assert p.kv_off.tolist() == [0, 1, 2, 3] and (p.pooled[:3] == 3).all()
+
+
+@pytest.mark.parametrize("bad", [torch.zeros(3, 5, DH), torch.zeros(2, 5, DH, dtype=BF16), torch.zeros(5, DH // 2, dtype=BF16),
+                                 torch.zeros(33, DH, dtype=BF16)])
+def test_recent_rows_are_checked(calls, bad):
+    with pytest.raises(ValueError, match="recent"):
+        layer(recent=bad)                                # start is 32
+
+
+@pytest.mark.parametrize("shape", [(7, DH), (3, 7, DH)])
+def test_recent_rows_precede_the_steps(calls, shape):
+    recent = torch.arange(shape[-2]).to(BF16)[:, None].expand(shape).clone()
+    p = layer(recent=recent)
+    assert (p.local[:, :7, 0] == torch.arange(7)).all() and (p.local[:, 7:] == 0).all()
+    assert p.local_pos0.tolist() == [25] * 3 and p.desc.W_max == 11 and p.rope_desc.y2_token == 11 * DH
+    p.step(rows(), rows())
+    assert p.local_len.tolist() == [8] * 3 and p.pos.tolist() == [33] * 3
