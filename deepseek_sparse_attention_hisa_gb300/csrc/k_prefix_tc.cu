@@ -431,11 +431,7 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
                 if (ok) commit_pair(&ms->ofull);
             }
         }
-        // MMAs in flight end, and their arrivals reach both CTAs, before TMEM is freed and a CTA leaves
-        // (bounded, whatever the abort flag says)
         if (rank == 0) commit_pair(&ms->drain);
-        __syncwarp();
-        mbar_wait(&ms->drain, 0, 1u << 24);
         __syncwarp();
     } else {
         // ---------------- softmax and epilogue: thread = TMEM lane ----------------
@@ -606,6 +602,13 @@ k_prefix_tc(PrefixParams p, int items, const __grid_constant__ CUtensorMap qmap,
     if (!ok) flag(p.status, HISA_DEV_TIMEOUT);
     fence_before_sync();
     __syncthreads();
+    if (warp == kMmaWarp) {
+        // MMAs in flight end, and their arrivals reach both CTAs, before TMEM is freed and a CTA leaves
+        // (bounded, whatever the abort flag says; begun only now, since CTA 1's issuing warps have
+        // nothing to do and a wait from their start would run out in a call of a quarter second)
+        mbar_wait(&ms->drain, 0, 1u << 24);
+        __syncwarp();
+    }
     cluster_sync();                                     // no CTA leaves while the other may signal it
     if (warp == kMmaWarp) {
         fence_after_sync();

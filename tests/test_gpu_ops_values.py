@@ -57,6 +57,15 @@ def test_prefix_values_of_many_rows(B, L, H, dt):
     check_rows(c, out, "f32", [(b, j) for b in (0, 1, B // 3, B // 2, B - 2, B - 1) for j in range(L)])
 
 
+def test_prefix_call_of_a_third_of_a_second():
+    # two prompt chunks of 2048 tokens before 1.2 million shared rows: a call that outlasts the limit of a
+    # wait, with the rows' values at its start, middle and end
+    c = prefix_case(2, 2048, 64, 1_200_000, [0, 37], "bf16", seed=3)
+    out, ws = run_prefix(c, "f32")
+    assert hb.device_status(ws) == 0 and torch.isfinite(out).all()
+    check_rows(c, out, "f32", [(0, 0), (0, 1), (0, 2047), (1, 0), (1, 1023), (1, 2047)])
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("lead", [0.0, 2.0, 5.4])
 def test_prefix_one_row_outweighs_all(dt, lead):
