@@ -5,7 +5,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from deepseek_sparse_attention_hisa_gb300 import binding as hb  # noqa: E402
-from test_gpu_ops import CODE, DT, U, _built, half_step, prefix_case, prefix_rows, randn, run_norm, run_prefix  # noqa: E402, F401
+from test_gpu_ops import (CODE, DT, U, _built, check_norm, half_step, prefix_case, prefix_rows, randn, run_norm,  # noqa: E402, F401
+                          run_prefix)
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -82,6 +83,19 @@ def test_prefix_one_row_outweighs_all(dt, lead):
     check_rows(c, out, "f32", [(0, 0), (1, 0), (2, 0)])
 
 
+@pytest.mark.parametrize("H,dt", [(16, "bf16"), (16, "f32"), (64, "bf16")])
+def test_prefix_local_lengths_that_do_not_fit(H, dt):
+    # more rows than the buffer has are those it has, fewer than none are none
+    c = prefix_case(3, 1, H, 70, [5, 0, 9], dt)
+    c["local"] = randn(tuple(c["local"].shape), dt, 50)
+    want = dict(c, len=torch.tensor([c["W"], 0, c["W"]], dtype=torch.int32, device="cuda"))
+    got = dict(c, len=torch.tensor([c["W"] + 50, -3, 2**31 - 1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(run_prefix(got, "f32")[0], run_prefix(want, "f32")[0])
+    far = dict(want, pos0=torch.tensor([-(2**31), 2**31 - 1, 2**31 - 1], dtype=torch.int32, device="cuda"))
+    none = dict(want, len=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    assert torch.equal(run_prefix(far, "f32")[0], run_prefix(none, "f32")[0])
+
+
 # ------------------------------------------------------------------------------------
 # chained calls
 # ------------------------------------------------------------------------------------
@@ -123,6 +137,21 @@ def test_norm_chained(cols, ld, xt, rt, ot):
     for _ in range(5):
         for a, b in zip(chain(hb.FLAG_CHAINED), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cols,xt,rt,ot,group", [(512, "bf16", None, "bf16", 0), (1001, "f32", "f32", "f32", 0),
+                                                 (7168, "bf16", "bf16", "bf16", 0), (5003, "bf16", None, "f32", 0),
+                                                 (4096, "bf16", "bf16", "e4m3", 128), (20000, "bf16", "bf16", "e4m3", 32),
+                                                 (32768, "f32", "f32", "f32", 0)])
+@pytest.mark.parametrize("off", [1, 2])
+def test_norm_weights_start_anywhere(cols, xt, rt, ot, group, off):
+    # the values do not depend on where the weights start
+    x, w = randn((40, cols), xt, 93), 1 + randn((cols,), "f32", 94, 0.1)
+    res = None if rt is None else randn((40, cols), rt, 95)
+    at = torch.full((cols + off,), float("nan"), device="cuda")
+    at[off:] = w
+    out, kept, s = run_norm(x, res, at[off:], ot, group)
+    check_norm(x, res, w, ot, out, kept, s, group)
 
 
 @pytest.mark.parametrize("rows,cols", [(900, 1001), (700, 5003), (500, 9001)])
