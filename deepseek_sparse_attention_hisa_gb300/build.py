@@ -56,6 +56,10 @@ KERNEL_SOURCES = {
     "k_attend_tc": ["k_attend_tc.cu", "hisa_internal.cuh", "tc_ptx.cuh"],
     "k_score_pipe": ["k_score_pipe.cu", "pipe_common.cuh", "select_core.cuh", "hisa_internal.cuh", "tc_ptx.cuh"],
     "k_score_gemm": ["k_score_gemm.cu", "hisa_internal.cuh", "tc_ptx.cuh"],
+    "k_norm": ["k_norm.cu", "ops_internal.cuh", "hisa_internal.cuh", "tc_ptx.cuh"],
+    "k_rope": ["k_rope.cu", "ops_internal.cuh", "hisa_internal.cuh"],
+    "k_prefix": ["k_prefix.cu", "prefix_common.cuh", "ops_internal.cuh", "hisa_internal.cuh", "tc_ptx.cuh"],
+    "k_prefix_tc": ["k_prefix_tc.cu", "prefix_common.cuh", "ops_internal.cuh", "hisa_internal.cuh", "tc_ptx.cuh"],
 }
 
 

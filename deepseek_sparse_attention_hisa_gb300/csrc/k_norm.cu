@@ -16,8 +16,8 @@
 // summed in another order.
 //
 // Measured: 16384 x 7168 bf16 with a bf16 residual to e4m3 by 128: 121 us, 6.8 TB/s, what a plain
-// copy reaches; without a residual 83 us, bound by its instructions (about 20 per element); 304 x
-// 7168: 4.3 us, one call, launch and one round trip to memory; 1001 x 5003 f32: 9.2 us, of which 5.9 are
+// copy reaches; without a residual 82 us, bound by its instructions (about 20 per element); 304 x
+// 7168: 4 to 5 us, one call, launch and one round trip to memory; 1001 x 5003 f32: 9.2 us, of which 5.9 are
 // its bytes (two to three rows per CTA, one after another, do not hide the latency); 16384 x 5003
 // bf16 60 us, 5.5 TB/s.
 #include <cuda_fp8.h>

@@ -12,7 +12,7 @@
 // 32 list rows per chunk, 16 threads per two or four rows, scores and sums in f32 registers, the
 // running maximum and sum per row (a rescale per chunk). Bound by the FMA pipe and its
 // shared-memory operands; two products go into one instruction. Measured: the own lists (up to
-// 512 rows) of 300 query rows of 16 x 128 bf16 62 us; a call of 7 x 3 query rows of 16 x 128 f32 over
+// 512 rows) of 300 query rows of 16 x 128 bf16 63 us; a call of 7 x 3 query rows of 16 x 128 f32 over
 // 1003 shared rows 21 us, the latency of three dependent kernels (its products would take 2.6); 76
 // query rows of 64 x 512 f32 over 1000 shared rows 330 us, 34 TFLOP/s.
 #include "prefix_common.cuh"

@@ -38,10 +38,11 @@
 // (of CTA 0) MMA issue for the pair. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and
 // the CTAs leave.
 //
-// Measured (one GB300, whole call): 304 query rows over 16384 shared and up to 512 own rows 484 us,
-// 1.38 PFLOP/s (75 % of a library product's rate); 152 query rows over 65536 shared rows 820 us, 1.58;
-// 64 query rows over 8191 shared rows 82 us, where 64 of 76 pairs work and the fill, the epilogues
-// and the merge are about 20 us of it; 3 x 2 query rows over 1000: 16 us, latency.
+// Measured (one GB300, whole call): 304 query rows over 16384 shared and up to 512 own rows 485 us,
+// 1.38 PFLOP/s (71 % of a library product's rate); 152 query rows over 65536 shared rows 835 us, 1.57;
+// 4096 query rows over 8192 3.04 ms, 1.47; 64 query rows over 8191 shared rows 82 us, where 64 of 76
+// pairs work and the fill, the epilogues and the merge are about 20 us of it; 3 x 2 query rows over
+// 1000: 16 us, latency.
 #include "prefix_common.cuh"
 #include "tc_ptx.cuh"
 

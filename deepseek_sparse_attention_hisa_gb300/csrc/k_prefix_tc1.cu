@@ -10,8 +10,8 @@
 // row exchange their maxima through shared memory. Lazy rescaling, rounding of P and sums as in
 // k_prefix_tc.cu.
 //
-// Measured: 304 query rows of 16 x 128 over 16384 shared rows 105 us with their own lists (62 us
-// before or beside them on CUDA cores) and the merge.
+// Measured: 304 query rows of 16 x 128 over 16384 shared rows 61 us, 102 us with their own lists
+// (63 us before or beside them on CUDA cores), the merge included.
 //
 // Warps: 0-7 softmax and epilogue, 8 loads, 9 S issue, 10 PV issue. Every wait is bounded; a
 // timeout sets HISA_DEV_TIMEOUT and the CTA leaves.

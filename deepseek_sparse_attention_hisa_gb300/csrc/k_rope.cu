@@ -15,9 +15,11 @@
 // sixth of this rate). In place only the rotated dims move.
 //
 // Measured: 4096 tokens of 64 + 1 heads of 512, f32 to bf16: 124 us, 6.6 TB/s, 97 % of a plain
-// copy's rate; 2047 tokens of 64 x 128 bf16, 64 dims rotated in the half layout: 15.6 us (9.9 are
-// its bytes; instructions, the angles' latency and the CTAs' start bound it); the last 64 dims of
-// 304 tokens of 64 + 1 heads in place: 4.3 us per call, which its launch bounds.
+// copy's rate; 2047 tokens of 64 x 128 bf16, 64 dims rotated in the half layout: 15.5 us (9.9 are
+// its bytes; the batches of a CTA, one after another, each expose a round trip to memory, the angles'
+// latency and a barrier); the last 64 dims of 304 tokens of 64 + 1 heads in place: 4.7 to 5.2 us per
+// call, which its launch bounds. Single elements, where a boundary is no multiple of 8: 4096 x 65 x 512
+// bf16 with dims 447 to 510 rotated 470 us (89 with 448 to 511), 304 tokens in place 6.8 us.
 #include "ops_internal.cuh"
 
 namespace hisa {

@@ -34,7 +34,10 @@ class PrefixDecode:
     """B sequences that decode in step behind one shared prefix of P pooled rows.
 
     weights: norm [hidden] f32, q [hidden, H * DH] bf16, kv [hidden, DH] bf16, sinks [H] f32 (or None).
-    prefix_kv: [P, DH] bf16. start: the position of the first token decoded. steps: how many tokens
+    prefix_kv: [P, DH] bf16; the combine is dense, as a layer's is whose pooled rows are few for its
+    context (one row for 128 tokens, or the first 512 of one for 4): longer streams of a ratio-4 layer
+    select rows instead (problem.py). r is that ratio; a step's single query row per sequence sees all
+    its pooled rows, whatever r. start: the position of the first token decoded. steps: how many tokens
     the window buffer takes. own_rows: pooled rows each sequence may add (set_pooled).
     recent: [n, DH] or, one's own for each sequence, [B, n, DH] bf16: the KV rows of the n positions
     before start, rotated, as far back as the window reaches (n up to window - 1 matter); without
