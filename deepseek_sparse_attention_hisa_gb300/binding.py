@@ -16,13 +16,13 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libhisa.so")
 
 HISA_OK, HISA_EINVAL, HISA_EDTYPE, HISA_EWORKSPACE, HISA_ECUDA, HISA_EDEVICE = 0, -1, -2, -3, -4, -5
-HISA_F32, HISA_BF16, HISA_E4M3 = 0, 1, 2
+HISA_F32, HISA_BF16, HISA_E4M3, HISA_E2M1 = 0, 1, 2, 3
 ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN = range(3)
 FLAG_CHAINED = 0x1
 DEV_BAD_OFFSETS, DEV_GATE, DEV_BAD_ID, DEV_NONFINITE, DEV_BAD_BLOCK, DEV_TIMEOUT = \
     0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 FLAT_NOALLOC_MAX_SCORES = 1 << 22
-OP_COMPRESS, OP_PREFIX_ATTEND = 6, 7
+OP_COMPRESS, OP_PREFIX_ATTEND, OP_CACHE, OP_CACHE_ATTEND = 6, 7, 8, 9
 OP_INDEX_SCORES, OP_BLOCK_MEANS, OP_BLOCK_FILTER, OP_SELECT_TOPK, OP_FLAT_TOPK, OP_SPARSE_ATTEND = \
     range(6)
 
@@ -91,6 +91,35 @@ class PrefixDesc(ctypes.Structure):
                 ("q_dtype", ctypes.c_int32), ("kv_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
+class NormRopeDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("heads", ctypes.c_int32), ("heads2", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("norm", ctypes.c_int32), ("norm2", ctypes.c_int32),
+                ("rope_dims", ctypes.c_int32), ("rope_first", ctypes.c_int32), ("half", ctypes.c_int32),
+                ("src_dtype", ctypes.c_int32), ("dst_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("mscale", ctypes.c_float), ("flags", ctypes.c_int32),
+                ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64), ("y_token", ctypes.c_int64),
+                ("y_head", ctypes.c_int64), ("x2_token", ctypes.c_int64), ("x2_head", ctypes.c_int64),
+                ("y2_token", ctypes.c_int64), ("y2_head", ctypes.c_int64)]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int64), ("page_rows", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("cache_dtype", ctypes.c_int32), ("cache_scale", ctypes.c_float), ("B", ctypes.c_int32),
+                ("table_cols", ctypes.c_int32), ("rows", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("rope_dims", ctypes.c_int32), ("rope_first", ctypes.c_int32),
+                ("half", ctypes.c_int32), ("r", ctypes.c_int32), ("mscale", ctypes.c_float)]
+
+
+class CacheAttnDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("L", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("Dh", ctypes.c_int32), ("window", ctypes.c_int32), ("W_max", ctypes.c_int32),
+                ("r", ctypes.c_int32), ("k", ctypes.c_int32), ("page_rows", ctypes.c_int32),
+                ("table_cols", ctypes.c_int32), ("pages", ctypes.c_int64), ("Np_max", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("cache_scale", ctypes.c_float), ("q_dtype", ctypes.c_int32),
+                ("cache_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
 _lib = None
 _lock = threading.Lock()
 _P = ctypes.c_void_p
@@ -112,6 +141,10 @@ _SIG = {
     "hisa_rope_table": (ctypes.c_int32, [_P] * 2),
     "hisa_rope": (ctypes.c_int32, [_P] * 8),
     "hisa_prefix_attend": (ctypes.c_int32, [_P] * 12 + [ctypes.c_size_t, _P]),
+    "hisa_norm_rope": (ctypes.c_int32, [_P] * 10),
+    "hisa_cache_append": (ctypes.c_int32, [_P] * 10 + [ctypes.c_size_t, _P]),
+    "hisa_cache_read": (ctypes.c_int32, [_P] * 9 + [ctypes.c_size_t, _P]),
+    "hisa_cache_attend": (ctypes.c_int32, [_P] * 14 + [ctypes.c_size_t, _P]),
 }
 
 
@@ -299,6 +332,30 @@ def prefix_attend(desc, q, local_kv, local_len, local_pos0, prefix_kv, pooled_kv
                                     _ptr(local_pos0), _ptr(prefix_kv), _ptr(pooled_kv), _ptr(kv_off),
                                     _ptr(sinks), _ptr(t0), _ptr(out), _ptr(ws), ws.numel(),
                                     _stream(stream)), "hisa_prefix_attend")
+
+
+def norm_rope(desc, table, pos, x, w, y, x2=None, w2=None, y2=None, stream=None):
+    _check(lib().hisa_norm_rope(ctypes.byref(desc), _ptr(table), _ptr(pos), _ptr(x), _ptr(w), _ptr(y), _ptr(x2),
+                                _ptr(w2), _ptr(y2), _stream(stream)), "hisa_norm_rope")
+
+
+def cache_append(desc, table, x, w, row_off, first, page_table, cache, scales, ws, stream=None):
+    _check(lib().hisa_cache_append(ctypes.byref(desc), _ptr(table), _ptr(x), _ptr(w), _ptr(row_off), _ptr(first),
+                                   _ptr(page_table), _ptr(cache), _ptr(scales), _ptr(ws), ws.numel(),
+                                   _stream(stream)), "hisa_cache_append")
+
+
+def cache_read(desc, row_off, first, page_table, cache, scales, out, ws, out_scales=None, stream=None):
+    _check(lib().hisa_cache_read(ctypes.byref(desc), _ptr(row_off), _ptr(first), _ptr(page_table), _ptr(cache),
+                                 _ptr(scales), _ptr(out), _ptr(out_scales), _ptr(ws), ws.numel(), _stream(stream)),
+           "hisa_cache_read")
+
+
+def cache_attend(desc, q, local_kv, local_len, local_pos0, cache, scales, page_table, cache_len, I, sinks, t0, out, ws,
+                 stream=None):
+    _check(lib().hisa_cache_attend(ctypes.byref(desc), _ptr(q), _ptr(local_kv), _ptr(local_len), _ptr(local_pos0),
+                                   _ptr(cache), _ptr(scales), _ptr(page_table), _ptr(cache_len), _ptr(I), _ptr(sinks),
+                                   _ptr(t0), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), "hisa_cache_attend")
 
 
 # ----------------------------------------------------------------------------

@@ -4,7 +4,7 @@
 #include <cstring>
 
 #include "hisa_internal.cuh"
-#include "ops_internal.cuh"
+#include "cache_internal.cuh"
 
 using namespace hisa;
 
@@ -254,6 +254,8 @@ size_t hisa_workspace_bytes(int32_t op, const void *desc) {
         return check_compress_desc(static_cast<const hisa_compress_desc *>(desc)) == HISA_OK
                    ? kStatusBytes : 0;
     if (op == HISA_OP_PREFIX_ATTEND) return prefix_workspace_bytes(static_cast<const hisa_prefix_desc *>(desc));
+    if (op == HISA_OP_CACHE) return cache_workspace_bytes(static_cast<const hisa_cache_desc *>(desc));
+    if (op == HISA_OP_CACHE_ATTEND) return cache_attn_workspace_bytes(static_cast<const hisa_cache_attn_desc *>(desc));
     if (op == HISA_OP_SPARSE_ATTEND) {
         const hisa_attn_desc *d = static_cast<const hisa_attn_desc *>(desc);
         if (check_attn_desc(d) != HISA_OK) return 0;

@@ -1,0 +1,272 @@
+// Rows into and out of a cache in pages.
+//
+// A warp takes a chunk of up to 32 consecutive packed rows: each lane finds the place of one of
+// them (its sequence, its index, its page: three dependent loads, taken once per chunk), then teams of
+// lanes (head_rows.cuh) take the rows in turn, the next one on its way while one is worked on.
+// Bound by memory; a call of a few rows by its chain of loads.
+//
+// Append, 4 bits: sixteen dims are two neighbouring lanes' units. Their largest magnitude is taken by
+// the bits of |y|, so that a NaN is larger than an infinity and both than any number. The quotient
+// y / (s g) is a product with the reciprocal and one correction by its exact remainder, which gives
+// back quotients that are exactly representable (the ties between codes are such).
+#include "cache_internal.cuh"
+#include "head_rows.cuh"
+
+namespace hisa {
+namespace {
+
+// The place in the pool of packed row n and its index in its sequence; -1 if it has none.
+struct Place {
+    int64_t slot, index;
+};
+__device__ __forceinline__ Place place_of(const CacheParams &p, int64_t n) {
+    if (n < p.row_off[0] || n >= p.row_off[p.B]) return {-1, 0};       // padding
+    // sequences of equal length are found at once
+    int lo = (int)((uint64_t)n * (uint64_t)p.B / (uint64_t)p.rows);
+    if (p.row_off[lo] > n || p.row_off[lo + 1] <= n) {
+        lo = 0;
+        int hi = p.B;
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            if (p.row_off[mid] <= n) lo = mid;
+            else hi = mid;
+        }
+        if (p.row_off[lo] > n || p.row_off[lo + 1] <= n) return {-1, 0};   // not ascending: reported by check_offsets
+    }
+    const int64_t first = p.row_first[lo], index = first + n - p.row_off[lo];
+    if (first < 0 || index >= (int64_t)p.table_cols * p.page_rows) {
+        flag(p.status, HISA_DEV_BAD_OFFSETS);
+        return {-1, 0};
+    }
+    const int64_t at = index < (int64_t)1 << 32 ? (int64_t)((uint32_t)index / (uint32_t)p.page_rows) : index / p.page_rows;
+    const int64_t page = p.page_table[(int64_t)lo * p.table_cols + at];
+    if (page < 0 || page >= p.pages) {
+        flag(p.status, HISA_DEV_BAD_OFFSETS);
+        return {-1, 0};
+    }
+    return {page * p.page_rows + (index - at * p.page_rows), index};
+}
+__device__ __forceinline__ void check_offsets(const CacheParams &p) {
+    if (blockIdx.x != 0) return;
+    bool bad = p.row_off[0] < 0 || p.row_off[p.B] > p.rows;
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) bad = bad || p.row_off[b + 1] < p.row_off[b];
+    if (bad) flag(p.status, HISA_DEV_BAD_OFFSETS);
+}
+
+constexpr uint32_t kE4m3Nan = 0x7fu;
+
+// Eight f32 of a 16-dim group (the other eight in the neighbouring lane) to codes and the scale's byte.
+__device__ __forceinline__ uint32_t quantise(const float (&y)[8], float g, uint32_t &scale) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    const float a = __uint_as_float(top);
+    uint16_t two;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(a / (6.f * g)));
+    scale = top < 0x7f800000u ? (uint32_t)two & 0xffu : kE4m3Nan;
+    const float step = e4m3_to_f32(scale) * g;
+    const float inv = step > 0.f ? 1.f / step : 0.f;         // NaN: 0 too, and its codes say nothing
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        float q[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float v = y[e + k] * inv;
+            q[k] = fabsf(v) < 8.f ? fmaf(fmaf(-v, step, y[e + k]), inv, v) : v;
+        }
+        uint32_t byte;
+        asm("{.reg .b8 t, z; .reg .b16 h; cvt.rn.satfinite.e2m1x2.f32 t, %2, %1; mov.b16 h, {t, 0}; cvt.u32.u16 %0, h;}"
+            : "=r"(byte) : "f"(q[0]), "f"(q[1]));
+        w |= byte << (4 * e);
+    }
+    return w;
+}
+
+template <typename S, int U, int FORM>
+__global__ void __launch_bounds__(128) k_cache_append(CacheParams p) {
+    extern __shared__ __align__(16) float sm[];
+    const RowShape g = row_shape(sm, p.D, p.lanes, p.first, p.dims, p.half, FORM == kAny);
+    const int lane = threadIdx.x & 31, per = 32 / p.lanes, sub = lane / p.lanes;
+    const int64_t n0 = ((int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32) * p.chunk;
+    grid_dep_wait();
+    grid_dep_trigger();
+    check_offsets(p);
+    if (n0 >= p.rows) return;
+    const int n = (int)(p.rows - n0 < p.chunk ? p.rows - n0 : p.chunk);
+    Place mine{-1, 0};
+    if (lane < n) mine = place_of(p, n0 + lane);
+    const S *x = static_cast<const S *>(p.x) + n0 * p.ld;
+    RowBuf<S, U, FORM> buf = {};
+    auto slot_of = [&](int r) { return __shfl_sync(0xffffffffu, mine.slot, r & 31); };
+    int64_t slot = slot_of(sub);
+    if (sub >= n) slot = -1;
+    if (slot >= 0) buf.load(x + (int64_t)sub * p.ld, g);
+    for (int r0 = 0; r0 < n; r0 += per) {
+        const int r = r0 + sub;
+        const int64_t index = __shfl_sync(0xffffffffu, mine.index, r & 31);
+        const RowBuf<S, U, FORM> cur = buf;
+        const int64_t here = slot;
+        slot = slot_of(r + per);
+        if (r + per >= n) slot = -1;
+        if (slot >= 0) buf.load(x + (int64_t)(r + per) * p.ld, g);
+        if (p.dims) {
+            if (here >= 0) team_angles(g, p.table, index * p.r, p.mscale);
+            __syncwarp();
+        }
+        float v[U][8];
+        cur.finish(g, p.norm, p.w, p.eps, v);
+        if (p.bits4) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int u = i * g.T + g.tl;             // lanes past the row have zeros
+                uint32_t scale;
+                const uint32_t w = quantise(v[i], p.g, scale);
+                if (here < 0 || u >= g.units) continue;
+                reinterpret_cast<uint32_t *>(p.cache)[here * (p.D / 8) + u] = w;
+                if (!(u & 1)) p.scales[here * (p.D / kScaleGroup) + u / 2] = (uint8_t)scale;
+            }
+        } else if (here >= 0) {
+            __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.cache) + here * p.D;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int u = i * g.T + g.tl;
+                if (u < g.units) store8(to + 8 * u, v[i]);
+            }
+        }
+        __syncwarp();                                     // the angles are read before the next row's are written
+    }
+}
+
+// The codes of eight dims as e4m3 bytes.
+__device__ __forceinline__ uint2 codes_to_e4m3(uint32_t w) {
+    uint32_t out[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t x = w >> (16 * k);
+        // 0, 0.5, 1, 1.5 and 2, 3, 4, 6
+        out[k] = __byte_perm(0x3c383000u, 0x4c484440u, x & 0x7777u) | (x << 4 & 0x80u) | (x << 8 & 0x8000u) |
+                 (x << 12 & 0x800000u) | (x << 16 & 0x80000000u);
+    }
+    return make_uint2(out[0], out[1]);
+}
+
+template <int OUT, int U>                                  // OUT: hisa_dtype
+__global__ void __launch_bounds__(128) k_cache_read(CacheParams p) {
+    constexpr int kK = U == 1 ? 4 : 2;                     // rows in flight per team
+    const int lane = threadIdx.x & 31, T = p.lanes, per = 32 / T, sub = lane / T, tl = lane & (T - 1);
+    const int64_t n0 = ((int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32) * p.chunk;
+    const int units = p.D / 8;
+    grid_dep_wait();
+    grid_dep_trigger();
+    check_offsets(p);
+    if (n0 >= p.rows) return;
+    const int n = (int)(p.rows - n0 < p.chunk ? p.rows - n0 : p.chunk);
+    int64_t mine = -1;
+    if (lane < n) mine = place_of(p, n0 + lane).slot;
+    for (int r0 = 0; r0 < n; r0 += per * kK) {
+        int64_t slot[kK];
+        uint32_t w[kK][U], sc[kK][U];
+        uint4 raw[kK][U];
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+            const int r = r0 + k * per + sub;
+            slot[k] = __shfl_sync(0xffffffffu, mine, r & 31);
+            if (r >= n) slot[k] = -1;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int u = i * T + tl;
+                if (slot[k] < 0 || u >= units) continue;
+                if (p.bits4) {
+                    w[k][i] = reinterpret_cast<const uint32_t *>(p.cache)[slot[k] * units + u];
+                    sc[k][i] = p.scales[slot[k] * (units / 2) + u / 2];
+                } else {
+                    raw[k][i] = reinterpret_cast<const uint4 *>(p.cache)[slot[k] * units + u];
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+            if (slot[k] < 0) continue;
+            const int64_t row = n0 + r0 + k * per + sub;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int u = i * T + tl;
+                if (u >= units) continue;
+                if constexpr (OUT == HISA_E4M3) {
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + row * p.ld + 8 * u) = codes_to_e4m3(w[k][i]);
+                    if (p.out_scales && !(u & 1)) p.out_scales[row * (units / 2) + u / 2] = e4m3_to_f32(sc[k][i]) * p.g;
+                } else {
+                    float f[8];
+                    if (p.bits4) {
+                        unpack_e2m1(w[k][i], f);
+                        const float s = e4m3_to_f32(sc[k][i]) * p.g;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] *= s;
+                    } else {
+                        Raw8<__nv_bfloat16> b;
+                        b.v[0] = raw[k][i];
+                        raw_to_f32(b, f);
+                    }
+                    if constexpr (OUT == HISA_F32) {
+                        float *to = static_cast<float *>(p.out) + row * p.ld + 8 * u;
+                        if (p.out32) store_sector(to, f);
+                        else store8(to, f);
+                    } else {
+                        store8(static_cast<__nv_bfloat16 *>(p.out) + row * p.ld + 8 * u, f);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Rows of a warp's chunk: whole rounds of its teams, up to 32, while there are warps for every
+// scheduler slot of the GPU.
+int chunk_of(int64_t rows, int per, int sms) {
+    int chunk = 32;
+    while (chunk > per && rows / chunk < 32 * (int64_t)sms) chunk /= 2;
+    return chunk;
+}
+
+template <typename K>
+cudaError_t launch_rows(K kernel, CacheParams p, size_t smem, cudaStream_t s) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    p.lanes = team_lanes(p.D);
+    p.chunk = chunk_of(p.rows, 32 / p.lanes, sms);
+    const int64_t warps = (p.rows + p.chunk - 1) / p.chunk, grid = (warps + 3) / 4;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(128), smem, s, 1, p);
+}
+
+template <typename S, int U, int FORM>
+cudaError_t append_as(const CacheParams &p, cudaStream_t s) {
+    return launch_rows(k_cache_append<S, U, FORM>, p, team_smem(p.D, p.dims, 4, FORM == kAny), s);
+}
+template <typename S>
+cudaError_t append(const CacheParams &p, cudaStream_t s) {
+    const int U = team_units(p.D);
+    if (!p.wide) return U == 1 ? append_as<S, 1, kAny>(p, s) : (U == 2 ? append_as<S, 2, kAny>(p, s) : append_as<S, 4, kAny>(p, s));
+    if (p.half) return U == 1 ? append_as<S, 1, kHalves>(p, s) : (U == 2 ? append_as<S, 2, kHalves>(p, s) : append_as<S, 4, kHalves>(p, s));
+    return U == 1 ? append_as<S, 1, kPairs>(p, s) : (U == 2 ? append_as<S, 2, kPairs>(p, s) : append_as<S, 4, kPairs>(p, s));
+}
+template <int OUT>
+cudaError_t read(const CacheParams &p, cudaStream_t s) {
+    const int U = team_units(p.D);
+    return U == 1 ? launch_rows(k_cache_read<OUT, 1>, p, 0, s) : (U == 2 ? launch_rows(k_cache_read<OUT, 2>, p, 0, s) : launch_rows(k_cache_read<OUT, 4>, p, 0, s));
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheParams &p, cudaStream_t s) {
+    return p.io_dtype == HISA_BF16 ? append<__nv_bfloat16>(p, s) : append<float>(p, s);
+}
+
+cudaError_t launch_cache_read(const CacheParams &p, cudaStream_t s) {
+    if (p.io_dtype == HISA_F32) return read<HISA_F32>(p, s);
+    return p.io_dtype == HISA_BF16 ? read<HISA_BF16>(p, s) : read<HISA_E4M3>(p, s);
+}
+
+}  // namespace hisa

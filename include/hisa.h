@@ -6,8 +6,9 @@
  * pooled indexer keys, select index_topk pooled rows (flat or hierarchical), gather
  * the selected pooled KV rows and combine them with the local window and the
  * per-head sinks in one split softmax. Beside it stand the operators that a layer runs
- * around the step: hisa_rms_norm, hisa_rope and, for a batch that shares a long prefix,
- * hisa_prefix_attend.
+ * around the step: hisa_rms_norm, hisa_rope, hisa_norm_rope, for a batch that shares a long
+ * prefix hisa_prefix_attend and, for pooled rows kept in pages (bf16 or 4 bits),
+ * hisa_cache_append, hisa_cache_read and hisa_cache_attend.
  *
  * Conventions shared by every entry point
  *  - Tensor pointers are DEVICE pointers owned by the caller; tensors are dense,
@@ -25,13 +26,15 @@
  *    output. Set the flag only when the kernel just before the call on the stream is
  *    another libhisa call and none of those early-read inputs is written by it (the
  *    usual chain: hisa_block_filter(_append) -> hisa_select_topk -> hisa_sparse_attend).
- *    With it hisa_rms_norm may read w before that kernel has completed; hisa_rope and
- *    hisa_prefix_attend take the flag and read nothing early.
+ *    With it hisa_rms_norm may read w before that kernel has completed; hisa_rope,
+ *    hisa_norm_rope, hisa_prefix_attend and the hisa_cache_* calls take the flag and read
+ *    nothing early.
  *    Without the flag (flags = 0) a call's kernels start after the previous work on the
  *    stream has completed, as with any ordinary launch, except kernels that read nothing
  *    before the previous grid has completed (the coarse stage's pipeline, the selects and
  *    merges that follow a call's scoring or combine kernel, and the kernels of
- *    hisa_rms_norm, hisa_rope and hisa_prefix_attend), which may always overlap its end.
+ *    hisa_rms_norm, hisa_rope, hisa_norm_rope, hisa_prefix_attend and the hisa_cache_*
+ *    calls), which may always overlap its end.
  *  - Ragged batches: sequence b owns pooled rows [key_off[b], key_off[b+1]) of the
  *    packed key / KV arrays, so Np_b = key_off[b+1] - key_off[b] (int64, device).
  *  - Positions: t0[b] (int32, device) is the absolute token position of query
@@ -88,7 +91,9 @@ typedef enum {
 typedef enum {
     HISA_F32 = 0,
     HISA_BF16 = 1,
-    HISA_E4M3 = 2         /* 8-bit float, 4 exponent bits, largest 448 (hisa_rms_norm's out only) */
+    HISA_E4M3 = 2,        /* 8-bit float, 4 exponent bits, largest 448 (out of hisa_rms_norm and hisa_cache_read) */
+    HISA_E2M1 = 3         /* rows in 4 bits: 4-bit floats 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives, with
+                             an e4m3 scale for every 16 of them (the pages of hisa_cache_* only) */
 } hisa_dtype;
 
 /* Bits of the device status word. */
@@ -112,6 +117,8 @@ typedef enum {
 #define HISA_OP_SPARSE_ATTEND 5
 #define HISA_OP_COMPRESS      6
 #define HISA_OP_PREFIX_ATTEND 7
+#define HISA_OP_CACHE         8   /* hisa_cache_append, hisa_cache_read */
+#define HISA_OP_CACHE_ATTEND  9
 
 /* Indexer problem ([HiSA issue] "Configuration", "Flat selection", "HiSA decode path"). */
 typedef struct {
@@ -247,8 +254,79 @@ typedef struct {
     int32_t out_dtype;    /* hisa_dtype of out: HISA_F32 or HISA_BF16 */
 } hisa_prefix_desc;
 
+/* The norm of each head and rotary positions in one pass over one or two tensors of heads
+ * (hisa_norm_rope), for instance queries and the shared KV row of each token. All strides in
+ * elements; heads need not be dense. */
+typedef struct {
+    int64_t tokens;       /* >= 0 (0 = nothing to do) */
+    int32_t heads;        /* heads of x (>= 1) */
+    int32_t heads2;       /* heads of x2 (0 = no second tensor) */
+    int32_t D;            /* head dim, 2..1024 */
+    int32_t norm, norm2;  /* 1: the heads of x, of x2, are normed; 0: only turned */
+    int32_t rope_dims;    /* rotated dims, even, 0..D (0 = none: table and pos are not read) */
+    int32_t rope_first;   /* first rotated dim, 0..D - rope_dims */
+    int32_t half;         /* pairs: 0 = (2i, 2i + 1), interleaved; 1 = (i, i + rope_dims / 2), halves */
+    int32_t src_dtype;    /* hisa_dtype of x and x2: HISA_F32 or HISA_BF16 */
+    int32_t dst_dtype;    /* hisa_dtype of y and y2 */
+    float eps;            /* > 0 where something is normed */
+    float mscale;         /* factor of the rotated dims (1 = none) */
+    int32_t flags;        /* HISA_FLAG_* bits (0 = none) */
+    int64_t x_token, x_head, y_token, y_head;       /* strides of x and y */
+    int64_t x2_token, x2_head, y2_token, y2_head;   /* strides of x2 and y2 */
+} hisa_norm_rope_desc;
+
+/* Rows written to or read from a cache in pages (hisa_cache_append, hisa_cache_read). The cache is
+ * `pages` pages of page_rows rows of D dims; row p of sequence b is row p % page_rows of page
+ * page_table[b][p / page_rows]. Rows in HISA_BF16: cache [pages, page_rows, D]. Rows in HISA_E2M1:
+ * cache [pages, page_rows, D / 2] bytes, dim 2i in the low half of byte i, dim 2i + 1 in the high one
+ * (bit 3 the sign, bits 2..1 the exponent, bit 0 the mantissa), and scales
+ * [pages, page_rows, D / 16] e4m3; a dim's value is 4-bit float * scale * cache_scale. */
+typedef struct {
+    int64_t pages;        /* pages allocated (1..2^31 - 1) */
+    int32_t page_rows;    /* rows of a page, 1..65536 */
+    int32_t D;            /* dims of a row: a multiple of 16, 16..1024 */
+    int32_t cache_dtype;  /* HISA_BF16 or HISA_E2M1 */
+    float cache_scale;    /* HISA_E2M1: a factor of all rows, 2^-60..2^60 (ignored for HISA_BF16) */
+    int32_t B;            /* sequences (>= 1) */
+    int32_t table_cols;   /* page numbers of each sequence in page_table (>= 1) */
+    int64_t rows;         /* rows allocated in x (append) or out (read); >= 0 */
+    int64_t ld;           /* elements from one row of x, or out, to the next (>= D) */
+    int32_t io_dtype;     /* hisa_dtype of x: HISA_F32 or HISA_BF16; of out: those, or HISA_E4M3 */
+    int32_t flags;        /* HISA_FLAG_* bits (0 = none) */
+    /* hisa_cache_append only: */
+    int32_t norm;         /* 1: rows are normed first; 0: not */
+    float eps;            /* > 0 with norm */
+    int32_t rope_dims;    /* rotated dims, even, 0..D (0 = none: table is not read) */
+    int32_t rope_first;   /* first rotated dim, 0..D - rope_dims */
+    int32_t half;         /* pairs, as in hisa_rope_desc */
+    int32_t r;            /* row p sits at position p r (>= 1): the compress ratio, 1 for tokens */
+    float mscale;         /* factor of the rotated dims (1 = none) */
+} hisa_cache_desc;
+
+/* The combine over a cache in pages (hisa_cache_attend). */
+typedef struct {
+    int32_t B, L;         /* sequences, query rows per sequence */
+    int32_t H;            /* query heads sharing the single KV head: 8, 16 or 64 */
+    int32_t Dh;           /* head dim: 64, 128 or 512 (with H = 8, 16, 64 respectively) */
+    int32_t window;       /* sliding window: local row s is visible to t iff 0 <= t-s < window */
+    int32_t W_max;        /* rows allocated per sequence in local_kv */
+    int32_t r;            /* compress ratio, for V(t) */
+    int32_t k;            /* width of I, 0..65536 (ignored when I == NULL) */
+    int32_t page_rows;    /* rows of a page, 1..65536 */
+    int32_t table_cols;   /* page numbers of each sequence in page_table (>= 1) */
+    int64_t pages;        /* pages allocated (1..2^31 - 1) */
+    int64_t Np_max;       /* an upper bound of cache_len[b] */
+    float scale;          /* softmax scale; <= 0 selects Dh^-1/2 */
+    float cache_scale;    /* HISA_E2M1: the factor of all rows, 2^-60..2^60 (ignored for HISA_BF16) */
+    int32_t q_dtype;      /* hisa_dtype of q and local_kv: HISA_F32 or HISA_BF16 */
+    int32_t cache_dtype;  /* HISA_BF16 or HISA_E2M1 */
+    int32_t out_dtype;    /* hisa_dtype of out: HISA_F32 or HISA_BF16 */
+    int32_t flags;        /* HISA_FLAG_* bits (0 = none) */
+} hisa_cache_attn_desc;
+
 /* Bytes of device workspace `op` needs for `desc` (a hisa_index_desc* for ops 0-4,
- * a hisa_attn_desc* for op 5, a hisa_compress_desc* for op 6, a hisa_prefix_desc* for op 7). Always >= 256 for a valid desc; 0 for an invalid one.
+ * a hisa_attn_desc* for op 5, a hisa_compress_desc* for op 6, a hisa_prefix_desc* for op 7, a
+ * hisa_cache_desc* for op 8, a hisa_cache_attn_desc* for op 9). Always >= 256 for a valid desc; 0 for an invalid one.
  * Pure host arithmetic: needs no GPU. */
 HISA_API size_t hisa_workspace_bytes(int32_t op, const void *desc);
 
@@ -486,6 +564,83 @@ HISA_API hisa_status hisa_prefix_attend(const hisa_prefix_desc *desc, const void
                                const void *prefix_kv, const void *pooled_kv, const int64_t *kv_off,
                                const float *sinks, const int32_t *t0, void *out, void *ws,
                                size_t ws_bytes, hisa_stream_t stream);
+
+/* The root-mean-square norm of each head, then rotary positions, in one pass: for head row x of
+ * token n
+ *   y = x / sqrt(mean(x^2) + eps) * w   (norm / norm2; else y = x),  then
+ *   (a, b) -> mscale * (a cos A - b sin A, a sin A + b cos A),  A = pos[n] * f_i
+ * for the i-th pair of dims [rope_first, rope_first + rope_dims) of y, all in f32 and rounded once
+ * to dst_dtype. A head whose squares overflow f32 gives 0 (NaN where x w does as well); a head that holds
+ * a NaN or an infinity gives NaN where the formula does, and the other heads are not affected.
+ *   table [rope_dims / 2] uint64 (device, from hisa_rope_table);  pos [tokens] int32 (any sign);
+ *         both NULL if rope_dims is 0
+ *   x, y  [tokens, heads, D] and x2, y2 [tokens, heads2, D] with the strides of the descriptor
+ *   w, w2 [D] f32, or NULL for ones (and without the norm)
+ * y == x (same strides and dtype) works in place; the same for y2 == x2, and both are in place or
+ * neither is. Otherwise no output may overlap an input. The heads of an output do not overlap one
+ * another (strides of neighbours below D are refused); those of an input may. Pointers are aligned to
+ * their element; fastest where every head starts at a multiple of 8 elements and rope_first and
+ * rope_dims (with halves rope_dims / 2) are such. No workspace. */
+HISA_API hisa_status hisa_norm_rope(const hisa_norm_rope_desc *desc, const uint64_t *table, const int32_t *pos,
+                           const void *x, const float *w, void *y, const void *x2, const float *w2,
+                           void *y2, hisa_stream_t stream);
+
+/* Appends rows to a cache in pages. Packed row n of x, row_off[b] <= n < row_off[b+1], becomes row
+ * p = first[b] + n - row_off[b] of sequence b: normed and turned as by hisa_norm_rope (the position is
+ * p r, any 64-bit number), rounded once to bf16, or in 4 bits: for each 16 dims of largest magnitude a
+ *   s = a / (6 cache_scale) rounded to e4m3 (at most 448), each dim y / (s cache_scale) rounded to
+ *   nearest even (at most 6), 0 where s is 0.
+ * The quotients carry an f32 rounding or two, so one that lies within them of the middle between two
+ * codes may take either. Sixteen dims that hold a NaN or an infinity get the scale NaN.
+ *   table      [rope_dims / 2] uint64 (NULL if rope_dims is 0)
+ *   x          [rows, D] io_dtype, rows ld apart;  w [D] f32 or NULL for ones
+ *   row_off    [B+1] int64, ascending;  first [B] int32 (>= 0);  page_table [B, table_cols] int32
+ *   cache, scales  as hisa_cache_desc says (scales NULL for HISA_BF16), 16-byte aligned
+ * Rows of x before row_off[0] or from row_off[B] on are not read. A row whose place does not fit
+ * (offsets that are not ascending or pass `rows`, an index past table_cols pages, a page outside
+ * [0, pages)) is left out and sets HISA_DEV_BAD_OFFSETS. No two rows of a call may have the same
+ * place. ws holds the status word (hisa_workspace_bytes(HISA_OP_CACHE, desc)). */
+HISA_API hisa_status hisa_cache_append(const hisa_cache_desc *desc, const uint64_t *table, const void *x,
+                              const float *w, const int64_t *row_off, const int32_t *first,
+                              const int32_t *page_table, void *cache, void *scales, void *ws,
+                              size_t ws_bytes, hisa_stream_t stream);
+
+/* Reads rows out of a cache in pages: packed row n of out, row_off[b] <= n < row_off[b+1], is row
+ * first[b] + n - row_off[b] of sequence b, as f32 or bf16 (the value, rounded once), or with
+ * HISA_E2M1 pages as HISA_E4M3: the 4-bit floats as 8-bit ones, without their scales.
+ *   out        [rows, D] io_dtype, rows ld apart, 16-byte aligned, ld a multiple of 8 (of 16 for HISA_E4M3)
+ *   out_scales [rows, D / 16] f32 dense: HISA_E4M3 only, scale * cache_scale; or NULL
+ * The other arguments and what a row that does not fit does are as in hisa_cache_append; such rows of
+ * out, and those before row_off[0] and from row_off[B] on, stay as they were. */
+HISA_API hisa_status hisa_cache_read(const hisa_cache_desc *desc, const int64_t *row_off, const int32_t *first,
+                            const int32_t *page_table, const void *cache, const void *scales, void *out,
+                            float *out_scales, void *ws, size_t ws_bytes, hisa_stream_t stream);
+
+/* The combine of hisa_sparse_attend over pooled rows kept in pages: for query row j of sequence b at
+ * t = t0[b] + j one softmax over the visible local rows, the pooled rows named by I (or all
+ * cache_len[b] of them, I = NULL) and the per-head sink, which joins the normaliser and carries no
+ * value; K = V. With L > 1 pooled row i is visible iff i < floor((t+1)/r); with L = 1 all are. A query
+ * row that sees nothing gives 0. Logits, maxima and sums are f32; with bf16 q of 64 heads of 512 dims
+ * each softmax weight is rounded to bf16 (by 2^-8 of it at most) for its product with the values, also where out
+ * is f32; otherwise it is not.
+ *   q          [B, L, H, Dh]  q_dtype (already roped)
+ *   local_kv   [B, W_max, Dh] q_dtype (NULL if W_max is 0); local_len [B] int32 rows present
+ *              (<= W_max); local_pos0 [B] int32 absolute position of local row 0
+ *   cache, scales  as hisa_cache_desc says with D = Dh (scales NULL for HISA_BF16), 16-byte aligned
+ *   page_table [B, table_cols] int32;  cache_len [B] int32: pooled rows of each sequence
+ *   I          [B, L, k] int32 pooled ids (-1 = skip), or NULL for all
+ *   sinks      [H] f32, or NULL for none (-inf is none for that head);  t0 [B] int32
+ *   out        [B, L, H, Dh] out_dtype, 16-byte aligned
+ * Two sequences may share pages. What rows hold that a query row does not see has no effect on it.
+ * A cache_len that is negative, above Np_max or above table_cols pages sets HISA_DEV_BAD_OFFSETS and
+ * that sequence has no pooled rows; a page outside [0, pages) sets it and its rows are skipped; an id
+ * outside [-1, cache_len[b]) sets HISA_DEV_BAD_ID and is skipped. A workspace that serves
+ * several batch sizes takes the maximum of hisa_workspace_bytes over them. */
+HISA_API hisa_status hisa_cache_attend(const hisa_cache_attn_desc *desc, const void *q, const void *local_kv,
+                              const int32_t *local_len, const int32_t *local_pos0, const void *cache,
+                              const void *scales, const int32_t *page_table, const int32_t *cache_len,
+                              const int32_t *I, const float *sinks, const int32_t *t0, void *out,
+                              void *ws, size_t ws_bytes, hisa_stream_t stream);
 
 #ifdef __cplusplus
 }
