@@ -68,9 +68,13 @@ struct CacheAttnParams {
     void *out;
     int q_bf16, bits4, out_bf16;
     int splits, split_rows;   // CUDA-core kernel: ranges of a query row's list, rows of each
+    int ctas, whole, least;   // tensor-core kernel: CTAs; whole rows in turn; else the fewest tiles of a span
+    void *cuts;               // its rows that spans cut, one entry per CTA
     float *part_o, *part_ml;  // partial sums
     uint32_t *status;
 };
+constexpr int kCacheCtas = kSmTarget;     // most CTAs of the tensor-core kernel
+constexpr size_t kCutBytes = 32;
 
 // What a query row sees: local rows [lo, lo + nloc) of its window buffer, then npool entries of its
 // list of pooled rows (ids of I, or rows 0, 1, ...), of which those below V are visible.
@@ -149,5 +153,8 @@ cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheParams &p, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheParams &p, cudaStream_t s);
 cudaError_t launch_cache_simt(const CacheAttnParams &p, cudaStream_t s);
+// The combine on the tensor cores (64 bf16 heads of 512 dims).
+bool cache_tc_supported(int H, int Dh, int q_bf16);
+cudaError_t launch_cache_tc(const CacheAttnParams &p, cudaStream_t s);
 
 }  // namespace hisa

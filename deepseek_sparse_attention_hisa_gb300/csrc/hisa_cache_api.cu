@@ -86,6 +86,25 @@ void attn_plan(const hisa_cache_attn_desc *d, int64_t pool, CacheAttnParams *p) 
     p->split_rows = (int)(per > 0 ? per : 32);
     p->splits = (int)(list > 0 ? (list + p->split_rows - 1) / p->split_rows : 1);
 }
+// The tensor-core kernel's CTAs: one per SM, or one for every few tiles of 64 rows that there can be.
+// Whole rows where the lists are all as long (ids: k each) and leave few SMs idle in the last round: no
+// sums go through memory (304 x 640 rows: see k_cache_tc.cu).
+void tc_plan(const hisa_cache_attn_desc *d, int64_t pool, bool ids, CacheAttnParams *p) {
+    const int64_t local = d->W_max < d->window ? d->W_max : d->window;
+    int64_t tiles = (local + 63) / 64 + (pool + 63) / 64;
+    tiles = tiles < 1 ? 1 : tiles;
+    const int64_t rows = (int64_t)d->B * d->L, rounds = (rows + kCacheCtas - 1) / kCacheCtas;
+    p->least = 3;
+    p->whole = ids && rows * 8 >= rounds * kCacheCtas * 7;
+    int64_t n = p->whole ? rows : (rows * tiles + p->least - 1) / p->least;
+    p->ctas = (int)(n > kCacheCtas ? kCacheCtas : n);
+}
+size_t tc_bytes(const hisa_cache_attn_desc *d, int64_t pool, bool ids) {
+    CacheAttnParams p{};
+    tc_plan(d, pool, ids, &p);
+    const size_t places = p.whole ? 0 : (size_t)2 * p.ctas;
+    return kStatusBytes + round_up(p.ctas * kCutBytes) + round_up(places * d->H * 2 * sizeof(float)) + places * d->H * d->Dh * sizeof(float);
+}
 size_t attn_sums(const hisa_cache_attn_desc *d, const CacheAttnParams &p) { return (size_t)d->B * d->L * d->H * p.splits; }
 size_t attn_bytes(const hisa_cache_attn_desc *d, int64_t pool) {
     CacheAttnParams p{};
@@ -124,7 +143,9 @@ size_t cache_workspace_bytes(const hisa_cache_desc *d) { return check_cache_desc
 
 size_t cache_attn_workspace_bytes(const hisa_cache_attn_desc *d) {
     if (check_cache_attn_desc(d) != HISA_OK) return 0;
-    const size_t all = attn_bytes(d, d->Np_max), some = attn_bytes(d, d->k);
+    const bool tc = cache_tc_supported(d->H, d->Dh, d->q_dtype == HISA_BF16);
+    const size_t all = tc ? tc_bytes(d, d->Np_max, false) : attn_bytes(d, d->Np_max);
+    const size_t some = tc ? tc_bytes(d, d->k, true) : attn_bytes(d, d->k);
     return all > some ? all : some;
 }
 
@@ -239,9 +260,17 @@ hisa_status hisa_cache_attend(const hisa_cache_attn_desc *d, const void *q, cons
     p.page_table = page_table; p.cache_len = cache_len; p.I = I; p.sinks = sinks; p.t0 = t0; p.out = out;
     p.q_bf16 = d->q_dtype == HISA_BF16; p.out_bf16 = d->out_dtype == HISA_BF16;
     p.status = static_cast<uint32_t *>(ws);
+    char *base = static_cast<char *>(ws) + kStatusBytes;
+    if (cache_tc_supported(d->H, d->Dh, p.q_bf16)) {
+        tc_plan(d, I ? d->k : d->Np_max, I != nullptr, &p);
+        p.cuts = base;
+        base += round_up(p.ctas * kCutBytes);
+        p.part_ml = reinterpret_cast<float *>(base);
+        p.part_o = reinterpret_cast<float *>(base + round_up((size_t)2 * p.ctas * d->H * 2 * sizeof(float)));
+        return from_cuda(launch_cache_tc(p, reinterpret_cast<cudaStream_t>(stream)));
+    }
     attn_plan(d, I ? d->k : d->Np_max, &p);
     const size_t rows = attn_sums(d, p);
-    char *base = static_cast<char *>(ws) + kStatusBytes;
     p.part_o = reinterpret_cast<float *>(base);
     p.part_ml = reinterpret_cast<float *>(base + round_up(rows * d->Dh * sizeof(float)));
     return from_cuda(launch_cache_simt(p, reinterpret_cast<cudaStream_t>(stream)));

@@ -183,7 +183,11 @@ cudaError_t types(const CacheAttnParams &p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_cache_simt(const CacheAttnParams &p, cudaStream_t s) {
-    cudaError_t e = p.Dh == 64 ? types<8, 64>(p, s) : (p.Dh == 128 ? types<16, 128>(p, s) : types<64, 512>(p, s));
+    cudaError_t e;
+    if (p.Dh == 64) e = types<8, 64>(p, s);
+    else if (p.Dh == 128) e = types<16, 128>(p, s);
+    else if (p.q_bf16) return cudaErrorInvalidValue;      // k_cache_tc.cu
+    else e = p.bits4 ? go<64, 512, float, true>(p, s) : go<64, 512, float, false>(p, s);
     if (e != cudaSuccess) return e;
     PrefixParams m{};
     m.B = p.B; m.L = p.L; m.H = p.H; m.Dh = p.Dh;
