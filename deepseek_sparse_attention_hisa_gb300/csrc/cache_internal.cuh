@@ -68,6 +68,7 @@ struct CacheAttnParams {
     void *out;
     int q_bf16, bits4, out_bf16;
     int splits, split_rows;   // CUDA-core kernel: ranges of a query row's list, rows of each
+    int cache32;              // rows in 4 bits start at multiples of 32 bytes
     int ctas, whole, least;   // tensor-core kernel: CTAs; whole rows in turn; else the fewest tiles of a span
     void *cuts;               // its rows that spans cut, one entry per CTA
     float *part_o, *part_ml;  // partial sums
@@ -83,8 +84,8 @@ struct CacheRow {
     int nloc, npool;
 };
 __device__ __forceinline__ CacheRow cache_row(const CacheAttnParams &p, int64_t row, bool report) {
-    const int b = (int)(row / p.L);
-    const int64_t t = (int64_t)p.t0[b] + row % p.L;
+    const uint32_t b = (uint32_t)row / (uint32_t)p.L;     // B L fits 32 bits
+    const int64_t t = (int64_t)p.t0[b] + ((uint32_t)row - b * (uint32_t)p.L);
     CacheRow x{0, 0, 0, 0, 0};
     if (p.W_max > 0) {
         const int64_t in = p.local_len[b], nl = in < 0 ? 0 : (in > p.W_max ? p.W_max : in);
@@ -102,7 +103,11 @@ __device__ __forceinline__ CacheRow cache_row(const CacheAttnParams &p, int64_t 
         if (report) flag(p.status, HISA_DEV_BAD_OFFSETS);
         x.len = 0;
     }
-    x.V = p.L > 1 ? visible_len(t, p.r, x.len) : x.len;
+    x.V = x.len;
+    if (p.L > 1) {
+        const int64_t v = t + 1 < 0 ? 0 : (int64_t)((uint32_t)(t + 1) / (uint32_t)p.r);   // t + 1 fits 32 bits: L < 2^25
+        x.V = v < x.len ? v : x.len;
+    }
     x.npool = p.I ? p.k : (int)x.V;
     return x;
 }
@@ -119,7 +124,7 @@ __device__ __forceinline__ int64_t cache_slot(const CacheAttnParams &p, int64_t 
         if (id < 0 || id >= x.V) return -1;
     }
     const uint32_t at = (uint32_t)id / (uint32_t)p.page_rows;
-    const int64_t page = p.page_table[(row / p.L) * p.table_cols + at];
+    const int64_t page = p.page_table[(int64_t)((uint32_t)row / (uint32_t)p.L) * p.table_cols + at];
     if (page < 0 || page >= p.pages) {
         flag(p.status, HISA_DEV_BAD_OFFSETS);
         return -1;

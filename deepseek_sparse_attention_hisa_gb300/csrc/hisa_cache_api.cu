@@ -256,7 +256,7 @@ hisa_status hisa_cache_attend(const hisa_cache_attn_desc *d, const void *q, cons
     p.bits4 = d->cache_dtype == HISA_E2M1;
     p.g = p.bits4 ? d->cache_scale : 1.f;
     p.q = q; p.local_kv = local_kv; p.local_len = local_len; p.local_pos0 = local_pos0;
-    p.cache = cache; p.scales = static_cast<const uint8_t *>(scales);
+    p.cache = cache; p.scales = static_cast<const uint8_t *>(scales); p.cache32 = aligned(cache, 32);
     p.page_table = page_table; p.cache_len = cache_len; p.I = I; p.sinks = sinks; p.t0 = t0; p.out = out;
     p.q_bf16 = d->q_dtype == HISA_BF16; p.out_bf16 = d->out_dtype == HISA_BF16;
     p.status = static_cast<uint32_t *>(ws);

@@ -21,11 +21,12 @@
 // places per CTA, and k_cache_join adds them up.
 //
 // The running maximum m is lazy: O^T and l are rescaled only when a tile's maximum exceeds m by more
-// than 8 (log2 units), so p <= 256.
+// than 64 (log2 units). bf16 has the exponents of f32, so a weight of 2^64 is held as exactly as one of 1, and
+// sums of 2^31 such weights and products stay far below 2^127; a rescaling costs as much as a tile.
 //
-// Warps: 0-3 softmax, 4 S issue (and q by TMA), 5 PV issue, 6-9 epilogue, 10-17 rows. A lane of the row
-// warps has one row of the tile and a quarter of its dims: the row's id is fetched three tiles ahead, its page
-// two, its codes one. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and the CTA leaves.
+// Warps: 0-7 softmax and epilogue, 8 S issue (and q by TMA), 9 PV issue, 10-11 places of the rows (ids,
+// pages), up to four tiles ahead, 12-27 rows: a lane has a row of the tile and an eighth of its dims, the next
+// tile's codes on their way while it writes this one's. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and the CTA leaves.
 #include "cache_internal.cuh"
 #include "prefix_common.cuh"
 
@@ -35,28 +36,30 @@ namespace {
 using namespace tc;
 
 constexpr int kH = 64, kDH = 512, kT = 64;              // heads, dims, rows of a tile
-constexpr int kSoftWarps = 4, kSWarp = 4, kPvWarp = 5, kEpiWarp0 = 6, kRowWarp0 = 10, kRowWarps = 8;
+constexpr int kSoftWarps = 8, kSWarp = 8, kPvWarp = 9, kIndexWarp0 = 10, kRowWarp0 = 12, kRowWarps = 16;
 constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
-static_assert(kEpiWarp0 % 4 == 2 && kRowWarp0 == kEpiWarp0 + 4, "each epilogue warp has a TMEM quadrant of its own");
-constexpr int kSlots = 2, kBufs = 2;
+constexpr int kSlots = 2, kBufs = 2, kPlaces = 8;        // staged tiles; S and P buffers; tiles whose rows' places are known
 constexpr uint32_t kChunk = 64 * 128;                   // 64 rows x 64 dims, 128-byte swizzle
 constexpr uint32_t kTile = 8 * kChunk;
 constexpr uint32_t kOffQ = 0, kOffKV = kTile, kOffP = kOffKV + kSlots * kTile, kOffMisc = kOffP + kBufs * kChunk;
 constexpr uint32_t kColS = 0, kColO = 128, kTmemCols = 512;
-constexpr float kLog2e = 1.4426950408889634f, kLazy = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLazy = 64.0f;
 constexpr int kBarSoft = 1;
 
 struct Misc {
-    uint64_t qfull, qfree, full[kSlots], empty[kSlots], sfull[kBufs], sfree[kBufs], pfull[kBufs], pfree[kBufs], ofull, ofree, stat,
-        drain;
-    uint64_t mask[kSlots];                              // rows of a tile that are seen
+    uint64_t qfull, qfree, full[kSlots], empty[kSlots], sfull[kBufs], sfree[kBufs], pfull[kBufs], pfree[kBufs], ofull, ofree, drain;
+    uint64_t ifull[kPlaces], ifree[kPlaces];
+    int64_t place[kPlaces][kT];                         // row of local_kv or of the pool; -1: not seen
+    uint32_t mask[kPlaces][2];                          // rows of a tile that are seen
+    int kind[kPlaces];                                  // TileKind
     uint32_t tmem;
     int abort;
     int t0, groups;                                     // the span: first tile of its first row; CTAs that have one
     int64_t row, left, total;                           // first row, tiles; all rows' tiles
     int64_t sums[kThreads / 32];
-    float alpha[2][kH];
-    float stat_m[kH], stat_l[kH], factor[kH];
+    float alpha[kH];
+    float top[4][kH], sum[4][kH];                       // of the four threads of a head
+    __align__(16) float factor[kH];
 };
 constexpr uint32_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -73,6 +76,12 @@ __device__ __forceinline__ int local_tiles(const CacheRow &x) { return (x.nloc +
 __device__ __forceinline__ int tiles_of(const CacheRow &x) {
     const int n = local_tiles(x) + (x.npool + kT - 1) / kT;
     return n > 0 ? n : 1;                               // a row that sees nothing has a tile of nothing
+}
+
+// The first tile of CTA c's span: c total / groups (a 64-bit division takes a few hundred cycles).
+__device__ __forceinline__ int64_t span_start(int c, int64_t total, int groups) {
+    if (total < (int64_t)1 << 24) return (uint32_t)c * (uint32_t)total / (uint32_t)groups;
+    return c * total / groups;
 }
 
 // What a CTA does, in order: items, each a range of one query row's tiles.
@@ -109,32 +118,21 @@ __device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap *map, int3
                  "[%0], [%1, {%2, %3, %4}], [%5];"
                  :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void prefetch_q(const CUtensorMap *map, int32_t row) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+                 :: "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" :: "r"(smem_u32(bar)), "r"(n) : "memory");
 }
-// Lanes 0-15 read columns [c, c + 32) of TMEM lanes base + 0 .. 15, lanes 16-31 columns [c + 32, c + 64) of
-// the same ones (an M = 64 accumulator's rows live in lanes 0-15 of each quadrant).
-__device__ __forceinline__ void tmem_ld32_x2(uint32_t addr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
-                 "%29,%30,%31}, [%32], 32;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-                   "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(addr));
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-// Barriers of the four softmax warps: true on all iff v is on one (any), on all (all).
+// Barriers of the softmax warps: true on all iff v is on one (any), on all (all).
 __device__ __forceinline__ bool soft_any(bool v) {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r) : "r"((uint32_t)v), "n"(kBarSoft) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)v), "n"(kBarSoft), "n"(32 * kSoftWarps) : "memory");
     return r != 0u;
 }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync %0, %1;" :: "n"(kBarSoft), "n"(32 * kSoftWarps) : "memory"); }
 __device__ __forceinline__ bool soft_all(bool v) { return !soft_any(!v); }
 
 // Eight codes times a scale (as bf16, times 2^118, in both halves of s), in bf16, times 2^-8.
@@ -166,25 +164,33 @@ __device__ __forceinline__ uint2 scales_to_bf16(uint32_t two) {
     return r;
 }
 
-// The tiles of a CTA, as one lane of the row warps sees them: its own row of each.
+// One elected lane of a warp (the same one every time).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+// The product of mma_bf16_warp, issued by the lane that holds e = 1. A descriptor is passed as its two words, of
+// which only the lower (the address) changes from product to product: what a product costs its issuing warp in
+// instructions, and not the tensor core, bounds a tile (an election and two 64-bit sums each: 39 cycles a
+// product of M = 64, N = 64; so: see below).
+__device__ __forceinline__ void mma_elected(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                            uint32_t accumulate, uint32_t e) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+                 "setp.ne.u32 p, %6, 0;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}"
+                 :: "r"(d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(e) : "memory");
+}
+
 enum TileKind : int { kEnd = 0, kLocal = 1, kPool = 2 };
-struct Wanted {                                          // its id is on its way
-    int kind, id, V, len;
-    const int32_t *table;                                // the sequence's pages
-    int64_t place;                                       // kLocal: the row of local_kv
+struct Codes {                                           // of 64 dims
+    uint4 c[2];
+    uint32_t s;
 };
-struct Paged {                                           // its page is on its way
-    int kind, page, rest;                                // row of the page; -1: none
-    int64_t place;
-};
-struct Placed {
-    int kind;
-    int64_t place;                                       // row of local_kv or of the pool; -1: not seen
-};
-struct Codes {
-    uint4 c[4];
-    uint32_t s[4];
-};
+__device__ __forceinline__ void load32(const uint8_t *from, uint4 &a, uint4 &b) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "l"(from));
+}
 
 template <bool BITS4>
 __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant__ CUtensorMap qmap, CacheAttnParams p) {
@@ -201,16 +207,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
         mbar_init(&misc->qfull, 1);
         mbar_init(&misc->qfree, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&misc->full[i], 33 * kRowWarps);
+            mbar_init(&misc->full[i], 32 * kRowWarps);
             mbar_init(&misc->empty[i], 1);
             mbar_init(&misc->sfull[i], 1);
             mbar_init(&misc->sfree[i], 32 * kSoftWarps);
             mbar_init(&misc->pfull[i], 32 * kSoftWarps);
             mbar_init(&misc->pfree[i], 1);
         }
+        for (int i = 0; i < kPlaces; ++i) {
+            mbar_init(&misc->ifull[i], 2);
+            mbar_init(&misc->ifree[i], kRowWarps + kSoftWarps);
+        }
         mbar_init(&misc->ofull, 1);
-        mbar_init(&misc->ofree, 128);
-        mbar_init(&misc->stat, 32 * kSoftWarps);
+        mbar_init(&misc->ofree, 32 * kSoftWarps);
         mbar_init(&misc->drain, 2);                      // one commit from each issuing warp
         mbar_fence_init();
         misc->abort = 0;
@@ -249,15 +258,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
             if (i == warp) before = total;
             total += misc->sums[i];
         }
-        int64_t groups = total / p.least;
-        groups = groups < 1 ? 1 : (groups > (int64_t)gridDim.x ? (int64_t)gridDim.x : groups);
-        const int64_t c = blockIdx.x;
-        const int64_t s0 = c < groups ? c * total / groups : total, s1 = c < groups ? (c + 1) * total / groups : total;
+        // at most as many spans as there are tiles: none is empty
+        const int64_t most = total < (int64_t)gridDim.x * p.least ? (int64_t)((uint32_t)total / (uint32_t)p.least) : (int64_t)gridDim.x;
+        const int groups = most < 1 ? 1 : (int)most, c = blockIdx.x;
+        const int64_t s0 = c < groups ? span_start(c, total, groups) : total, s1 = c < groups ? span_start(c + 1, total, groups) : total;
         int64_t at = before + upto - sum;
         if (tid == 0) {
             misc->left = s1 - s0;
             misc->total = total;
-            misc->groups = (int)groups;
+            misc->groups = groups;
             cuts[blockIdx.x].row = -1;
         }
         if (s0 >= at && s0 < at + sum) {
@@ -285,127 +294,151 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
     Item it;
 
     if (warp >= kRowWarp0) {
-        // ---------------- rows: this lane's row and quarter of each tile ----------------
-        const int rw = warp - kRowWarp0, r = 8 * rw + (lane & 7), qd = lane >> 3;
+        // ---------------- rows: 8 rows of each tile per two warps, a row and 64 of its dims per lane ------
+        const int rw = warp - kRowWarp0, r = 8 * (rw >> 1) + (lane & 7), part = 4 * (rw & 1) + (lane >> 3), sw = r & 7;
+        // the place of this lane's row of tile g
+        auto fetch = [&](uint32_t g, int &kind, int64_t &place) -> bool {
+            const int e = g % kPlaces;
+            if (!wait_warp(&misc->ifull[e], (g / kPlaces) & 1, abort)) return false;
+            kind = *reinterpret_cast<volatile int *>(&misc->kind[e]);
+            place = *reinterpret_cast<volatile int64_t *>(&misc->place[e][r]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&misc->ifree[e]);
+            return true;
+        };
+        auto load = [&](int kind, int64_t place, Codes &x) {
+            x.c[0] = x.c[1] = make_uint4(0u, 0u, 0u, 0u);
+            x.s = 0u;
+            if (!BITS4 || kind != kPool || place < 0) return;
+            const uint8_t *codes = static_cast<const uint8_t *>(p.cache) + place * (kDH / 2) + part * 32;
+            if (p.cache32) {
+                load32(codes, x.c[0], x.c[1]);
+            } else {
+                x.c[0] = reinterpret_cast<const uint4 *>(codes)[0];
+                x.c[1] = reinterpret_cast<const uint4 *>(codes)[1];
+            }
+            x.s = reinterpret_cast<const uint32_t *>(p.scales + place * (kDH / kScaleGroup))[part];
+        };
+        int kind = kEnd, kind2 = kEnd;
+        int64_t place = -1, place2 = -1;
+        uint32_t g = 0;
+        // one tile: its codes x are here, those of the next one (y) are asked for
+        auto step = [&](const Codes &x, Codes &y) -> bool {
+            if (kind == kEnd) return false;
+            if (!fetch(g + 1, kind2, place2)) { fail(); return false; }
+            load(kind2, place2, y);
+            const int s = g % kSlots;
+            if (g >= kSlots && !wait_warp(&misc->empty[s], ((g / kSlots) - 1) & 1, abort)) { fail(); return false; }
+            const uint32_t slot = sbase + kOffKV + s * kTile + r * 128;
+            if (BITS4 && kind == kPool) {
+                const uint2 s0 = scales_to_bf16(x.s & 0xffffu), s1 = scales_to_bf16(x.s >> 16);
+                const uint32_t cw[8] = {x.c[0].x, x.c[0].y, x.c[0].z, x.c[0].w, x.c[1].x, x.c[1].y, x.c[1].z, x.c[1].w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4 v = codes_to_bf16(cw[k], k < 2 ? s0.x : (k < 4 ? s0.y : (k < 6 ? s1.x : s1.y)));
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                 :: "r"(slot + part * kChunk + ((k ^ sw) << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_n(&misc->full[s], 32);
+            } else {
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(kind == kLocal ? p.local_kv : p.cache);
+                const bool there = place >= 0;
+                const __nv_bfloat16 *row = there ? src + place * kDH : static_cast<const __nv_bfloat16 *>(p.q);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {            // four lanes copy 64 contiguous bytes
+                    const uint32_t c = 4 * (rw & 1) + (k >> 1), u = 4 * (k & 1) + (lane >> 3);
+                    cp_async16_zfill(slot + c * kChunk + ((u ^ sw) << 4), there ? row + c * 64 + u * 8 : row, there);
+                }
+                cp_async_arrive(&misc->full[s]);
+            }
+            kind = kind2;
+            place = place2;
+            ++g;
+            return true;
+        };
+        Codes x, y;                                      // in turn: a copy from one to the other would wait for its loads
+        if (!fetch(0, kind, place)) fail();
+        load(kind, place, x);
+        while (step(x, y) && step(y, x)) {}
+        cp_async_wait_all();
+    } else if (warp == kIndexWarp0 || warp == kIndexWarp0 + 1) {
+        // ---------------- places: a row of each tile per lane; ids two tiles ahead, pages one ----------------
+        const int iw = warp - kIndexWarp0, r = 32 * iw + lane;
         bool have = walk_item(p, w, it);
         int ti = 0;                                      // the next tile of the item
-        // the next tile of the walk: its ids are asked for
-        auto want = [&]() -> Wanted {
-            Wanted a{kEnd, -1, 0, 0, nullptr, -1};
-            if (!have) return a;
-            const int t = w.t0 + ti;
-            const int b = (int)(w.row / p.L);
+        int akind = kEnd, aid = -1, aV = 0, alen = 0;    // its id is on its way
+        const int32_t *atable = nullptr;
+        int64_t aplace = -1;
+        int bkind = kEnd, bpage = -1, brest = -1;        // its page is on its way
+        int64_t bplace = -1;
+        auto want = [&]() {
+            akind = kEnd;
+            aid = -1;
+            aplace = -1;
+            if (!have) return;
+            const int t = w.t0 + ti, b = (int)((uint32_t)w.row / (uint32_t)p.L);
             if (t < it.nl) {
                 const int e = t * kT + r;
-                a.kind = kLocal;
-                if (e < it.x.nloc) a.place = (int64_t)b * p.W_max + it.x.lo + e;
+                akind = kLocal;
+                if (e < it.x.nloc) aplace = (int64_t)b * p.W_max + it.x.lo + e;
             } else {
                 const int kk = (t - it.nl) * kT + r;
-                a.kind = kPool;
-                a.V = (int)it.x.V;
-                a.len = (int)it.x.len;
-                a.table = p.page_table + (int64_t)b * p.table_cols;
-                if (kk < it.x.npool) a.id = p.I ? p.I[w.row * p.k + kk] : kk;
+                akind = kPool;
+                aV = (int)it.x.V;
+                alen = (int)it.x.len;
+                atable = p.page_table + (int64_t)b * p.table_cols;
+                if (kk < it.x.npool) aid = p.I ? p.I[w.row * p.k + kk] : kk;
             }
             if (++ti == it.T) {
                 walk_next(p, w, it);
                 have = walk_item(p, w, it);
                 ti = 0;
             }
-            return a;
         };
-        auto page = [&](const Wanted &a) -> Paged {
-            Paged b{a.kind, -1, -1, a.place};
-            if (a.kind != kPool) return b;
-            if (a.id < -1 || a.id >= a.len) {
-                if (a.id != -1) flag(p.status, HISA_DEV_BAD_ID);
-            } else if (a.id >= 0 && a.id < a.V) {
-                const uint32_t at = (uint32_t)a.id / (uint32_t)p.page_rows;
-                b.rest = a.id - (int)(at * (uint32_t)p.page_rows);
-                b.page = a.table[at];
-            }
-            return b;
-        };
-        auto put = [&](const Paged &b) -> Placed {
-            Placed c{b.kind, b.place};
-            if (b.kind != kPool || b.rest < 0) return c;
-            if (b.page < 0 || b.page >= p.pages) flag(p.status, HISA_DEV_BAD_OFFSETS);
-            else c.place = (int64_t)b.page * p.page_rows + b.rest;
-            return c;
-        };
-        auto load = [&](const Placed &c, Codes &x) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x.c[i] = make_uint4(0u, 0u, 0u, 0u);
-                x.s[i] = 0u;
-            }
-            if (!BITS4 || c.kind != kPool || c.place < 0) return;
-            // 16 bytes (32 dims, two scales) of every 64 of the row: four lanes read 64 contiguous ones
-            const uint4 *codes = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.cache) + c.place * (kDH / 2));
-            const uint16_t *sc = reinterpret_cast<const uint16_t *>(p.scales + c.place * (kDH / kScaleGroup));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x.c[i] = codes[4 * i + qd];
-                x.s[i] = sc[4 * i + qd];
+        auto page = [&]() {
+            bkind = akind;
+            bplace = aplace;
+            brest = -1;
+            if (akind != kPool) return;
+            if (aid < -1 || aid >= alen) {
+                if (aid != -1) flag(p.status, HISA_DEV_BAD_ID);
+            } else if (aid >= 0 && aid < aV) {
+                const uint32_t at = (uint32_t)aid / (uint32_t)p.page_rows;
+                brest = aid - (int)(at * (uint32_t)p.page_rows);
+                bpage = atable[at];
             }
         };
-        Wanted a = want();
-        Paged b = page(a);
-        a = want();
-        Placed cur = put(b);
-        Codes x;
-        load(cur, x);
-        b = page(a);
-        a = want();
-        uint32_t g = 0;
-        while (cur.kind != kEnd) {
-            const Placed next = put(b);
-            Codes y;
-            load(next, y);
-            b = page(a);
-            a = want();
-            const int s = g % kSlots;
-            if (g >= kSlots && !wait_warp(&misc->empty[s], ((g / kSlots) - 1) & 1, abort)) { fail(); break; }
-            const uint32_t seen = __ballot_sync(0xffffffffu, cur.place >= 0);
-            if (lane == 0) reinterpret_cast<uint8_t *>(&misc->mask[s])[rw] = (uint8_t)seen;
-            const uint32_t slot = sbase + kOffKV + s * kTile, base = slot + r * 128, sw = r & 7;
-            if (BITS4 && cur.kind == kPool) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint2 sc = scales_to_bf16(x.s[i]);
-                    const uint32_t cw[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
-                    const uint32_t chunk = base + (2 * i + (qd >> 1)) * kChunk;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint4 v = codes_to_bf16(cw[k], k < 2 ? sc.x : sc.y);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                                     :: "r"(chunk + ((((qd & 1) * 4 + k) ^ sw) << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-                    }
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_n(&misc->full[s], 33);
-            } else {
-                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(cur.kind == kLocal ? p.local_kv : p.cache);
-                const bool v = cur.place >= 0;
-                const __nv_bfloat16 *row = v ? src + cur.place * kDH : static_cast<const __nv_bfloat16 *>(p.q);
-#pragma unroll 4
-                for (int i = 0; i < 16; ++i) {
-                    const uint32_t u = 4 * i + qd;       // 16-byte unit of the row
-                    cp_async16_zfill(base + (u >> 3) * kChunk + (((u & 7) ^ sw) << 4), v ? row + u * 8 : row, v);
-                }
-                cp_async_arrive(&misc->full[s]);
-                if (lane == 0) mbar_arrive(&misc->full[s]);   // after the mask
+        want();
+        page();
+        want();
+        for (uint32_t g = 0;; ++g) {
+            int64_t place = bplace;
+            const int kind = bkind;
+            if (kind == kPool && brest >= 0) {
+                if (bpage < 0 || bpage >= p.pages) flag(p.status, HISA_DEV_BAD_OFFSETS);
+                else place = (int64_t)bpage * p.page_rows + brest;
             }
-            ++g;
-            cur = next;
-            x = y;
+            const int e = g % kPlaces;
+            if (g >= kPlaces && !wait_warp(&misc->ifree[e], ((g / kPlaces) - 1) & 1, abort)) { fail(); break; }
+            misc->place[e][r] = place;
+            const uint32_t seen = __ballot_sync(0xffffffffu, place >= 0);
+            if (lane == 0) {
+                misc->mask[e][iw] = seen;
+                if (iw == 0) misc->kind[e] = kind;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&misc->ifull[e]);
+            if (kind == kEnd) break;
+            page();
+            want();
         }
-        cp_async_wait_all();
     } else if (warp == kSWarp) {
         // ---------------- S = Q . K^T of every tile; q of each item ----------------
         const uint32_t id_s = idesc_bf16_f32(64, kT, 0, 0);
-        const uint64_t qdesc = smem_desc_sw128(sbase + kOffQ, 16, 1024);
+        const uint64_t qdesc = smem_desc_sw128(sbase + kOffQ, 16, 1024), kdesc = smem_desc_sw128(sbase + kOffKV, 16, 1024);
+        const uint32_t qlo = (uint32_t)qdesc, klo = (uint32_t)kdesc, hi = (uint32_t)(qdesc >> 32), e = elect_one();
         uint32_t g = 0;
         int n = 0;
         for (; walk_item(p, w, it); walk_next(p, w, it), ++n) {
@@ -413,6 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
             if (lane == 0) {
                 mbar_arrive_expect_tx(&misc->qfull, kTile);
                 tma_q(sbase + kOffQ, &qmap, (int32_t)(w.row * kH), &misc->qfull);
+                const int64_t row = w.row + (p.whole ? gridDim.x : 1);   // the next item's
+                if (row < rows && w.left > it.T) prefetch_q(&qmap, (int32_t)(row * kH));
             }
             __syncwarp();
             if (!wait_warp(&misc->qfull, n & 1, abort)) { fail(); break; }
@@ -425,12 +460,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 }
                 fence_async_smem();                       // the rows were written through the generic proxy
                 fence_after_sync();
-                const uint64_t kd = smem_desc_sw128(sbase + kOffKV + s * kTile, 16, 1024);
-                const uint32_t d = tmem + kColS + sb * kT;
+                const uint32_t kd = klo + s * (kTile >> 4), d = tmem + kColS + sb * kT;
 #pragma unroll
                 for (int ks = 0; ks < kDH / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * kChunk + (ks & 3) * 32;
-                    mma_bf16_warp(d, desc_add(qdesc, off), desc_add(kd, off), id_s, ks > 0);
+                    const uint32_t off = ((ks >> 2) * kChunk + (ks & 3) * 32) >> 4;
+                    mma_elected(d, qlo + off, hi, kd + off, hi, id_s, ks > 0, e);
                 }
                 mma_commit_warp(&misc->sfull[sb]);
             }
@@ -444,6 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
     } else if (warp == kPvWarp) {
         // ---------------- O^T += V^T . P^T of every tile ----------------
         const uint32_t id_o = idesc_bf16_f32(128, kH, 1, 0);
+        const uint64_t vdesc = smem_desc_sw128(sbase + kOffKV, kChunk, 1024), pdesc = smem_desc_sw128(sbase + kOffP, 16, 1024);
+        const uint32_t vlo = (uint32_t)vdesc, vhi = (uint32_t)(vdesc >> 32), plo = (uint32_t)pdesc, phi = (uint32_t)(pdesc >> 32);
+        const uint32_t e = elect_one();
         uint32_t g = 0;
         int n = 0;
         for (; walk_item(p, w, it); walk_next(p, w, it), ++n) {
@@ -454,14 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 if (!wait_warp(&misc->pfull[pb], (g / kBufs) & 1, abort)) { fail(); break; }
                 fence_async_smem();
                 fence_after_sync();
-                const uint64_t vd = smem_desc_sw128(sbase + kOffKV + s * kTile, kChunk, 1024);
-                const uint64_t pd = smem_desc_sw128(sbase + kOffP + pb * kChunk, 16, 1024);
+                const uint32_t vd = vlo + s * (kTile >> 4), pd = plo + pb * (kChunk >> 4);
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                     for (int ks = 0; ks < kT / 16; ++ks)
-                        mma_bf16_warp(tmem + kColO + mt * kH, desc_add(vd, 2 * mt * kChunk + ks * 2048), desc_add(pd, ks * 32), id_o,
-                                      ks > 0 || i > 0);
+                        mma_elected(tmem + kColO + mt * kH, vd + ((2 * mt * kChunk + ks * 2048) >> 4), vhi, pd + ((ks * 32) >> 4), phi, id_o,
+                                    ks > 0 || i > 0, e);
                 mma_commit_warp(&misc->empty[s]);
                 mma_commit_warp(&misc->pfree[pb]);
             }
@@ -472,168 +508,155 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
         __syncwarp();
         mbar_wait(&misc->drain, 0, 1u << 24);
         __syncwarp();
-    } else if (warp < kSoftWarps) {
-        // ---------------- softmax: lane l owns head 16 warp + l % 16 and tile rows 32 (l / 16) .. + 31 ------
-        const bool lead = lane < 16;
-        const int h = warp * 16 + (lane & 15), half = lane >> 4;
+    } else {
+        // ---------------- softmax and epilogue ----------------
+        // S has head 16 quad + l of lane l < 16 of a TMEM quadrant. Four threads share a head: lanes l and l + 16
+        // of the two warps of a quadrant, 16 tile rows each.
+        const int quad = warp & 3, side = warp >> 2, h = quad * 16 + (lane & 15), part = 2 * side + (lane >> 4);
+        const uint32_t quadrant = tmem + ((uint32_t)(32 * quad) << 16);
         const float sink2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
-        const float cl = p.scale * kLog2e, gp = BITS4 ? p.g * 256.f : 1.f;
-        uint32_t g = 0, pv_seen[kBufs] = {};
-        auto wait_pv = [&](uint32_t tile) -> bool {       // the PV product of a tile is done
-            const int b = tile % kBufs;
-            while (pv_seen[b] <= tile / kBufs) {
-                if (!wait_warp(&misc->pfree[b], pv_seen[b] & 1, abort)) return false;
-                ++pv_seen[b];
-            }
-            return true;
-        };
+        const float cl = p.scale * kLog2e, gp = BITS4 ? p.g * 256.f : 1.f, lg = BITS4 ? log2f(gp) : 0.f, unf = BITS4 ? 1.f / gp : 1.f;
+        uint32_t g = 0;
         int n = 0;
         for (; walk_item(p, w, it); walk_next(p, w, it), ++n) {
-            float m2 = -INFINITY, l = 0.f;
+            float m2 = -INFINITY, l = 0.f;                // l: this thread's rows
             for (int i = 0; i < it.T; ++i, ++g) {
-                const int s = g % kSlots, sb = g % kBufs;
+                const int sb = g % kBufs, e = g % kPlaces;
                 const bool pool = w.t0 + i >= it.nl;
-                const float f = pool ? gp : 1.f, c2 = cl * f;
-                bool good = wait_warp(&misc->full[s], (g / kSlots) & 1, abort) && wait_warp(&misc->sfull[sb], (g / kBufs) & 1, abort);
+                const float c2 = pool ? cl * gp : cl;
+                bool good = wait_warp(&misc->ifull[e], (g / kPlaces) & 1, abort) && wait_warp(&misc->sfull[sb], (g / kBufs) & 1, abort);
                 fence_after_sync();
-                const uint32_t mask = (uint32_t)(*reinterpret_cast<volatile uint64_t *>(&misc->mask[s]) >> (32 * half));
-                float v[32];
-                tmem_ld32_x2(tmem + ((uint32_t)(32 * warp) << 16) + kColS + sb * kT, v);
+                const uint32_t mask = *reinterpret_cast<volatile uint32_t *>(&misc->mask[e][side]) >> (lane & 16);
+                float v[16];
+                tmem_ld16_x2(quadrant + kColS + sb * kT + 32 * side, v);
+                tmem_ld_wait();
                 fence_before_sync();
                 mbar_arrive(&misc->sfree[sb]);
-                float top = -INFINITY;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&misc->ifree[e]);
+                if ((mask & 0xffffu) != 0xffffu) {        // unseen rows are staged as zeros
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    v[k] = ((mask >> k) & 1u) ? v[k] * c2 : -INFINITY;
-                    top = fmaxf(top, v[k]);
+                    for (int k = 0; k < 16; ++k)
+                        if (!((mask >> k) & 1u)) v[k] = -INFINITY;
                 }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                float alpha = 1.f;
-                bool rescale = false;
-                if (top > m2 + kLazy) {
-                    if (m2 != -INFINITY) {
-                        alpha = ex2(m2 - top);
-                        rescale = true;
-                    }
-                    m2 = top;
-                }
-                // ex2(-inf - m) = +0; m2 is finite once a row of this head was seen, and logits are -inf when masked
-                const float ref = m2 == -INFINITY ? 0.f : m2;
-                float sum = 0.f;
-                uint32_t packed[16];
+                float t4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    const float a = ex2(v[k] - ref), b = ex2(v[k + 1] - ref);
-                    sum += a + b;
-                    const __nv_bfloat162 two = __floats2bfloat162_rn(a * f, b * f);
-                    packed[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
-                }
-                l = l * alpha + sum + __shfl_xor_sync(0xffffffffu, sum, 16);
-                if (lead) misc->alpha[g & 1][h] = alpha;
-                if (good && g >= kBufs) good = wait_pv(g - kBufs);       // P's buffer is free
-                if (soft_any(rescale || !good)) {
+                for (int k = 4; k < 16; ++k) t4[k & 3] = fmaxf(t4[k & 3], v[k]);
+                const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c2;
+                misc->top[part][h] = top;
+                // P's buffer is free (phases of a buffer's barrier are waited for one after another)
+                good = good && (g < kBufs || wait_warp(&misc->pfree[sb], ((g / kBufs) - 1) & 1, abort));
+                if (soft_any(top > m2 + kLazy || !good)) {
                     if (!soft_all(good)) { fail(); break; }
-                    // heads whose reference moved up: O^T after the product of the tile before (of this item)
-                    if (!soft_all(i < 1 || wait_pv(g - 1))) { fail(); break; }
-                    fence_after_sync();
-#pragma unroll 1
-                    for (int c = 0; c < 4 * kH; c += 16) {
-                        float o[16];
-                        const uint32_t ta = tmem + ((uint32_t)(32 * warp) << 16) + kColO + c;
-                        tmem_ld16(ta, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) o[q] *= misc->alpha[g & 1][(c & (kH - 1)) + q];
-                        tmem_st16(ta, o);
+                    const float all = fmaxf(fmaxf(misc->top[0][h], misc->top[1][h]), fmaxf(misc->top[2][h], misc->top[3][h]));
+                    float alpha = 1.f;
+                    if (all > m2 + kLazy) {
+                        if (m2 != -INFINITY) alpha = ex2(m2 - all);
+                        m2 = all;
                     }
-                    tmem_st_wait();
+                    l *= alpha;
+                    if (part == 0) misc->alpha[h] = alpha;
+                    // O^T of this item so far, after the product of the tile before
+                    if (!soft_all(i < 1 || wait_warp(&misc->pfree[sb ^ 1], ((g - 1) / kBufs) & 1, abort))) { fail(); break; }
+                    if (i > 0) {
+                        fence_after_sync();
+#pragma unroll 1
+                        for (int c = 2 * kH * side; c < 2 * kH * (side + 1); c += 16) {
+                            float o[16];
+                            tmem_ld16(quadrant + kColO + c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int q = 0; q < 16; ++q) o[q] *= misc->alpha[(c & (kH - 1)) + q];
+                            tmem_st16(quadrant + kColO + c, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                // P f = ex2(logit - m + log2 f), so that its sum is f times theirs. ex2(-inf) = +0; m2 is finite
+                // once a row of this head was seen, and logits are -inf when masked
+                const float ref = (m2 == -INFINITY ? 0.f : m2) - (pool ? lg : 0.f);
+                const float2 cc = make_float2(c2, c2), rr = make_float2(-ref, -ref);
+                float2 sums = make_float2(0.f, 0.f);
+                uint32_t packed[8];
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    const float2 z = fma2(make_float2(v[k], v[k + 1]), cc, rr), x = make_float2(ex2(z.x), ex2(z.y));
+                    sums = add2(sums, x);
+                    const __nv_bfloat162 two = __floats2bfloat162_rn(x.x, x.y);
+                    packed[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
                 }
                 uint8_t *pbuf = smem + kOffP + sb * kChunk;
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    *reinterpret_cast<uint4 *>(pbuf + sw128_offset(h, (half * 4 + u) * 8)) =
+                for (int u = 0; u < 2; ++u)
+                    *reinterpret_cast<uint4 *>(pbuf + sw128_offset(h, (part * 2 + u) * 8)) =
                         make_uint4(packed[4 * u], packed[4 * u + 1], packed[4 * u + 2], packed[4 * u + 3]);
                 fence_async_smem();
                 fence_before_sync();
                 mbar_arrive(&misc->pfull[sb]);
+                l += (sums.x + sums.y) * (pool ? unf : 1.f);
             }
             if (!ok) break;
-            // the item's statistics, once the epilogue has read the previous item's
-            if (n > 0 && !soft_all(wait_warp(&misc->ofree, (n - 1) & 1, abort))) { fail(); break; }
-            if (lead) {
+            // the item's statistics; then O^T -> out, or a cut row's sums
+            misc->sum[part][h] = l;
+            if (!soft_all(wait_warp(&misc->ofull, n & 1, abort))) { fail(); break; }
+            if (part == 0) {
+                l = (misc->sum[0][h] + misc->sum[1][h]) + (misc->sum[2][h] + misc->sum[3][h]);
                 const float M = fmaxf(m2, sink2);
-                const float wm = m2 == -INFINITY ? 0.f : exp2f(m2 - M);
-                const float den = l * wm + (sink2 == -INFINITY ? 0.f : exp2f(sink2 - M));
+                const float wm = m2 == -INFINITY ? 0.f : ex2(m2 - M);
+                const float den = l * wm + (sink2 == -INFINITY ? 0.f : ex2(sink2 - M));
                 misc->factor[h] = den == 0.f ? 0.f : wm / den;           // nothing seen, no sink: 0
-                misc->stat_m[h] = m2;
-                misc->stat_l[h] = l;
             }
-            mbar_arrive(&misc->stat);
-        }
-    } else {
-        // ---------------- epilogue: O^T -> out, or a cut row's sums ----------------
-        const int quad = warp & 3;                        // TMEM lanes 32 quad .. + 31 = dims
-        const uint32_t to = tmem + ((uint32_t)(32 * quad) << 16) + kColO;
-        int n = 0;
-        for (; walk_item(p, w, it); walk_next(p, w, it), ++n) {
-            // an item may be long: as many bounded waits as it has tiles
-            bool done = false;
-            for (int k = 0; k <= it.T && !done && !*abort; ++k)
-                done = wait_warp(&misc->stat, n & 1, abort) && wait_warp(&misc->ofull, n & 1, abort);
-            if (!__all_sync(0xffffffffu, done)) { fail(); break; }
+            soft_sync();
             fence_after_sync();
             const bool cut = it.T < it.tiles;
             if (!cut) {
-                for (int mt = 0; mt < 4; ++mt)
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {             // 32 heads of 128 dims
+                    const int mt = 2 * side + (k >> 1), c = 32 * (k & 1), d = mt * 128 + quad * 32 + lane;
+                    float o[32];
+                    tmem_ld32(quadrant + kColO + mt * kH + c, o);
 #pragma unroll
-                    for (int c = 0; c < kH; c += 16) {
-                        float o[16];
-                        tmem_ld16(to + mt * kH + c, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) o[q] *= misc->factor[c + q];
-                        const int d = mt * 128 + quad * 32 + lane;
-                        if (p.out_bf16) {
-                            // two dims per store: even lanes take the first eight heads, odd ones the others
-                            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + w.row * kH * kDH + (d & ~1);
-                            const bool odd = lane & 1;
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                const float mine = odd ? o[q + 8] : o[q], yours = __shfl_xor_sync(0xffffffffu, odd ? o[q] : o[q + 8], 1);
-                                const __nv_bfloat162 two = odd ? __floats2bfloat162_rn(yours, mine) : __floats2bfloat162_rn(mine, yours);
-                                *reinterpret_cast<__nv_bfloat162 *>(out + (int64_t)(c + q + (odd ? 8 : 0)) * kDH) = two;
-                            }
-                        } else {
-                            float *out = static_cast<float *>(p.out) + w.row * kH * kDH + d;
-#pragma unroll
-                            for (int q = 0; q < 16; ++q) out[(int64_t)(c + q) * kDH] = o[q];
-                        }
+                    for (int q = 0; q < 32; q += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&misc->factor[c + q]);
+                        o[q] *= f.x; o[q + 1] *= f.y; o[q + 2] *= f.z; o[q + 3] *= f.w;
                     }
+                    if (p.out_bf16) {
+                        // two dims per store: even lanes take the first sixteen heads, odd ones the others
+                        const bool odd = lane & 1;
+                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + (w.row * kH + c + (odd ? 16 : 0)) * kDH + (d & ~1);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const float mine = odd ? o[q + 16] : o[q], yours = __shfl_xor_sync(0xffffffffu, odd ? o[q] : o[q + 16], 1);
+                            const __nv_bfloat162 two = odd ? __floats2bfloat162_rn(yours, mine) : __floats2bfloat162_rn(mine, yours);
+                            *reinterpret_cast<__nv_bfloat162 *>(out + q * kDH) = two;
+                        }
+                    } else {
+                        float *out = static_cast<float *>(p.out) + (w.row * kH + c) * kDH + d;
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) out[q * kDH] = o[q];
+                    }
+                }
             } else {
                 const int place = 2 * (int)blockIdx.x + (n > 0);
                 float *sums = p.part_o + (int64_t)place * kH * kDH;
-                if (quad == 0) {
-                    for (int hh = lane; hh < kH; hh += 32)
-                        reinterpret_cast<float2 *>(p.part_ml)[place * kH + hh] = make_float2(misc->stat_m[hh], misc->stat_l[hh]);
-                    if (lane == 0 && w.t0 == 0) {         // the row begins here: its last tile of the span is the span's last
-                        const int64_t s1 = (int64_t)(blockIdx.x + 1) * misc->total / misc->groups;
-                        Cut &k = cuts[blockIdx.x];
-                        k.total = misc->total;
-                        k.groups = misc->groups;
-                        k.last = (int)(((s1 - it.T + it.tiles) * misc->groups - 1) / misc->total);
-                        k.place = place;
-                        k.row = w.row;
-                    }
+                if (part == 0) reinterpret_cast<float2 *>(p.part_ml)[place * kH + h] = make_float2(m2, l);
+                if (tid == 0 && w.t0 == 0) {              // the row begins here: its last tile of the span is the span's last
+                    const int64_t s1 = span_start(blockIdx.x + 1, misc->total, misc->groups);
+                    Cut &k = cuts[blockIdx.x];
+                    k.total = misc->total;
+                    k.groups = misc->groups;
+                    k.last = (int)(((s1 - it.T + it.tiles) * misc->groups - 1) / misc->total);
+                    k.place = place;
+                    k.row = w.row;
                 }
-                for (int mt = 0; mt < 4; ++mt)
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    const int mt = 2 * side + (k >> 1), c = 32 * (k & 1);
+                    float o[32];
+                    tmem_ld32(quadrant + kColO + mt * kH + c, o);
 #pragma unroll
-                    for (int c = 0; c < kH; c += 16) {
-                        float o[16];
-                        tmem_ld16(to + mt * kH + c, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) sums[(c + q) * kDH + mt * 128 + quad * 32 + lane] = o[q];
-                    }
+                    for (int q = 0; q < 32; ++q) sums[(c + q) * kDH + mt * 128 + quad * 32 + lane] = o[q];
+                }
             }
             fence_before_sync();
             mbar_arrive(&misc->ofree);
@@ -654,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
 constexpr int kJoinThreads = 512;
 template <int GROUPS>
 __global__ void __launch_bounds__(kJoinThreads) k_cache_join(CacheAttnParams p) {
-    __shared__ float weight[4 / GROUPS][kCacheCtas];
+    __shared__ float2 stat[4 / GROUPS][kCacheCtas];      // a segment's maximum, then weight; its sum
     __shared__ float4 part[GROUPS == 1 ? 1 : GROUPS - 1][128];
     grid_dep_wait();
     grid_dep_trigger();
@@ -662,34 +685,24 @@ __global__ void __launch_bounds__(kJoinThreads) k_cache_join(CacheAttnParams p) 
     if (cut.row < 0) return;
     const int team = threadIdx.x / 128, grp = team % GROUPS, hs = team / GROUPS, d = (threadIdx.x % 128) * 4;
     const int h = blockIdx.y * (4 / GROUPS) + hs, first = blockIdx.x, segs = cut.last - first + 1;
-    const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml);
+    // every span has a tile, so every CTA from the first to the last has a part of the row
     auto place = [&](int s) { return s == 0 ? cut.place : 2 * (first + s); };
-    // a span between may be empty (fewer tiles than CTAs)
-    auto empty = [&](int s) {
-        const int64_t c = first + s;
-        return c * cut.total / cut.groups == (c + 1) * cut.total / cut.groups;
-    };
     const float sink2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
-    float M = sink2;
-    for (int s = 0; s < segs; ++s)
-        if (!empty(s)) M = fmaxf(M, ml[place(s) * kH + h].x);
-    const float ref = M == -INFINITY ? 0.f : M;
-    for (int s = threadIdx.x % 128 + 128 * grp; s < segs; s += 128 * GROUPS) {
-        const float m = empty(s) ? -INFINITY : ml[place(s) * kH + h].x;
-        weight[hs][s] = m == -INFINITY ? -1.f : exp2f(m - ref);          // -1: nothing there, unless NaN
-    }
+    for (int s = threadIdx.x % 128 + 128 * grp; s < segs; s += 128 * GROUPS)
+        stat[hs][s] = reinterpret_cast<const float2 *>(p.part_ml)[place(s) * kH + h];
     __syncthreads();
+    float M = sink2;
+    for (int s = 0; s < segs; ++s) M = fmaxf(M, stat[hs][s].x);
+    const float ref = M == -INFINITY ? 0.f : M;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = sink2 == -INFINITY ? 0.f : exp2f(sink2 - ref);
+    float den = sink2 == -INFINITY ? 0.f : ex2(sink2 - ref);
 #pragma unroll 4
-    for (int s = 0; s < segs; ++s) {
-        if (empty(s)) continue;
-        const float l = ml[place(s) * kH + h].y, a = weight[hs][s] < 0.f ? 0.f : weight[hs][s];
-        den += l * a;
-        if (s % GROUPS != grp) continue;
+    for (int s = grp; s < segs; s += GROUPS) {
         const float4 v = __ldcs(reinterpret_cast<const float4 *>(p.part_o + ((int64_t)place(s) * kH + h) * kDH + d));
+        const float a = ex2(stat[hs][s].x - ref);        // a part that saw nothing: 0 of sums that are 0
         o.x += v.x * a; o.y += v.y * a; o.z += v.z * a; o.w += v.w * a;
     }
+    for (int s = 0; s < segs; ++s) den += stat[hs][s].y * ex2(stat[hs][s].x - ref);
     if constexpr (GROUPS > 1) {
         if (grp) part[grp - 1][d / 4] = o;
         __syncthreads();
