@@ -76,6 +76,7 @@ struct CacheAttnParams {
 };
 constexpr int kCacheCtas = kSmTarget;     // most CTAs of the tensor-core kernel
 constexpr size_t kCutBytes = 32;
+constexpr int kCacheTile = 48;            // its list rows per tile
 
 // What a query row sees: local rows [lo, lo + nloc) of its window buffer, then npool entries of its
 // list of pooled rows (ids of I, or rows 0, 1, ...), of which those below V are visible.

@@ -1,11 +1,11 @@
 // Combine over a cache in pages on the tensor cores: 64 bf16 query heads of 512 dims, K = V, pooled rows in
 // 4 bits or bf16.
 //
-// A query row's list (its visible window, then the pooled rows it sees) is cut into tiles of 64 rows, all
+// A query row's list (its visible window, then the pooled rows it sees) is cut into tiles of 48 rows, all
 // of one kind. Per tile:
-//   S  = Q . K^T      tcgen05, M = 64 heads, N = 64 rows, K = 512           (TMEM, 2 buffers)
+//   S  = Q . K^T      tcgen05, M = 64 heads, N = 48 rows, K = 512           (TMEM, 2 buffers)
 //   P  = exp2(S scale log2e - m) per head, in the threads that own the head's TMEM lane
-//   O^T += V^T . P^T  tcgen05, M = 128 dims x 4, N = 64 heads, K = 64       (TMEM, f32)
+//   O^T += V^T . P^T  tcgen05, M = 128 dims x 4, N = 64 heads, K = 48       (TMEM, f32)
 // The tile is staged once in bf16 (128-byte swizzle): K-major for the first product, MN-major for the
 // second.
 //
@@ -25,7 +25,7 @@
 // sums of 2^31 such weights and products stay far below 2^127; a rescaling costs as much as a tile.
 //
 // Warps: 0-7 softmax and epilogue, 8 S issue (and q by TMA), 9 PV issue, 10-11 places of the rows (ids,
-// pages), up to four tiles ahead, 12-27 rows: a lane has a row of the tile and an eighth of its dims, the next
+// pages), up to four tiles ahead, 12-23 rows: a lane has a row of the tile and an eighth of its dims, the next
 // tile's codes on their way while it writes this one's. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and the CTA leaves.
 #include "cache_internal.cuh"
 #include "prefix_common.cuh"
@@ -35,22 +35,24 @@ namespace {
 
 using namespace tc;
 
-constexpr int kH = 64, kDH = 512, kT = 64;              // heads, dims, rows of a tile
-constexpr int kSoftWarps = 8, kSWarp = 8, kPvWarp = 9, kIndexWarp0 = 10, kRowWarp0 = 12, kRowWarps = 16;
+constexpr int kH = 64, kDH = 512, kT = kCacheTile;      // heads, dims, rows of a tile
+constexpr int kSoftWarps = 8, kSWarp = 8, kPvWarp = 9, kIndexWarp0 = 10, kRowWarp0 = 12, kRowWarps = kT / 4;
 constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
-constexpr int kSlots = 2, kBufs = 2, kPlaces = 8;        // staged tiles; S and P buffers; tiles whose rows' places are known
-constexpr uint32_t kChunk = 64 * 128;                   // 64 rows x 64 dims, 128-byte swizzle
+constexpr int kSlots = 3, kBufs = 2, kPlaces = 8;        // staged tiles; S buffers; tiles whose rows' places are known
+constexpr uint32_t kChunk = kT * 128;                   // 64 dims of a tile, 128-byte swizzle
 constexpr uint32_t kTile = 8 * kChunk;
-constexpr uint32_t kOffQ = 0, kOffKV = kTile, kOffP = kOffKV + kSlots * kTile, kOffMisc = kOffP + kBufs * kChunk;
-constexpr uint32_t kColS = 0, kColO = 128, kTmemCols = 512;
+constexpr uint32_t kQChunk = kH * 128, kQBytes = 8 * kQChunk, kPBytes = kH * 128;
+constexpr uint32_t kOffQ = 0, kOffKV = kQBytes, kOffP = kOffKV + kSlots * kTile, kOffMisc = kOffP + kPBytes;
+constexpr uint32_t kColS = 0, kSCols = 64, kColO = kBufs * kSCols, kTmemCols = 512;
+constexpr int kC = kT / 4;                               // tile rows of a softmax thread
 constexpr float kLog2e = 1.4426950408889634f, kLazy = 64.0f;
 constexpr int kBarSoft = 1;
 
 struct Misc {
-    uint64_t qfull, qfree, full[kSlots], empty[kSlots], sfull[kBufs], sfree[kBufs], pfull[kBufs], pfree[kBufs], ofull, ofree, drain;
+    uint64_t qfull, qfree, full[kSlots], empty[kSlots], sfull[kBufs], sfree[kBufs], pfull, pfree, ofull, ofree, drain;
     uint64_t ifull[kPlaces], ifree[kPlaces];
     int64_t place[kPlaces][kT];                         // row of local_kv or of the pool; -1: not seen
-    uint32_t mask[kPlaces][2];                          // rows of a tile that are seen
+    uint64_t mask[kPlaces];                             // rows of a tile that are seen
     int kind[kPlaces];                                  // TileKind
     uint32_t tmem;
     int abort;
@@ -135,6 +137,20 @@ __device__ __forceinline__ bool soft_any(bool v) {
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync %0, %1;" :: "n"(kBarSoft), "n"(32 * kSoftWarps) : "memory"); }
 __device__ __forceinline__ bool soft_all(bool v) { return !soft_any(!v); }
 
+// Lanes 0-15 read columns [c, c + 12) of TMEM lanes base + 0 .. 15, lanes 16-31 columns [c + 12, c + 24) of
+// the same ones (an M = 64 accumulator's rows live in lanes 0-15 of each quadrant).
+__device__ __forceinline__ void tmem_ld12_x2(uint32_t addr, float (&v)[12]) {
+    uint32_t r[12];
+    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%12], 12;\n\t"
+                 "tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%8,%9,%10,%11}, [%13], 12;"
+                 : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]), "=&r"(r[8]),
+                   "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11])
+                 : "r"(addr), "r"(addr + 8));
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 12; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // Eight codes times a scale (as bf16, times 2^118, in both halves of s), in bf16, times 2^-8.
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -206,14 +222,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
     if (tid == 0) {
         mbar_init(&misc->qfull, 1);
         mbar_init(&misc->qfree, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(&misc->full[i], 32 * kRowWarps);
             mbar_init(&misc->empty[i], 1);
+        }
+        for (int i = 0; i < kBufs; ++i) {
             mbar_init(&misc->sfull[i], 1);
             mbar_init(&misc->sfree[i], 32 * kSoftWarps);
-            mbar_init(&misc->pfull[i], 32 * kSoftWarps);
-            mbar_init(&misc->pfree[i], 1);
         }
+        mbar_init(&misc->pfull, 32 * kSoftWarps);
+        mbar_init(&misc->pfree, 1);
         for (int i = 0; i < kPlaces; ++i) {
             mbar_init(&misc->ifull[i], 2);
             mbar_init(&misc->ifree[i], kRowWarps + kSoftWarps);
@@ -382,14 +400,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
             if (t < it.nl) {
                 const int e = t * kT + r;
                 akind = kLocal;
-                if (e < it.x.nloc) aplace = (int64_t)b * p.W_max + it.x.lo + e;
+                if (r < kT && e < it.x.nloc) aplace = (int64_t)b * p.W_max + it.x.lo + e;
             } else {
                 const int kk = (t - it.nl) * kT + r;
                 akind = kPool;
                 aV = (int)it.x.V;
                 alen = (int)it.x.len;
                 atable = p.page_table + (int64_t)b * p.table_cols;
-                if (kk < it.x.npool) aid = p.I ? p.I[w.row * p.k + kk] : kk;
+                if (r < kT && kk < it.x.npool) aid = p.I ? p.I[w.row * p.k + kk] : kk;
             }
             if (++ti == it.T) {
                 walk_next(p, w, it);
@@ -422,10 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
             }
             const int e = g % kPlaces;
             if (g >= kPlaces && !wait_warp(&misc->ifree[e], ((g / kPlaces) - 1) & 1, abort)) { fail(); break; }
-            misc->place[e][r] = place;
-            const uint32_t seen = __ballot_sync(0xffffffffu, place >= 0);
+            if (r < kT) misc->place[e][r] = place;
+            const uint32_t seen = __ballot_sync(0xffffffffu, r < kT && place >= 0);
             if (lane == 0) {
-                misc->mask[e][iw] = seen;
+                reinterpret_cast<uint32_t *>(&misc->mask[e])[iw] = seen;
                 if (iw == 0) misc->kind[e] = kind;
             }
             __syncwarp();
@@ -444,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
         for (; walk_item(p, w, it); walk_next(p, w, it), ++n) {
             if (n > 0 && !wait_warp(&misc->qfree, (n - 1) & 1, abort)) { fail(); break; }
             if (lane == 0) {
-                mbar_arrive_expect_tx(&misc->qfull, kTile);
+                mbar_arrive_expect_tx(&misc->qfull, kQBytes);
                 tma_q(sbase + kOffQ, &qmap, (int32_t)(w.row * kH), &misc->qfull);
                 const int64_t row = w.row + (p.whole ? gridDim.x : 1);   // the next item's
                 if (row < rows && w.left > it.T) prefetch_q(&qmap, (int32_t)(row * kH));
@@ -460,11 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 }
                 fence_async_smem();                       // the rows were written through the generic proxy
                 fence_after_sync();
-                const uint32_t kd = klo + s * (kTile >> 4), d = tmem + kColS + sb * kT;
+                const uint32_t kd = klo + s * (kTile >> 4), d = tmem + kColS + sb * kSCols;
 #pragma unroll
                 for (int ks = 0; ks < kDH / 16; ++ks) {
-                    const uint32_t off = ((ks >> 2) * kChunk + (ks & 3) * 32) >> 4;
-                    mma_elected(d, qlo + off, hi, kd + off, hi, id_s, ks > 0, e);
+                    const uint32_t in = (ks & 3) * 32;
+                    mma_elected(d, qlo + (((ks >> 2) * kQChunk + in) >> 4), hi, kd + (((ks >> 2) * kChunk + in) >> 4), hi, id_s, ks > 0, e);
                 }
                 mma_commit_warp(&misc->sfull[sb]);
             }
@@ -487,19 +505,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
             if (n > 0 && !wait_warp(&misc->ofree, (n - 1) & 1, abort)) { fail(); break; }
             fence_after_sync();
             for (int i = 0; i < it.T; ++i, ++g) {
-                const int s = g % kSlots, pb = g % kBufs;
-                if (!wait_warp(&misc->pfull[pb], (g / kBufs) & 1, abort)) { fail(); break; }
+                const int s = g % kSlots;
+                if (!wait_warp(&misc->pfull, g & 1, abort)) { fail(); break; }
                 fence_async_smem();
                 fence_after_sync();
-                const uint32_t vd = vlo + s * (kTile >> 4), pd = plo + pb * (kChunk >> 4);
+                const uint32_t vd = vlo + s * (kTile >> 4);
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                     for (int ks = 0; ks < kT / 16; ++ks)
-                        mma_elected(tmem + kColO + mt * kH, vd + ((2 * mt * kChunk + ks * 2048) >> 4), vhi, pd + ((ks * 32) >> 4), phi, id_o,
+                        mma_elected(tmem + kColO + mt * kH, vd + ((2 * mt * kChunk + ks * 2048) >> 4), vhi, plo + ((ks * 32) >> 4), phi, id_o,
                                     ks > 0 || i > 0, e);
                 mma_commit_warp(&misc->empty[s]);
-                mma_commit_warp(&misc->pfree[pb]);
+                mma_commit_warp(&misc->pfree);
             }
             if (!ok) break;
             mma_commit_warp(&misc->ofull);
@@ -518,34 +536,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
         const float cl = p.scale * kLog2e, gp = BITS4 ? p.g * 256.f : 1.f, lg = BITS4 ? log2f(gp) : 0.f, unf = BITS4 ? 1.f / gp : 1.f;
         uint32_t g = 0;
         int n = 0;
+        bool good = true;
         for (; walk_item(p, w, it); walk_next(p, w, it), ++n) {
             float m2 = -INFINITY, l = 0.f;                // l: this thread's rows
             for (int i = 0; i < it.T; ++i, ++g) {
                 const int sb = g % kBufs, e = g % kPlaces;
                 const bool pool = w.t0 + i >= it.nl;
                 const float c2 = pool ? cl * gp : cl;
-                bool good = wait_warp(&misc->ifull[e], (g / kPlaces) & 1, abort) && wait_warp(&misc->sfull[sb], (g / kBufs) & 1, abort);
+                good = good && wait_warp(&misc->ifull[e], (g / kPlaces) & 1, abort) && wait_warp(&misc->sfull[sb], (g / kBufs) & 1, abort);
                 fence_after_sync();
-                const uint32_t mask = *reinterpret_cast<volatile uint32_t *>(&misc->mask[e][side]) >> (lane & 16);
-                float v[16];
-                tmem_ld16_x2(quadrant + kColS + sb * kT + 32 * side, v);
-                tmem_ld_wait();
+                const uint32_t mask = (uint32_t)(*reinterpret_cast<volatile uint64_t *>(&misc->mask[e]) >> (kC * part)) & ((1u << kC) - 1u);
+                float v[kC];
+                tmem_ld12_x2(quadrant + kColS + sb * kSCols + 2 * kC * side, v);
                 fence_before_sync();
                 mbar_arrive(&misc->sfree[sb]);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&misc->ifree[e]);
-                if ((mask & 0xffffu) != 0xffffu) {        // unseen rows are staged as zeros
+                if (mask != (1u << kC) - 1u) {            // unseen rows are staged as zeros
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
+                    for (int k = 0; k < kC; ++k)
                         if (!((mask >> k) & 1u)) v[k] = -INFINITY;
                 }
                 float t4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                for (int k = 4; k < 16; ++k) t4[k & 3] = fmaxf(t4[k & 3], v[k]);
+                for (int k = 4; k < kC; ++k) t4[k & 3] = fmaxf(t4[k & 3], v[k]);
                 const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c2;
                 misc->top[part][h] = top;
-                // P's buffer is free (phases of a buffer's barrier are waited for one after another)
-                good = good && (g < kBufs || wait_warp(&misc->pfree[sb], ((g / kBufs) - 1) & 1, abort));
                 if (soft_any(top > m2 + kLazy || !good)) {
                     if (!soft_all(good)) { fail(); break; }
                     const float all = fmaxf(fmaxf(misc->top[0][h], misc->top[1][h]), fmaxf(misc->top[2][h], misc->top[3][h]));
@@ -557,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                     l *= alpha;
                     if (part == 0) misc->alpha[h] = alpha;
                     // O^T of this item so far, after the product of the tile before
-                    if (!soft_all(i < 1 || wait_warp(&misc->pfree[sb ^ 1], ((g - 1) / kBufs) & 1, abort))) { fail(); break; }
+                    if (!soft_all(i < 1 || wait_warp(&misc->pfree, (g - 1) & 1, abort))) { fail(); break; }
                     if (i > 0) {
                         fence_after_sync();
 #pragma unroll 1
@@ -577,28 +593,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 const float ref = (m2 == -INFINITY ? 0.f : m2) - (pool ? lg : 0.f);
                 const float2 cc = make_float2(c2, c2), rr = make_float2(-ref, -ref);
                 float2 sums = make_float2(0.f, 0.f);
-                uint32_t packed[8];
+                uint32_t packed[kC / 2];
 #pragma unroll
-                for (int k = 0; k < 16; k += 2) {
+                for (int k = 0; k < kC; k += 2) {
                     const float2 z = fma2(make_float2(v[k], v[k + 1]), cc, rr), x = make_float2(ex2(z.x), ex2(z.y));
                     sums = add2(sums, x);
                     const __nv_bfloat162 two = __floats2bfloat162_rn(x.x, x.y);
                     packed[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
                 }
-                uint8_t *pbuf = smem + kOffP + sb * kChunk;
+                // P's buffer: the product of the tile before has read it. One that never ends is met at the next
+                // tile's barrier, by all
+                good = g < 1 || wait_warp(&misc->pfree, (g - 1) & 1, abort);
+                uint8_t *prow = smem + kOffP + h * 128;
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    *reinterpret_cast<uint4 *>(pbuf + sw128_offset(h, (part * 2 + u) * 8)) =
-                        make_uint4(packed[4 * u], packed[4 * u + 1], packed[4 * u + 2], packed[4 * u + 3]);
+                for (int u = 0; u < kC / 4; ++u) {        // 8 bytes: four rows
+                    const uint32_t at = part * (2 * kC) + 8 * u;
+                    *reinterpret_cast<uint2 *>(prow + (((at >> 4) ^ (h & 7)) << 4 | (at & 8))) = make_uint2(packed[2 * u], packed[2 * u + 1]);
+                }
                 fence_async_smem();
                 fence_before_sync();
-                mbar_arrive(&misc->pfull[sb]);
+                mbar_arrive(&misc->pfull);
                 l += (sums.x + sums.y) * (pool ? unf : 1.f);
             }
             if (!ok) break;
             // the item's statistics; then O^T -> out, or a cut row's sums
             misc->sum[part][h] = l;
-            if (!soft_all(wait_warp(&misc->ofull, n & 1, abort))) { fail(); break; }
+            if (!soft_all(good && wait_warp(&misc->ofull, n & 1, abort))) { fail(); break; }
             if (part == 0) {
                 l = (misc->sum[0][h] + misc->sum[1][h]) + (misc->sum[2][h] + misc->sum[3][h]);
                 const float M = fmaxf(m2, sink2);
