@@ -9,8 +9,8 @@
 // k_rope.cu). A team computes the sines and cosines of a position together, one pair per lane at a
 // time, into its own part of shared memory; the lanes of rotated units read them from there (a lane
 // that computed those of its own units would take four to eight in turn while the other lanes wait).
-// In the half layout a rotated unit's lane loads the unit of its partners as well: a second read of a
-// line that the warp reads anyway.
+// In the half layout a rotated unit's partners are a shuffle away where a lane has one unit; where it has
+// more, it loads the unit of its partners as well: a second read of a line that the warp reads anyway.
 //
 // Where units do not fit (rows or rotated dims that start anywhere, D no multiple of 8) elements are
 // loaded and stored one by one and partners are exchanged through shared memory (ANY).
@@ -39,11 +39,16 @@ __device__ __forceinline__ void raw_to_f32(const Raw8<float> &r, float (&f)[8]) 
         f[4 * i + 2] = __uint_as_float(r.v[i].z); f[4 * i + 3] = __uint_as_float(r.v[i].w);
     }
 }
-template <typename S>
-__device__ __forceinline__ Raw8<S> raw_load(const S *p) {
-    Raw8<S> r;
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(S) / 2); ++i) r.v[i] = reinterpret_cast<const uint4 *>(p)[i];
+__device__ __forceinline__ Raw8<__nv_bfloat16> raw_load(const __nv_bfloat16 *p) {
+    Raw8<__nv_bfloat16> r;
+    r.v[0] = *reinterpret_cast<const uint4 *>(p);
+    return r;
+}
+__device__ __forceinline__ Raw8<float> raw_load(const float *p) {        // a whole sector per lane and access
+    Raw8<float> r;
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r.v[0].x), "=r"(r.v[0].y), "=r"(r.v[0].z), "=r"(r.v[0].w), "=r"(r.v[1].x), "=r"(r.v[1].y), "=r"(r.v[1].z), "=r"(r.v[1].w)
+                 : "l"(p));
     return r;
 }
 // n of 8 elements, one by one; the others 0
@@ -68,10 +73,7 @@ __device__ __forceinline__ Raw8<__nv_bfloat16> raw_load_any(const __nv_bfloat16 
     r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
     return r;
 }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) { store_sector(p, v); }
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
     uint32_t u[4];
 #pragma unroll
@@ -114,7 +116,8 @@ __device__ __forceinline__ void team_angles(const RowShape &g, const uint64_t *t
 
 template <typename S, int U, int FORM>
 struct RowBuf {
-    Raw8<S> a[U], b[FORM == kHalves ? U : 1];            // units, their partners
+    static constexpr bool kSecond = FORM == kHalves && U > 1;
+    Raw8<S> a[U], b[kSecond ? U : 1];                    // units, their partners
 
     __device__ __forceinline__ void load(const S *x, const RowShape &g) {
 #pragma unroll
@@ -125,7 +128,7 @@ struct RowBuf {
                 a[i] = raw_load_any(x + 8 * u, g.D - 8 * u);
             } else {
                 a[i] = raw_load(x + 8 * u);
-                if constexpr (FORM == kHalves) {
+                if constexpr (kSecond) {
                     const int n = g.dims / 8, ru = u - g.first / 8;
                     if (ru >= 0 && ru < n) b[i] = raw_load(x + 8 * (ru < n / 2 ? u + n / 2 : u - n / 2));
                 }
@@ -146,22 +149,24 @@ struct RowBuf {
                 for (int e = 0; e < 8; ++e) y[i][e] = 0.f;
             }
         }
-        float f = 1.f;
-        if (norm) {
+        // teams of one warp may differ in whether they norm: all take part in the sum
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                float2 q = make_float2(0.f, 0.f);
+        for (int i = 0; i < U; ++i) {
+            float2 q = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) q = fma2(make_float2(y[i][e], y[i][e + 1]), make_float2(y[i][e], y[i][e + 1]), q);
-                sum += q.x + q.y;
-            }
-            for (int o = g.T >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            f = 1.f / sqrtf(sum / (float)g.D + eps);
+            for (int e = 0; e < 8; e += 2) q = fma2(make_float2(y[i][e], y[i][e + 1]), make_float2(y[i][e], y[i][e + 1]), q);
+            sum += q.x + q.y;
         }
+        for (int o = g.T >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float f = rsqrtf(sum / (float)g.D + eps);       // within 2 steps of f32
         auto scaled = [&](float (&v)[8], int u) {
             if (!norm) return;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= f;
+            for (int e = 0; e < 8; e += 2) {
+                const float2 s = mul2(make_float2(v[e], v[e + 1]), make_float2(f, f));
+                v[e] = s.x;
+                v[e + 1] = s.y;
+            }
             if (!w) return;
             if constexpr (FORM == kAny) {
 #pragma unroll
@@ -169,43 +174,70 @@ struct RowBuf {
                     if (8 * u + e < g.D) v[e] *= __ldg(w + 8 * u + e);
             } else {
                 const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + 8 * u)), w1 = __ldg(reinterpret_cast<const float4 *>(w + 8 * u) + 1);
-                v[0] *= w0.x; v[1] *= w0.y; v[2] *= w0.z; v[3] *= w0.w;
-                v[4] *= w1.x; v[5] *= w1.y; v[6] *= w1.z; v[7] *= w1.w;
+                const float2 ww[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y), make_float2(w1.z, w1.w)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 s = mul2(make_float2(v[2 * e], v[2 * e + 1]), ww[e]);
+                    v[2 * e] = s.x;
+                    v[2 * e + 1] = s.y;
+                }
             }
         };
+        if constexpr (FORM == kHalves && U == 1) {
+            // one unit per lane: the partner's is in the lane half the rotated units away
+            const int n = g.dims / 8, ru = g.tl - g.first / 8;
+            const bool low = ru < n / 2;
+            if (g.tl < g.units) scaled(y[0], g.tl);
+            if (n) {
+                float q[8];
+                const int from = (threadIdx.x & 31) + (low ? n / 2 : -(n / 2));
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int u = i * g.T + g.tl;
-            if (u >= g.units) continue;
-            scaled(y[i], u);
-            if constexpr (FORM == kAny) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) g.row[8 * u + e] = y[i][e];
-            } else {
-                const int n = g.dims / 8, ru = u - g.first / 8;
-                if (ru < 0 || ru >= n) continue;
-                if constexpr (FORM == kPairs) {
-                    const float4 *cs = reinterpret_cast<const float4 *>(g.turn + 4 * ru);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float4 t = cs[k];
-                        const float a0 = y[i][4 * k], b0 = y[i][4 * k + 1], a1 = y[i][4 * k + 2], b1 = y[i][4 * k + 3];
-                        y[i][4 * k] = a0 * t.x - b0 * t.y;
-                        y[i][4 * k + 1] = a0 * t.y + b0 * t.x;
-                        y[i][4 * k + 2] = a1 * t.z - b1 * t.w;
-                        y[i][4 * k + 3] = a1 * t.w + b1 * t.z;
-                    }
-                } else {
-                    const bool low = ru < n / 2;
-                    float q[8];
-                    raw_to_f32(b[i], q);
-                    scaled(q, low ? u + n / 2 : u - n / 2);
+                for (int e = 0; e < 8; ++e) q[e] = __shfl_sync(0xffffffffu, y[0][e], from & 31);
+                if (ru >= 0 && ru < n) {
                     const float4 *cs = reinterpret_cast<const float4 *>(g.turn + 8 * (low ? ru : ru - n / 2));
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float4 t = cs[k];
-                        y[i][2 * k] = y[i][2 * k] * t.x + q[2 * k] * (low ? -t.y : t.y);
-                        y[i][2 * k + 1] = y[i][2 * k + 1] * t.z + q[2 * k + 1] * (low ? -t.w : t.w);
+                        y[0][2 * k] = y[0][2 * k] * t.x + q[2 * k] * (low ? -t.y : t.y);
+                        y[0][2 * k + 1] = y[0][2 * k + 1] * t.z + q[2 * k + 1] * (low ? -t.w : t.w);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int u = i * g.T + g.tl;
+                if (u >= g.units) continue;
+                scaled(y[i], u);
+                if constexpr (FORM == kAny) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g.row[8 * u + e] = y[i][e];
+                } else {
+                    const int n = g.dims / 8, ru = u - g.first / 8;
+                    if (ru < 0 || ru >= n) continue;
+                    if constexpr (FORM == kPairs) {
+                        const float4 *cs = reinterpret_cast<const float4 *>(g.turn + 4 * ru);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float4 t = cs[k];
+                            const float a0 = y[i][4 * k], b0 = y[i][4 * k + 1], a1 = y[i][4 * k + 2], b1 = y[i][4 * k + 3];
+                            y[i][4 * k] = a0 * t.x - b0 * t.y;
+                            y[i][4 * k + 1] = a0 * t.y + b0 * t.x;
+                            y[i][4 * k + 2] = a1 * t.z - b1 * t.w;
+                            y[i][4 * k + 3] = a1 * t.w + b1 * t.z;
+                        }
+                    } else {
+                        const bool low = ru < n / 2;
+                        float q[8];
+                        raw_to_f32(b[i], q);
+                        scaled(q, low ? u + n / 2 : u - n / 2);
+                        const float4 *cs = reinterpret_cast<const float4 *>(g.turn + 8 * (low ? ru : ru - n / 2));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 t = cs[k];
+                            y[i][2 * k] = y[i][2 * k] * t.x + q[2 * k] * (low ? -t.y : t.y);
+                            y[i][2 * k + 1] = y[i][2 * k + 1] * t.z + q[2 * k + 1] * (low ? -t.w : t.w);
+                        }
                     }
                 }
             }

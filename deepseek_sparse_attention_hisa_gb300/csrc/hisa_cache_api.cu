@@ -186,10 +186,11 @@ hisa_status hisa_norm_rope(const hisa_norm_rope_desc *d, const uint64_t *table, 
     p.x = x; p.x2 = x2; p.w = w; p.w2 = w2; p.y = y; p.y2 = y2;
     p.x_token = d->x_token; p.x_head = d->x_head; p.y_token = d->y_token; p.y_head = d->y_head;
     p.x2_token = d->x2_token; p.x2_head = d->x2_head; p.y2_token = d->y2_token; p.y2_head = d->y2_head;
-    auto wide = [](const void *a, int64_t token, int64_t head) { return aligned(a, 16) && token % 8 == 0 && head % 8 == 0; };
+    // units of 8 dims: 32 or 16 bytes at every boundary
+    auto wide = [](const void *a, int64_t token, int64_t head, size_t es) { return aligned(a, 8 * es) && token % 8 == 0 && head % 8 == 0; };
     p.wide = d->D % 8 == 0 && rope_wide(p.dims, p.first, p.half) && aligned(w, 16) && aligned(w2, 16) &&
-             wide(x, d->x_token, d->x_head) && wide(y, d->y_token, d->y_head) &&
-             (!d->heads2 || (wide(x2, d->x2_token, d->x2_head) && wide(y2, d->y2_token, d->y2_head)));
+             wide(x, d->x_token, d->x_head, ss) && wide(y, d->y_token, d->y_head, sd) &&
+             (!d->heads2 || (wide(x2, d->x2_token, d->x2_head, ss) && wide(y2, d->y2_token, d->y2_head, sd)));
     return from_cuda(launch_norm_rope(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -211,7 +212,7 @@ hisa_status hisa_cache_append(const hisa_cache_desc *d, const uint64_t *table, c
     p.norm = d->norm; p.eps = d->eps;
     p.dims = d->rope_dims; p.first = d->rope_dims ? d->rope_first : 0; p.half = d->half; p.r = d->r; p.mscale = d->mscale;
     p.table = table; p.x = x; p.w = w;
-    p.wide = rope_wide(p.dims, p.first, p.half) && aligned(x, 16) && d->ld % 8 == 0 && aligned(w, 16);
+    p.wide = rope_wide(p.dims, p.first, p.half) && aligned(x, 8 * dtype_bytes(d->io_dtype)) && d->ld % 8 == 0 && aligned(w, 16);
     return from_cuda(launch_cache_append(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -56,7 +56,7 @@ __device__ __forceinline__ void check_offsets(const CacheParams &p) {
 constexpr uint32_t kE4m3Nan = 0x7fu;
 
 // Eight f32 of a 16-dim group (the other eight in the neighbouring lane) to codes and the scale's byte.
-__device__ __forceinline__ uint32_t quantise(const float (&y)[8], float g, uint32_t &scale) {
+__device__ __forceinline__ uint32_t quantise(float (&y)[8], float g, uint32_t &scale) {
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
@@ -67,25 +67,35 @@ __device__ __forceinline__ uint32_t quantise(const float (&y)[8], float g, uint3
     scale = top < 0x7f800000u ? (uint32_t)two & 0xffu : kE4m3Nan;
     const float step = e4m3_to_f32(scale) * g;
     const float inv = step > 0.f ? 1.f / step : 0.f;         // NaN: 0 too, and its codes say nothing
+    if (a > 7.f * step) {                                     // the scale is at its largest, or 0
+        const float most = 8.f * step;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = fminf(fmaxf(y[e], -most), most);
+    }
+    const float2 ii = make_float2(inv, inv), ss = make_float2(step, step);
     uint32_t w = 0;
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
-        float q[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float v = y[e + k] * inv;
-            q[k] = fabsf(v) < 8.f ? fmaf(fmaf(-v, step, y[e + k]), inv, v) : v;
-        }
+        const float2 z = make_float2(y[e], y[e + 1]), v = mul2(z, ii), rest = fma2(make_float2(-v.x, -v.y), ss, z), q = fma2(rest, ii, v);
         uint32_t byte;
         asm("{.reg .b8 t, z; .reg .b16 h; cvt.rn.satfinite.e2m1x2.f32 t, %2, %1; mov.b16 h, {t, 0}; cvt.u32.u16 %0, h;}"
-            : "=r"(byte) : "f"(q[0]), "f"(q[1]));
+            : "=r"(byte) : "f"(q.x), "f"(q.y));
         w |= byte << (4 * e);
     }
     return w;
 }
 
+#ifndef AB
+#define AB 8
+#endif
+#ifndef RK
+#define RK 4
+#endif
+#ifndef CW
+#define CW 32
+#endif
 template <typename S, int U, int FORM>
-__global__ void __launch_bounds__(128) k_cache_append(CacheParams p) {
+__global__ void __launch_bounds__(128, FORM == kAny || U == 4 ? 1 : AB) k_cache_append(CacheParams p) {
     extern __shared__ __align__(16) float sm[];
     const RowShape g = row_shape(sm, p.D, p.lanes, p.first, p.dims, p.half, FORM == kAny);
     const int lane = threadIdx.x & 31, per = 32 / p.lanes, sub = lane / p.lanes;
@@ -152,12 +162,13 @@ __device__ __forceinline__ uint2 codes_to_e4m3(uint32_t w) {
     return make_uint2(out[0], out[1]);
 }
 
-template <int OUT, int U>                                  // OUT: hisa_dtype
+// A lane has units of 16 dims, those that share a scale: l, l + T, ... of its team of T lanes.
+template <int OUT, bool BITS4, int U>                      // OUT: hisa_dtype
 __global__ void __launch_bounds__(128) k_cache_read(CacheParams p) {
-    constexpr int kK = U == 1 ? 4 : 2;                     // rows in flight per team
+    constexpr int kK = RK / U;                             // rows in flight per team
     const int lane = threadIdx.x & 31, T = p.lanes, per = 32 / T, sub = lane / T, tl = lane & (T - 1);
     const int64_t n0 = ((int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32) * p.chunk;
-    const int units = p.D / 8;
+    const int units = p.D / 16;
     grid_dep_wait();
     grid_dep_trigger();
     check_offsets(p);
@@ -167,8 +178,9 @@ __global__ void __launch_bounds__(128) k_cache_read(CacheParams p) {
     if (lane < n) mine = place_of(p, n0 + lane).slot;
     for (int r0 = 0; r0 < n; r0 += per * kK) {
         int64_t slot[kK];
-        uint32_t w[kK][U], sc[kK][U];
-        uint4 raw[kK][U];
+        uint2 w[kK][U];
+        uint32_t sc[kK][U];
+        Raw8<__nv_bfloat16> raw[kK][U][2];
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
             const int r = r0 + k * per + sub;
@@ -178,11 +190,12 @@ __global__ void __launch_bounds__(128) k_cache_read(CacheParams p) {
             for (int i = 0; i < U; ++i) {
                 const int u = i * T + tl;
                 if (slot[k] < 0 || u >= units) continue;
-                if (p.bits4) {
-                    w[k][i] = reinterpret_cast<const uint32_t *>(p.cache)[slot[k] * units + u];
-                    sc[k][i] = p.scales[slot[k] * (units / 2) + u / 2];
+                if constexpr (BITS4) {
+                    w[k][i] = reinterpret_cast<const uint2 *>(p.cache)[slot[k] * units + u];
+                    sc[k][i] = p.scales[slot[k] * units + u];
                 } else {
-                    raw[k][i] = reinterpret_cast<const uint4 *>(p.cache)[slot[k] * units + u];
+                    raw[k][i][0].v[0] = reinterpret_cast<const uint4 *>(p.cache)[(slot[k] * units + u) * 2];
+                    raw[k][i][1].v[0] = reinterpret_cast<const uint4 *>(p.cache)[(slot[k] * units + u) * 2 + 1];
                 }
             }
         }
@@ -195,26 +208,37 @@ __global__ void __launch_bounds__(128) k_cache_read(CacheParams p) {
                 const int u = i * T + tl;
                 if (u >= units) continue;
                 if constexpr (OUT == HISA_E4M3) {
-                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + row * p.ld + 8 * u) = codes_to_e4m3(w[k][i]);
-                    if (p.out_scales && !(u & 1)) p.out_scales[row * (units / 2) + u / 2] = e4m3_to_f32(sc[k][i]) * p.g;
+                    const uint2 lo = codes_to_e4m3(w[k][i].x), hi = codes_to_e4m3(w[k][i].y);
+                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + row * p.ld + 16 * u) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    if (p.out_scales) p.out_scales[row * units + u] = e4m3_to_f32(sc[k][i]) * p.g;
                 } else {
-                    float f[8];
-                    if (p.bits4) {
-                        unpack_e2m1(w[k][i], f);
-                        const float s = e4m3_to_f32(sc[k][i]) * p.g;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] *= s;
-                    } else {
-                        Raw8<__nv_bfloat16> b;
-                        b.v[0] = raw[k][i];
-                        raw_to_f32(b, f);
-                    }
-                    if constexpr (OUT == HISA_F32) {
-                        float *to = static_cast<float *>(p.out) + row * p.ld + 8 * u;
-                        if (p.out32) store_sector(to, f);
-                        else store8(to, f);
-                    } else {
-                        store8(static_cast<__nv_bfloat16 *>(p.out) + row * p.ld + 8 * u, f);
+                    for (int half = 0; half < 2; ++half) {
+                        float f[8];
+                        if constexpr (BITS4) {
+                            unpack_e2m1(half ? w[k][i].y : w[k][i].x, f);
+                            const float s = e4m3_to_f32(sc[k][i]) * p.g;
+#pragma unroll
+                            for (int e = 0; e < 8; e += 2) {
+                                const float2 z = mul2(make_float2(f[e], f[e + 1]), make_float2(s, s));
+                                f[e] = z.x;
+                                f[e + 1] = z.y;
+                            }
+                        } else {
+                            raw_to_f32(raw[k][i][half], f);
+                        }
+                        const int64_t at = row * p.ld + 16 * u + 8 * half;
+                        if constexpr (OUT == HISA_F32) {
+                            float *to = static_cast<float *>(p.out) + at;
+                            if (p.out32) {
+                                store_sector(to, f);
+                            } else {
+                                reinterpret_cast<float4 *>(to)[0] = make_float4(f[0], f[1], f[2], f[3]);
+                                reinterpret_cast<float4 *>(to)[1] = make_float4(f[4], f[5], f[6], f[7]);
+                            }
+                        } else {
+                            store8(static_cast<__nv_bfloat16 *>(p.out) + at, f);
+                        }
                     }
                 }
             }
@@ -226,15 +250,15 @@ __global__ void __launch_bounds__(128) k_cache_read(CacheParams p) {
 // scheduler slot of the GPU.
 int chunk_of(int64_t rows, int per, int sms) {
     int chunk = 32;
-    while (chunk > per && rows / chunk < 32 * (int64_t)sms) chunk /= 2;
+    while (chunk > per && rows / chunk < CW * (int64_t)sms) chunk /= 2;
     return chunk;
 }
 
 template <typename K>
-cudaError_t launch_rows(K kernel, CacheParams p, size_t smem, cudaStream_t s) {
+cudaError_t launch_rows(K kernel, CacheParams p, int lanes, size_t smem, cudaStream_t s) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    p.lanes = team_lanes(p.D);
+    p.lanes = lanes;
     p.chunk = chunk_of(p.rows, 32 / p.lanes, sms);
     const int64_t warps = (p.rows + p.chunk - 1) / p.chunk, grid = (warps + 3) / 4;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -243,7 +267,7 @@ cudaError_t launch_rows(K kernel, CacheParams p, size_t smem, cudaStream_t s) {
 
 template <typename S, int U, int FORM>
 cudaError_t append_as(const CacheParams &p, cudaStream_t s) {
-    return launch_rows(k_cache_append<S, U, FORM>, p, team_smem(p.D, p.dims, 4, FORM == kAny), s);
+    return launch_rows(k_cache_append<S, U, FORM>, p, team_lanes(p.D), team_smem(p.D, p.dims, 4, FORM == kAny), s);
 }
 template <typename S>
 cudaError_t append(const CacheParams &p, cudaStream_t s) {
@@ -252,10 +276,11 @@ cudaError_t append(const CacheParams &p, cudaStream_t s) {
     if (p.half) return U == 1 ? append_as<S, 1, kHalves>(p, s) : (U == 2 ? append_as<S, 2, kHalves>(p, s) : append_as<S, 4, kHalves>(p, s));
     return U == 1 ? append_as<S, 1, kPairs>(p, s) : (U == 2 ? append_as<S, 2, kPairs>(p, s) : append_as<S, 4, kPairs>(p, s));
 }
-template <int OUT>
-cudaError_t read(const CacheParams &p, cudaStream_t s) {
-    const int U = team_units(p.D);
-    return U == 1 ? launch_rows(k_cache_read<OUT, 1>, p, 0, s) : (U == 2 ? launch_rows(k_cache_read<OUT, 2>, p, 0, s) : launch_rows(k_cache_read<OUT, 4>, p, 0, s));
+template <int OUT, bool BITS4>
+cudaError_t read_as(const CacheParams &p, cudaStream_t s) {
+    int T = 2;
+    while (T < p.D / 16 && T < 32) T *= 2;
+    return p.D <= 512 ? launch_rows(k_cache_read<OUT, BITS4, 1>, p, T, 0, s) : launch_rows(k_cache_read<OUT, BITS4, 2>, p, T, 0, s);
 }
 
 }  // namespace
@@ -265,8 +290,9 @@ cudaError_t launch_cache_append(const CacheParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_cache_read(const CacheParams &p, cudaStream_t s) {
-    if (p.io_dtype == HISA_F32) return read<HISA_F32>(p, s);
-    return p.io_dtype == HISA_BF16 ? read<HISA_BF16>(p, s) : read<HISA_E4M3>(p, s);
+    if (p.io_dtype == HISA_E4M3) return read_as<HISA_E4M3, true>(p, s);
+    if (p.io_dtype == HISA_F32) return p.bits4 ? read_as<HISA_F32, true>(p, s) : read_as<HISA_F32, false>(p, s);
+    return p.bits4 ? read_as<HISA_BF16, true>(p, s) : read_as<HISA_BF16, false>(p, s);
 }
 
 }  // namespace hisa

@@ -1,8 +1,14 @@
 // The norm of each head and rotary positions in one pass over queries and keys.
 //
 // Bound by memory: each head is read once and written once. A team of lanes (head_rows.cuh) takes a run
-// of heads of one token, so that a token's sines and cosines are computed once per run; two heads
-// are in flight per team.
+// of up to 8 heads of one token, so that a token's sines and cosines are computed once per run. In flight are
+// 32 warps per SM, each with one head of more than 256 dims or, for each of its teams, four of fewer (two in f32): 4096 x 65 x 512 f32
+// to bf16 133 us with one head per team, 150 with two (more than memory serves at once, and registers);
+// 2047 x 64 x 128 bf16 with halves 25.1, 21.3 and 19.9 us with one, two and four. Runs of 16 heads:
+// 147 us and the same.
+//
+// Measured: the first of these 6.1 TB/s, 90 % of a plain copy's rate; the second 3.4 TB/s: a chain of load,
+// sum over lanes, angles and store per head, with too few bytes in flight; a token of 64 + 1 heads of 512 4.7 us per call.
 #include "cache_internal.cuh"
 #include "head_rows.cuh"
 
@@ -13,8 +19,8 @@ template <int FORM>
 constexpr int kWarps = FORM == kAny ? 4 : 8;
 
 template <typename S, typename Y, int U, int FORM>
-__global__ void __launch_bounds__(32 * kWarps<FORM>) k_norm_rope(NormRopeParams p) {
-    constexpr int kK = U == 4 ? 1 : 2;                    // heads in flight
+__global__ void __launch_bounds__(32 * kWarps<FORM>, FORM == kAny ? 1 : (U == 4 ? 2 : 4)) k_norm_rope(NormRopeParams p) {
+    constexpr int kK = U > 1 ? 1 : (sizeof(S) == 2 ? 4 : 2);   // heads in flight per team
     extern __shared__ __align__(16) float sm[];
     const RowShape g = row_shape(sm, p.D, p.lanes, p.first, p.dims, p.half, FORM == kAny);
     const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / p.lanes;
@@ -61,7 +67,7 @@ cudaError_t go(NormRopeParams p, cudaStream_t s) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     // heads of a run: as many as leave a warp for every scheduler slot of the GPU
-    p.run = 16;
+    p.run = 8;
     auto teams = [&](int run) { return p.tokens * ((p.heads + run - 1) / run + (p.heads2 + run - 1) / run); };
     while (p.run > 1 && teams(p.run) * p.lanes / 32 < 32 * (int64_t)sms) p.run /= 2;
     p.runs1 = (p.heads + p.run - 1) / p.run;
