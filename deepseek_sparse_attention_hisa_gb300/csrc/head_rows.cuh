@@ -100,6 +100,7 @@ struct RowShape {
     int units;                // of 8 dims, the last one cut if D is no multiple of 8 (ANY)
     int first, dims;          // the rotated dims
     int half;
+    float inv;                // 1 / D
     float2 *turn;             // the team's [dims / 2] (cos, sin), times mscale
     float *row;               // ANY: the team's [8 units] f32
 };
@@ -137,8 +138,10 @@ struct RowBuf {
     }
 
     // The row's f32 values, normed (norm) and turned, in y[i] for unit i T + tl. All lanes of the warp
-    // take part.
-    __device__ __forceinline__ void finish(const RowShape &g, bool norm, const float *w, float eps, float (&y)[U][8]) const {
+    // take part. HELD: w's values of this lane's units are in held, and w only says that there are any.
+    template <bool HELD = false>
+    __device__ __forceinline__ void finish(const RowShape &g, bool norm, const float *w, float eps, float (&y)[U][8],
+                                           const float2 (*held)[4] = nullptr) const {
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -158,8 +161,8 @@ struct RowBuf {
             sum += q.x + q.y;
         }
         for (int o = g.T >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float f = rsqrtf(sum / (float)g.D + eps);       // within 2 steps of f32
-        auto scaled = [&](float (&v)[8], int u) {
+        const float f = rsqrtf(sum * g.inv + eps);            // within 2 steps of f32
+        auto scaled = [&](float (&v)[8], int u, int own) {
             if (!norm) return;
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
@@ -172,6 +175,13 @@ struct RowBuf {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (8 * u + e < g.D) v[e] *= __ldg(w + 8 * u + e);
+            } else if (HELD && own >= 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 s = mul2(make_float2(v[2 * e], v[2 * e + 1]), held[own < 0 ? 0 : own][e]);
+                    v[2 * e] = s.x;
+                    v[2 * e + 1] = s.y;
+                }
             } else {
                 const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + 8 * u)), w1 = __ldg(reinterpret_cast<const float4 *>(w + 8 * u) + 1);
                 const float2 ww[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y), make_float2(w1.z, w1.w)};
@@ -187,7 +197,7 @@ struct RowBuf {
             // one unit per lane: the partner's is in the lane half the rotated units away
             const int n = g.dims / 8, ru = g.tl - g.first / 8;
             const bool low = ru < n / 2;
-            if (g.tl < g.units) scaled(y[0], g.tl);
+            if (g.tl < g.units) scaled(y[0], g.tl, 0);
             if (n) {
                 float q[8];
                 const int from = (threadIdx.x & 31) + (low ? n / 2 : -(n / 2));
@@ -208,7 +218,7 @@ struct RowBuf {
             for (int i = 0; i < U; ++i) {
                 const int u = i * g.T + g.tl;
                 if (u >= g.units) continue;
-                scaled(y[i], u);
+                scaled(y[i], u, i);
                 if constexpr (FORM == kAny) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) g.row[8 * u + e] = y[i][e];
@@ -230,7 +240,7 @@ struct RowBuf {
                         const bool low = ru < n / 2;
                         float q[8];
                         raw_to_f32(b[i], q);
-                        scaled(q, low ? u + n / 2 : u - n / 2);
+                        scaled(q, low ? u + n / 2 : u - n / 2, -1);
                         const float4 *cs = reinterpret_cast<const float4 *>(g.turn + 8 * (low ? ru : ru - n / 2));
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -282,7 +292,7 @@ inline size_t team_smem(int D, int dims, int warps, bool any) {
 // This lane's RowShape: the CTA's shared memory holds all teams' angles, then (ANY) their rows.
 __device__ __forceinline__ RowShape row_shape(float *sm, int D, int T, int first, int dims, int half, bool any) {
     RowShape g;
-    g.D = D; g.T = T; g.units = (D + 7) / 8;
+    g.D = D; g.T = T; g.units = (D + 7) / 8; g.inv = 1.f / (float)D;
     g.first = first; g.dims = dims; g.half = half;
     const int lane = threadIdx.x & 31;
     g.tl = lane & (T - 1);

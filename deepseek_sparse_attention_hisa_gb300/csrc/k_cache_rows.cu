@@ -56,17 +56,22 @@ __device__ __forceinline__ void check_offsets(const CacheParams &p) {
 constexpr uint32_t kE4m3Nan = 0x7fu;
 
 // Eight f32 of a 16-dim group (the other eight in the neighbouring lane) to codes and the scale's byte.
-__device__ __forceinline__ uint32_t quantise(float (&y)[8], float g, uint32_t &scale) {
+__device__ __forceinline__ uint32_t quantise(float (&y)[8], float g, float inv6g, uint32_t &scale) {
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     const float a = __uint_as_float(top);
+    // a / 6 g by the reciprocal, corrected by the exact remainder; past 448 it does not matter by how much
+    float t = fminf(a * inv6g, 1e6f);
+    t = fmaf(fmaf(-t, 6.f * g, a), inv6g, t);
     uint16_t two;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(a / (6.f * g)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(t));
     scale = top < 0x7f800000u ? (uint32_t)two & 0xffu : kE4m3Nan;
     const float step = e4m3_to_f32(scale) * g;
-    const float inv = step > 0.f ? 1.f / step : 0.f;         // NaN: 0 too, and its codes say nothing
+    float inv;                                                // to a step or two: what it scales is corrected
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+    inv = step > 0.f ? inv : 0.f;                             // NaN: 0 too, and its codes say nothing
     if (a > 7.f * step) {                                     // the scale is at its largest, or 0
         const float most = 8.f * step;
 #pragma unroll
@@ -85,17 +90,12 @@ __device__ __forceinline__ uint32_t quantise(float (&y)[8], float g, uint32_t &s
     return w;
 }
 
-#ifndef AB
-#define AB 8
-#endif
-#ifndef RK
-#define RK 4
-#endif
-#ifndef CW
-#define CW 32
-#endif
+// CTAs per SM that the registers leave room for: as many as there is no spilling with
 template <typename S, int U, int FORM>
-__global__ void __launch_bounds__(128, FORM == kAny || U == 4 ? 1 : AB) k_cache_append(CacheParams p) {
+constexpr int kAppendCtas = FORM == kAny || U == 4 ? 2 : (U == 2 && (sizeof(S) == 4 || FORM == kHalves) ? 4 : (sizeof(S) == 4 ? 6 : 8));
+
+template <typename S, int U, int FORM>
+__global__ void __launch_bounds__(128, kAppendCtas<S, U, FORM>) k_cache_append(CacheParams p) {
     extern __shared__ __align__(16) float sm[];
     const RowShape g = row_shape(sm, p.D, p.lanes, p.first, p.dims, p.half, FORM == kAny);
     const int lane = threadIdx.x & 31, per = 32 / p.lanes, sub = lane / p.lanes;
@@ -108,6 +108,18 @@ __global__ void __launch_bounds__(128, FORM == kAny || U == 4 ? 1 : AB) k_cache_
     Place mine{-1, 0};
     if (lane < n) mine = place_of(p, n0 + lane);
     const S *x = static_cast<const S *>(p.x) + n0 * p.ld;
+    const float inv6g = 1.f / (6.f * p.g);
+    constexpr bool kHeld = FORM != kAny && U <= 2;
+    float2 held[U][4];
+    if (kHeld && p.w) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int u = i * g.T + g.tl;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                held[i][e] = u < g.units ? __ldg(reinterpret_cast<const float2 *>(p.w + 8 * u) + e) : make_float2(0.f, 0.f);
+        }
+    }
     RowBuf<S, U, FORM> buf = {};
     auto slot_of = [&](int r) { return __shfl_sync(0xffffffffu, mine.slot, r & 31); };
     int64_t slot = slot_of(sub);
@@ -126,13 +138,13 @@ __global__ void __launch_bounds__(128, FORM == kAny || U == 4 ? 1 : AB) k_cache_
             __syncwarp();
         }
         float v[U][8];
-        cur.finish(g, p.norm, p.w, p.eps, v);
+        cur.template finish<kHeld>(g, p.norm, p.w, p.eps, v, held);
         if (p.bits4) {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int u = i * g.T + g.tl;             // lanes past the row have zeros
                 uint32_t scale;
-                const uint32_t w = quantise(v[i], p.g, scale);
+                const uint32_t w = quantise(v[i], p.g, inv6g, scale);
                 if (here < 0 || u >= g.units) continue;
                 reinterpret_cast<uint32_t *>(p.cache)[here * (p.D / 8) + u] = w;
                 if (!(u & 1)) p.scales[here * (p.D / kScaleGroup) + u / 2] = (uint8_t)scale;
@@ -165,7 +177,7 @@ __device__ __forceinline__ uint2 codes_to_e4m3(uint32_t w) {
 // A lane has units of 16 dims, those that share a scale: l, l + T, ... of its team of T lanes.
 template <int OUT, bool BITS4, int U>                      // OUT: hisa_dtype
 __global__ void __launch_bounds__(128) k_cache_read(CacheParams p) {
-    constexpr int kK = RK / U;                             // rows in flight per team
+    constexpr int kK = 4 / U;                              // rows in flight per team
     const int lane = threadIdx.x & 31, T = p.lanes, per = 32 / T, sub = lane / T, tl = lane & (T - 1);
     const int64_t n0 = ((int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32) * p.chunk;
     const int units = p.D / 16;
@@ -246,28 +258,29 @@ __global__ void __launch_bounds__(128) k_cache_read(CacheParams p) {
     }
 }
 
-// Rows of a warp's chunk: whole rounds of its teams, up to 32, while there are warps for every
-// scheduler slot of the GPU.
-int chunk_of(int64_t rows, int per, int sms) {
+// Rows of a warp's chunk: whole rounds of its teams, up to 32, while there are `warps` warps per SM.
+// Reading wants as many as fit (65536 rows of 512 dims to f32 29 us with 64 per SM, 36 with 32), appending
+// half of that (20000 rows of 128 f32 dims 6.9 us with 32, 8.1 with 64): a chunk's places cost a chain of loads.
+int chunk_of(int64_t rows, int per, int warps, int sms) {
     int chunk = 32;
-    while (chunk > per && rows / chunk < CW * (int64_t)sms) chunk /= 2;
+    while (chunk > per && rows / chunk < warps * (int64_t)sms) chunk /= 2;
     return chunk;
 }
 
 template <typename K>
-cudaError_t launch_rows(K kernel, CacheParams p, int lanes, size_t smem, cudaStream_t s) {
+cudaError_t launch_rows(K kernel, CacheParams p, int lanes, int warps, size_t smem, cudaStream_t s) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     p.lanes = lanes;
-    p.chunk = chunk_of(p.rows, 32 / p.lanes, sms);
-    const int64_t warps = (p.rows + p.chunk - 1) / p.chunk, grid = (warps + 3) / 4;
+    p.chunk = chunk_of(p.rows, 32 / p.lanes, warps, sms);
+    const int64_t all = (p.rows + p.chunk - 1) / p.chunk, grid = (all + 3) / 4;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_pdl(kernel, dim3((unsigned)grid), dim3(128), smem, s, 1, p);
 }
 
 template <typename S, int U, int FORM>
 cudaError_t append_as(const CacheParams &p, cudaStream_t s) {
-    return launch_rows(k_cache_append<S, U, FORM>, p, team_lanes(p.D), team_smem(p.D, p.dims, 4, FORM == kAny), s);
+    return launch_rows(k_cache_append<S, U, FORM>, p, team_lanes(p.D), 32, team_smem(p.D, p.dims, 4, FORM == kAny), s);
 }
 template <typename S>
 cudaError_t append(const CacheParams &p, cudaStream_t s) {
@@ -280,7 +293,7 @@ template <int OUT, bool BITS4>
 cudaError_t read_as(const CacheParams &p, cudaStream_t s) {
     int T = 2;
     while (T < p.D / 16 && T < 32) T *= 2;
-    return p.D <= 512 ? launch_rows(k_cache_read<OUT, BITS4, 1>, p, T, 0, s) : launch_rows(k_cache_read<OUT, BITS4, 2>, p, T, 0, s);
+    return p.D <= 512 ? launch_rows(k_cache_read<OUT, BITS4, 1>, p, T, 64, 0, s) : launch_rows(k_cache_read<OUT, BITS4, 2>, p, T, 64, 0, s);
 }
 
 }  // namespace

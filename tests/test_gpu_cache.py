@@ -779,3 +779,23 @@ def test_calls_follow_one_another():
             p = torch.softmax(q[n, b, 0].double() @ v.t() / math.sqrt(Dh), -1)
             err = (outs[n, b, 0].double() - p @ v).abs()
             assert (err <= (p @ v.abs()) * (half_step("bf16") + 1e-3)).all()
+
+
+# ------------------------------------------------------------------------------------
+# together: a layer's decode step
+# ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("batch,pooled,hidden,steps,select,bits4,page", [(5, 300, 1024, 9, 0, True, 64), (3, 70, 1000, 6, 0, False, 16),
+                                                                          (9, 900, 1024, 5, 128, True, 48), (2, 10, 512, 5, 64, False, 1)])
+def test_paged_decode(batch, pooled, hidden, steps, select, bits4, page):
+    # Queries and rows, the weights of the softmax, and the output are each rounded to bf16 (half a
+    # step, 2^-8 of a value at most); normed queries of weight 2 give logits of about 2 standard deviations, up to
+    # 10, whose share turns into 2 * 2^-8 * 10 of the weights. The last rotation rounds once more. All of it
+    # stays below a tenth of the largest output.
+    import os
+    import sys
+
+    import deepseek_sparse_attention_hisa_gb300 as pkg
+    root = os.path.dirname(os.path.dirname(os.path.abspath(pkg.__file__)))
+    sys.path.insert(0, os.path.join(root, "examples"))
+    import paged_decode
+    assert paged_decode.run(batch, pooled, hidden, steps, select, bits4, page, say=lambda *_: None) < 0.1

@@ -1,0 +1,147 @@
+"""PagedDecode without a GPU: what it refuses before any call, how it shares out pages, and the
+descriptors it passes on."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from deepseek_sparse_attention_hisa_gb300 import binding as hb  # noqa: E402
+from deepseek_sparse_attention_hisa_gb300 import build  # noqa: E402
+from deepseek_sparse_attention_hisa_gb300.paged import DH, H, PagedDecode  # noqa: E402
+
+BF16, HIDDEN = torch.bfloat16, 64
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The entry points that need a GPU record their descriptors instead of running."""
+    build.build_library()
+    seen = []
+    monkeypatch.setattr(hb, "alloc_workspace", lambda n, device: torch.zeros(max(n, 256), dtype=torch.uint8))
+    monkeypatch.setattr(hb, "rms_norm", lambda d, x, r, *a: seen.append(("norm", d.ld_x, d.ld_res, x.data_ptr(), r.data_ptr())))
+    monkeypatch.setattr(hb, "norm_rope", lambda d, *a: seen.append(("heads", d.y2_token, a[-1].data_ptr())))
+    monkeypatch.setattr(hb, "rope", lambda *a: seen.append(("rope",)))
+    monkeypatch.setattr(hb, "cache_append", lambda d, t, x, w, off, first, *a: seen.append(
+        ("append", d.rows, d.ld, off.tolist(), first.tolist())))
+    monkeypatch.setattr(hb, "cache_read", lambda d, *a: seen.append(("read", d.rows)))
+    monkeypatch.setattr(hb, "cache_attend", lambda d, *a: seen.append(("attend", d.k, a[8] is None, a[7].tolist())))
+    return seen
+
+
+def weights(**kw):
+    w = {"norm": torch.ones(HIDDEN), "q": torch.zeros(HIDDEN, H * DH, dtype=BF16), "kv": torch.zeros(HIDDEN, DH, dtype=BF16),
+         "sinks": torch.zeros(H), "q_norm": None, "kv_norm": torch.ones(DH)}
+    w.update(kw)
+    return w
+
+
+def layer(B=3, w=None, **kw):
+    d = dict(start=32, steps=4, pages=6, max_rows=12, page_rows=4, device="cpu")
+    d.update(kw)
+    return PagedDecode(B, w or weights(), **d)
+
+
+def rows(n=3, hidden=HIDDEN, dtype=BF16):
+    return torch.zeros(n, hidden, dtype=dtype)
+
+
+def test_pages_are_shared_out(calls):
+    p = layer()
+    p.append(rows(9, DH), [1, 4, 4])
+    assert calls[-1] == ("append", 9, DH, [0, 1, 5, 9], [0, 0, 0])
+    assert [len(x) for x in p.owned] == [1, 1, 1] and p.cache_len.tolist() == [1, 4, 4]
+    p.append(rows(4, DH, torch.float32), [3, 0, 1])
+    assert calls[-1] == ("append", 4, DH, [0, 3, 3, 4], [1, 4, 4])
+    assert [len(x) for x in p.owned] == [1, 1, 2] and len(p.free) == 2
+    used = p.page_table[p.page_table >= 0].tolist()
+    assert sorted(used) == sorted(sum(p.owned, [])) and len(set(used)) == 4
+    with pytest.raises(ValueError, match="pages"):
+        p.append(rows(16, DH), [8, 8, 0])
+    assert p.lens == [4, 4, 5] and len(p.free) == 2              # nothing has changed
+    with pytest.raises(ValueError, match="max_rows"):
+        p.append(rows(9, DH), [9, 0, 0])
+    p.release(2)
+    assert len(p.free) == 4 and p.cache_len.tolist() == [4, 4, 0] and (p.page_table[2] == -1).all()
+    p.append(rows(8, DH), [0, 8, 0])
+    assert calls[-1][3:] == ([0, 0, 8, 8], [4, 4, 0]) and p.lens == [4, 12, 0]
+    n = len(calls)
+    p.append(rows(0, DH), [0, 0, 0])
+    assert len(calls) == n
+
+
+@pytest.mark.parametrize("bad,counts", [(rows(3, DH), [1, 1]), (rows(3, DH), [2, 2, 0]), (rows(2, DH), [3, -1, 0]), (rows(3, DH, torch.float16), [1, 1, 1]),
+                                        (rows(3, DH // 2), [1, 1, 1]), (rows(3, 2 * DH)[:, ::2], [1, 1, 1])])
+def test_appended_rows_are_checked(calls, bad, counts):
+    p = layer()
+    with pytest.raises(ValueError):
+        p.append(bad, counts)
+    assert calls == [] and p.lens == [0, 0, 0] and len(p.free) == 6
+
+
+def test_rows_are_read_by_their_length(calls):
+    p = layer()
+    assert p.rows(0).shape == (0, DH) and calls == []
+    p.append(rows(5, 2 * DH)[:, DH:], [0, 5, 0])
+    assert calls[-1][2] == 2 * DH
+    assert p.rows(1).shape == (5, DH) and calls[-1] == ("read", 5)
+    assert p.rows(1, torch.float32).dtype == torch.float32
+    with pytest.raises(ValueError):
+        p.rows(1, torch.float16)
+
+
+def test_a_step_in_order(calls):
+    p = layer(start=[5, 6, 7])
+    x, r = rows(3, 3 * HIDDEN)[:, HIDDEN:2 * HIDDEN], rows(6)[::2]
+    p.step(x, r)
+    assert [c[0] for c in calls] == ["norm", "heads", "attend", "rope"]
+    assert calls[0] == ("norm", 3 * HIDDEN, 2 * HIDDEN, x.data_ptr(), r.data_ptr())
+    assert calls[1][1:] == (4 * DH, p.local.data_ptr())
+    assert p.pos.tolist() == [6, 7, 8] and p.local_pos0.tolist() == [5, 6, 7] and p.local_len.tolist() == [1, 1, 1]
+    p.step(rows(), rows(), torch.zeros(3, 2, dtype=torch.int32))
+    assert calls[5][2] == p.local[:, 1].data_ptr() and calls[6][:3] == ("attend", 2, False)
+    p.step(rows(), rows(), torch.zeros(3, 0, dtype=torch.int32))
+    assert calls[10][:3] == ("attend", 0, True)
+    p.step(rows(), rows())
+    with pytest.raises(ValueError, match="full"):
+        p.step(rows(), rows())
+
+
+@pytest.mark.parametrize("which", ["x", "residual"])
+@pytest.mark.parametrize("bad", [rows(2), rows(3, HIDDEN - 8), rows(dtype=torch.float32), rows()[0], rows(HIDDEN, 3).t(), rows(3, 2 * HIDDEN)[:, ::2],
+                                 rows(1).expand(3, HIDDEN), torch.empty(3, HIDDEN, dtype=BF16, device="meta")])
+def test_step_refuses_other_tensors(calls, which, bad):
+    p = layer()
+    with pytest.raises(ValueError):
+        p.step(*((bad, rows()) if which == "x" else (rows(), bad)))
+    assert calls == [] and p.n == 0
+
+
+@pytest.mark.parametrize("bad", [torch.zeros(2, 4, dtype=torch.int32), torch.zeros(3, 4, dtype=torch.int64), torch.zeros(3, dtype=torch.int32),
+                                 torch.zeros(3, 8, dtype=torch.int32)[:, ::2], torch.zeros(3, 65537, dtype=torch.int32)])
+def test_step_refuses_other_ids(calls, bad):
+    p = layer()
+    with pytest.raises(ValueError):
+        p.step(rows(), rows(), bad)
+    assert calls == [] and p.n == 0
+
+
+@pytest.mark.parametrize("name,bad", [("norm", torch.ones(HIDDEN, dtype=BF16)), ("q", torch.zeros(HIDDEN, DH, dtype=BF16)),
+                                      ("kv", torch.zeros(HIDDEN, DH)), ("sinks", torch.zeros(H - 1)), ("q_norm", torch.ones(H)),
+                                      ("kv_norm", torch.ones(DH, dtype=BF16)), ("kv_norm", torch.ones(2 * DH)[::2])])
+def test_weights_are_checked(calls, name, bad):
+    with pytest.raises(ValueError, match=name):
+        layer(w=weights(**{name: bad}))
+
+
+@pytest.mark.parametrize("kw", [dict(B=0), dict(steps=0), dict(start=-1), dict(start=2**31 - 3), dict(start=[1, 2]), dict(pages=0), dict(page_rows=0),
+                                dict(max_rows=-1), dict(r=0)])
+def test_sizes_are_checked(calls, kw):
+    with pytest.raises(ValueError):
+        layer(**kw)
+
+
+def test_bf16_pages(calls):
+    p = layer(bits4=False, w=weights(sinks=None, kv_norm=None))
+    assert p.scales is None and p.pool.dtype == BF16 and p.pool.shape == (6, 4, DH)
+    p.append(rows(3, DH), [1, 1, 1])
+    p.step(rows(), rows())
+    assert [c[0] for c in calls] == ["append", "norm", "heads", "attend", "rope"]
