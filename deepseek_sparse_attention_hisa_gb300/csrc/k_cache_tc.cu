@@ -228,16 +228,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
         }
         for (int i = 0; i < kBufs; ++i) {
             mbar_init(&misc->sfull[i], 1);
-            mbar_init(&misc->sfree[i], 32 * kSoftWarps);
+            mbar_init(&misc->sfree[i], kSoftWarps);
         }
-        mbar_init(&misc->pfull, 32 * kSoftWarps);
+        mbar_init(&misc->pfull, kSoftWarps);
         mbar_init(&misc->pfree, 1);
         for (int i = 0; i < kPlaces; ++i) {
             mbar_init(&misc->ifull[i], 2);
             mbar_init(&misc->ifree[i], kRowWarps + kSoftWarps);
         }
         mbar_init(&misc->ofull, 1);
-        mbar_init(&misc->ofree, 32 * kSoftWarps);
+        mbar_init(&misc->ofree, kSoftWarps);
         mbar_init(&misc->drain, 2);                      // one commit from each issuing warp
         mbar_fence_init();
         misc->abort = 0;
@@ -271,11 +271,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
         }
         if (lane == 31) misc->sums[warp] = upto;
         __syncthreads();
-        int64_t total = 0, before = 0;
-        for (int i = 0; i < kThreads / 32; ++i) {
-            if (i == warp) before = total;
-            total += misc->sums[i];
+        int64_t before = lane < kThreads / 32 ? misc->sums[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
         }
+        const int64_t total = __shfl_sync(0xffffffffu, before, 31);
+        before = __shfl_sync(0xffffffffu, before, warp > 0 ? warp - 1 : 0);
+        if (warp == 0) before = 0;
         // at most as many spans as there are tiles: none is empty
         const int64_t most = total < (int64_t)gridDim.x * p.least ? (int64_t)((uint32_t)total / (uint32_t)p.least) : (int64_t)gridDim.x;
         const int groups = most < 1 ? 1 : (int)most, c = blockIdx.x;
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
         }
         if (s0 >= at && s0 < at + sum) {
             for (int64_t r = r0; r < r1; ++r) {
-                const int n = tiles_of(cache_row(p, r, false));
+                const int n = per == 1 ? (int)sum : tiles_of(cache_row(p, r, false));
                 if (s0 < at + n) {
                     misc->row = r;
                     misc->t0 = (int)(s0 - at);
@@ -536,8 +540,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
         const float cl = p.scale * kLog2e, gp = BITS4 ? p.g * 256.f : 1.f, lg = BITS4 ? log2f(gp) : 0.f, unf = BITS4 ? 1.f / gp : 1.f;
         uint32_t g = 0;
         int n = 0;
-        bool good = true;
-        for (; walk_item(p, w, it); walk_next(p, w, it), ++n) {
+        bool good = true, have = walk_item(p, w, it);
+        for (; have; ++n) {
+            // the next item, now: its loads would otherwise stand between this one's end and its first tile
+            Walk w_next = w;
+            Item it_next;
+            walk_next(p, w_next, it);
+            have = walk_item(p, w_next, it_next);
             float m2 = -INFINITY, l = 0.f;                // l: this thread's rows
             for (int i = 0; i < it.T; ++i, ++g) {
                 const int sb = g % kBufs, e = g % kPlaces;
@@ -549,9 +558,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 float v[kC];
                 tmem_ld12_x2(quadrant + kColS + sb * kSCols + 2 * kC * side, v);
                 fence_before_sync();
-                mbar_arrive(&misc->sfree[sb]);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&misc->ifree[e]);
+                if (lane == 0) {
+                    mbar_arrive(&misc->sfree[sb]);
+                    mbar_arrive(&misc->ifree[e]);
+                }
                 if (mask != (1u << kC) - 1u) {            // unseen rows are staged as zeros
 #pragma unroll
                     for (int k = 0; k < kC; ++k)
@@ -612,7 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 }
                 fence_async_smem();
                 fence_before_sync();
-                mbar_arrive(&misc->pfull);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&misc->pfull);
                 l += (sums.x + sums.y) * (pool ? unf : 1.f);
             }
             if (!ok) break;
@@ -679,7 +691,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 }
             }
             fence_before_sync();
-            mbar_arrive(&misc->ofree);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&misc->ofree);
+            w = w_next;
+            it = it_next;
         }
     }
     if (!ok) flag(p.status, HISA_DEV_TIMEOUT);
@@ -691,38 +706,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
     }
 }
 
-// Joins the sums of the rows that spans cut: one row (by the CTA that has its first tile) and 4 / GROUPS
-// heads per CTA, 128 threads of four dims to a head; GROUPS of them share one head's sums where few rows
-// have many.
-constexpr int kJoinThreads = 512;
+// Joins the sums of the rows that spans cut: one row (by the CTA that has its first tile) and kJoinHeads
+// heads per CTA, 128 threads of four dims to a head; where few rows have many parts, GROUPS times as many
+// share one head's.
 template <int GROUPS>
-__global__ void __launch_bounds__(kJoinThreads) k_cache_join(CacheAttnParams p) {
-    __shared__ float2 stat[4 / GROUPS][kCacheCtas];      // a segment's maximum, then weight; its sum
+constexpr int kJoinHeads = GROUPS == 1 ? 4 : 1;
+template <int GROUPS>
+constexpr int kJoinThreads = 128 * GROUPS * kJoinHeads<GROUPS>;
+template <int GROUPS>
+__global__ void __launch_bounds__(kJoinThreads<GROUPS>) k_cache_join(CacheAttnParams p) {
+    __shared__ float weight[kJoinHeads<GROUPS>][kCacheCtas];
     __shared__ float4 part[GROUPS == 1 ? 1 : GROUPS - 1][128];
     grid_dep_wait();
     grid_dep_trigger();
     const Cut cut = reinterpret_cast<const Cut *>(p.cuts)[blockIdx.x];
     if (cut.row < 0) return;
-    const int team = threadIdx.x / 128, grp = team % GROUPS, hs = team / GROUPS, d = (threadIdx.x % 128) * 4;
-    const int h = blockIdx.y * (4 / GROUPS) + hs, first = blockIdx.x, segs = cut.last - first + 1;
+    const int team = threadIdx.x / 128, lane = threadIdx.x & 31, grp = team % GROUPS, hs = team / GROUPS, d = (threadIdx.x % 128) * 4;
+    const int h = blockIdx.y * kJoinHeads<GROUPS> + hs, first = blockIdx.x, segs = cut.last - first + 1;
     // every span has a tile, so every CTA from the first to the last has a part of the row
     auto place = [&](int s) { return s == 0 ? cut.place : 2 * (first + s); };
     const float sink2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
-    for (int s = threadIdx.x % 128 + 128 * grp; s < segs; s += 128 * GROUPS)
-        stat[hs][s] = reinterpret_cast<const float2 *>(p.part_ml)[place(s) * kH + h];
-    __syncthreads();
+    // maximum and normaliser by each warp for itself, a few parts per lane
+    constexpr int kMine = (kCacheCtas + 31) / 32;
+    float2 ml[kMine];
     float M = sink2;
-    for (int s = 0; s < segs; ++s) M = fmaxf(M, stat[hs][s].x);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int s = lane + 32 * i;
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (s < segs) ml[i] = reinterpret_cast<const float2 *>(p.part_ml)[place(s) * kH + h];
+        M = fmaxf(M, ml[i].x);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float ref = M == -INFINITY ? 0.f : M;
+    float den = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const float a = ex2(ml[i].x - ref);              // a part that saw nothing: 0 of sums that are 0
+        den += ml[i].y * a;
+        if (lane + 32 * i < segs) weight[hs][lane + 32 * i] = a;      // the same from every warp of the head
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    den += sink2 == -INFINITY ? 0.f : ex2(sink2 - ref);
+    __syncwarp();
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = sink2 == -INFINITY ? 0.f : ex2(sink2 - ref);
-#pragma unroll 4
+#pragma unroll 8
     for (int s = grp; s < segs; s += GROUPS) {
         const float4 v = __ldcs(reinterpret_cast<const float4 *>(p.part_o + ((int64_t)place(s) * kH + h) * kDH + d));
-        const float a = ex2(stat[hs][s].x - ref);        // a part that saw nothing: 0 of sums that are 0
+        const float a = weight[hs][s];
         o.x += v.x * a; o.y += v.y * a; o.z += v.z * a; o.w += v.w * a;
     }
-    for (int s = 0; s < segs; ++s) den += stat[hs][s].y * ex2(stat[hs][s].x - ref);
     if constexpr (GROUPS > 1) {
         if (grp) part[grp - 1][d / 4] = o;
         __syncthreads();
@@ -753,9 +788,9 @@ cudaError_t go(const CacheAttnParams &p, cudaStream_t s) {
     if (!encode_bf16_chunks(&qmap, p.q, (uint64_t)p.B * p.L * kH, kDH, kH, 8)) return cudaErrorInvalidValue;
     const cudaError_t e = launch_pdl(k_cache_tc<BITS4>, dim3((unsigned)p.ctas), dim3(kThreads), kSmemBytes, s, 1, qmap, p);
     if (e != cudaSuccess || p.whole) return e;
-    if ((int64_t)p.B * p.L <= 16)
-        return launch_pdl(k_cache_join<4>, dim3((unsigned)p.ctas, kH), dim3(kJoinThreads), 0, s, 1, p);
-    return launch_pdl(k_cache_join<1>, dim3((unsigned)p.ctas, kH / 4), dim3(kJoinThreads), 0, s, 1, p);
+    if ((int64_t)p.B * p.L <= 8)
+        return launch_pdl(k_cache_join<8>, dim3((unsigned)p.ctas, kH), dim3(kJoinThreads<8>), 0, s, 1, p);
+    return launch_pdl(k_cache_join<1>, dim3((unsigned)p.ctas, kH / 4), dim3(kJoinThreads<1>), 0, s, 1, p);
 }
 
 }  // namespace
