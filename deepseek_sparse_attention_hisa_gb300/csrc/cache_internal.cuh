@@ -70,7 +70,8 @@ struct CacheAttnParams {
     int splits, split_rows;   // CUDA-core kernel: ranges of a query row's list, rows of each
     int cache32;              // rows in 4 bits start at multiples of 32 bytes
     int ctas, whole, least;   // tensor-core kernel: CTAs; whole rows in turn; else the fewest tiles of a span
-    void *cuts;               // its rows that spans cut, one entry per CTA
+    void *cuts;               // its rows that spans cut: an entry per row (by_row) or per CTA
+    int by_row;
     float *part_o, *part_ml;  // partial sums
     uint32_t *status;
 };

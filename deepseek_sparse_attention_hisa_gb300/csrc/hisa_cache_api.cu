@@ -98,6 +98,7 @@ void tc_plan(const hisa_cache_attn_desc *d, int64_t pool, bool ids, CacheAttnPar
     p->whole = ids && rows * 8 >= rounds * kCacheCtas * 7;
     int64_t n = p->whole ? rows : (rows * tiles + p->least - 1) / p->least;
     p->ctas = (int)(n > kCacheCtas ? kCacheCtas : n);
+    p->by_row = !p->whole && rows <= p->ctas;
 }
 size_t tc_bytes(const hisa_cache_attn_desc *d, int64_t pool, bool ids) {
     CacheAttnParams p{};

@@ -66,11 +66,12 @@ struct Misc {
 constexpr uint32_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-// A row whose tiles lie in the spans of several CTAs, by the CTA that has its first tile.
+// A row whose tiles lie in the spans of several CTAs: entry `row` of p.cuts if there are as few rows as CTAs
+// (p.by_row), else the entry of the CTA that has its first tile.
 struct Cut {
-    int64_t row, total;                                 // -1: none
-    int last, groups;                                   // the CTA that has its last tile
-    int place, pad;                                     // of the first CTA's sums
+    int64_t row;                                        // -1: none
+    int first, last;                                    // the CTAs that have its first and its last tile
+    int place, pad[3];                                  // of the first CTA's sums
 };
 static_assert(sizeof(Cut) == kCutBytes, "workspace layout");
 
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
             misc->left = s1 - s0;
             misc->total = total;
             misc->groups = groups;
-            cuts[blockIdx.x].row = -1;
+            if (!p.by_row) cuts[blockIdx.x].row = -1;
         }
         if (s0 >= at && s0 < at + sum) {
             for (int64_t r = r0; r < r1; ++r) {
@@ -642,6 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
             fence_after_sync();
             const bool cut = it.T < it.tiles;
             if (!cut) {
+                if (p.by_row && tid == 0) cuts[w.row].row = -1;
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {             // 32 heads of 128 dims
                     const int mt = 2 * side + (k >> 1), c = 32 * (k & 1), d = mt * 128 + quad * 32 + lane;
@@ -674,9 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 if (part == 0) reinterpret_cast<float2 *>(p.part_ml)[place * kH + h] = make_float2(m2, l);
                 if (tid == 0 && w.t0 == 0) {              // the row begins here: its last tile of the span is the span's last
                     const int64_t s1 = span_start(blockIdx.x + 1, misc->total, misc->groups);
-                    Cut &k = cuts[blockIdx.x];
-                    k.total = misc->total;
-                    k.groups = misc->groups;
+                    Cut &k = cuts[p.by_row ? w.row : (int64_t)blockIdx.x];
+                    k.first = (int)blockIdx.x;
                     k.last = (int)(((s1 - it.T + it.tiles) * misc->groups - 1) / misc->total);
                     k.place = place;
                     k.row = w.row;
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(kJoinThreads<GROUPS>) k_cache_join(CacheAttnPa
     const Cut cut = reinterpret_cast<const Cut *>(p.cuts)[blockIdx.x];
     if (cut.row < 0) return;
     const int team = threadIdx.x / 128, lane = threadIdx.x & 31, grp = team % GROUPS, hs = team / GROUPS, d = (threadIdx.x % 128) * 4;
-    const int h = blockIdx.y * kJoinHeads<GROUPS> + hs, first = blockIdx.x, segs = cut.last - first + 1;
+    const int h = blockIdx.y * kJoinHeads<GROUPS> + hs, first = cut.first, segs = cut.last - first + 1;
     // every span has a tile, so every CTA from the first to the last has a part of the row
     auto place = [&](int s) { return s == 0 ? cut.place : 2 * (first + s); };
     const float sink2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
@@ -788,9 +789,10 @@ cudaError_t go(const CacheAttnParams &p, cudaStream_t s) {
     if (!encode_bf16_chunks(&qmap, p.q, (uint64_t)p.B * p.L * kH, kDH, kH, 8)) return cudaErrorInvalidValue;
     const cudaError_t e = launch_pdl(k_cache_tc<BITS4>, dim3((unsigned)p.ctas), dim3(kThreads), kSmemBytes, s, 1, qmap, p);
     if (e != cudaSuccess || p.whole) return e;
-    if ((int64_t)p.B * p.L <= 8)
-        return launch_pdl(k_cache_join<8>, dim3((unsigned)p.ctas, kH), dim3(kJoinThreads<8>), 0, s, 1, p);
-    return launch_pdl(k_cache_join<1>, dim3((unsigned)p.ctas, kH / 4), dim3(kJoinThreads<1>), 0, s, 1, p);
+    const unsigned entries = p.by_row ? (unsigned)(p.B * p.L) : (unsigned)p.ctas;
+    if (p.by_row && entries <= 8)
+        return launch_pdl(k_cache_join<8>, dim3(entries, kH), dim3(kJoinThreads<8>), 0, s, 1, p);
+    return launch_pdl(k_cache_join<1>, dim3(entries, kH / 4), dim3(kJoinThreads<1>), 0, s, 1, p);
 }
 
 }  // namespace
