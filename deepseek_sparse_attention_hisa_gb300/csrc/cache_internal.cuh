@@ -69,7 +69,7 @@ struct CacheAttnParams {
     int q_bf16, bits4, out_bf16;
     int splits, split_rows;   // CUDA-core kernel: ranges of a query row's list, rows of each
     int cache32;              // rows in 4 bits start at multiples of 32 bytes
-    int ctas, whole, least;   // tensor-core kernel: CTAs; whole rows in turn; else the fewest tiles of a span
+    int ctas, whole;          // tensor-core kernel: CTAs; whole rows in turn, not spans of all rows' tiles
     void *cuts;               // its rows that spans cut: an entry per row (by_row) or per CTA
     int by_row;
     float *part_o, *part_ml;  // partial sums

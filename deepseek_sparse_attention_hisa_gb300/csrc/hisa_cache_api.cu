@@ -86,7 +86,7 @@ void attn_plan(const hisa_cache_attn_desc *d, int64_t pool, CacheAttnParams *p) 
     p->split_rows = (int)(per > 0 ? per : 32);
     p->splits = (int)(list > 0 ? (list + p->split_rows - 1) / p->split_rows : 1);
 }
-// The tensor-core kernel's CTAs: one per SM, or one for every few tiles of 48 rows that there can be.
+// The tensor-core kernel's CTAs: one per SM, or one for every tile of 48 rows that there can be.
 // Whole rows where the lists are all as long (ids: k each) and leave few SMs idle in the last round: no
 // sums go through memory (304 x 640 rows: see k_cache_tc.cu).
 void tc_plan(const hisa_cache_attn_desc *d, int64_t pool, bool ids, CacheAttnParams *p) {
@@ -94,9 +94,9 @@ void tc_plan(const hisa_cache_attn_desc *d, int64_t pool, bool ids, CacheAttnPar
     int64_t tiles = (local + kCacheTile - 1) / kCacheTile + (pool + kCacheTile - 1) / kCacheTile;
     tiles = tiles < 1 ? 1 : tiles;
     const int64_t rows = (int64_t)d->B * d->L, rounds = (rows + kCacheCtas - 1) / kCacheCtas;
-    p->least = 4;
     p->whole = ids && rows * 8 >= rounds * kCacheCtas * 7;
-    int64_t n = p->whole ? rows : (rows * tiles + p->least - 1) / p->least;
+    const double best = std::ceil(std::sqrt(10.0 * (double)(rows * tiles) * (double)rows));     // as on the device, of all that there can be
+    const int64_t n = p->whole ? rows : (best < (double)(rows * tiles) ? (int64_t)best : rows * tiles);
     p->ctas = (int)(n > kCacheCtas ? kCacheCtas : n);
     p->by_row = !p->whole && rows <= p->ctas;
 }
