@@ -76,10 +76,11 @@ hisa_status check_cache_attn_desc(const hisa_cache_attn_desc *d) {
 // sizes the workspace, for the wider of the two lists that a call may have: I, or all rows).
 void attn_plan(const hisa_cache_attn_desc *d, int64_t pool, CacheAttnParams *p) {
     const int64_t local = d->W_max < d->window ? d->W_max : d->window, list = local + pool;
-    // about as many CTAs as fit the GPU at once (one per SM for 512 dims, else eight), of 64 rows at least
+    // about as many CTAs as fit the GPU at once (one per SM for 512 dims, else eight), of a chunk of 32 rows at
+    // least (64 for 512 dims, whose sums are large)
     const int64_t items = (int64_t)d->B * d->L, ctas = d->Dh == 512 ? kSmTarget : 8 * kSmTarget;
     int64_t n = ctas / items;
-    const int64_t most = (list + 63) / 64;
+    const int64_t least = d->Dh == 512 ? 64 : 32, most = (list + least - 1) / least;
     n = n > most ? most : n;
     n = n < 1 ? 1 : (n > 128 ? 128 : n);
     const int64_t per = ((list + n - 1) / n + 31) / 32 * 32;

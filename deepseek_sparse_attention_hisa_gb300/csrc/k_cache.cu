@@ -3,7 +3,8 @@
 // One softmax over [visible window | pooled rows seen | sink] per query row and head, K = V. A query
 // row's list is cut into ranges; a CTA takes all H heads of one query row and one range, 32 list rows
 // at a time: their places are found by one warp, their values staged in f32, scores and sums kept in f32
-// registers with a running maximum and sum per head. The ranges' sums join in k_prefix_merge.
+// registers with a running maximum and sum per head. The ranges' sums join in k_prefix_merge; a list of one
+// range is finished by its CTA.
 //
 // Bound by the FMA pipe and its shared-memory operands.
 #include "cache_internal.cuh"
@@ -41,7 +42,7 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_cach
     constexpr int RP = kPer<R>, TR = R / RP, NT = TR * 16, DJ = DH / 64;
     extern __shared__ __align__(16) float sm[];
     float *sq = sm, *skv = sq + R * S::kStride, *sp = skv + kChunk * S::kStride;
-    __shared__ int64_t place[kChunk];                    // -1: not seen; local rows from 1 << 62 on
+    __shared__ int64_t places[2][kChunk];                // of a chunk's rows. -1: not seen; local rows from 1 << 62 on
     constexpr int64_t kLocal = (int64_t)1 << 62;
     const int tid = threadIdx.x, tr = tid / 16, tc = tid % 16;
     const int64_t row = blockIdx.x, rows = (int64_t)p.B * p.L * p.H;
@@ -65,33 +66,74 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_cach
 #pragma unroll
         for (int j = 0; j < DJ; ++j) acc[i][j][0] = acc[i][j][1] = make_float2(0.f, 0.f);
     }
-    for (int64_t c0 = e0; c0 < e1; c0 += kChunk) {
-        __syncthreads();                                  // the previous chunk has been read
+    // Rows 4 dims at a time (in 4 bits two bytes); a chunk waits in registers while the one before is worked
+    // on, but for 512 dims, whose sums leave no registers
+    constexpr int kUnits = kChunk * (DH / 4) / NT;
+    constexpr bool kAhead = kUnits <= 8;
+    using Raw = typename std::conditional<sizeof(T) == 4, float4, uint2>::type;
+    Raw raw[kAhead ? kUnits : 1];
+    auto find = [&](int64_t c0, int64_t *place) {
         if (tid < kChunk) {
             const int64_t e = c0 + tid;
             place[tid] = e >= e1 ? -1 : (e < x.nloc ? kLocal + e : cache_slot(p, row, x, (int)(e - x.nloc)));
         }
-        __syncthreads();
-        for (int i = tid; i < kChunk * (DH / 4); i += NT) {
-            const int64_t at = place[i / (DH / 4)];
-            const int d = (i % (DH / 4)) * 4;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (at >= kLocal) {
-                v = load4(loc + (at - kLocal) * DH + d);
-            } else if (at >= 0) {
-                if constexpr (BITS4) {
-                    const uint32_t w = *reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(p.cache) + at * (DH / 2) + d / 2);
-                    const float s = e4m3_to_f32(p.scales[at * (DH / kScaleGroup) + d / kScaleGroup]) * p.g;
-                    float f[8];
-                    unpack_e2m1(w, f);
-                    v = make_float4(f[0] * s, f[1] * s, f[2] * s, f[3] * s);
-                } else {
-                    v = load4(static_cast<const __nv_bfloat16 *>(p.cache) + at * DH + d);
-                }
+    };
+    auto fetch = [&](int i, const int64_t *place) -> Raw {   // local rows as they are, others in their first bytes
+        const int64_t at = place[i / (DH / 4)];
+        const int d = (i % (DH / 4)) * 4;
+        Raw v{};
+        if (at >= kLocal) {
+            v = *reinterpret_cast<const Raw *>(loc + (at - kLocal) * DH + d);
+        } else if (at >= 0) {
+            if constexpr (BITS4) {
+                const uint32_t w = *reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(p.cache) + at * (DH / 2) + d / 2);
+                const uint32_t s = p.scales[at * (DH / kScaleGroup) + d / kScaleGroup];
+                reinterpret_cast<uint32_t &>(v) = w | s << 16;
+            } else {
+                reinterpret_cast<uint2 &>(v) = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.cache) + at * DH + d);
             }
-            *reinterpret_cast<float4 *>(skv + i / (DH / 4) * S::kStride + d) = v;
         }
-        __syncthreads();
+        return v;
+    };
+    auto stage = [&](int i, const Raw &r, const int64_t *place) {
+        const int64_t at = place[i / (DH / 4)];
+        float4 v;
+        if (at >= kLocal || (!BITS4 && sizeof(T) == 2)) {
+            v = load4(reinterpret_cast<const T *>(&r));
+        } else if constexpr (BITS4) {
+            const uint32_t w = reinterpret_cast<const uint32_t &>(r);
+            const float s = e4m3_to_f32(w >> 16) * p.g;
+            float f[8];
+            unpack_e2m1(w & 0xffffu, f);
+            v = make_float4(f[0] * s, f[1] * s, f[2] * s, f[3] * s);
+        } else {
+            v = load4(reinterpret_cast<const __nv_bfloat16 *>(&r));
+        }
+        *reinterpret_cast<float4 *>(skv + i / (DH / 4) * S::kStride + (i % (DH / 4)) * 4) = v;
+    };
+    find(e0, places[0]);
+    find(e0 + kChunk, places[1]);
+    __syncthreads();
+    if constexpr (kAhead) {
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) raw[k] = fetch(tid + k * NT, places[0]);
+    }
+    int at_c = 0;
+    for (int64_t c0 = e0; c0 < e1; c0 += kChunk, at_c ^= 1) {
+        int64_t *place = places[at_c];
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) stage(tid + k * NT, raw[k], place);
+        } else {
+            for (int i = tid; i < kChunk * (DH / 4); i += NT) stage(i, fetch(i, place), place);
+        }
+        const bool seen0 = place[tc] >= 0, seen1 = place[tc + 16] >= 0;
+        __syncthreads();                                  // staged, and the places read
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) raw[k] = fetch(tid + k * NT, places[at_c ^ 1]);
+        }
+        find(c0 + 2 * kChunk, place);
         float2 s[RP][2];                                  // even and odd dims' sums
 #pragma unroll
         for (int i = 0; i < RP; ++i) s[i][0] = s[i][1] = make_float2(0.f, 0.f);
@@ -107,7 +149,6 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_cach
                 s[i][1] = fma2(hi, make_float2(k1.z, k1.w), fma2(lo, make_float2(k1.x, k1.y), s[i][1]));
             }
         }
-        const bool seen0 = place[tc] >= 0, seen1 = place[tc + 16] >= 0;
         float al[RP];
 #pragma unroll
         for (int i = 0; i < RP; ++i) {
@@ -153,7 +194,28 @@ __global__ void __launch_bounds__(R / kPer<R> * 16, R == 64 ? 1 : 64 / R) k_cach
                 }
             }
         }
-        __syncwarp();                                     // sp is read before the next chunk's is written
+        __syncthreads();                                  // the chunk has been read, places are written
+    }
+    if (p.splits == 1) {                                  // the whole list: the output itself
+#pragma unroll
+        for (int i = 0; i < RP; ++i) {
+            const int h = tr + TR * i;
+            const float sink = p.sinks ? p.sinks[h] : -INFINITY, M = fmaxf(m[i], sink), ref = M == -INFINITY ? 0.f : M;
+            const float a = expf(m[i] - ref), den = l[i] * a + expf(sink - ref), f = den == 0.f ? 0.f : a / den;
+            const int64_t at = (row * R + h) * DH + 4 * tc;
+#pragma unroll
+            for (int j = 0; j < DJ; ++j) {
+                const float4 o = make_float4(acc[i][j][0].x * f, acc[i][j][0].y * f, acc[i][j][1].x * f, acc[i][j][1].y * f);
+                if (p.out_bf16) {
+                    const __nv_bfloat162 u = __floats2bfloat162_rn(o.x, o.y), v = __floats2bfloat162_rn(o.z, o.w);
+                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at + 64 * j) =
+                        make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
+                } else {
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + 64 * j) = o;
+                }
+            }
+        }
+        return;
     }
     const int64_t g0 = (int64_t)seg * rows + row * R;
 #pragma unroll
@@ -188,7 +250,7 @@ cudaError_t launch_cache_simt(const CacheAttnParams &p, cudaStream_t s) {
     else if (p.Dh == 128) e = types<16, 128>(p, s);
     else if (p.q_bf16) return cudaErrorInvalidValue;      // k_cache_tc.cu
     else e = p.bits4 ? go<64, 512, float, true>(p, s) : go<64, 512, float, false>(p, s);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.splits == 1) return e;
     PrefixParams m{};
     m.B = p.B; m.L = p.L; m.H = p.H; m.Dh = p.Dh;
     m.sinks = p.sinks; m.out = p.out; m.out_bf16 = p.out_bf16;
