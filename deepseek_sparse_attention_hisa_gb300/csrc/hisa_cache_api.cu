@@ -87,16 +87,20 @@ void attn_plan(const hisa_cache_attn_desc *d, int64_t pool, CacheAttnParams *p) 
     p->split_rows = (int)(per > 0 ? per : 32);
     p->splits = (int)(list > 0 ? (list + p->split_rows - 1) / p->split_rows : 1);
 }
-// The tensor-core kernel's CTAs: one per SM, or one for every tile of 48 rows that there can be.
-// Whole rows where the lists are all as long (ids: k each) and leave few SMs idle in the last round: no
-// sums go through memory (304 x 640 rows: see k_cache_tc.cu).
+// The tensor-core kernel's CTAs: one per SM, or as many as the device makes spans of all tiles that there can be.
+// Whole rows in turn, or spans that cut rows? Cutting evens out what the CTAs do, but its sums go through memory
+// and a second kernel joins them: 6 us for one row, 20 for a hundred, against 1.4 us for each tile that the busiest
+// CTA is spared. Rows are taken as full with ids (k each), else as filled to 60 %. Measured, whole and cut, in us:
+// 50 rows of up to 4 tiles 9.1 and 16.0, 100 of 14 25 and 37, 152 of up to 16 29 and 42, 304 of up to 16 54 and
+// 65, 230 of 14 50 and 62; 16 of up to 16 26 and 21, 1 of 9 19 and 13.
 void tc_plan(const hisa_cache_attn_desc *d, int64_t pool, bool ids, CacheAttnParams *p) {
     const int64_t local = d->W_max < d->window ? d->W_max : d->window;
     int64_t tiles = (local + kCacheTile - 1) / kCacheTile + (pool + kCacheTile - 1) / kCacheTile;
     tiles = tiles < 1 ? 1 : tiles;
     const int64_t rows = (int64_t)d->B * d->L, rounds = (rows + kCacheCtas - 1) / kCacheCtas;
-    p->whole = ids && rows * 8 >= rounds * kCacheCtas * 7;
-    const double best = std::ceil(std::sqrt(10.0 * (double)(rows * tiles) * (double)rows));     // as on the device, of all that there can be
+    const double spared = (double)tiles * ((double)rounds - (ids ? 1.0 : 0.6) * (double)rows / kCacheCtas);
+    p->whole = spared <= 6.0 + 0.1 * (double)(rows < 100 ? rows : 100);
+    const double best = std::ceil(std::sqrt(10.0 * (double)(rows * tiles) * (double)rows));     // as on the device
     const int64_t n = p->whole ? rows : (best < (double)(rows * tiles) ? (int64_t)best : rows * tiles);
     p->ctas = (int)(n > kCacheCtas ? kCacheCtas : n);
     p->by_row = !p->whole && rows <= p->ctas;
