@@ -5,10 +5,9 @@
 // lanes (head_rows.cuh) take the rows in turn, the next one on its way while one is worked on.
 // Bound by memory; a call of a few rows by its chain of loads.
 //
-// Append, 4 bits: sixteen dims are two neighbouring lanes' units. Their largest magnitude is taken by
-// the bits of |y|, so that a NaN is larger than an infinity and both than any number. The quotient
-// y / (s g) is a product with the reciprocal and one correction by its exact remainder, which gives
-// back quotients that are exactly representable (the ties between codes are such).
+// Append, 4 bits: sixteen dims are two neighbouring lanes' units; their largest magnitude is NaN if one of
+// them is. The quotient y / (s g) is a product with the reciprocal and one correction by its exact
+// remainder, which gives back quotients that are exactly representable (the ties between codes are such).
 #include "cache_internal.cuh"
 #include "head_rows.cuh"
 
@@ -55,19 +54,23 @@ __device__ __forceinline__ void check_offsets(const CacheParams &p) {
 
 constexpr uint32_t kE4m3Nan = 0x7fu;
 
+// The largest magnitude of three, NaN if one is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Eight f32 of a 16-dim group (the other eight in the neighbouring lane) to codes and the scale's byte.
 __device__ __forceinline__ uint32_t quantise(float (&y)[8], float g, float inv6g, uint32_t &scale) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    const float a = __uint_as_float(top);
+    const float a8 = max3_abs(max3_abs(y[0], y[1], y[2]), max3_abs(y[3], y[4], y[5]), max3_abs(y[6], y[7], y[7]));
+    const float a = max3_abs(a8, a8, __shfl_xor_sync(0xffffffffu, a8, 1));
     // a / 6 g by the reciprocal, corrected by the exact remainder; past 448 it does not matter by how much
     float t = fminf(a * inv6g, 1e6f);
     t = fmaf(fmaf(-t, 6.f * g, a), inv6g, t);
     uint16_t two;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(t));
-    scale = top < 0x7f800000u ? (uint32_t)two & 0xffu : kE4m3Nan;
+    scale = a < INFINITY ? (uint32_t)two & 0xffu : kE4m3Nan;
     const float step = e4m3_to_f32(scale) * g;
     float inv;                                                // to a step or two: what it scales is corrected
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
@@ -77,16 +80,17 @@ __device__ __forceinline__ uint32_t quantise(float (&y)[8], float g, float inv6g
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = fminf(fmaxf(y[e], -most), most);
     }
-    const float2 ii = make_float2(inv, inv), ss = make_float2(step, step);
-    uint32_t w = 0;
+    const float2 ii = make_float2(inv, inv), ss = make_float2(-step, -step);
+    float2 q[4];
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        const float2 z = make_float2(y[e], y[e + 1]), v = mul2(z, ii), rest = fma2(make_float2(-v.x, -v.y), ss, z), q = fma2(rest, ii, v);
-        uint32_t byte;
-        asm("{.reg .b8 t, z; .reg .b16 h; cvt.rn.satfinite.e2m1x2.f32 t, %2, %1; mov.b16 h, {t, 0}; cvt.u32.u16 %0, h;}"
-            : "=r"(byte) : "f"(q.x), "f"(q.y));
-        w |= byte << (4 * e);
+    for (int e = 0; e < 4; ++e) {
+        const float2 z = make_float2(y[2 * e], y[2 * e + 1]), v = mul2(z, ii);
+        q[e] = fma2(fma2(v, ss, z), ii, v);
     }
+    uint32_t w;
+    asm("{.reg .b8 a, b, c, d; cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b, %4, %3; "
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; cvt.rn.satfinite.e2m1x2.f32 d, %8, %7; mov.b32 %0, {a, b, c, d};}"
+        : "=r"(w) : "f"(q[0].x), "f"(q[0].y), "f"(q[1].x), "f"(q[1].y), "f"(q[2].x), "f"(q[2].y), "f"(q[3].x), "f"(q[3].y));
     return w;
 }
 
