@@ -20,9 +20,12 @@
 // as long). A row that lies in one span is finished there; the sums of one that is cut go to memory, two
 // places per CTA, and k_cache_join adds them up.
 //
+// An output in f32 wants weights of more than 8 bits: P then goes to the second product as two bf16 planes, its
+// rounded value and what that leaves (2^-18 of a weight stays out), one after the other through the same buffer.
+//
 // The running maximum m is lazy: O^T and l are rescaled only when a tile's maximum exceeds m by more
-// than 64 (log2 units). bf16 has the exponents of f32, so a weight of 2^64 is held as exactly as one of 1, and
-// sums of 2^31 such weights and products stay far below 2^127; a rescaling costs as much as a tile.
+// than 32 (log2 units). bf16 has the exponents of f32, so a weight of 2^32 is held as exactly as one of 1, and
+// its products and sums stay far below 2^127; a rescaling costs as much as a tile.
 //
 // Warps: 0-7 softmax and epilogue, 8 S issue (and q by TMA), 9 PV issue, 10-11 places of the rows (ids,
 // pages), up to four tiles ahead, 12-23 rows: a lane has a row of the tile and an eighth of its dims, the next
@@ -45,7 +48,7 @@ constexpr uint32_t kQChunk = kH * 128, kQBytes = 8 * kQChunk, kPBytes = kH * 128
 constexpr uint32_t kOffQ = 0, kOffKV = kQBytes, kOffP = kOffKV + kSlots * kTile, kOffMisc = kOffP + kPBytes;
 constexpr uint32_t kColS = 0, kSCols = 64, kColO = kBufs * kSCols, kTmemCols = 512;
 constexpr int kC = kT / 4;                               // tile rows of a softmax thread
-constexpr float kLog2e = 1.4426950408889634f, kLazy = 64.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLazy = 32.0f;
 constexpr int kBarSoft = 1;
 
 struct Misc {
@@ -188,9 +191,8 @@ __device__ __forceinline__ uint32_t elect_one() {
     return e;
 }
 // The product of mma_bf16_warp, issued by the lane that holds e = 1. A descriptor is passed as its two words, of
-// which only the lower (the address) changes from product to product: what a product costs its issuing warp in
-// instructions, and not the tensor core, bounds a tile (an election and two 64-bit sums each: 39 cycles a
-// product of M = 64, N = 64; so: see below).
+// which only the lower (the address) changes from product to product, and the lane is elected once: with an
+// election and two 64-bit sums for each, the issuing warp and not the tensor core sets the pace (39 cycles a product).
 __device__ __forceinline__ void mma_elected(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                             uint32_t accumulate, uint32_t e) {
     asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
@@ -209,7 +211,7 @@ __device__ __forceinline__ void load32(const uint8_t *from, uint4 &a, uint4 &b) 
                  : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "l"(from));
 }
 
-template <bool BITS4>
+template <bool BITS4, bool OUT32>
 __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant__ CUtensorMap qmap, CacheAttnParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -507,25 +509,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
         const uint64_t vdesc = smem_desc_sw128(sbase + kOffKV, kChunk, 1024), pdesc = smem_desc_sw128(sbase + kOffP, 16, 1024);
         const uint32_t vlo = (uint32_t)vdesc, vhi = (uint32_t)(vdesc >> 32), plo = (uint32_t)pdesc, phi = (uint32_t)(pdesc >> 32);
         const uint32_t e = elect_one();
-        uint32_t g = 0;
+        constexpr int planes = OUT32 ? 2 : 1;
+        uint32_t g = 0, np = 0;                           // np: planes of P so far
         int n = 0;
         for (; walk_item(p, w, it); walk_next(p, w, it), ++n) {
             if (n > 0 && !wait_warp(&misc->ofree, (n - 1) & 1, abort)) { fail(); break; }
             fence_after_sync();
-            for (int i = 0; i < it.T; ++i, ++g) {
+            for (int i = 0; ok && i < it.T; ++i, ++g) {
                 const int s = g % kSlots;
-                if (!wait_warp(&misc->pfull, g & 1, abort)) { fail(); break; }
-                fence_async_smem();
-                fence_after_sync();
                 const uint32_t vd = vlo + s * (kTile >> 4);
+                for (int pl = 0; pl < planes; ++pl, ++np) {
+                    if (!wait_warp(&misc->pfull, np & 1, abort)) { fail(); break; }
+                    fence_async_smem();
+                    fence_after_sync();
 #pragma unroll
-                for (int mt = 0; mt < 4; ++mt)
+                    for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                    for (int ks = 0; ks < kT / 16; ++ks)
-                        mma_elected(tmem + kColO + mt * kH, vd + ((2 * mt * kChunk + ks * 2048) >> 4), vhi, plo + ((ks * 32) >> 4), phi, id_o,
-                                    ks > 0 || i > 0, e);
-                mma_commit_warp(&misc->empty[s]);
-                mma_commit_warp(&misc->pfree);
+                        for (int ks = 0; ks < kT / 16; ++ks)
+                            mma_elected(tmem + kColO + mt * kH, vd + ((2 * mt * kChunk + ks * 2048) >> 4), vhi, plo + ((ks * 32) >> 4), phi, id_o,
+                                        ks > 0 || i > 0 || pl > 0, e);
+                    if (pl == planes - 1) mma_commit_warp(&misc->empty[s]);
+                    mma_commit_warp(&misc->pfree);
+                }
             }
             if (!ok) break;
             mma_commit_warp(&misc->ofull);
@@ -542,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
         const uint32_t quadrant = tmem + ((uint32_t)(32 * quad) << 16);
         const float sink2 = p.sinks ? p.sinks[h] * kLog2e : -INFINITY;
         const float cl = p.scale * kLog2e, gp = BITS4 ? p.g * 256.f : 1.f, lg = BITS4 ? log2f(gp) : 0.f, unf = BITS4 ? 1.f / gp : 1.f;
-        uint32_t g = 0;
+        uint32_t g = 0, np = 0;                           // np: planes of P so far
         int n = 0;
         bool good = true, have = walk_item(p, w, it);
         for (; have; ++n) {
@@ -588,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                     l *= alpha;
                     if (part == 0) misc->alpha[h] = alpha;
                     // O^T of this item so far, after the product of the tile before
-                    if (!soft_all(i < 1 || wait_warp(&misc->pfree, (g - 1) & 1, abort))) { fail(); break; }
+                    if (!soft_all(i < 1 || wait_warp(&misc->pfree, (np - 1) & 1, abort))) { fail(); break; }
                     if (i > 0) {
                         fence_after_sync();
 #pragma unroll 1
@@ -608,27 +613,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 const float ref = (m2 == -INFINITY ? 0.f : m2) - (pool ? lg : 0.f);
                 const float2 cc = make_float2(c2, c2), rr = make_float2(-ref, -ref);
                 float2 sums = make_float2(0.f, 0.f);
-                uint32_t packed[kC / 2];
+                uint32_t packed[kC / 2], rest[kC / 2];
 #pragma unroll
                 for (int k = 0; k < kC; k += 2) {
                     const float2 z = fma2(make_float2(v[k], v[k + 1]), cc, rr), x = make_float2(ex2(z.x), ex2(z.y));
                     sums = add2(sums, x);
                     const __nv_bfloat162 two = __floats2bfloat162_rn(x.x, x.y);
                     packed[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                    if (OUT32) {                          // what the rounding left (an infinite weight leaves NaN, as its row is)
+                        const __nv_bfloat162 low = __floats2bfloat162_rn(x.x - __low2float(two), x.y - __high2float(two));
+                        rest[k / 2] = *reinterpret_cast<const uint32_t *>(&low);
+                    }
                 }
-                // P's buffer: the product of the tile before has read it. One that never ends is met at the next
-                // tile's barrier, by all
-                good = g < 1 || wait_warp(&misc->pfree, (g - 1) & 1, abort);
-                uint8_t *prow = smem + kOffP + h * 128;
+                auto put = [&](const uint32_t (&w)[kC / 2]) {
+                    // P's buffer: the product before has read it. One that never ends is met at the next tile's
+                    // barrier, by all
+                    good = good && (np < 1 || wait_warp(&misc->pfree, (np - 1) & 1, abort));
+                    uint8_t *prow = smem + kOffP + h * 128;
 #pragma unroll
-                for (int u = 0; u < kC / 4; ++u) {        // 8 bytes: four rows
-                    const uint32_t at = part * (2 * kC) + 8 * u;
-                    *reinterpret_cast<uint2 *>(prow + (((at >> 4) ^ (h & 7)) << 4 | (at & 8))) = make_uint2(packed[2 * u], packed[2 * u + 1]);
-                }
-                fence_async_smem();
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&misc->pfull);
+                    for (int u = 0; u < kC / 4; ++u) {    // 8 bytes: four rows
+                        const uint32_t at = part * (2 * kC) + 8 * u;
+                        *reinterpret_cast<uint2 *>(prow + (((at >> 4) ^ (h & 7)) << 4 | (at & 8))) = make_uint2(w[2 * u], w[2 * u + 1]);
+                    }
+                    fence_async_smem();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&misc->pfull);
+                    ++np;
+                };
+                put(packed);
+                if (OUT32) put(rest);
                 l += (sums.x + sums.y) * (pool ? unf : 1.f);
             }
             if (!ok) break;
@@ -657,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                         const float4 f = *reinterpret_cast<const float4 *>(&misc->factor[c + q]);
                         o[q] *= f.x; o[q + 1] *= f.y; o[q + 2] *= f.z; o[q + 3] *= f.w;
                     }
-                    if (p.out_bf16) {
+                    if (!OUT32) {
                         // two dims per store: even lanes take the first sixteen heads, odd ones the others
                         const bool odd = lane & 1;
                         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + (w.row * kH + c + (odd ? 16 : 0)) * kDH + (d & ~1);
@@ -784,13 +798,13 @@ __global__ void __launch_bounds__(kJoinThreads<GROUPS>) k_cache_join(CacheAttnPa
     }
 }
 
-template <bool BITS4>
+template <bool BITS4, bool OUT32>
 cudaError_t go(const CacheAttnParams &p, cudaStream_t s) {
-    const cudaError_t attr = smem_attr_once<k_cache_tc<BITS4>>((int)kSmemBytes);
+    const cudaError_t attr = smem_attr_once<k_cache_tc<BITS4, OUT32>>((int)kSmemBytes);
     if (attr != cudaSuccess) return attr;
     CUtensorMap qmap;
     if (!encode_bf16_chunks(&qmap, p.q, (uint64_t)p.B * p.L * kH, kDH, kH, 8)) return cudaErrorInvalidValue;
-    const cudaError_t e = launch_pdl(k_cache_tc<BITS4>, dim3((unsigned)p.ctas), dim3(kThreads), kSmemBytes, s, 1, qmap, p);
+    const cudaError_t e = launch_pdl(k_cache_tc<BITS4, OUT32>, dim3((unsigned)p.ctas), dim3(kThreads), kSmemBytes, s, 1, qmap, p);
     if (e != cudaSuccess || p.whole) return e;
     const unsigned entries = p.by_row ? (unsigned)(p.B * p.L) : (unsigned)p.ctas;
     if (p.by_row && entries <= 8)
@@ -802,6 +816,9 @@ cudaError_t go(const CacheAttnParams &p, cudaStream_t s) {
 
 bool cache_tc_supported(int H, int Dh, int q_bf16) { return H == kH && Dh == kDH && q_bf16; }
 
-cudaError_t launch_cache_tc(const CacheAttnParams &p, cudaStream_t s) { return p.bits4 ? go<true>(p, s) : go<false>(p, s); }
+cudaError_t launch_cache_tc(const CacheAttnParams &p, cudaStream_t s) {
+    if (p.out_bf16) return p.bits4 ? go<true, false>(p, s) : go<false, false>(p, s);
+    return p.bits4 ? go<true, true>(p, s) : go<false, true>(p, s);
+}
 
 }  // namespace hisa

@@ -511,7 +511,7 @@ def run_attend(c, out_dt, ws=None, stream=None, sinks="own", out=None, flags=0):
     return out, ws
 
 
-def check_attend(c, out, out_dt, sinks="own", rows=None, skip=None):
+def check_attend(c, out, out_dt, sinks="own", rows=None, skip=None, weight=None):
     """Logits: Dh products summed in f32, off by e = Dh u scale sum|q k| + 4 u |z|; rows in 4 bits by 2 u
     of theirs; weights by 2 e, and their f32 sums over n rows by n u. bf16 queries may round each weight
     to bf16 (2^-8) before its product with the values."""
@@ -541,7 +541,7 @@ def check_attend(c, out, out_dt, sinks="own", rows=None, skip=None):
             e = ((c["Dh"] + 2) * U * (q.abs() @ v.abs().t() * scale) + 4 * U * z.abs()).amax(-1, keepdim=True)
             p = torch.softmax(torch.cat([z, s[:, None]], -1), -1)[:, :-1]
             want, mag = p @ v, p @ v.abs()
-            tol = mag * (4 * e + (2 * v.shape[0] + 2) * U + (half_step("bf16") if c["qt"] == "bf16" else 0)) \
+            tol = mag * (4 * e + (2 * v.shape[0] + 2) * U + (weight if weight is not None else half_step("bf16") if c["qt"] == "bf16" else 0)) \
                 + want.abs() * half_step(out_dt) + 1e-37
             err = (got - want).abs()
             assert (err <= tol).all(), (b, j, (err / tol).max().item())
@@ -638,6 +638,33 @@ def test_attend_scale_range(H, q, cache):
         c["scales"].view(-1, c["Dh"] // 16)[at] = torch.arange(127, device="cuda", dtype=torch.uint8)[:, None].expand(-1, c["Dh"] // 16)
     out, _ = run_attend(c, "f32")
     check_attend(c, out, "f32")
+
+
+@pytest.mark.parametrize("H,q", [(64, "bf16"), (64, "f32"), (16, "bf16")])
+@pytest.mark.parametrize("lens,select", [([70, 0, 130], 0), ([900, 400], 200), ([9000, 5000], 0)])
+@pytest.mark.parametrize("cache", ["4bit", "bf16"])
+def test_attend_f32_output_keeps_the_weights(H, q, lens, select, cache):
+    # bf16 queries with an output in f32: a weight is the sum of two bf16 numbers, off by 2^-8 of 2^-8 of it, and
+    # 2^-22 by its exponential; all else is f32
+    c = attend_case(lens, 1, H, cache, q, 16, select, seed=8)
+    out, ws = run_attend(c, "f32")
+    assert hb.device_status(ws) == 0
+    check_attend(c, out, "f32", weight=2.0**-16 + 2.0**-22)
+
+
+@pytest.mark.parametrize("H,q", [(64, "bf16"), (64, "f32"), (16, "bf16"), (8, "f32")])
+@pytest.mark.parametrize("power", [-60, -7, 60])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_attend_cache_scale(H, q, power, out):
+    # factors at the ends of their range, with queries that bring the logits back; a window of ordinary rows beside them
+    c = attend_case([200, 50], 1, H, "4bit", q, 16, q_std=2.0**-power, g=2.0**power, seed=6)
+    if power > 0:
+        c["len"].zero_()                                         # rows that queries this small could not tell apart
+    else:
+        c["local"] *= 2.0**power
+    got, ws = run_attend(c, out)
+    assert hb.device_status(ws) == 0
+    check_attend(c, got, out)
 
 
 @pytest.mark.parametrize("H,q", [(64, "bf16"), (16, "f32")])
