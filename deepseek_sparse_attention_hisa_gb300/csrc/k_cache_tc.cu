@@ -20,8 +20,9 @@
 // as long). A row that lies in one span is finished there; the sums of one that is cut go to memory, two
 // places per CTA, and k_cache_join adds them up.
 //
-// An output in f32 wants weights of more than 8 bits: P then goes to the second product as two bf16 planes, its
-// rounded value and what that leaves (2^-18 of a weight stays out), one after the other through the same buffer.
+// An output in f32 takes all of a weight: P goes to the second product as three bf16 planes (the rounded value,
+// the rounding of what that leaves, and again), one after the other through the same buffer. Two would leave 2^-18
+// of a weight out, 1.6e-6 of an output's norm, against 5e-7 of f32 sums.
 //
 // The running maximum m is lazy: O^T and l are rescaled only when a tile's maximum exceeds m by more
 // than 32 (log2 units). bf16 has the exponents of f32, so a weight of 2^32 is held as exactly as one of 1, and
@@ -213,6 +214,7 @@ __device__ __forceinline__ void load32(const uint8_t *from, uint4 &a, uint4 &b) 
 
 template <bool BITS4, bool OUT32>
 __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant__ CUtensorMap qmap, CacheAttnParams p) {
+    constexpr int kPlanes = OUT32 ? 3 : 1;               // of P
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -509,7 +511,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
         const uint64_t vdesc = smem_desc_sw128(sbase + kOffKV, kChunk, 1024), pdesc = smem_desc_sw128(sbase + kOffP, 16, 1024);
         const uint32_t vlo = (uint32_t)vdesc, vhi = (uint32_t)(vdesc >> 32), plo = (uint32_t)pdesc, phi = (uint32_t)(pdesc >> 32);
         const uint32_t e = elect_one();
-        constexpr int planes = OUT32 ? 2 : 1;
         uint32_t g = 0, np = 0;                           // np: planes of P so far
         int n = 0;
         for (; walk_item(p, w, it); walk_next(p, w, it), ++n) {
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
             for (int i = 0; ok && i < it.T; ++i, ++g) {
                 const int s = g % kSlots;
                 const uint32_t vd = vlo + s * (kTile >> 4);
-                for (int pl = 0; pl < planes; ++pl, ++np) {
+                for (int pl = 0; pl < kPlanes; ++pl, ++np) {
                     if (!wait_warp(&misc->pfull, np & 1, abort)) { fail(); break; }
                     fence_async_smem();
                     fence_after_sync();
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                         for (int ks = 0; ks < kT / 16; ++ks)
                             mma_elected(tmem + kColO + mt * kH, vd + ((2 * mt * kChunk + ks * 2048) >> 4), vhi, plo + ((ks * 32) >> 4), phi, id_o,
                                         ks > 0 || i > 0 || pl > 0, e);
-                    if (pl == planes - 1) mma_commit_warp(&misc->empty[s]);
+                    if (pl == kPlanes - 1) mma_commit_warp(&misc->empty[s]);
                     mma_commit_warp(&misc->pfree);
                 }
             }
@@ -613,36 +614,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 const float ref = (m2 == -INFINITY ? 0.f : m2) - (pool ? lg : 0.f);
                 const float2 cc = make_float2(c2, c2), rr = make_float2(-ref, -ref);
                 float2 sums = make_float2(0.f, 0.f);
-                uint32_t packed[kC / 2], rest[kC / 2];
 #pragma unroll
                 for (int k = 0; k < kC; k += 2) {
                     const float2 z = fma2(make_float2(v[k], v[k + 1]), cc, rr), x = make_float2(ex2(z.x), ex2(z.y));
                     sums = add2(sums, x);
-                    const __nv_bfloat162 two = __floats2bfloat162_rn(x.x, x.y);
-                    packed[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
-                    if (OUT32) {                          // what the rounding left (an infinite weight leaves NaN, as its row is)
-                        const __nv_bfloat162 low = __floats2bfloat162_rn(x.x - __low2float(two), x.y - __high2float(two));
-                        rest[k / 2] = *reinterpret_cast<const uint32_t *>(&low);
-                    }
+                    v[k] = x.x;
+                    v[k + 1] = x.y;
                 }
-                auto put = [&](const uint32_t (&w)[kC / 2]) {
-                    // P's buffer: the product before has read it. One that never ends is met at the next tile's
-                    // barrier, by all
+#pragma unroll
+                for (int pl = 0; pl < kPlanes; ++pl) {
+                    uint32_t packed[kC / 2];
+#pragma unroll
+                    for (int k = 0; k < kC; k += 2) {
+                        const __nv_bfloat162 two = __floats2bfloat162_rn(v[k], v[k + 1]);
+                        packed[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                        if (pl + 1 < kPlanes) {           // what the rounding left (an infinite weight leaves NaN, as its row is)
+                            v[k] -= __low2float(two);
+                            v[k + 1] -= __high2float(two);
+                        }
+                    }
+                    // P's buffer: the product before has read it. One that never ends is met at the next
+                    // tile's barrier, by all
                     good = good && (np < 1 || wait_warp(&misc->pfree, (np - 1) & 1, abort));
                     uint8_t *prow = smem + kOffP + h * 128;
 #pragma unroll
                     for (int u = 0; u < kC / 4; ++u) {    // 8 bytes: four rows
                         const uint32_t at = part * (2 * kC) + 8 * u;
-                        *reinterpret_cast<uint2 *>(prow + (((at >> 4) ^ (h & 7)) << 4 | (at & 8))) = make_uint2(w[2 * u], w[2 * u + 1]);
+                        *reinterpret_cast<uint2 *>(prow + (((at >> 4) ^ (h & 7)) << 4 | (at & 8))) = make_uint2(packed[2 * u], packed[2 * u + 1]);
                     }
                     fence_async_smem();
                     fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&misc->pfull);
                     ++np;
-                };
-                put(packed);
-                if (OUT32) put(rest);
+                }
                 l += (sums.x + sums.y) * (pool ? unf : 1.f);
             }
             if (!ok) break;

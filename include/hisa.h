@@ -620,9 +620,9 @@ HISA_API hisa_status hisa_cache_read(const hisa_cache_desc *desc, const int64_t 
  * t = t0[b] + j one softmax over the visible local rows, the pooled rows named by I (or all
  * cache_len[b] of them, I = NULL) and the per-head sink, which joins the normaliser and carries no
  * value; K = V. With L > 1 pooled row i is visible iff i < floor((t+1)/r); with L = 1 all are. A query
- * row that sees nothing gives 0. Logits, maxima and sums are f32; with bf16 q of 64 heads of 512 dims
- * each softmax weight is rounded for its product with the values: to bf16 (by 2^-8 of it at most) where
- * out is bf16, to the sum of two bf16 numbers (by 2^-17) where it is f32; otherwise it is not.
+ * row that sees nothing gives 0. Logits, weights, maxima and sums are f32; with bf16 q of 64 heads of 512
+ * dims and a bf16 out each softmax weight is rounded to bf16 (by 2^-8 of it at most) for its product with
+ * the values.
  *   q          [B, L, H, Dh]  q_dtype (already roped)
  *   local_kv   [B, W_max, Dh] q_dtype (NULL if W_max is 0); local_len [B] int32 rows present
  *              (<= W_max); local_pos0 [B] int32 absolute position of local row 0
