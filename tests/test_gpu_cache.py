@@ -541,8 +541,10 @@ def check_attend(c, out, out_dt, sinks="own", rows=None, skip=None, weight=None)
             e = ((c["Dh"] + 2) * U * (q.abs() @ v.abs().t() * scale) + 4 * U * z.abs()).amax(-1, keepdim=True)
             p = torch.softmax(torch.cat([z, s[:, None]], -1), -1)[:, :-1]
             want, mag = p @ v, p @ v.abs()
-            tol = mag * (4 * e + (2 * v.shape[0] + 2) * U + (weight if weight is not None else half_step("bf16") if c["qt"] == "bf16" else 0)) \
-                + want.abs() * half_step(out_dt) + 1e-37
+            # weights w (1 + d) with |d| <= r, in the sum and in the normaliser: off by the sum of w d (v - out), so
+            # by r (mag + |out|) at most
+            r = weight if weight is not None else half_step("bf16") if c["qt"] == "bf16" else 0
+            tol = mag * (4 * e + (2 * v.shape[0] + 2) * U + r) + want.abs() * (r + half_step(out_dt)) + 1e-37
             err = (got - want).abs()
             assert (err <= tol).all(), (b, j, (err / tol).max().item())
 
