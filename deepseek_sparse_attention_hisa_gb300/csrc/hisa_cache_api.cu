@@ -66,6 +66,9 @@ hisa_status check_cache_attn_desc(const hisa_cache_attn_desc *d) {
     if (st != HISA_OK) return st;
     if (d->B < 1 || d->L < 1 || d->window < 0 || d->W_max < 0 || d->r < 1 || d->k < 0 || d->k > 65536) return HISA_EINVAL;
     if (d->Np_max < 0 || d->Np_max > kMaxRows - 65536) return HISA_EINVAL;
+    // a list's entries are counted in 32 bits
+    const int64_t pool = d->Np_max > d->k ? d->Np_max : d->k, local = d->W_max < d->window ? d->W_max : d->window;
+    if (local + pool > kMaxRows - 65536) return HISA_EINVAL;
     if ((int64_t)d->B * d->L > kMaxRows / 64 || (d->flags & ~(int32_t)HISA_FLAG_CHAINED)) return HISA_EINVAL;
     if (!dtype_ok(d->q_dtype) || !dtype_ok(d->out_dtype)) return HISA_EDTYPE;
     if (!attend_simt_supported(d->H, d->Dh)) return HISA_EDTYPE;

@@ -315,7 +315,8 @@ typedef struct {
     int32_t page_rows;    /* rows of a page, 1..65536 */
     int32_t table_cols;   /* page numbers of each sequence in page_table (>= 1) */
     int64_t pages;        /* pages allocated (1..2^31 - 1) */
-    int64_t Np_max;       /* an upper bound of cache_len[b] */
+    int64_t Np_max;       /* an upper bound of cache_len[b]; Np_max and k each with
+                             min(window, W_max) below 2^31 - 65536 */
     float scale;          /* softmax scale; <= 0 selects Dh^-1/2 */
     float cache_scale;    /* HISA_E2M1: the factor of all rows, 2^-60..2^60 (ignored for HISA_BF16) */
     int32_t q_dtype;      /* hisa_dtype of q and local_kv: HISA_F32 or HISA_BF16 */

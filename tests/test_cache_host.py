@@ -181,6 +181,7 @@ def test_read_refuses_pointers(lib):
 
 ATTN = COMMON + [(dict(L=0), EINVAL), (dict(window=-1), EINVAL), (dict(W_max=-1), EINVAL), (dict(r=0), EINVAL), (dict(k=-1), EINVAL),
                  (dict(k=65537), EINVAL), (dict(Np_max=-1), EINVAL), (dict(Np_max=(1 << 31) - 1), EINVAL), (dict(B=1 << 20, L=64), EINVAL),
+                 (dict(Np_max=1 << 30, W_max=1 << 30, window=1 << 30), EINVAL), (dict(W_max=(1 << 31) - 1, window=(1 << 31) - 1), EINVAL),
                  (dict(H=32), EDTYPE), (dict(Dh=128), EDTYPE), (dict(q_dtype=hb.HISA_E2M1), EDTYPE), (dict(out_dtype=hb.HISA_E4M3), EDTYPE)]
 
 
