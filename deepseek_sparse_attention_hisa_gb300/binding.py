@@ -353,8 +353,10 @@ def cache_read(desc, row_off, first, page_table, cache, scales, out, ws, out_sca
 
 def cache_attend(desc, q, local_kv, local_len, local_pos0, cache, scales, page_table, cache_len, I, sinks, t0, out, ws,
                  stream=None):
+    # ids of no rows (k = 0) are not the null that stands for all rows: an address that is not read
+    ids = _ptr(t0 if I is not None and I.numel() == 0 else I)
     _check(lib().hisa_cache_attend(ctypes.byref(desc), _ptr(q), _ptr(local_kv), _ptr(local_len), _ptr(local_pos0),
-                                   _ptr(cache), _ptr(scales), _ptr(page_table), _ptr(cache_len), _ptr(I), _ptr(sinks),
+                                   _ptr(cache), _ptr(scales), _ptr(page_table), _ptr(cache_len), ids, _ptr(sinks),
                                    _ptr(t0), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), "hisa_cache_attend")
 
 

@@ -154,7 +154,8 @@ class PagedDecode:
             if need == 0:
                 raise ValueError(f"I: {k} rows are too many")
             if need > self.ws.numel():
-                self.ws = hb.alloc_workspace(need, self.device)
+                old, self.ws = self.ws, hb.alloc_workspace(need, self.device)
+                self.ws[:256] = old[:256]                # the status so far
             self.ws_k = k
         self.norm_desc.ld_x = x.stride(0) if self.B > 1 else self.hidden
         self.norm_desc.ld_res = residual.stride(0) if self.B > 1 else self.hidden
@@ -164,7 +165,7 @@ class PagedDecode:
         self.n += 1
         self.local_len.fill_(self.n)
         hb.cache_attend(self.desc, self.q, self.local, self.local_len, self.local_pos0, self.pool, self.scales, self.page_table,
-                        self.cache_len, I if k else None, self.w["sinks"], self.pos, self.out, self.ws)
+                        self.cache_len, I, self.w["sinks"], self.pos, self.out, self.ws)
         hb.rope(self.back_desc, self.table, self.pos, self.out, self.out)
         self.pos += 1
         return self.out

@@ -653,6 +653,16 @@ def test_attend_f32_output_keeps_the_weights(H, q, lens, select, cache):
     check_attend(c, out, "f32", weight=2.0**-22)
 
 
+@pytest.mark.parametrize("H,q", [(64, "bf16"), (64, "f32"), (16, "bf16")])
+@pytest.mark.parametrize("W", [0, 128])
+def test_attend_ids_of_no_rows(H, q, W):
+    c = attend_case([70, 5], 1, H, "4bit", q, 16, W=W, seed=3)
+    c["I"] = torch.empty((2, 1, 0), dtype=torch.int32, device="cuda")
+    out, ws = run_attend(c, "f32")
+    assert hb.device_status(ws) == 0
+    check_attend(c, out, "f32")
+
+
 @pytest.mark.parametrize("H,q", [(64, "bf16"), (64, "f32"), (16, "bf16"), (8, "f32")])
 @pytest.mark.parametrize("power", [-60, -7, 60])
 @pytest.mark.parametrize("out", ["f32", "bf16"])

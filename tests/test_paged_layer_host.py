@@ -99,10 +99,19 @@ def test_a_step_in_order(calls):
     p.step(rows(), rows(), torch.zeros(3, 2, dtype=torch.int32))
     assert calls[5][2] == p.local[:, 1].data_ptr() and calls[6][:3] == ("attend", 2, False)
     p.step(rows(), rows(), torch.zeros(3, 0, dtype=torch.int32))
-    assert calls[10][:3] == ("attend", 0, True)
+    assert calls[10][:3] == ("attend", 0, False)                  # ids of no rows are not all rows
     p.step(rows(), rows())
     with pytest.raises(ValueError, match="full"):
         p.step(rows(), rows())
+
+
+def test_the_status_survives_a_larger_workspace(calls, monkeypatch):
+    p = layer()
+    before = p.ws
+    monkeypatch.setattr(hb, "workspace_bytes", lambda op, d: before.numel() + d.k)
+    before[0] = hb.DEV_BAD_ID
+    p.step(rows(), rows(), torch.zeros(3, 8, dtype=torch.int32))
+    assert p.ws.numel() == before.numel() + 8 and p.ws[0] == hb.DEV_BAD_ID
 
 
 @pytest.mark.parametrize("which", ["x", "residual"])
