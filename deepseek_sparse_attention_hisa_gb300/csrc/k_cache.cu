@@ -6,7 +6,8 @@
 // registers with a running maximum and sum per head. The ranges' sums join in k_prefix_merge; a list of one
 // range is finished by its CTA.
 //
-// Bound by the FMA pipe and its shared-memory operands.
+// Bound by the FMA pipe and its shared-memory operands where the list is long, else by the latency of its few chunks
+// (load, score, maximum, sum: 3 to 4 us each): 7 sequences of 3 rows of 16 x 128 in f32 over up to 1003 rows in bf16 16.6 us with the merge.
 #include "cache_internal.cuh"
 
 namespace hisa {

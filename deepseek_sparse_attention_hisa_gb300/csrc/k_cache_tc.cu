@@ -22,14 +22,20 @@
 //
 // An output in f32 takes all of a weight: P goes to the second product as three bf16 planes (the rounded value,
 // the rounding of what that leaves, and again), one after the other through the same buffer. Two would leave 2^-18
-// of a weight out, 1.6e-6 of an output's norm, against 5e-7 of f32 sums. (128 rows of 4096: 222 us, and 128 us
-// with a bf16 output.) An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values
+// of a weight out, 1.6e-6 of an output's norm, against 5e-7 of f32 sums. (64 rows over up to 16384: 222 us, and 128 us
+// with a bf16 output; 304 over 512 selected: 84 and 52.) An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values
 // too: what a large weight is off by then divides out (an output is 1.9e-3 to 2.0e-3 of its norm off, 2.3e-3 with
 // a normaliser of unrounded weights; the output's own rounding is 1.7e-3).
 //
 // The running maximum m is lazy: O^T and l are rescaled only when a tile's maximum exceeds m by more
 // than 32 (log2 units). bf16 has the exponents of f32, so a weight of 2^32 is held as exactly as one of 1, and
 // its products and sums stay far below 2^127; a rescaling costs as much as a tile.
+//
+// Bound by latency chains, not by a pipe: a tile takes 2600 cycles, of which the tensor core works 940, the row warps'
+// conversion of it 1800 (and 850 of waits), the softmax 1800; with two tiles under way neither hides the other wholly. 64 rows
+// over up to 16384: 128 us, 550 TFLOP/s, 36 % of the tensor pipe, 2.3 instructions per cycle. Without the
+// conversion and half of the products it still takes 111 us. 304 rows over 512 selected (a row per CTA, twice): 52 us, 2.4 TB/s, of
+// which a CTA's first tile, last tile and output take some 8 us per row.
 //
 // Warps: 0-7 softmax and epilogue, 8 S issue (and q by TMA), 9 PV issue, 10-11 places of the rows (ids,
 // pages), up to four tiles ahead, 12-23 rows: a lane has a row of the tile and an eighth of its dims, the next
