@@ -13,7 +13,7 @@
 // its scale 4, the product 6 of bf16's 8. A code's three magnitude bits placed at the end of bf16's
 // exponent and the start of its mantissa are the code times 2^-126 (its 0.5 a subnormal number), so a
 // product with the scale times 2^118 leaves code * scale * 2^-8; the 2^8 and the cache's factor go into
-// the logits and into P. Two dims take a byte permute, two shifts, two masks and the product.
+// the logits and into P. Two dims take a byte permute, a shift, two masks and the product.
 //
 // Work: one CTA per SM. Lists differ in length and only the device knows them, so every CTA adds up
 // all rows' tiles and takes an equal span of them (p.whole: whole rows in turn, where all lists are
@@ -22,7 +22,7 @@
 //
 // An output in f32 takes all of a weight: P goes to the second product as three bf16 planes (the rounded value,
 // the rounding of what that leaves, and again), one after the other through the same buffer. Two would leave 2^-18
-// of a weight out, 1.6e-6 of an output's norm, against 5e-7 of f32 sums. (64 rows over up to 16384: 222 us, and 128 us
+// of a weight out, 1.6e-6 of an output's norm, against 5e-7 of f32 sums. (64 rows over up to 16384: 222 us, and 125 us
 // with a bf16 output; 304 over 512 selected: 84 and 52.) An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values
 // too: what a large weight is off by then divides out (an output is 1.9e-3 to 2.0e-3 of its norm off, 2.3e-3 with
 // a normaliser of unrounded weights; the output's own rounding is 1.7e-3).
@@ -33,7 +33,7 @@
 //
 // Bound by latency chains, not by a pipe: a tile takes 2600 cycles, of which the tensor core works 940, the row warps'
 // conversion of it 1800 (and 850 of waits), the softmax 1800; with two tiles under way neither hides the other wholly. 64 rows
-// over up to 16384: 128 us, 550 TFLOP/s, 36 % of the tensor pipe, 2.3 instructions per cycle. Without the
+// over up to 16384: 125 us, 567 TFLOP/s, 36 % of the tensor pipe, 2.3 instructions per cycle. Without the
 // conversion and half of the products it still takes 111 us. 304 rows over 512 selected (a row per CTA, twice): 52 us, 2.4 TB/s, of
 // which a CTA's first tile, last tile and output take some 8 us per row.
 //
@@ -172,12 +172,12 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 __device__ __forceinline__ uint4 codes_to_bf16(uint32_t w, uint32_t s) {
-    const uint32_t odd = w >> 4;
+    const uint32_t even = w << 4;
     uint32_t r[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {                       // the even dim's code at bit 0, the odd one's at bit 16
-        const uint32_t u = __byte_perm(w, odd, (j | j << 4 | (4 + j) << 8 | (4 + j) << 12));
-        r[j] = mul_bf16x2((u << 6 & 0x01c001c0u) | (u << 12 & 0x80008000u), s);
+    for (int j = 0; j < 4; ++j) {                       // the even dim's code at bit 12, the odd one's at bit 28
+        const uint32_t u = __byte_perm(w, even, (4 + j) | (4 + j) << 4 | j << 8 | j << 12);
+        r[j] = mul_bf16x2((u >> 6 & 0x01c001c0u) | (u & 0x80008000u), s);
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                     if (!wait_warp(&misc->pfull, np & 1, abort)) { fail(); break; }
                     fence_async_smem();
                     fence_after_sync();
-#pragma unroll
+#pragma unroll 1                                         // less code for a warp that waits most of the time: 126.3 -> 125 us
                     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                         for (int ks = 0; ks < kT / 16; ++ks)
