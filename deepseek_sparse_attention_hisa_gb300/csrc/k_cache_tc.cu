@@ -21,11 +21,13 @@
 // places per CTA, and k_cache_join adds them up.
 //
 // An output in f32 takes all of a weight: P goes to the second product as three bf16 planes (the rounded value,
-// the rounding of what that leaves, and again), one after the other through the same buffer. Two would leave 2^-18
-// of a weight out, 1.6e-6 of an output's norm, against 5e-7 of f32 sums. (64 rows over up to 16384: 222 us, and 125 us
-// with a bf16 output; 304 over 512 selected: 84 and 52.) An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values
-// too: what a large weight is off by then divides out (an output is 1.9e-3 to 2.0e-3 of its norm off, 2.3e-3 with
-// a normaliser of unrounded weights; the output's own rounding is 1.7e-3).
+// the rounding of what that leaves, and again), one after the other through the same buffer; two would leave 2^-18
+// of a weight out. And its logits are sums of two accumulators of 256 dims: the tensor core cuts its f32 sums off instead of
+// rounding them, which adds up over the 32 steps of one (outputs 1.5e-6 to 1.9e-6 of their norm off with one, 7e-7 to 1.1e-6 with
+// two, at no cost). 64 rows over up to 16384: 204 us, and 125 us with a bf16 output; 304 over 512 selected: 82 and 51.5.
+// An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values too: what a large
+// weight is off by then divides out (an output is 1.9e-3 to 2.0e-3 of its norm off, 2.3e-3 with a normaliser of
+// unrounded weights; the output's own rounding is 1.7e-3).
 //
 // The running maximum m is lazy: O^T and l are rescaled only when a tile's maximum exceeds m by more
 // than 32 (log2 units). bf16 has the exponents of f32, so a weight of 2^32 is held as exactly as one of 1, and
@@ -56,7 +58,7 @@ constexpr uint32_t kChunk = kT * 128;                   // 64 dims of a tile, 12
 constexpr uint32_t kTile = 8 * kChunk;
 constexpr uint32_t kQChunk = kH * 128, kQBytes = 8 * kQChunk, kPBytes = kH * 128;
 constexpr uint32_t kOffQ = 0, kOffKV = kQBytes, kOffP = kOffKV + kSlots * kTile, kOffMisc = kOffP + kPBytes;
-constexpr uint32_t kColS = 0, kSCols = 64, kColO = kBufs * kSCols, kTmemCols = 512;
+constexpr uint32_t kColS = 0, kSCols = 64, kColO = kBufs * kSCols, kColS2 = kColO + 4 * kH, kTmemCols = 512;
 constexpr int kC = kT / 4;                               // tile rows of a softmax thread
 constexpr float kLog2e = 1.4426950408889634f, kLazy = 32.0f;
 constexpr int kBarSoft = 1;
@@ -224,6 +226,7 @@ __device__ __forceinline__ void load32(const uint8_t *from, uint4 &a, uint4 &b) 
 template <bool BITS4, bool OUT32>
 __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant__ CUtensorMap qmap, CacheAttnParams p) {
     constexpr int kPlanes = OUT32 ? 3 : 1;               // of P
+    constexpr int kSums = OUT32 ? 2 : 1;                 // of a logit
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -499,11 +502,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 }
                 fence_async_smem();                       // the rows were written through the generic proxy
                 fence_after_sync();
-                const uint32_t kd = klo + s * (kTile >> 4), d = tmem + kColS + sb * kSCols;
+                const uint32_t kd = klo + s * (kTile >> 4), d = tmem + kColS + sb * kSCols, d2 = tmem + kColS2 + sb * kSCols;
+                constexpr int kSteps = kDH / 16 / kSums;  // of one sum
 #pragma unroll
                 for (int ks = 0; ks < kDH / 16; ++ks) {
                     const uint32_t in = (ks & 3) * 32;
-                    mma_elected(d, qlo + (((ks >> 2) * kQChunk + in) >> 4), hi, kd + (((ks >> 2) * kChunk + in) >> 4), hi, id_s, ks > 0, e);
+                    mma_elected(ks < kSteps ? d : d2, qlo + (((ks >> 2) * kQChunk + in) >> 4), hi, kd + (((ks >> 2) * kChunk + in) >> 4), hi, id_s,
+                                ks % kSteps > 0, e);
                 }
                 mma_commit_warp(&misc->sfull[sb]);
             }
@@ -576,6 +581,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 const uint32_t mask = (uint32_t)(*reinterpret_cast<volatile uint64_t *>(&misc->mask[e]) >> (kC * part)) & ((1u << kC) - 1u);
                 float v[kC];
                 tmem_ld12_x2(quadrant + kColS + sb * kSCols + 2 * kC * side, v);
+                if (kSums == 2) {
+                    float rest[kC];
+                    tmem_ld12_x2(quadrant + kColS2 + sb * kSCols + 2 * kC * side, rest);
+#pragma unroll
+                    for (int k = 0; k < kC; ++k) v[k] += rest[k];
+                }
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
