@@ -3,7 +3,7 @@
 //
 // A query row's list (its visible window, then the pooled rows it sees) is cut into tiles of 48 rows, all
 // of one kind. Per tile:
-//   S  = Q . K^T      tcgen05, M = 64 heads, N = 48 rows, K = 512           (TMEM, 2 buffers)
+//   S  = Q . K^T      tcgen05, M = 64 heads, N = 48 rows, K = 512           (TMEM; bf16 out: 2 buffers, f32 out: 4 sums)
 //   P  = exp2(S scale log2e - m) per head, in the threads that own the head's TMEM lane
 //   O^T += V^T . P^T  tcgen05, M = 128 dims x 4, N = 64 heads, K = 48       (TMEM, f32)
 // The tile is staged once in bf16 (128-byte swizzle): K-major for the first product, MN-major for the
@@ -22,9 +22,11 @@
 //
 // An output in f32 takes all of a weight: P goes to the second product as three bf16 planes (the rounded value,
 // the rounding of what that leaves, and again), one after the other through the same buffer; two would leave 2^-18
-// of a weight out. And its logits are sums of two accumulators of 256 dims: the tensor core cuts its f32 sums off instead of
-// rounding them, which adds up over the 32 steps of one (outputs 1.5e-6 to 1.9e-6 of their norm off with one, 7e-7 to 1.1e-6 with
-// two, at no cost). 64 rows over up to 16384: 204 us, and 125 us with a bf16 output; 304 over 512 selected: 82 and 51.5.
+// of a weight out. And its logits are sums of four accumulators of 128 dims: the tensor core cuts its f32 sums off instead of
+// rounding them, which adds up over the 32 steps of one. Outputs over 8 to 175 rows are 1.6e-6 to 1.9e-6 of their norm off
+// with one accumulator, 0.7e-6 to 1.1e-6 with two, below 0.9e-6 with four; those over 512 rows in one span 2.0e-6 with two and
+// 1.6e-6 with four, most of it from the second product's sums, for which there is no room (f32 sums of the plain formula: 0.5e-6
+// to 1e-6). 64 rows over up to 16384: 197 us, and 125 us with a bf16 output; 304 over 512 selected: 80 and 51.5.
 // An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values too: what a large
 // weight is off by then divides out (an output is 1.9e-3 to 2.0e-3 of its norm off, 2.3e-3 with a normaliser of
 // unrounded weights; the output's own rounding is 1.7e-3).
@@ -53,18 +55,18 @@ using namespace tc;
 constexpr int kH = 64, kDH = 512, kT = kCacheTile;      // heads, dims, rows of a tile
 constexpr int kSoftWarps = 8, kSWarp = 8, kPvWarp = 9, kIndexWarp0 = 10, kRowWarp0 = 12, kRowWarps = kT / 4;
 constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
-constexpr int kSlots = 3, kBufs = 2, kPlaces = 8;        // staged tiles; S buffers; tiles whose rows' places are known
+constexpr int kSlots = 3, kPlaces = 8;                   // staged tiles; tiles whose rows' places are known
 constexpr uint32_t kChunk = kT * 128;                   // 64 dims of a tile, 128-byte swizzle
 constexpr uint32_t kTile = 8 * kChunk;
 constexpr uint32_t kQChunk = kH * 128, kQBytes = 8 * kQChunk, kPBytes = kH * 128;
 constexpr uint32_t kOffQ = 0, kOffKV = kQBytes, kOffP = kOffKV + kSlots * kTile, kOffMisc = kOffP + kPBytes;
-constexpr uint32_t kColS = 0, kSCols = 64, kColO = kBufs * kSCols, kColS2 = kColO + 4 * kH, kTmemCols = 512;
+constexpr uint32_t kColS = 0, kSCols = 64, kColO = 4 * kSCols, kTmemCols = 512;
 constexpr int kC = kT / 4;                               // tile rows of a softmax thread
 constexpr float kLog2e = 1.4426950408889634f, kLazy = 32.0f;
 constexpr int kBarSoft = 1;
 
 struct Misc {
-    uint64_t qfull, qfree, full[kSlots], empty[kSlots], sfull[kBufs], sfree[kBufs], pfull, pfree, ofull, ofree, drain;
+    uint64_t qfull, qfree, full[kSlots], empty[kSlots], sfull[2], sfree[2], pfull, pfree, ofull, ofree, drain;
     uint64_t ifull[kPlaces], ifree[kPlaces];
     int64_t place[kPlaces][kT];                         // row of local_kv or of the pool; -1: not seen
     uint64_t mask[kPlaces];                             // rows of a tile that are seen
@@ -226,7 +228,7 @@ __device__ __forceinline__ void load32(const uint8_t *from, uint4 &a, uint4 &b) 
 template <bool BITS4, bool OUT32>
 __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant__ CUtensorMap qmap, CacheAttnParams p) {
     constexpr int kPlanes = OUT32 ? 3 : 1;               // of P
-    constexpr int kSums = OUT32 ? 2 : 1;                 // of a logit
+    constexpr int kSums = OUT32 ? 4 : 1, kBufs = OUT32 ? 1 : 2;   // accumulators of a logit; S buffers
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -502,12 +504,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 }
                 fence_async_smem();                       // the rows were written through the generic proxy
                 fence_after_sync();
-                const uint32_t kd = klo + s * (kTile >> 4), d = tmem + kColS + sb * kSCols, d2 = tmem + kColS2 + sb * kSCols;
-                constexpr int kSteps = kDH / 16 / kSums;  // of one sum
+                const uint32_t kd = klo + s * (kTile >> 4), d = tmem + kColS + sb * kSCols;
+                constexpr int kSteps = kDH / 16 / kSums;  // of one accumulator
 #pragma unroll
                 for (int ks = 0; ks < kDH / 16; ++ks) {
                     const uint32_t in = (ks & 3) * 32;
-                    mma_elected(ks < kSteps ? d : d2, qlo + (((ks >> 2) * kQChunk + in) >> 4), hi, kd + (((ks >> 2) * kChunk + in) >> 4), hi, id_s,
+                    mma_elected(d + ks / kSteps * kSCols, qlo + (((ks >> 2) * kQChunk + in) >> 4), hi, kd + (((ks >> 2) * kChunk + in) >> 4), hi, id_s,
                                 ks % kSteps > 0, e);
                 }
                 mma_commit_warp(&misc->sfull[sb]);
@@ -581,11 +583,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 const uint32_t mask = (uint32_t)(*reinterpret_cast<volatile uint64_t *>(&misc->mask[e]) >> (kC * part)) & ((1u << kC) - 1u);
                 float v[kC];
                 tmem_ld12_x2(quadrant + kColS + sb * kSCols + 2 * kC * side, v);
-                if (kSums == 2) {
-                    float rest[kC];
-                    tmem_ld12_x2(quadrant + kColS2 + sb * kSCols + 2 * kC * side, rest);
 #pragma unroll
-                    for (int k = 0; k < kC; ++k) v[k] += rest[k];
+                for (int j = 1; j < kSums; ++j) {
+                    float more[kC];
+                    tmem_ld12_x2(quadrant + kColS + j * kSCols + 2 * kC * side, more);
+#pragma unroll
+                    for (int k = 0; k < kC; ++k) v[k] += more[k];
                 }
                 fence_before_sync();
                 __syncwarp();
