@@ -1,5 +1,5 @@
-// Combine over a cache in pages on the tensor cores: 64 bf16 query heads of 512 dims, K = V, pooled rows in
-// 4 bits or bf16.
+// Combine over a cache in pages on the tensor cores: 64 bf16 query heads of 512 dims, K = V, pooled rows in 4 bits or
+// bf16.
 //
 // A query row's list (its visible window, then the pooled rows it sees) is cut into tiles of 48 rows, all
 // of one kind. Per tile:
@@ -9,41 +9,40 @@
 // The tile is staged once in bf16 (128-byte swizzle): K-major for the first product, MN-major for the
 // second.
 //
-// Rows in 4 bits become bf16 on their way into the tile, exactly: a 4-bit float has 2 significant bits,
-// its scale 4, the product 6 of bf16's 8. A code's three magnitude bits placed at the end of bf16's
-// exponent and the start of its mantissa are the code times 2^-126 (its 0.5 a subnormal number), so a
-// product with the scale times 2^118 leaves code * scale * 2^-8; the 2^8 and the cache's factor go into
-// the logits and into P. Two dims take a byte permute, a shift, two masks and the product.
+// Rows in 4 bits become bf16 on their way into the tile, exactly: a 4-bit float has 2 significant bits, its scale 4, the
+// product 6 of bf16's 8. A code's three magnitude bits placed at the end of bf16's exponent and the start of its
+// mantissa are the code times 2^-126 (its 0.5 a subnormal number), so a product with the scale times 2^118 leaves code *
+// scale * 2^-8; the 2^8 and the cache's factor go into the logits and into P. Two dims take a byte permute, a shift, two
+// masks and the product.
 //
-// Work: one CTA per SM. Lists differ in length and only the device knows them, so every CTA adds up
-// all rows' tiles and takes an equal span of them (p.whole: whole rows in turn, where all lists are
-// as long). A row that lies in one span is finished there; the sums of one that is cut go to memory, two
-// places per CTA, and k_cache_join adds them up.
+// Work: one CTA per SM. Lists differ in length and only the device knows them, so every CTA adds up all rows' tiles and
+// takes an equal span of them (p.whole: whole rows in turn, where all lists are as long). A row that lies in one span is
+// finished there; the sums of one that is cut go to memory, two places per CTA, and k_cache_join adds them up.
 //
-// An output in f32 takes all of a weight: P goes to the second product as three bf16 planes (the rounded value,
-// the rounding of what that leaves, and again), one after the other through the same buffer; two would leave 2^-18
-// of a weight out. And its logits are sums of four accumulators of 128 dims: the tensor core cuts its f32 sums off instead of
-// rounding them, which adds up over the 32 steps of one. Outputs over 8 to 175 rows are 1.6e-6 to 1.9e-6 of their norm off
-// with one accumulator, 0.7e-6 to 1.1e-6 with two, below 0.9e-6 with four; those over 512 rows in one span 2.0e-6 with two and
-// 1.6e-6 with four, most of it from the second product's sums, for which there is no room (f32 sums of the plain formula: 0.5e-6
-// to 1e-6). 64 rows over up to 16384: 197 us, and 125 us with a bf16 output; 304 over 512 selected: 80 and 51.5.
-// An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values too: what a large
-// weight is off by then divides out (an output is 1.9e-3 to 2.0e-3 of its norm off, 2.3e-3 with a normaliser of
-// unrounded weights; the output's own rounding is 1.7e-3).
+// An output in f32 takes all of a weight: P goes to the second product as three bf16 planes (the rounded value, the
+// rounding of what that leaves, and again), one after the other through the same buffer; two would leave 2^-18 of a
+// weight out. And its logits are sums of four accumulators of 128 dims: the tensor core cuts its f32 sums off instead of
+// rounding them, which adds up over the 32 steps of one. Outputs over 8 to 175 rows are 1.6e-6 to 1.9e-6 of their norm
+// off with one accumulator, 0.7e-6 to 1.1e-6 with two, below 0.9e-6 with four; those over 512 rows in one span 2.0e-6
+// with two and 1.6e-6 with four, most of it from the second product's sums, for which there is no room (f32 sums of the
+// plain formula: 0.5e-6 to 1e-6). 64 rows over up to 16384: 197 us, and 125 us with a bf16 output; 304 over 512
+// selected: 80 and 51.5. An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values
+// too: what a large weight is off by then divides out (an output is 1.9e-3 to 2.0e-3 of its norm off, 2.3e-3 with a
+// normaliser of unrounded weights; the output's own rounding is 1.7e-3).
 //
-// The running maximum m is lazy: O^T and l are rescaled only when a tile's maximum exceeds m by more
-// than 32 (log2 units). bf16 has the exponents of f32, so a weight of 2^32 is held as exactly as one of 1, and
-// its products and sums stay far below 2^127; a rescaling costs as much as a tile.
+// The running maximum m is lazy: O^T and l are rescaled only when a tile's maximum exceeds m by more than 32 (log2
+// units). bf16 has the exponents of f32, so a weight of 2^32 is held as exactly as one of 1, and its products and sums
+// stay far below 2^127; a rescaling costs as much as a tile.
 //
 // Bound by latency chains, not by a pipe: a tile takes 2600 cycles, of which the tensor core works 940, the row warps'
-// conversion of it 1800 (and 850 of waits), the softmax 1800; with two tiles under way neither hides the other wholly. 64 rows
-// over up to 16384: 125 us, 567 TFLOP/s, 36 % of the tensor pipe, 2.3 instructions per cycle. Without the
-// conversion and half of the products it still takes 111 us. 304 rows over 512 selected (a row per CTA, twice): 52 us, 2.4 TB/s, of
-// which a CTA's first tile, last tile and output take some 8 us per row.
+// conversion of it 1800 (and 850 of waits), the softmax 1800; with two tiles under way neither hides the other wholly.
+// 64 rows over up to 16384: 125 us, 567 TFLOP/s, 36 % of the tensor pipe, 2.2 instructions per cycle. Without the
+// conversion and half of the products it still takes 111 us. 304 rows over 512 selected (a row per CTA, twice): 51.5 us,
+// 2.4 TB/s, of which a CTA's first tile, last tile and output take some 8 us per row.
 //
-// Warps: 0-7 softmax and epilogue, 8 S issue (and q by TMA), 9 PV issue, 10-11 places of the rows (ids,
-// pages), up to four tiles ahead, 12-23 rows: a lane has a row of the tile and an eighth of its dims, the next
-// tile's codes on their way while it writes this one's. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and the CTA leaves.
+// Warps: 0-7 softmax and epilogue, 8 S issue (and q by TMA), 9 PV issue, 10-11 places of the rows (ids, pages), up to
+// four tiles ahead, 12-23 rows: a lane has a row of the tile and an eighth of its dims, the next tile's codes on their
+// way while it writes this one's. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and the CTA leaves.
 #include "cache_internal.cuh"
 #include "prefix_common.cuh"
 

@@ -1,14 +1,13 @@
 // The norm of each head and rotary positions in one pass over queries and keys.
 //
-// Bound by memory: each head is read once and written once. A team of lanes (head_rows.cuh) takes a run
-// of up to 8 heads of one token, so that a token's sines and cosines are computed once per run. In flight are
-// 32 warps per SM, each with one head of more than 256 dims or, for each of its teams, four of fewer (two in f32): 4096 x 65 x 512 f32
-// to bf16 133 us with one head per team, 150 with two (more than memory serves at once, and registers);
-// 2047 x 64 x 128 bf16 with halves 25.1, 21.3 and 19.9 us with one, two and four. Runs of 16 heads:
-// 147 us and the same.
+// Bound by memory: each head is read once and written once. A team of lanes (head_rows.cuh) takes a run of up to 8 heads
+// of one token, so that a token's sines and cosines are computed once per run. In flight are 32 warps per SM, each with
+// one head of more than 256 dims or, for each of its teams, four of fewer (two in f32): 4096 x 65 x 512 f32 to bf16 133
+// us with one head per team, 150 with two (more than memory serves at once, and registers); 2047 x 64 x 128 bf16 with
+// halves 25.1, 21.3 and 19.9 us with one, two and four. Runs of 16 heads: 147 us and the same.
 //
-// Measured: the first of these 6.1 TB/s, 90 % of a plain copy's rate; the second 3.4 TB/s: a chain of load,
-// sum over lanes, angles and store per head, with too few bytes in flight; a token of 64 + 1 heads of 512 4.7 us per call.
+// Measured: the first of these 6.1 TB/s, 90 % of a plain copy's rate; the second 18.2 us now, 3.7 TB/s: a chain of load, sum over
+// lanes, angles and store per head, with too few bytes in flight; a token of 64 + 1 heads of 512 4.7 us per call.
 #include "cache_internal.cuh"
 #include "head_rows.cuh"
 
