@@ -82,25 +82,10 @@ struct Misc {
 constexpr uint32_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-// A row whose tiles lie in the spans of several CTAs: entry `row` of p.cuts if there are as few rows as CTAs
-// (p.by_row), else the entry of the CTA that has its first tile.
-struct Cut {
-    int64_t row;                                        // -1: none
-    int first, last;                                    // the CTAs that have its first and its last tile
-    int place, pad[3];                                  // of the first CTA's sums
-};
-static_assert(sizeof(Cut) == kCutBytes, "workspace layout");
-
 __device__ __forceinline__ int local_tiles(const CacheRow &x) { return (x.nloc + kT - 1) / kT; }
 __device__ __forceinline__ int tiles_of(const CacheRow &x) {
     const int n = local_tiles(x) + (x.npool + kT - 1) / kT;
     return n > 0 ? n : 1;                               // a row that sees nothing has a tile of nothing
-}
-
-// The first tile of CTA c's span: c total / groups (a 64-bit division takes a few hundred cycles).
-__device__ __forceinline__ int64_t span_start(int c, int64_t total, int groups) {
-    if (total < (int64_t)1 << 24) return (uint32_t)c * (uint32_t)total / (uint32_t)groups;
-    return c * total / groups;
 }
 
 // What a CTA does, in order: items, each a range of one query row's tiles.
@@ -312,6 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
             misc->groups = groups;
             if (!p.by_row) cuts[blockIdx.x].row = -1;
         }
+        // by_row a thread has one row at most; its entry is cleared by the CTA that has its first tile, which alone writes it,
+        // before anything can be given up
+        if (p.by_row && r0 < r1 && at >= s0 && at < s1) cuts[r0].row = -1;
         if (s0 >= at && s0 < at + sum) {
             for (int64_t r = r0; r < r1; ++r) {
                 const int n = per == 1 ? (int)sum : tiles_of(cache_row(p, r, false));
@@ -688,7 +676,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
             fence_after_sync();
             const bool cut = it.T < it.tiles;
             if (!cut) {
-                if (p.by_row && tid == 0) cuts[w.row].row = -1;
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {             // 32 heads of 128 dims
                     const int mt = 2 * side + (k >> 1), c = 32 * (k & 1), d = mt * 128 + quad * 32 + lane;
@@ -723,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                     const int64_t s1 = span_start(blockIdx.x + 1, misc->total, misc->groups);
                     Cut &k = cuts[p.by_row ? w.row : (int64_t)blockIdx.x];
                     k.first = (int)blockIdx.x;
-                    k.last = (int)(((s1 - it.T + it.tiles) * misc->groups - 1) / misc->total);
+                    k.last = span_of(s1 - it.T + it.tiles - 1, misc->total, misc->groups);
                     k.place = place;
                     k.row = w.row;
                 }
@@ -766,7 +753,7 @@ __global__ void __launch_bounds__(kJoinThreads<GROUPS>) k_cache_join(CacheAttnPa
     grid_dep_wait();
     grid_dep_trigger();
     const Cut cut = reinterpret_cast<const Cut *>(p.cuts)[blockIdx.x];
-    if (cut.row < 0) return;
+    if (!cut_fits(cut, (int64_t)p.B * p.L, p.ctas)) return;
     const int team = threadIdx.x / 128, lane = threadIdx.x & 31, grp = team % GROUPS, hs = team / GROUPS, d = (threadIdx.x % 128) * 4;
     const int h = blockIdx.y * kJoinHeads<GROUPS> + hs, first = cut.first, segs = cut.last - first + 1;
     // every span has a tile, so every CTA from the first to the last has a part of the row

@@ -218,3 +218,50 @@ def test_one_workspace_with_and_without_ids(lib):
     assert need >= 256 + 64 * 16 * (128 + 2) * 4
     big = hb.workspace_bytes(hb.OP_CACHE_ATTEND, attn_desc(B=1 << 15, L=16, q_dtype=hb.HISA_F32))
     assert big >= (1 << 15) * 16 * 64 * 514 * 4
+
+
+CUTS = r"""
+#include <cstdio>
+#include <cstring>
+#include "cache_cuts.h"
+using namespace hisa;
+static int bad = 0;
+static void want(bool v, const char *what) { if (!v) { std::printf("%s\n", what); bad = 1; } }
+int main() {
+    // every tile lies in the span that span_of names
+    const int64_t totals[] = {1, 2, 7, 100, 151, 152, 153, 999, 65536, (1 << 24) - 1, 1 << 24, (1 << 24) + 1, (int64_t)1 << 40};
+    for (int64_t total : totals)
+        for (int groups = 1; groups <= 152 && groups <= total; ++groups) {
+            want(span_start(0, total, groups) == 0 && span_start(groups, total, groups) == total, "ends");
+            for (int c = 0; c < groups; ++c) {
+                const int64_t s0 = span_start(c, total, groups), s1 = span_start(c + 1, total, groups);
+                want(s0 < s1 && span_of(s0, total, groups) == c && span_of(s1 - 1, total, groups) == c, "span_of");
+            }
+        }
+    // an entry is used only if it names a row and parts that there are
+    const Cut good = {9, 3, 5, 7, {0, 0, 0}};
+    want(cut_fits(good, 10, 6), "a good one");
+    auto with = [&](int64_t row, int first, int last, int place) { Cut k = good; k.row = row; k.first = first; k.last = last; k.place = place; return cut_fits(k, 10, 6); };
+    want(with(0, 0, 0, 0) && with(0, 0, 5, 1) && with(9, 5, 5, 11), "the ends");
+    want(!with(-1, 3, 5, 7) && !with(10, 3, 5, 7) && !with((int64_t)1 << 40, 3, 5, 7), "row");
+    want(!with(9, -1, 5, 7) && !with(9, 5, 3, 7) && !with(9, 3, 6, 7) && !with(9, 6, 6, 12), "span");
+    want(!with(9, 3, 5, 5) && !with(9, 3, 5, 8) && !with(9, 3, 5, -1) && !with(9, 2147483647, 2147483647, 0), "place");
+    for (int byte = 1; byte < 256; ++byte) {            // memory that nothing has written
+        Cut k;
+        std::memset(static_cast<void *>(&k), byte, sizeof k);
+        want(!cut_fits(k, 152, 152), "garbage");
+    }
+    return bad;
+}
+"""
+
+
+def test_the_join_takes_addresses_from_entries_that_fit(tmp_path):
+    # after a wait that ran out, entries of the list of cuts may hold anything
+    gxx = shutil.which("g++") or shutil.which("c++")
+    if gxx is None:
+        pytest.skip("no C++ compiler")
+    (tmp_path / "p.cc").write_text(CUTS)
+    subprocess.run([gxx, "-std=c++17", "-O1", "-I", build.CSRC, str(tmp_path / "p.cc"), "-o", str(tmp_path / "p")], check=True)
+    r = subprocess.run([str(tmp_path / "p")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout[:400]
