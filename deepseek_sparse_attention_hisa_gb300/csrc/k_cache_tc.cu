@@ -481,7 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 if (row < rows && w.left > it.T) prefetch_q(&qmap, (int32_t)(row * kH));
             }
             __syncwarp();
-            if (!wait_warp(&misc->qfull, n & 1, abort)) { fail(); break; }
+            if (!wait_warp(&misc->qfull, n & 1, abort)) {
+                fail();
+                mbar_wait(&misc->qfull, n & 1, 1u << 24); // the copy lands before the CTA leaves (bounded, whatever abort says)
+                __syncwarp();
+                break;
+            }
             for (int i = 0; i < it.T; ++i, ++g) {
                 const int s = g % kSlots, sb = g % kBufs;
                 if (!wait_warp(&misc->full[s], (g / kSlots) & 1, abort) ||
