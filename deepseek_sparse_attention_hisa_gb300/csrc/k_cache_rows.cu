@@ -25,7 +25,8 @@ __device__ __forceinline__ Place place_of(const CacheParams &p, int64_t n) {
     if (n < p.row_off[0] || n >= p.row_off[p.B]) return {-1, 0};       // padding
     // sequences of equal length are found at once
     int lo = (int)((uint64_t)n * (uint64_t)p.B / (uint64_t)p.rows);
-    if (p.row_off[lo] > n || p.row_off[lo + 1] <= n) {
+    int64_t begin = p.row_off[lo], end = p.row_off[lo + 1];
+    if (begin > n || end <= n) {
         lo = 0;
         int hi = p.B;
         while (hi - lo > 1) {
@@ -33,9 +34,12 @@ __device__ __forceinline__ Place place_of(const CacheParams &p, int64_t n) {
             if (p.row_off[mid] <= n) lo = mid;
             else hi = mid;
         }
-        if (p.row_off[lo] > n || p.row_off[lo + 1] <= n) return {-1, 0};   // not ascending: reported by check_offsets
+        begin = p.row_off[lo];
+        end = p.row_off[lo + 1];
     }
-    const int64_t first = p.row_first[lo], index = first + n - p.row_off[lo];
+    // not ascending (the search may end beside the row), or past the rows: reported by check_offsets
+    if (begin < 0 || begin > n || end <= n || end > p.rows) return {-1, 0};
+    const int64_t first = p.row_first[lo], index = first + n - begin;
     if (first < 0 || index >= (int64_t)p.table_cols * p.page_rows) {
         flag(p.status, HISA_DEV_BAD_OFFSETS);
         return {-1, 0};

@@ -597,10 +597,11 @@ HISA_API hisa_status hisa_norm_rope(const hisa_norm_rope_desc *desc, const uint6
  *   x          [rows, D] io_dtype, rows ld apart;  w [D] f32 or NULL for ones
  *   row_off    [B+1] int64, ascending;  first [B] int32 (>= 0);  page_table [B, table_cols] int32
  *   cache, scales  as hisa_cache_desc says (scales NULL for HISA_BF16), 16-byte aligned
- * Rows of x before row_off[0] or from row_off[B] on are not read. A row whose place does not fit
- * (offsets that are not ascending or pass `rows`, an index past table_cols pages, a page outside
- * [0, pages)) is left out and sets HISA_DEV_BAD_OFFSETS. No two rows of a call may have the same
- * place. ws holds the status word (hisa_workspace_bytes(HISA_OP_CACHE, desc)). */
+ * Rows of x before row_off[0] or from row_off[B] on are not read. A row whose place does not fit (an
+ * index past table_cols pages, a page outside [0, pages), a negative first) is left out, and so is a
+ * sequence whose rows [row_off[b], row_off[b+1]) do not lie in [0, rows); both set HISA_DEV_BAD_OFFSETS.
+ * Offsets that go back set it too: a row that then lies in several sequences is left out or goes to one
+ * of them. No two rows of a call may have the same place. ws holds the status word (hisa_workspace_bytes(HISA_OP_CACHE, desc)). */
 HISA_API hisa_status hisa_cache_append(const hisa_cache_desc *desc, const uint64_t *table, const void *x,
                               const float *w, const int64_t *row_off, const int32_t *first,
                               const int32_t *page_table, void *cache, void *scales, void *ws,

@@ -837,3 +837,61 @@ def test_paged_decode(batch, pooled, hidden, steps, select, bits4, page):
     sys.path.insert(0, os.path.join(root, "examples"))
     import paged_decode
     assert paged_decode.run(batch, pooled, hidden, steps, select, bits4, page, say=lambda *_: None) < 0.1
+
+
+# ------------------------------------------------------------------------------------
+# what offsets that do not fit leave in the cache, and in the rows read
+# ------------------------------------------------------------------------------------
+FAR = 1 << 62
+BAD_OFFSETS = [
+    # offsets, first rows; the packed rows that have a place, with their sequence
+    ([-3, 10, 20, 30], [0, 0, 0], {n: n // 10 for n in range(10, 30)}),
+    ([-FAR, 10, 20, 30], [0, 0, 0], {n: n // 10 for n in range(10, 30)}),
+    ([-2 * FAR, 10, 20, 30], [5, 0, 0], {n: n // 10 for n in range(10, 30)}),
+    ([0, 10, 20, 60], [0, 0, 0], {n: n // 10 for n in range(20)}),
+    ([0, 10, 20, FAR], [0, 0, 0], {n: n // 10 for n in range(20)}),
+    ([0, 10, 20, 30], [0, -1, 0], {n: n // 10 for n in (*range(10), *range(20, 30))}),
+    ([0, 10, -2 * FAR, 30], [0, 0, 0], {n: 0 for n in range(10)}),
+    ([40, 30, 20, 10], [0, 0, 0], {}),
+]
+
+
+@pytest.mark.parametrize("off,first,rows", BAD_OFFSETS)
+@pytest.mark.parametrize("cache", ["4bit", "bf16"])
+def test_offsets_that_do_not_fit_leave_their_rows_out(off, first, rows, cache):
+    page, D, n = 8, 64, 50
+    x = randn((n, D), "bf16", 5)
+    pool, scales = empty_pool(24, page, D, cache)
+    table = torch.arange(24, device="cuda", dtype=torch.int32).view(3, 8)
+    d = append_desc(x, pool, 3, 8, page, cache)
+    ws = workspace(hb.OP_CACHE, d)
+    off, first = ints(off, torch.int64), ints(first)
+    hb.cache_append(d, None, x, None, off, first, table, pool, scales, ws)
+    assert hb.device_status(ws) == hb.DEV_BAD_OFFSETS
+    want = torch.zeros(24 * page, dtype=torch.bool, device="cuda")
+    for i, b in rows.items():
+        want[64 * b + int(first[b]) + i - int(off[b])] = True
+    assert torch.equal(~pool_rows(pool, scales, 0.75).isnan().any(-1), want)
+    full, full_s = random_pool(24, page, D, cache, 3)
+    out = torch.full((n, D), NAN, device="cuda")
+    hb.workspace_init(ws)
+    hb.cache_read(append_desc(out, pool, 3, 8, page, cache), off, first, table, full, full_s, out, ws)
+    assert hb.device_status(ws) == hb.DEV_BAD_OFFSETS
+    assert (~out.isnan().any(-1)).nonzero().flatten().tolist() == sorted(rows)
+
+
+@pytest.mark.parametrize("cache", ["4bit", "bf16"])
+def test_offsets_that_go_back(cache):
+    # rows 20 to 29 lie in sequences 0 and 2: each goes to one of them, or to none; all others have their place
+    page, D, n = 8, 64, 50
+    x = randn((n, D), "bf16", 5)
+    pool, scales = empty_pool(24, page, D, cache)
+    table = torch.arange(24, device="cuda", dtype=torch.int32).view(3, 8)
+    d = append_desc(x, pool, 3, 8, page, cache)
+    ws = workspace(hb.OP_CACHE, d)
+    hb.cache_append(d, None, x, None, ints([0, 30, 20, 50], torch.int64), ints([0, 0, 0]), table, pool, scales, ws)
+    assert hb.device_status(ws) == hb.DEV_BAD_OFFSETS
+    there = (~pool_rows(pool, scales, 0.75).isnan().any(-1)).view(3, 64).cpu()
+    assert there[0, :20].all() and not there[0, 30:].any() and not there[1].any()
+    assert there[2, 10:30].all() and not there[2, 30:].any()
+    assert not (there[0, 20:30] & there[2, :10]).any()
