@@ -179,11 +179,9 @@ hisa_status hisa_norm_rope(const hisa_norm_rope_desc *d, const uint64_t *table, 
     if (d->heads2 && ((x2 == y2) != inplace ||
                       (inplace && (d->x2_token != d->y2_token || d->x2_head != d->y2_head))))
         return HISA_EINVAL;
-    // neighbouring heads of an output that overlap would be written by several warps, in no order
-    auto apart = [&](int64_t heads, int64_t token, int64_t head) {
-        return (d->tokens == 1 || token >= d->D) && (heads <= 1 || head >= d->D) && (d->tokens == 1 || heads <= 1 || token != head);
-    };
-    if (!apart(d->heads, d->y_token, d->y_head) || (d->heads2 && !apart(d->heads2, d->y2_token, d->y2_head)))
+    // heads of an output that overlap would be written by several warps, in no order
+    if (!heads_apart(d->tokens, d->heads, d->y_token, d->y_head, d->D) ||
+        (d->heads2 && !heads_apart(d->tokens, d->heads2, d->y2_token, d->y2_head, d->D)))
         return HISA_EINVAL;
     NormRopeParams p{};
     p.tokens = d->tokens; p.heads = d->heads; p.heads2 = d->heads2; p.D = d->D;

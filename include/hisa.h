@@ -532,8 +532,8 @@ HISA_API hisa_status hisa_rope_table(const hisa_rope_scaling *scaling, uint64_t 
  *   x, y  [tokens, heads, D] and x2, y2 [tokens, heads2, D] with the strides of the descriptor
  * y == x (same strides and dtype) rotates in place and touches the rotated dims alone; the
  * same for y2 == x2, and both are in place or neither is. Otherwise no output may overlap an
- * input. The heads of an output do not overlap one another (strides of neighbours below D, or in
- * place below rope_dims, are refused); those of an input may (a stride of 0 repeats a row).
+ * input. The heads of an output do not overlap one another (strides by which any two do, in place in their
+ * rotated dims, are refused); those of an input may (a stride of 0 repeats a row).
  * Pointers are aligned to their element. No workspace. */
 HISA_API hisa_status hisa_rope(const hisa_rope_desc *desc, const uint64_t *table, const int32_t *pos,
                       const void *x, void *y, const void *x2, void *y2, hisa_stream_t stream);
@@ -579,7 +579,7 @@ HISA_API hisa_status hisa_prefix_attend(const hisa_prefix_desc *desc, const void
  *   w, w2 [D] f32, or NULL for ones (and without the norm)
  * y == x (same strides and dtype) works in place; the same for y2 == x2, and both are in place or
  * neither is. Otherwise no output may overlap an input. The heads of an output do not overlap one
- * another (strides of neighbours below D are refused); those of an input may. Pointers are aligned to
+ * another (strides by which any two do are refused); those of an input may. Pointers are aligned to
  * their element; fastest where every head starts at a multiple of 8 elements and rope_first and
  * rope_dims (with halves rope_dims / 2) are such. No workspace. */
 HISA_API hisa_status hisa_norm_rope(const hisa_norm_rope_desc *desc, const uint64_t *table, const int32_t *pos,

@@ -265,3 +265,61 @@ def test_the_join_takes_addresses_from_entries_that_fit(tmp_path):
     subprocess.run([gxx, "-std=c++17", "-O1", "-I", build.CSRC, str(tmp_path / "p.cc"), "-o", str(tmp_path / "p")], check=True)
     r = subprocess.run([str(tmp_path / "p")], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout[:400]
+
+
+APART = r"""
+#include <cstdio>
+#include "heads_apart.h"
+using namespace hisa;
+int main() {
+    // against every pair of heads
+    for (int64_t w = 1; w <= 4; ++w)
+        for (int64_t tokens = 1; tokens <= 5; ++tokens)
+            for (int64_t heads = 1; heads <= 4; ++heads)
+                for (int64_t token = 0; token <= 26; ++token)
+                    for (int64_t head = 0; head <= 26; ++head) {
+                        bool apart = true;
+                        for (int64_t i = 0; i < tokens * heads && apart; ++i)
+                            for (int64_t j = 0; j < i && apart; ++j) {
+                                const int64_t d = (i / heads - j / heads) * token + (i % heads - j % heads) * head;
+                                apart = d >= w || d <= -w;
+                            }
+                        if (apart != heads_apart(tokens, heads, token, head, w)) {
+                            std::printf("%d x %d, %d and %d apart, %d wide\n", (int)tokens, (int)heads, (int)token, (int)head, (int)w);
+                            return 1;
+                        }
+                    }
+    const int64_t far = (int64_t)1 << 40;
+    return heads_apart(((int64_t)1 << 31) - 1, 1, 512, far, 512) && heads_apart(1 << 20, 65536, far, 512, 512) &&
+           heads_apart(1 << 20, 65536, 512, far, 512) && !heads_apart(1 << 20, 65536, far, far, 512) &&
+           !heads_apart(65536, 65536, far - 1, far, 512) ? 0 : 2;
+}
+"""
+
+
+def test_strides_that_keep_heads_apart(tmp_path):
+    gxx = shutil.which("g++") or shutil.which("c++")
+    if gxx is None:
+        pytest.skip("no C++ compiler")
+    (tmp_path / "p.cc").write_text(APART)
+    subprocess.run([gxx, "-std=c++17", "-O1", "-I", build.CSRC, str(tmp_path / "p.cc"), "-o", str(tmp_path / "p")], check=True)
+    r = subprocess.run([str(tmp_path / "p")], capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stdout)
+
+
+# tokens token apart and heads head apart such that a head of one token is one of another's, or overlaps it
+CROSSED = [(3, 2, 512, 1024), (2, 3, 1024, 512), (4, 3, 1024, 1536), (3, 8, 700, 1300), (9, 2, 600, 4700)]
+
+
+@pytest.mark.parametrize("tokens,heads,token,head", CROSSED)
+def test_outputs_whose_heads_cross_are_refused(lib, tokens, heads, token, head):
+    far = P(1 << 32)
+    d = heads_desc(tokens=tokens, heads=heads, heads2=0, y_token=token, y_head=head)
+    assert lib.hisa_norm_rope(ctypes.byref(d), FAKE, FAKE, FAKE, None, far, None, None, None, None) == EINVAL
+    d = heads_desc(tokens=tokens, heads=1, heads2=heads, y2_token=token, y2_head=head)
+    assert lib.hisa_norm_rope(ctypes.byref(d), FAKE, FAKE, FAKE, None, far, FAKE, None, P(1 << 33), None) == EINVAL
+    kw = dict(tokens=tokens, heads=heads, heads2=0, D=512, rope_dims=64, rope_first=448, src_dtype=hb.HISA_BF16, dst_dtype=hb.HISA_BF16,
+              mscale=1.0, x_token=heads * 512, x_head=512, y_token=token, y_head=head)
+    assert lib.hisa_rope(ctypes.byref(hb.RopeDesc(**kw)), FAKE, FAKE, FAKE, far, None, None, None) == EINVAL
+    kw.update(x_token=token, x_head=token, y_head=token)   # in place, token after token at the same dims
+    assert lib.hisa_rope(ctypes.byref(hb.RopeDesc(**kw)), FAKE, FAKE, FAKE, FAKE, None, None, None) == EINVAL

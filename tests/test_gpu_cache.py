@@ -895,3 +895,16 @@ def test_offsets_that_go_back(cache):
     assert there[0, :20].all() and not there[0, 30:].any() and not there[1].any()
     assert there[2, 10:30].all() and not there[2, 30:].any()
     assert not (there[0, 20:30] & there[2, :10]).any()
+
+
+@pytest.mark.parametrize("token,head", [(512, 5 * 512), (512, 4 * 512 + 600), (1600, 520), (1536, 1024)])
+def test_norm_rope_heads_before_tokens(token, head):
+    # tokens within heads, or heads between those of the tokens beside: all apart
+    tokens, heads = (5, 3) if token != 1536 else (2, 2)
+    buf = torch.full((8 * 5 * 1536,), 7.0, device="cuda", dtype=torch.bfloat16)
+    x, pos, w = randn((tokens, heads, 512), "bf16", 2), positions(tokens), 1 + randn((512,), "f32", 3, 0.1)
+    y = buf.as_strided((tokens, heads, 512), (token, head, 1))
+    run_norm_rope(x, y, pos, 64, 448, 0, w)
+    check_turned(y, *turned(x, w, True, pos, 64, 448, 0), "bf16")
+    y.fill_(7.0)
+    assert (buf == 7.0).all()
