@@ -29,14 +29,17 @@ class PagedDecode:
     tokens the window buffer takes. pages: pages of page_rows rows that the sequences share out among
     themselves; max_rows: pooled rows of a sequence at most. r: tokens per pooled row; pooled row p sits at
     position p r. bits4: rows in 4 bits (16 dims share a scale), else bf16; cache_scale: the factor of
-    all rows in 4 bits.
+    all rows in 4 bits. recent: the KV rows of the positions before start, normed and rotated, bf16: [B, n, DH], or a
+    list of [n_b, DH] (the last window - 1 matter); without them the first tokens see nothing of the
+    prompt but its pooled rows.
     Tensors of another shape, type, device or layout raise ValueError, and so does a cache that is full."""
 
     def __init__(self, B, weights, start, steps, pages, max_rows, page_rows=64, window=128, r=4, bits4=True, cache_scale=1.0,
-                 eps=1e-6, theta=160000.0, device="cuda"):
+                 eps=1e-6, theta=160000.0, device="cuda", recent=None):
         import torch
         self.B, self.w, self.n, self.r = B, weights, 0, r
         self.steps, self.hidden, self.page_rows, self.max_rows = steps, weights["norm"].numel(), page_rows, max_rows
+        self.window = window
         if B < 1 or steps < 1 or pages < 1 or max_rows < 0 or page_rows < 1 or r < 1:
             raise ValueError("B, steps, pages, page_rows and r of 1 at least expected")
         starts = [int(start)] * B if not hasattr(start, "__len__") else [int(t) for t in start]
@@ -55,12 +58,25 @@ class PagedDecode:
                                      eps=eps, ld_x=self.hidden, ld_res=self.hidden, ld_out=self.hidden)
         self.act = torch.empty((B, self.hidden), **bf16)
         self.table = hb.rope_table(hb.RopeScaling(rope_dims=ROPE_DIMS, kind=hb.ROPE_PLAIN, theta=theta), device)
-        self.local = torch.zeros((B, steps, DH), **bf16)
+        # sequence b's next row of the window buffer is n + ahead[b]: where all are the same, the KV rows go straight
+        # into it, else by way of kv_row
+        recent = [None] * B if recent is None else list(recent)
+        if len(recent) != B:
+            raise ValueError(f"recent: rows of {B} sequences expected, got {len(recent)}")
+        recent = [self._reached(x, t) for x, t in zip(recent, starts)]
+        self.ahead = [x.shape[0] for x in recent]
+        self.top, self.together = max(self.ahead), min(self.ahead) == max(self.ahead)
+        self.capacity = self.top + steps
+        self.local = torch.zeros((B, self.capacity, DH), **bf16)
+        for b, x in enumerate(recent):
+            self.local[b, :x.shape[0]] = x
+        self.kv_row = torch.empty((B, DH), **bf16)
+        self.row0 = torch.arange(B, device=device) * self.capacity
         self.q, self.out = torch.empty((B, H, DH), **bf16), torch.empty((B, H, DH), **bf16)
         dense = dict(x_token=H * DH, x_head=DH, y_token=H * DH, y_head=DH)
         self.head_desc = hb.NormRopeDesc(tokens=B, heads=H, heads2=1, D=DH, norm=1, norm2=1, rope_dims=ROPE_DIMS, rope_first=DH - ROPE_DIMS,
                                          src_dtype=hb.HISA_BF16, dst_dtype=hb.HISA_BF16, eps=eps, mscale=1.0, x2_token=DH, x2_head=DH,
-                                         y2_token=self.local.stride(0), y2_head=DH, **dense)
+                                         y2_head=DH, **dense)
         self.back_desc = hb.RopeDesc(tokens=B, heads=H, heads2=0, D=DH, rope_dims=ROPE_DIMS, rope_first=DH - ROPE_DIMS, inverse=1,
                                      src_dtype=hb.HISA_BF16, dst_dtype=hb.HISA_BF16, mscale=1.0, **dense)
         cols = max(1, -(-max_rows // page_rows))
@@ -72,13 +88,27 @@ class PagedDecode:
         self.cache_len = torch.zeros(B, **i32)
         self.cache_desc = dict(pages=pages, page_rows=page_rows, D=DH, cache_dtype=kind, cache_scale=cache_scale, table_cols=cols,
                                norm=1, eps=eps, rope_dims=ROPE_DIMS, rope_first=DH - ROPE_DIMS, r=r, mscale=1.0)
-        self.desc = hb.CacheAttnDesc(B=B, L=1, H=H, Dh=DH, window=window, W_max=steps, r=r, k=0, page_rows=page_rows, table_cols=cols,
+        self.desc = hb.CacheAttnDesc(B=B, L=1, H=H, Dh=DH, window=window, W_max=self.capacity, r=r, k=0, page_rows=page_rows, table_cols=cols,
                                      pages=pages, Np_max=max_rows, scale=0.0, cache_scale=cache_scale, q_dtype=hb.HISA_BF16,
                                      cache_dtype=kind, out_dtype=hb.HISA_BF16)
         self.pos = torch.tensor(starts, **i32)
-        self.local_pos0, self.local_len = self.pos.clone(), torch.zeros(B, **i32)
+        self.local_len = torch.tensor(self.ahead, **i32)
+        self.local_pos0 = self.pos - self.local_len
         self.cache_ws = hb.alloc_workspace(256, device)
         self.ws, self.ws_k = hb.alloc_workspace(hb.workspace_bytes(hb.OP_CACHE_ATTEND, self.desc), device), 0
+
+    def _reached(self, rows, start):
+        """The rows before position start that the window reaches."""
+        import torch
+        if rows is None:
+            return torch.empty((0, DH), device=self.device, dtype=torch.bfloat16)
+        if rows.dim() != 2:
+            raise ValueError("recent: [n, DH] expected for a sequence")
+        n = rows.shape[0]
+        _expect(rows, "recent", (n, DH), torch.bfloat16, self.device, "any")
+        if n > start:
+            raise ValueError(f"recent: {n} rows before position {start}")
+        return rows[n - min(n, max(self.window - 1, 0)):]
 
     def append(self, rows, counts):
         """Pooled rows that have completed, counts[b] of sequence b, packed in the sequences' order: [n, DH] bf16 or
@@ -138,7 +168,7 @@ class PagedDecode:
         Returns the combine's output [B, H, DH] bf16, turned back to position-free dims; the next step
         writes it anew."""
         import torch
-        if self.n == self.steps:
+        if self.n + self.top == self.capacity:
             raise ValueError("the window buffer is full")
         for t, name in ((x, "x"), (residual, "residual")):
             _expect(t, name, (self.B, self.hidden), torch.bfloat16, self.device, "rows")
@@ -161,9 +191,13 @@ class PagedDecode:
         self.norm_desc.ld_res = residual.stride(0) if self.B > 1 else self.hidden
         hb.rms_norm(self.norm_desc, x, residual, self.w["norm"], residual, self.act)
         q, kv = self.act @ self.w["q"], self.act @ self.w["kv"]
-        hb.norm_rope(self.head_desc, self.table, self.pos, q, self.w["q_norm"], self.q, kv, self.w["kv_norm"], self.local[:, self.n])
+        row = self.local[:, self.n + self.top] if self.together else self.kv_row
+        self.head_desc.y2_token = row.stride(0)
+        hb.norm_rope(self.head_desc, self.table, self.pos, q, self.w["q_norm"], self.q, kv, self.w["kv_norm"], row)
+        if not self.together:
+            self.local.view(-1, DH).index_copy_(0, self.row0 + self.local_len, row)
         self.n += 1
-        self.local_len.fill_(self.n)
+        self.local_len += 1
         hb.cache_attend(self.desc, self.q, self.local, self.local_len, self.local_pos0, self.pool, self.scales, self.page_table,
                         self.cache_len, I, self.w["sinks"], self.pos, self.out, self.ws)
         hb.rope(self.back_desc, self.table, self.pos, self.out, self.out)

@@ -2,11 +2,11 @@
 
   python examples/paged_decode.py [--batch 64] [--pooled 4096] [--hidden 4096] [--steps 16] [--select 512] [--bf16]
 
-Weights and states are random; each sequence's prompt has left between none and --pooled pooled rows, and
-every fourth token completes one more. With --select each step combines that many rows of each
-sequence, drawn at random. Every step's output is compared with the same step in f64 on the cached rows as they
-stand and the queries and KV rows rounded as the layer stores them, and the time of a step is
-printed.
+Weights and states are random; each sequence's prompt has left between none and --pooled pooled rows and the
+KV rows of its last positions (as far back as the window reaches), and every fourth token completes one more.
+With --select each step combines that many rows of each sequence, drawn at random. Every step's output is
+compared with the same step in f64 on the cached rows as they stand and the queries and KV rows rounded as
+the layer stores them, and the time of a step is printed.
 """
 import argparse
 import math
@@ -51,11 +51,12 @@ def run(batch=64, pooled=4096, hidden=4096, steps=16, select=0, bits4=True, page
     have[0] = pooled
     start = [4 * n for n in have]
     most = pooled + steps
-    layer = PagedDecode(batch, w, start, steps, batch * -(-most // page_rows), most, page_rows, window, bits4=bits4, eps=EPS)
+    recent = [normal(min(t, window - 1), DH).to(bf16) for t in start]
+    layer = PagedDecode(batch, w, start, steps, batch * -(-most // page_rows), most, page_rows, window, bits4=bits4, eps=EPS, recent=recent)
     layer.append(normal(sum(have), DH, std=2).to(bf16), have)
     worst, spent = 0.0, []
     check = sorted({0, batch // 2, batch - 1})
-    local = {b: [] for b in check}
+    local = {b: list(recent[b].double()) for b in check}
     for n in range(steps):
         x, residual = normal(batch, hidden).to(bf16), normal(batch, hidden, std=3).to(bf16)
         I = None

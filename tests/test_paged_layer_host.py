@@ -154,3 +154,46 @@ def test_bf16_pages(calls):
     p.append(rows(3, DH), [1, 1, 1])
     p.step(rows(), rows())
     assert [c[0] for c in calls] == ["append", "norm", "heads", "attend", "rope"]
+
+
+def kv_rows(n, first=1):
+    return torch.arange(first, first + n, dtype=BF16)[:, None].repeat(1, DH)
+
+
+def test_the_window_holds_the_prompts_last_rows(calls):
+    # as many as the window reaches, for all the same: KV rows go straight behind them
+    p = layer(window=5, start=[9, 7, 4], recent=torch.stack([kv_rows(4, b) for b in (1, 11, 21)]))
+    assert p.local.shape == (3, 8, DH) and p.local[:, :4, 0].tolist() == [[1, 2, 3, 4], [11, 12, 13, 14], [21, 22, 23, 24]]
+    assert p.local_len.tolist() == [4, 4, 4] and p.local_pos0.tolist() == [5, 3, 0] and p.desc.W_max == 8
+    for n in range(4):
+        p.step(rows(), rows())
+        assert calls[-3][1:] == (8 * DH, p.local[:, 4 + n].data_ptr())
+    assert p.local_len.tolist() == [8, 8, 8] and p.local_pos0.tolist() == [5, 3, 0] and p.pos.tolist() == [13, 11, 8]
+    with pytest.raises(ValueError, match="full"):
+        p.step(rows(), rows())
+
+
+def test_sequences_may_have_unequal_rows_before(calls, monkeypatch):
+    # more than the window reaches are cut; each sequence's KV row goes behind its own
+    p = layer(window=3, steps=2, start=[9, 1, 4], recent=[kv_rows(5), kv_rows(1, 40), kv_rows(0)])
+    assert p.local.shape == (3, 4, DH) and p.local[0, :2, 0].tolist() == [4, 5] and p.local[1, 0, 0] == 40
+    assert p.local_len.tolist() == [2, 1, 0] and p.local_pos0.tolist() == [7, 0, 4]
+
+    def heads(d, *a):
+        assert d.y2_token == DH
+        a[-1].copy_(torch.tensor([100.0, 110.0, 120.0])[:, None] + p.n)
+
+    monkeypatch.setattr(hb, "norm_rope", heads)
+    p.step(rows(), rows())
+    p.step(rows(), rows())
+    assert p.local[..., 0].tolist() == [[4, 5, 100, 101], [40, 110, 111, 0], [120, 121, 0, 0]]
+    assert p.local_len.tolist() == [4, 3, 2] and p.local_pos0.tolist() == [7, 0, 4]
+    with pytest.raises(ValueError, match="full"):
+        p.step(rows(), rows())
+
+
+@pytest.mark.parametrize("bad", [[kv_rows(1)] * 2, [kv_rows(33)] * 3, [kv_rows(1).float()] * 3, [kv_rows(1)[0]] * 3, [kv_rows(1)[:, 1:]] * 3,
+                                 torch.zeros(4, 2, DH, dtype=BF16), torch.zeros(3, 2, DH // 2, dtype=BF16)])
+def test_rows_before_are_checked(calls, bad):
+    with pytest.raises(ValueError):
+        layer(recent=bad)
