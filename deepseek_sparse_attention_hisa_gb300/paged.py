@@ -27,11 +27,11 @@ class PagedDecode:
     q_norm [DH], kv_norm [DH] (heads and KV rows are normed), sinks [H] f32 (or None).
     start: the position of the first token decoded, one for all or a list of one each. steps: how many
     tokens the window buffer takes. pages: pages of page_rows rows that the sequences share out among
-    themselves; max_rows: pooled rows of a sequence at most. r: tokens per pooled row; pooled row p sits at
-    position p r. bits4: rows in 4 bits (16 dims share a scale), else bf16; cache_scale: the factor of
-    all rows in 4 bits. recent: the KV rows of the positions before start, normed and rotated, bf16: [B, n, DH], or a
-    list of [n_b, DH] (the last window - 1 matter); without them the first tokens see nothing of the
-    prompt but its pooled rows.
+    themselves, also with those that begin later in the place of others (admit); max_rows: pooled rows of a
+    sequence at most. r: tokens per pooled row; pooled row p sits at position p r. bits4: rows in 4 bits (16
+    dims share a scale), else bf16; cache_scale: the factor of all rows in 4 bits. recent: the KV rows of the
+    positions before start, normed and rotated, bf16: [B, n, DH], or a list of [n_b, DH] (the last window - 1
+    matter); without them the first tokens see nothing of the prompt but its pooled rows.
     Tensors of another shape, type, device or layout raise ValueError, and so does a cache that is full."""
 
     def __init__(self, B, weights, start, steps, pages, max_rows, page_rows=64, window=128, r=4, bits4=True, cache_scale=1.0,
@@ -65,7 +65,7 @@ class PagedDecode:
             raise ValueError(f"recent: rows of {B} sequences expected, got {len(recent)}")
         recent = [self._reached(x, t) for x, t in zip(recent, starts)]
         self.ahead = [x.shape[0] for x in recent]
-        self.top, self.together = max(self.ahead), min(self.ahead) == max(self.ahead)
+        self._order()
         self.capacity = self.top + steps
         self.local = torch.zeros((B, self.capacity, DH), **bf16)
         for b, x in enumerate(recent):
@@ -96,6 +96,9 @@ class PagedDecode:
         self.local_pos0 = self.pos - self.local_len
         self.cache_ws = hb.alloc_workspace(256, device)
         self.ws, self.ws_k = hb.alloc_workspace(hb.workspace_bytes(hb.OP_CACHE_ATTEND, self.desc), device), 0
+
+    def _order(self):
+        self.top, self.together = max(self.ahead), min(self.ahead) == max(self.ahead)
 
     def _reached(self, rows, start):
         """The rows before position start that the window reaches."""
@@ -155,12 +158,32 @@ class PagedDecode:
         return out
 
     def release(self, b):
-        """Sequence b's pages are free again; it has no pooled rows."""
+        """Sequence b's pages are free again; it has no pooled rows. It decodes on behind its window alone, and rows
+        appended to it start at position 0: admit begins another sequence in its place."""
         import torch
         self.free += self.owned[b][::-1]
         self.owned[b], self.lens[b] = [], 0
         self.page_table[b].fill_(-1)
         self.cache_len.copy_(torch.tensor(self.lens, dtype=torch.int32))
+
+    def admit(self, b, start, recent=None):
+        """Another sequence begins in the place of sequence b, which ends: its first token decoded has position start,
+        recent [n, DH] are the KV rows before it (as the constructor takes them), and its pooled rows are those that are
+        appended from now on. Of the sequence before it nothing is seen any more."""
+        start = int(start)
+        if not 0 <= b < self.B:
+            raise ValueError(f"no sequence {b} of {self.B}")
+        recent = self._reached(recent, start)
+        n = recent.shape[0]
+        if start < 0 or start + self.capacity - n > 2**31:
+            raise ValueError("positions from 0 to 2^31 - 1 expected")
+        if n >= self.capacity:
+            raise ValueError(f"recent: {n} rows fill the window buffer of {self.capacity}")
+        self.release(b)
+        self.local[b, :n] = recent.clone()               # it may be rows of this buffer
+        self.ahead[b] = n - self.n
+        self._order()
+        self.local_len[b], self.local_pos0[b], self.pos[b] = n, start - n, start
 
     def step(self, x, residual, I=None):
         """One token per sequence: x, residual [B, hidden] bf16, rows dense (residual is updated in place).

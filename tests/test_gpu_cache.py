@@ -908,3 +908,53 @@ def test_norm_rope_heads_before_tokens(token, head):
     check_turned(y, *turned(x, w, True, pos, 64, 448, 0), "bf16")
     y.fill_(7.0)
     assert (buf == 7.0).all()
+
+
+@pytest.mark.parametrize("bits4", [True, False])
+def test_a_sequence_begins_behind_its_own_rows(bits4):
+    # three sequences with unequal rows before them; the second is released, then another takes its place twice. Queries, rows,
+    # weights and outputs are rounded to bf16 (2^-8 each, weights by logits up to 10 more): below a tenth of the largest output, where
+    # a row too many or too few of the 20 that a window holds shows as several tenths.
+    import os
+    import sys
+
+    import deepseek_sparse_attention_hisa_gb300 as pkg
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(pkg.__file__))), "examples"))
+    from paged_decode import normed, turn
+
+    from deepseek_sparse_attention_hisa_gb300.paged import DH, H, PagedDecode
+    B, hidden, window = 3, 512, 20
+    w = {"norm": 1 + randn((hidden,), "f32", 1, 0.1), "q": randn((hidden, H * DH), "bf16", 2, hidden**-0.5),
+         "kv": randn((hidden, DH), "bf16", 3, hidden**-0.5), "sinks": randn((H,), "f32", 4) + 1, "q_norm": 1 + randn((DH,), "f32", 5, 0.1),
+         "kv_norm": 1 + randn((DH,), "f32", 6, 0.1)}
+    start = [100, 3, 40]
+    recent = [randn((n, DH), "bf16", 7 + n) for n in (19, 3, 30)]
+    p = PagedDecode(B, w, start, 12, pages=40, max_rows=30, page_rows=4, window=window, bits4=bits4, recent=recent)
+    p.append(randn((35, DH), "bf16", 8, 2.0), [25, 0, 10])
+    local, at = [list(x.double()) for x in recent], list(start)
+
+    def begin(b, t, n, seed):
+        x = randn((n, DH), "bf16", seed)
+        p.admit(b, t, x)
+        local[b], at[b] = list(x.double()), t
+
+    for n in range(10):
+        if n == 3:
+            p.release(1)
+        if n == 4:
+            begin(1, 50, 0, 0)
+            p.append(randn((7, DH), "bf16", 21, 2.0), [0, 7, 0])
+        if n == 7:
+            begin(1, 9, 9, 22)
+        out = p.step(randn((B, hidden), "bf16", 30 + n), randn((B, hidden), "bf16", 50 + n))
+        q = normed((p.act @ w["q"]).view(B, H, DH), w["q_norm"])
+        kv = normed(p.act @ w["kv"], w["kv_norm"])
+        for b in range(B):
+            local[b].append(turn(kv[b], at[b], 1).to(torch.bfloat16).double())
+            v = torch.cat([torch.stack(local[b][-window:]), p.rows(b, torch.float32).double()])
+            z = turn(q[b], at[b], 1).to(torch.bfloat16).double() @ v.t() / math.sqrt(DH)
+            pr = torch.softmax(torch.cat([z, w["sinks"].double()[:, None]], -1), -1)[:, :-1]
+            want = turn(pr @ v, at[b], -1)
+            assert (out[b].double() - want).abs().max() < 0.1 * want.abs().max(), (n, b)
+            at[b] += 1
+    assert p.status() == 0 and p.lens == [25, 0, 10]

@@ -197,3 +197,39 @@ def test_sequences_may_have_unequal_rows_before(calls, monkeypatch):
 def test_rows_before_are_checked(calls, bad):
     with pytest.raises(ValueError):
         layer(recent=bad)
+
+
+def test_a_sequence_begins_in_the_place_of_another(calls, monkeypatch):
+    p = layer(window=4, steps=5, start=[40, 50, 60])
+    monkeypatch.setattr(hb, "norm_rope", lambda d, *a: a[-1].copy_(torch.tensor([100.0, 110.0, 120.0])[:, None] + p.n))
+    p.append(rows(9, DH), [4, 4, 1])
+    p.step(rows(), rows())
+    p.step(rows(), rows())
+    p.admit(1, 7, kv_rows(6))
+    assert p.lens == [4, 0, 1] and len(p.free) == 4 and p.cache_len.tolist() == [4, 0, 1] and (p.page_table[1] == -1).all()
+    assert p.local_len.tolist() == [2, 3, 2] and p.local_pos0.tolist() == [40, 4, 60] and p.pos.tolist() == [42, 7, 62]
+    p.append(rows(2, DH), [0, 2, 0])
+    assert calls[-1] == ("append", 2, DH, [0, 0, 2, 2], [4, 0, 1])
+    p.step(rows(), rows())
+    assert p.local[..., 0].tolist() == [[100, 101, 102, 0, 0], [4, 5, 6, 112, 0], [120, 121, 122, 0, 0]]
+    assert p.local_len.tolist() == [3, 4, 3] and p.local_pos0.tolist() == [40, 4, 60] and p.pos.tolist() == [43, 8, 63]
+    p.admit(1, 0)
+    p.step(rows(), rows())
+    p.step(rows(), rows())
+    assert p.local[1, :2, 0].tolist() == [113, 114] and p.local_len.tolist() == [5, 2, 5] and p.local_pos0.tolist() == [40, 0, 60]
+    with pytest.raises(ValueError, match="full"):                 # the buffers of those that were there
+        p.step(rows(), rows())
+    p.admit(0, 5, p.local[0, 2:5])
+    p.admit(2, 9, p.local[2, 3:5])
+    p.step(rows(), rows())
+    assert p.local[0, :4, 0].tolist() == [102, 103, 104, 105] and p.local[2, :3, 0].tolist() == [123, 124, 125]
+
+
+@pytest.mark.parametrize("b,start,recent", [(3, 0, None), (-1, 0, None), (0, -1, None), (0, 2**31 - 3, None), (0, 2, kv_rows(3)), (0, 9, kv_rows(2).float()),
+                                            (0, 9, kv_rows(4)), (0, 9, kv_rows(1)[0])])
+def test_what_cannot_begin(calls, b, start, recent):
+    p = layer(window=9)
+    p.append(rows(3, DH), [1, 1, 1])
+    with pytest.raises(ValueError):
+        p.admit(b, start, recent)
+    assert p.lens == [1, 1, 1] and p.pos.tolist() == [32] * 3 and p.local_len.tolist() == [0] * 3
