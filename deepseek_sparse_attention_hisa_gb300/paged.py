@@ -97,6 +97,10 @@ class PagedDecode:
         self.cache_ws = hb.alloc_workspace(256, device)
         self.ws, self.ws_k = hb.alloc_workspace(hb.workspace_bytes(hb.OP_CACHE_ATTEND, self.desc), device), 0
 
+    def _there(self, b):
+        if not 0 <= b < self.B:                          # -1 would name the last one here and no row of the page table there
+            raise ValueError(f"no sequence {b} of {self.B}")
+
     def _order(self):
         self.top, self.together = max(self.ahead), min(self.ahead) == max(self.ahead)
 
@@ -147,6 +151,7 @@ class PagedDecode:
     def rows(self, b, dtype=None):
         """Sequence b's pooled rows as the combine sees them, [len, DH] in bf16 (or f32)."""
         import torch
+        self._there(b)
         out = torch.empty((self.lens[b], DH), device=self.device, dtype=dtype or torch.bfloat16)
         if out.dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("bf16 or f32 expected")
@@ -161,6 +166,7 @@ class PagedDecode:
         """Sequence b's pages are free again; it has no pooled rows. It decodes on behind its window alone, and rows
         appended to it start at position 0: admit begins another sequence in its place."""
         import torch
+        self._there(b)
         self.free += self.owned[b][::-1]
         self.owned[b], self.lens[b] = [], 0
         self.page_table[b].fill_(-1)
@@ -171,8 +177,7 @@ class PagedDecode:
         recent [n, DH] are the KV rows before it (as the constructor takes them), and its pooled rows are those that are
         appended from now on. Of the sequence before it nothing is seen any more."""
         start = int(start)
-        if not 0 <= b < self.B:
-            raise ValueError(f"no sequence {b} of {self.B}")
+        self._there(b)
         recent = self._reached(recent, start)
         n = recent.shape[0]
         if start < 0 or start + self.capacity - n > 2**31:

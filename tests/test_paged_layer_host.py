@@ -233,3 +233,14 @@ def test_what_cannot_begin(calls, b, start, recent):
     with pytest.raises(ValueError):
         p.admit(b, start, recent)
     assert p.lens == [1, 1, 1] and p.pos.tolist() == [32] * 3 and p.local_len.tolist() == [0] * 3
+
+
+@pytest.mark.parametrize("b", [-1, 3])
+def test_sequences_that_are_not_there(calls, b):
+    p = layer()
+    p.append(rows(3, DH), [1, 1, 1])
+    n = len(calls)
+    for f in (p.rows, p.release):
+        with pytest.raises(ValueError, match="no sequence"):
+            f(b)
+    assert len(calls) == n and p.lens == [1, 1, 1]
