@@ -95,7 +95,10 @@ class PagedDecode:
         self.local_len = torch.tensor(self.ahead, **i32)
         self.local_pos0 = self.pos - self.local_len
         self.cache_ws = hb.alloc_workspace(256, device)
-        self.ws, self.ws_k = hb.alloc_workspace(hb.workspace_bytes(hb.OP_CACHE_ATTEND, self.desc), device), 0
+        need = hb.workspace_bytes(hb.OP_CACHE_ATTEND, self.desc)
+        if need == 0 or hb.workspace_bytes(hb.OP_CACHE, hb.CacheDesc(B=B, ld=DH, **self.cache_desc)) == 0 or not eps > 0:
+            raise ValueError("sizes, a cache_scale or an eps that the library's calls do not take")
+        self.ws, self.ws_k = hb.alloc_workspace(need, device), 0
 
     def _there(self, b):
         if not 0 <= b < self.B:                          # -1 would name the last one here and no row of the page table there

@@ -244,3 +244,11 @@ def test_sequences_that_are_not_there(calls, b):
         with pytest.raises(ValueError, match="no sequence"):
             f(b)
     assert len(calls) == n and p.lens == [1, 1, 1]
+
+
+@pytest.mark.parametrize("kw", [dict(cache_scale=0.0), dict(cache_scale=2.0**61), dict(page_rows=65537), dict(max_rows=2**31 - 1, page_rows=65536),
+                                dict(window=-1), dict(eps=0.0)])
+def test_what_no_call_would_take_is_refused_at_once(calls, kw):
+    # not by the first append, when pages have changed hands
+    with pytest.raises(ValueError, match="do not take"):
+        layer(**kw)
