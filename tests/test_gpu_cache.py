@@ -958,3 +958,211 @@ def test_a_sequence_begins_behind_its_own_rows(bits4):
             assert (out[b].double() - want).abs().max() < 0.1 * want.abs().max(), (n, b)
             at[b] += 1
     assert p.status() == 0 and p.lens == [25, 0, 10]
+
+
+# ------------------------------------------------------------------------------------
+# how near the combine's outputs are by norm, and what an f32 output keeps of a weight
+# ------------------------------------------------------------------------------------
+def wanted(c, b, j):
+    """Query row j of sequence b in f64, [H, Dh]."""
+    t, n, p0 = int(c["t0"][b]) + j, int(c["len"][b]), int(c["pos0"][b])
+    loc = [s for s in range(n) if 0 <= t - (p0 + s) < c["window"]]
+    seen = c["lens"][b] if c["L"] == 1 else max(0, min(c["lens"][b], (t + 1) // 4))
+    i = torch.arange(seen, device="cuda")
+    if c["I"] is not None:
+        i = c["I"][b, j].long()
+        i = i[(i >= 0) & (i < seen)]
+    v = torch.cat([c["local"][b, loc].double(), pool_rows(c["pool"], c["scales"], c["g"])[slots(c["table"], b, i, c["page"])]])
+    z = c["q"][b, j].double() @ v.t() * c["Dh"] ** -0.5
+    return torch.softmax(torch.cat([z, c["sinks"].double()[:, None]], -1), -1)[:, :-1] @ v
+
+
+@pytest.mark.parametrize("H,q", [(64, "bf16"), (64, "f32"), (16, "bf16"), (16, "f32"), (8, "bf16")])
+@pytest.mark.parametrize("lens,L,select", [([70, 0, 130], 1, 0), ([70, 5, 130], 3, 0), ([900, 400], 1, 200), ([2000, 600], 1, 512), ([9000, 5000], 1, 0)])
+@pytest.mark.parametrize("cache", ["4bit", "bf16"])
+def test_attend_f32_output_by_norm(H, q, lens, L, select, cache):
+    # Twice the 2e-6 of an output's norm that the header gives for 64 bf16 heads (f32 sums of the tensor cores, cut off by up to 2^-23 at
+    # each of some 70 steps over 512 rows and a window, half of that in the mean and of a sum that grows). Weights
+    # rounded to bf16 alone are 0.6e-3 to 1e-3 off.
+    c = attend_case(lens, L, H, cache, q, 16, select, seed=8)
+    out, ws = run_attend(c, "f32")
+    assert hb.device_status(ws) == 0
+    for b in range(c["B"]):
+        for j in range(L):
+            want = wanted(c, b, j)
+            assert (out[b, j].double() - want).norm() <= 4e-6 * want.norm(), (b, j)
+
+
+@pytest.mark.parametrize("H,q", [(64, "bf16"), (64, "f32"), (16, "bf16"), (8, "bf16")])
+@pytest.mark.parametrize("cache", ["4bit", "bf16"])
+def test_attend_f32_output_takes_all_of_a_weight(H, q, cache):
+    # Two rows: the first has a logit of (h + 1) scale for head h and one dim, the second a logit of 0 and the other dims, all ones, so
+    # that an output is w / (1 + w) there, w = exp(-(h + 1) scale), and 1 / (1 + w) in the first dim. The products are exact.
+    # The exponent's argument, up to 4.1 in log2 units, carries 4 roundings (scale, log2 e, their product, the sum): 4 * 4.1 ln 2 u
+    # = 6.8e-7 of w; the exponential 2^-22; sums, quotient and product 5 u; three sums of planes 2^-23 each: 1.6e-6 in all, below
+    # 2^-19. Weights as two bf16 planes would be up to 5e-6 off.
+    c = attend_case([2], 1, H, cache, q, 16, window=0, W=0, g=1.0)
+    at = slots(c["table"], 0, torch.arange(2, device="cuda"), 16)
+    rows = torch.zeros((2, c["Dh"]), device="cuda")
+    rows[0, 0] = rows[1, 1:] = 1.0
+    if cache == "bf16":
+        c["pool"].view(-1, c["Dh"])[at] = rows.to(torch.bfloat16)
+    else:
+        codes = (rows * 2).to(torch.uint8)                       # code 2 is 1
+        c["pool"].view(-1, c["Dh"] // 2)[at] = codes[:, ::2] | codes[:, 1::2] << 4
+        c["scales"].view(-1, c["Dh"] // 16)[at] = 0x38
+    h = torch.arange(1, H + 1, device="cuda", dtype=torch.float64)
+    c["q"].zero_()
+    c["q"][0, 0, :, 0] = h.to(DT[q])
+    out, ws = run_attend(c, "f32", sinks=None)
+    assert hb.device_status(ws) == 0
+    w = torch.exp(-h * c["Dh"] ** -0.5)
+    if H == 64:
+        two = w.float()
+        for _ in range(2):
+            two = two - two.bfloat16().float()
+        assert (two / w).abs().max() > 2.0**-18                 # the inputs tell two planes from three
+    want = torch.where(torch.arange(c["Dh"], device="cuda") == 0, (1 / (1 + w))[:, None], (w / (1 + w))[:, None])
+    assert ((out[0, 0].double() - want).abs() <= 2.0**-19 * want).all(), ((out[0, 0].double() - want).abs() / want).max().item()
+
+
+@pytest.mark.parametrize("H,q", [(64, "f32"), (16, "bf16"), (16, "f32"), (8, "bf16"), (8, "f32")])
+@pytest.mark.parametrize("lens,L,select", [([130, 64, 1, 0, 200], 1, 0), ([70, 5], 3, 40), ([5000, 3], 1, 0)])
+@pytest.mark.parametrize("cache", ["4bit", "bf16"])
+def test_attend_bf16_output_is_the_f32_one_rounded(H, q, lens, L, select, cache):
+    # on CUDA cores weights and sums are f32 whatever the output's type
+    c = attend_case(lens, L, H, cache, q, 16, select, seed=9)
+    assert torch.equal(run_attend(c, "bf16")[0], run_attend(c, "f32")[0].bfloat16())
+
+
+# ------------------------------------------------------------------------------------
+# calls that nothing above makes
+# ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("D,dims,first", [(512, 64, 448), (512, 512, 0), (320, 128, 96), (272, 32, 240), (128, 64, 64), (1024, 128, 512), (272, 28, 5)])
+@pytest.mark.parametrize("cache", ["4bit", "bf16"])
+@pytest.mark.parametrize("src", ["bf16", "f32"])
+def test_append_halves_with_a_norm(D, dims, first, cache, src):
+    n, page = 150, 48
+    x, w = randn((n, D), src, 1, 2.0), 1 + randn((D,), "f32", 2, 0.3)
+    table, pages = page_tables([n + 7], 5, page)
+    pool, scales = empty_pool(pages, page, D, cache)
+    d = append_desc(x, pool, 1, 5, page, cache, 1, dims, first, 1, mscale=1.25)
+    ws = workspace(hb.OP_CACHE, d)
+    hb.cache_append(d, table_of(dims), x, w, ints([0, n], torch.int64), ints([7]), table, pool, scales, ws)
+    assert hb.device_status(ws) == 0
+    i = torch.arange(7, n + 7, device="cuda")
+    check_appended(x, w, 1, 4 * i, dims, first, 1, 1.25, pool, scales, slots(table, 0, i, page), 0.75)
+
+
+@pytest.mark.parametrize("power", [-60, 60])
+@pytest.mark.parametrize("like", [True, False])
+def test_append_cache_scale(power, like):
+    # factors at the ends of their range: rows of their size, and rows of size 1, which saturate or vanish
+    x = randn((40, 128), "f32", 3) * (2.0**power if like else 1.0)
+    table, pages = page_tables([40], 2, 32)
+    pool, scales = empty_pool(pages, 32, 128, "4bit")
+    d = append_desc(x, pool, 1, 2, 32, "4bit", 0, 64, 64, g=2.0**power)
+    ws = workspace(hb.OP_CACHE, d)
+    hb.cache_append(d, table_of(64), x, None, ints([0, 40], torch.int64), ints([0]), table, pool, scales, ws)
+    i = torch.arange(40, device="cuda")
+    check_appended(x, None, 0, 4 * i, 64, 64, 0, 1.0, pool, scales, slots(table, 0, i, 32), 2.0**power)
+
+
+def moved(t, by=16):
+    """The same tensor `by` bytes past where it would begin."""
+    skip = by // t.element_size()
+    u = torch.empty(t.numel() + skip, device="cuda", dtype=t.dtype)[skip:].view(t.shape)
+    u.copy_(t)
+    assert u.data_ptr() % 32 == by % 32
+    return u
+
+
+@pytest.mark.parametrize("H,q", [(64, "bf16"), (64, "f32"), (16, "bf16"), (8, "f32")])
+@pytest.mark.parametrize("cache", ["4bit", "bf16"])
+def test_attend_tensors_16_bytes_on(H, q, cache):
+    c = attend_case([300, 0, 70], 1, H, cache, q, 16, 40)
+    want, _ = run_attend(c, "f32")
+    d = dict(c, **{k: moved(c[k]) for k in ("q", "local", "pool")}, scales=None if c["scales"] is None else moved(c["scales"]))
+    out, ws = run_attend(d, "f32", out=moved(torch.full_like(want, NAN)))
+    assert hb.device_status(ws) == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("D", [512, 1024, 48])
+@pytest.mark.parametrize("cache,out", [("4bit", "f32"), ("4bit", "bf16"), ("4bit", "e4m3"), ("bf16", "f32"), ("bf16", "bf16")])
+def test_rows_16_bytes_on(D, cache, out):
+    n, page = 100, 16
+    table, pages = page_tables([n], 7, page)
+    off, first = ints([0, n], torch.int64), ints([0])
+    got = []
+    for at in (lambda t: t, moved):
+        x = at(randn((n, D), "bf16", 4))
+        pool, scales = empty_pool(pages, page, D, cache)
+        pool, scales = at(pool), None if scales is None else at(scales)
+        d = append_desc(x, pool, 1, 7, page, cache, 1, 16, 16)
+        ws = workspace(hb.OP_CACHE, d)
+        hb.cache_append(d, table_of(16), x, None, off, first, table, pool, scales, ws)
+        rows = at(torch.zeros((n, D), device="cuda").to(DT[out]))
+        r = hb.CacheDesc(pages=pages, page_rows=page, D=D, cache_dtype=CODE[cache], cache_scale=0.75, B=1, table_cols=7, rows=n, ld=D,
+                         io_dtype=CODE[out])
+        hb.cache_read(r, off, first, table, pool, scales, rows, ws)
+        assert hb.device_status(ws) == 0 and (rows.float() != 0).any()
+        got.append(rows.float())
+    assert torch.equal(*got)
+
+
+def test_chained_calls():
+    # calls that may overlap the end of the one before them give the same bits
+    c = attend_case([300, 0, 70], 1, 64, "4bit", "bf16", 16)
+    e = attend_case([300, 0, 70], 1, 16, "bf16", "f32", 16)
+    x, pos = randn((4, 9, 512), "bf16", 1), positions(4)
+    rows, tab, off, first = randn((2, 512), "bf16", 4), c["table"][:2].contiguous(), ints([0, 1, 2], torch.int64), ints([299, 0])
+    tab[1, 0] = c["table"][2, 0]
+    got = []
+    for flags in (0, hb.FLAG_CHAINED):
+        y, read, pool, scales = torch.zeros_like(x), torch.zeros((2, 512), device="cuda"), c["pool"].clone(), c["scales"].clone()
+        ad, rd = append_desc(rows, pool, 2, c["cols"], 16, "4bit", 1, 64, 448), append_desc(read, pool, 2, c["cols"], 16, "4bit")
+        ad.flags = rd.flags = flags
+        ws = workspace(hb.OP_CACHE, ad)
+        turns = table_of(64)
+        run_norm_rope(x, y, pos, 64, 448, flags=flags)
+        hb.cache_append(ad, turns, rows, None, off, first, tab, pool, scales, ws)
+        hb.cache_read(rd, off, first, tab, pool, scales, read, ws)
+        a, ws2 = run_attend(dict(c, pool=pool, scales=scales), "f32", flags=flags)
+        b, ws3 = run_attend(e, "f32", flags=flags)
+        assert hb.device_status(ws) == hb.device_status(ws2) == hb.device_status(ws3) == 0
+        got.append((y, read, pool, scales, a, b))
+    for u, v in zip(*got):
+        assert torch.equal(u, v)
+
+
+def test_paged_decode_combines_what_the_selection_names():
+    # the step's selection, then a layer's decode over the rows it names; bounds as in test_a_sequence_begins_behind_its_own_rows
+    import os
+    import sys
+
+    import deepseek_sparse_attention_hisa_gb300 as pkg
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(pkg.__file__))), "examples"))
+    from paged_decode import normed, turn
+
+    from deepseek_sparse_attention_hisa_gb300 import inputs
+    from deepseek_sparse_attention_hisa_gb300.paged import DH, H, PagedDecode
+    from deepseek_sparse_attention_hisa_gb300.problem import Problem
+    B, hidden = 3, 512
+    prob = Problem(inputs.generate(inputs.WORKLOADS["ragged_decode"].replace(B=B, Np_range=(1024, 2000), with_attention=False, seed=31)))
+    prob.block_means()
+    prob.hisa_step()
+    have = [int(n) for n in prob.Np]
+    w = {"norm": 1 + randn((hidden,), "f32", 1, 0.1), "q": randn((hidden, H * DH), "bf16", 2, hidden**-0.5),
+         "kv": randn((hidden, DH), "bf16", 3, hidden**-0.5), "sinks": None, "q_norm": 1 + randn((DH,), "f32", 5, 0.1), "kv_norm": None}
+    p = PagedDecode(B, w, [4 * n for n in have], 2, pages=100, max_rows=2000, recent=randn((B, 127, DH), "bf16", 6))
+    p.append(randn((sum(have), DH), "bf16", 7, 2.0), have)
+    out = p.step(randn((B, hidden), "bf16", 8), randn((B, hidden), "bf16", 9), prob.I)
+    assert p.status() == 0 and prob.status() == 0
+    q = normed((p.act @ w["q"]).view(B, H, DH), w["q_norm"])
+    for b in range(B):
+        ids = prob.I[b].long()
+        assert (ids >= 0).all() and (ids < have[b]).all() and len(set(ids.tolist())) == 512
+        v = torch.cat([p.local[b, :128].double(), p.rows(b, torch.float32).double()[ids]])
+        pr = torch.softmax(turn(q[b], 4 * have[b], 1).to(torch.bfloat16).double() @ v.t() / math.sqrt(DH), -1)
+        want = turn(pr @ v, 4 * have[b], -1)
+        assert (out[b].double() - want).abs().max() < 0.1 * want.abs().max()
