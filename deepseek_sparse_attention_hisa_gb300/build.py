@@ -56,14 +56,14 @@ KERNEL_SOURCES = {
     "k_attend_tc": ["k_attend_tc.cu", "hisa_internal.cuh", "tc_ptx.cuh"],
     "k_score_pipe": ["k_score_pipe.cu", "pipe_common.cuh", "select_core.cuh", "hisa_internal.cuh", "tc_ptx.cuh"],
     "k_score_gemm": ["k_score_gemm.cu", "hisa_internal.cuh", "tc_ptx.cuh"],
-    "k_norm": ["k_norm.cu", "ops_internal.cuh", "heads_apart.h", "hisa_internal.cuh", "tc_ptx.cuh"],
-    "k_rope": ["k_rope.cu", "ops_internal.cuh", "heads_apart.h", "hisa_internal.cuh"],
-    "k_prefix": ["k_prefix.cu", "prefix_common.cuh", "ops_internal.cuh", "heads_apart.h", "hisa_internal.cuh", "tc_ptx.cuh"],
-    "k_prefix_tc": ["k_prefix_tc.cu", "prefix_common.cuh", "ops_internal.cuh", "heads_apart.h", "hisa_internal.cuh", "tc_ptx.cuh"],
-    "k_norm_rope": ["k_norm_rope.cu", "head_rows.cuh", "cache_internal.cuh", "cache_cuts.h", "ops_internal.cuh", "heads_apart.h", "hisa_internal.cuh"],
-    "k_cache_rows": ["k_cache_rows.cu", "head_rows.cuh", "cache_internal.cuh", "cache_cuts.h", "ops_internal.cuh", "heads_apart.h", "hisa_internal.cuh"],
-    "k_cache": ["k_cache.cu", "cache_internal.cuh", "cache_cuts.h", "ops_internal.cuh", "heads_apart.h", "hisa_internal.cuh"],
-    "k_cache_tc": ["k_cache_tc.cu", "cache_internal.cuh", "cache_cuts.h", "prefix_common.cuh", "ops_internal.cuh", "heads_apart.h", "hisa_internal.cuh", "tc_ptx.cuh"],
+    "k_norm": ["k_norm.cu", "ops_internal.cuh", "hisa_internal.cuh", "tc_ptx.cuh"],
+    "k_rope": ["k_rope.cu", "ops_internal.cuh", "hisa_internal.cuh"],
+    "k_prefix": ["k_prefix.cu", "prefix_common.cuh", "ops_internal.cuh", "hisa_internal.cuh", "tc_ptx.cuh"],
+    "k_prefix_tc": ["k_prefix_tc.cu", "prefix_common.cuh", "ops_internal.cuh", "hisa_internal.cuh", "tc_ptx.cuh"],
+    "k_norm_rope": ["k_norm_rope.cu", "head_rows.cuh", "cache_internal.cuh", "ops_internal.cuh", "hisa_internal.cuh"],
+    "k_cache_rows": ["k_cache_rows.cu", "head_rows.cuh", "cache_internal.cuh", "ops_internal.cuh", "hisa_internal.cuh"],
+    "k_cache": ["k_cache.cu", "cache_internal.cuh", "ops_internal.cuh", "hisa_internal.cuh"],
+    "k_cache_tc": ["k_cache_tc.cu", "cache_cuts.h", "cache_internal.cuh", "prefix_common.cuh", "ops_internal.cuh", "hisa_internal.cuh", "tc_ptx.cuh"],
 }
 
 

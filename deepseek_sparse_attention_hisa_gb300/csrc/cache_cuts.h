@@ -2,7 +2,6 @@
 // (k_cache_tc.cu) and the join of its parts have in common. Plain C++, so that the host can check it.
 #pragma once
 
-#include <cstddef>
 #include <cstdint>
 
 #ifdef __CUDACC__
@@ -20,8 +19,6 @@ struct Cut {
     int first, last;                                    // the CTAs that have its first and its last tile
     int place, pad[3];                                  // of the first CTA's sums
 };
-constexpr size_t kCutBytes = 32;
-static_assert(sizeof(Cut) == kCutBytes, "workspace layout");
 
 // The first tile of CTA c's span: c total / groups (a 64-bit division takes a few hundred cycles).
 HISA_HOST_DEVICE int64_t span_start(int c, int64_t total, int groups) {

@@ -2,7 +2,6 @@
 // appended and read back, the combine. Nothing here is part of the C ABI (see include/hisa.h).
 #pragma once
 
-#include "cache_cuts.h"
 #include "ops_internal.cuh"
 
 namespace hisa {
@@ -77,6 +76,7 @@ struct CacheAttnParams {
     uint32_t *status;
 };
 constexpr int kCacheCtas = kSmTarget;     // most CTAs of the tensor-core kernel
+constexpr size_t kCutBytes = 32;
 constexpr int kCacheTile = 48;            // its list rows per tile
 
 // What a query row sees: local rows [lo, lo + nloc) of its window buffer, then npool entries of its

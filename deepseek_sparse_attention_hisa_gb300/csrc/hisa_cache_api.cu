@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "cache_internal.cuh"
+#include "heads_apart.h"
 
 using namespace hisa;
 

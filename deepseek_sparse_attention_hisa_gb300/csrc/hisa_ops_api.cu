@@ -2,6 +2,7 @@
 // and kernel dispatch. Declarations and the contract live in include/hisa.h.
 #include <cmath>
 
+#include "heads_apart.h"
 #include "ops_internal.cuh"
 
 using namespace hisa;

@@ -3,10 +3,10 @@
 // A warp takes a chunk of up to 32 consecutive packed rows: each lane finds the place of one of
 // them (its sequence, its index, its page: three dependent loads, taken once per chunk), then teams of
 // lanes (head_rows.cuh) take the rows in turn, the next one on its way while one is worked on.
-// Reading is bound by memory: 65536 rows of 512 dims in 4 bits to f32 28 us, 5.6 TB/s. A call of a few rows is bound by its
+// Reading is bound by memory: 65536 rows of 512 dims in 4 bits to f32 26 to 30 us, 5.3 to 5.8 TB/s. A call of a few rows is bound by its
 // chain of loads (304 rows 4 to 5 us). Appending in 4 bits is bound by instructions: 440 of a warp per row of 512 dims (two
-// units of 8 per lane: the norm, the quotients with their remainders, 32 angles), 2.8 per cycle, 33 us for 65536 rows,
-// 2.6 TB/s.
+// units of 8 per lane: the norm, the quotients with their remainders, 32 angles), 2.9 per cycle, 65536 rows 36 us alone (2.4
+// TB/s), 41 one call after another.
 //
 // Append, 4 bits: sixteen dims are two neighbouring lanes' units; their largest magnitude is NaN if one of
 // them is. The quotient y / (s g) is a product with the reciprocal and one correction by its exact

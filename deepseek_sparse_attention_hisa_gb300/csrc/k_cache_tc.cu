@@ -25,8 +25,8 @@
 // rounding them, which adds up over the 32 steps of one. Outputs over 8 to 175 rows are 1.6e-6 to 1.9e-6 of their norm
 // off with one accumulator, 0.7e-6 to 1.1e-6 with two, below 0.9e-6 with four; those over 512 rows in one span 2.0e-6
 // with two and 1.6e-6 with four, most of it from the second product's sums, for which there is no room (f32 sums of the
-// plain formula: 0.5e-6 to 1e-6). 64 rows over up to 16384: 197 us, and 125 us with a bf16 output; 304 over 512
-// selected: 80 and 51.5. An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values
+// plain formula: 0.5e-6 to 1e-6). 64 rows over up to 16384: 200 us, and 125 us with a bf16 output; 304 over 512
+// selected: 80 and 51. An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values
 // too: what a large weight is off by then divides out (an output is 1.9e-3 to 2.0e-3 of its norm off, 2.3e-3 with a
 // normaliser of unrounded weights; the output's own rounding is 1.7e-3).
 //
@@ -36,13 +36,15 @@
 //
 // Bound by latency chains, not by a pipe: a tile takes 2600 cycles, of which the tensor core works 940, the row warps'
 // conversion of it 1800 (and 850 of waits), the softmax 1800; with two tiles under way neither hides the other wholly.
-// 64 rows over up to 16384: 125 us, 567 TFLOP/s, 36 % of the tensor pipe, 2.2 instructions per cycle. Without the
-// conversion and half of the products it still takes 111 us. 304 rows over 512 selected (a row per CTA, twice): 51.5 us,
-// 2.4 TB/s, of which a CTA's first tile, last tile and output take some 8 us per row.
+// 64 rows over up to 16384: 125 us (runs of one program 116 to 135), 567 TFLOP/s, 36 % of the tensor pipe, 2.2
+// instructions per cycle. Without the conversion and half of the products it still takes 111 us. 304 rows over 512
+// selected (a row per CTA, twice): 51 us, 2.4 TB/s, of which a CTA's first tile, last tile and output take some 8 us per
+// row.
 //
 // Warps: 0-7 softmax and epilogue, 8 S issue (and q by TMA), 9 PV issue, 10-11 places of the rows (ids, pages), up to
 // four tiles ahead, 12-23 rows: a lane has a row of the tile and an eighth of its dims, the next tile's codes on their
 // way while it writes this one's. Every wait is bounded; a timeout sets HISA_DEV_TIMEOUT and the CTA leaves.
+#include "cache_cuts.h"
 #include "cache_internal.cuh"
 #include "prefix_common.cuh"
 
@@ -81,6 +83,7 @@ struct Misc {
 };
 constexpr uint32_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+static_assert(sizeof(Cut) == kCutBytes, "workspace layout");
 
 __device__ __forceinline__ int local_tiles(const CacheRow &x) { return (x.nloc + kT - 1) / kT; }
 __device__ __forceinline__ int tiles_of(const CacheRow &x) {

@@ -2,7 +2,6 @@
 // shared-prefix combine). Nothing here is part of the C ABI (see include/hisa.h).
 #pragma once
 
-#include "heads_apart.h"
 #include "hisa_internal.cuh"
 
 namespace hisa {
