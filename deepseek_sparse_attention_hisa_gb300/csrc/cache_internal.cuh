@@ -72,12 +72,16 @@ struct CacheAttnParams {
     int ctas, whole;          // tensor-core kernel: CTAs; whole rows in turn, not spans of all rows' tiles
     void *cuts;               // its rows that spans cut: an entry per row (by_row) or per CTA
     int by_row;
+    int carries;              // a list may be long enough for sums to be carried
     float *part_o, *part_ml;  // partial sums
+    float *carry;             // tensor-core kernel: sums of long lists, kCarryFloats per CTA
     uint32_t *status;
 };
 constexpr int kCacheCtas = kSmTarget;     // most CTAs of the tensor-core kernel
 constexpr size_t kCutBytes = 32;
 constexpr int kCacheTile = 48;            // its list rows per tile
+constexpr int kCacheCarry = 16;           // its tiles after which an f32 output's sums move to memory
+constexpr size_t kCarryFloats = 64 * 512;
 
 // What a query row sees: local rows [lo, lo + nloc) of its window buffer, then npool entries of its
 // list of pooled rows (ids of I, or rows 0, 1, ...), of which those below V are visible.

@@ -108,12 +108,21 @@ void tc_plan(const hisa_cache_attn_desc *d, int64_t pool, bool ids, CacheAttnPar
     const int64_t n = p->whole ? rows : (best < (double)(rows * tiles) ? (int64_t)best : rows * tiles);
     p->ctas = (int)(n > kCacheCtas ? kCacheCtas : n);
     p->by_row = !p->whole && rows <= p->ctas;
+    p->carries = d->out_dtype == HISA_F32 && tiles > kCacheCarry;
 }
+// The workspace behind the status: rows that spans cut, their sums (maximum and normaliser, then outputs), sums carried.
+struct TcLayout {
+    size_t cuts, ml, o, carry;
+    explicit TcLayout(const CacheAttnParams &p)
+        : cuts(round_up(p.ctas * kCutBytes)), ml(round_up(places(p) * 64 * 2 * sizeof(float))), o(places(p) * kCarryFloats * sizeof(float)),
+          carry(p.carries ? p.ctas * kCarryFloats * sizeof(float) : 0) {}
+    static size_t places(const CacheAttnParams &p) { return p.whole ? 0 : (size_t)2 * p.ctas; }
+};
 size_t tc_bytes(const hisa_cache_attn_desc *d, int64_t pool, bool ids) {
     CacheAttnParams p{};
     tc_plan(d, pool, ids, &p);
-    const size_t places = p.whole ? 0 : (size_t)2 * p.ctas;
-    return kStatusBytes + round_up(p.ctas * kCutBytes) + round_up(places * d->H * 2 * sizeof(float)) + places * d->H * d->Dh * sizeof(float);
+    const TcLayout w(p);
+    return kStatusBytes + w.cuts + w.ml + w.o + w.carry;
 }
 size_t attn_sums(const hisa_cache_attn_desc *d, const CacheAttnParams &p) { return (size_t)d->B * d->L * d->H * p.splits; }
 size_t attn_bytes(const hisa_cache_attn_desc *d, int64_t pool) {
@@ -272,10 +281,11 @@ hisa_status hisa_cache_attend(const hisa_cache_attn_desc *d, const void *q, cons
     char *base = static_cast<char *>(ws) + kStatusBytes;
     if (cache_tc_supported(d->H, d->Dh, p.q_bf16)) {
         tc_plan(d, I ? d->k : d->Np_max, I != nullptr, &p);
+        const TcLayout w(p);
         p.cuts = base;
-        base += round_up(p.ctas * kCutBytes);
-        p.part_ml = reinterpret_cast<float *>(base);
-        p.part_o = reinterpret_cast<float *>(base + round_up((size_t)2 * p.ctas * d->H * 2 * sizeof(float)));
+        p.part_ml = reinterpret_cast<float *>(base + w.cuts);
+        p.part_o = reinterpret_cast<float *>(base + w.cuts + w.ml);
+        p.carry = reinterpret_cast<float *>(base + w.cuts + w.ml + w.o);
         return from_cuda(launch_cache_tc(p, reinterpret_cast<cudaStream_t>(stream)));
     }
     attn_plan(d, I ? d->k : d->Np_max, &p);

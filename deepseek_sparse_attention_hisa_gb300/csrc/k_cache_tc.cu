@@ -19,14 +19,21 @@
 // takes an equal span of them (p.whole: whole rows in turn, where all lists are as long). A row that lies in one span is
 // finished there; the sums of one that is cut go to memory, two places per CTA, and k_cache_join adds them up.
 //
+// The tensor core cuts its f32 sums off, by 1.8e-8 of a sum per product step in the mean, always towards zero: an output in
+// f32 would lose 8e-6 over 3000 rows in one span and 4e-4 over 200000. Its sums therefore move to memory every 16 tiles
+// and are added up there with rounding: 2.1e-6 to 2.6e-6 whatever the length. Every 8 tiles would give 1.2e-6 to 1.5e-6, but
+// 64 rows over up to 16384 take 239 us instead of 220 then and 304 over 512 selected 94 instead of 83 (202 and 80 if they
+// never moved). An output in bf16 takes a third of the steps and is rounded by up to 2^-8 in the end: its sums stay (2e-4
+// over 200000 rows in one span).
+//
 // An output in f32 takes all of a weight: P goes to the second product as three bf16 planes (the rounded value, the
 // rounding of what that leaves, and again), one after the other through the same buffer; two would leave 2^-18 of a
 // weight out. And its logits are sums of four accumulators of 128 dims: the tensor core cuts its f32 sums off instead of
 // rounding them, which adds up over the 32 steps of one. Outputs over 8 to 175 rows are 1.6e-6 to 1.9e-6 of their norm
-// off with one accumulator, 0.7e-6 to 1.1e-6 with two, below 0.9e-6 with four; those over 512 rows in one span 2.0e-6
-// with two and 1.6e-6 with four, most of it from the second product's sums, for which there is no room (f32 sums of the
-// plain formula: 0.5e-6 to 1e-6). 64 rows over up to 16384: 200 us, and 125 us with a bf16 output; 304 over 512
-// selected: 80 and 51. An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values
+// off with one accumulator, 0.7e-6 to 1.1e-6 with two, 0.9e-6 to 1.2e-6 with four; those over 512 rows and a window
+// in one span up to 2.6e-6, most of it from the second product's sums, for which there is no room (f32 sums of the
+// plain formula: 0.5e-6 to 1e-6). 64 rows over up to 16384: 220 us, and 125 us with a bf16 output; 304 over 512
+// selected: 83 and 51. An output in bf16 takes the rounded value alone, and its normaliser adds up the rounded values
 // too: what a large weight is off by then divides out (an output is 1.9e-3 to 2.0e-3 of its norm off, 2.3e-3 with a
 // normaliser of unrounded weights; the output's own rounding is 1.7e-3).
 //
@@ -79,7 +86,8 @@ struct Misc {
     int64_t sums[kThreads / 32];
     float alpha[kH];
     float top[4][kH], sum[4][kH];                       // of the four threads of a head
-    __align__(16) float factor[kH];
+    __align__(16) float factor[kH], back[kH];            // back: of the carried sums, which refer to the maximum base
+    float base[kH];
 };
 constexpr uint32_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -212,10 +220,50 @@ __device__ __forceinline__ void load32(const uint8_t *from, uint4 &a, uint4 &b) 
                  : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "l"(from));
 }
 
+// A list's sums so far, carried in memory: those in TMEM are put there, added to them, or take them up at the list's end. back: what a
+// head's carried sums are to be multiplied by. A softmax thread has its own part, four heads of a dim per access. A call, so
+// that its registers are not those of every tile.
+enum CarryStep : int { kPut, kAdd, kJoin };
+template <int STEP>
+__device__ __noinline__ void carry_sums(float *carry, const float *back, uint32_t tmem_o) {
+    const int side = threadIdx.x >> 7;
+#pragma unroll 1
+    for (int c = 0; c < 2 * kH; c += 16) {
+        float4 *at = reinterpret_cast<float4 *>(carry + blockIdx.x * kCarryFloats) + c / 4 * (32 * kSoftWarps) + threadIdx.x;
+        float4 was[4];
+        if (STEP != kPut) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) was[q] = __ldcg(at + q * (32 * kSoftWarps));
+        }
+        float o[16];
+        tmem_ld16(tmem_o + 2 * kH * side + c, o);
+        tmem_ld_wait();
+        if (STEP != kPut) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 f = *reinterpret_cast<const float4 *>(back + (c & (kH - 1)) + 4 * q);
+                o[4 * q] = fmaf(was[q].x, f.x, o[4 * q]);
+                o[4 * q + 1] = fmaf(was[q].y, f.y, o[4 * q + 1]);
+                o[4 * q + 2] = fmaf(was[q].z, f.z, o[4 * q + 2]);
+                o[4 * q + 3] = fmaf(was[q].w, f.w, o[4 * q + 3]);
+            }
+        }
+        if (STEP != kJoin) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) __stcg(at + q * (32 * kSoftWarps), make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
+        } else {
+            tmem_st16(tmem_o + 2 * kH * side + c, o);
+        }
+    }
+    if (STEP == kJoin) tmem_st_wait();
+}
+__device__ __forceinline__ float rescaled(float from, float to) { return from == to ? 1.f : ex2(from - to); }   // both -inf: sums of nothing
+
 template <bool BITS4, bool OUT32>
 __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant__ CUtensorMap qmap, CacheAttnParams p) {
     constexpr int kPlanes = OUT32 ? 3 : 1;               // of P
     constexpr int kSums = OUT32 ? 4 : 1, kBufs = OUT32 ? 1 : 2;   // accumulators of a logit; S buffers
+    constexpr int kCarry = kCacheCarry;                  // tiles after which sums move (OUT32)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -539,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
 #pragma unroll
                         for (int ks = 0; ks < kT / 16; ++ks)
                             mma_elected(tmem + kColO + mt * kH, vd + ((2 * mt * kChunk + ks * 2048) >> 4), vhi, plo + ((ks * 32) >> 4), phi, id_o,
-                                        ks > 0 || i > 0 || pl > 0, e);
+                                        ks > 0 || (OUT32 ? i % kCarry : i) > 0 || pl > 0, e);
                     if (pl == kPlanes - 1) mma_commit_warp(&misc->empty[s]);
                     mma_commit_warp(&misc->pfree);
                 }
@@ -570,6 +618,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
             have = walk_item(p, w_next, it_next);
             float m2 = -INFINITY, l = 0.f;                // l: this thread's rows
             for (int i = 0; i < it.T; ++i, ++g) {
+                if (OUT32 && i > 0 && i % kCarry == 0) {
+                    // the sums so far move to memory, and the next product begins anew
+                    if (part == 0) {
+                        if (i > kCarry) misc->back[h] = rescaled(misc->base[h], m2);
+                        misc->base[h] = m2;
+                    }
+                    if (!soft_all(good && wait_warp(&misc->pfree, (np - 1) & 1, abort))) { fail(); break; }
+                    fence_after_sync();
+                    if (i == kCarry) carry_sums<kPut>(p.carry, misc->back, quadrant + kColO);
+                    else carry_sums<kAdd>(p.carry, misc->back, quadrant + kColO);
+                }
                 const int sb = g % kBufs, e = g % kPlaces;
                 const bool pool = w.t0 + i >= it.nl;
                 const float c2 = pool ? cl * gp : cl;
@@ -612,8 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                     l *= alpha;
                     if (part == 0) misc->alpha[h] = alpha;
                     // O^T of this item so far, after the product of the tile before
-                    if (!soft_all(i < 1 || wait_warp(&misc->pfree, (np - 1) & 1, abort))) { fail(); break; }
-                    if (i > 0) {
+                    if (!soft_all((OUT32 ? i % kCarry : i) == 0 || wait_warp(&misc->pfree, (np - 1) & 1, abort))) { fail(); break; }
+                    if ((OUT32 ? i % kCarry : i) > 0) {
                         fence_after_sync();
 #pragma unroll 1
                         for (int c = 2 * kH * side; c < 2 * kH * (side + 1); c += 16) {
@@ -679,9 +738,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_tc(const __grid_constant_
                 const float wm = m2 == -INFINITY ? 0.f : ex2(m2 - M);
                 const float den = l * wm + (sink2 == -INFINITY ? 0.f : ex2(sink2 - M));
                 misc->factor[h] = den == 0.f ? 0.f : wm / den;           // nothing seen, no sink: 0
+                if (OUT32 && it.T > kCarry) misc->back[h] = rescaled(misc->base[h], m2);
             }
             soft_sync();
             fence_after_sync();
+            if (OUT32 && it.T > kCarry) carry_sums<kJoin>(p.carry, misc->back, quadrant + kColO);
             const bool cut = it.T < it.tiles;
             if (!cut) {
 #pragma unroll 1

@@ -625,7 +625,8 @@ HISA_API hisa_status hisa_cache_read(const hisa_cache_desc *desc, const int64_t 
  * row that sees nothing gives 0. Logits, weights, maxima and sums are f32; with bf16 q of 64 heads of 512
  * dims and a bf16 out each softmax weight is rounded to bf16 (by 2^-8 of it at most), in its product with
  * the values and in the normaliser; with an f32 out it is not, and what is left is the tensor cores' f32
- * sums, which are cut off rather than rounded (1e-6 to 2e-6 of an output's norm).
+ * sums, which are cut off rather than rounded (1e-6 to 3e-6 of an output's norm, whatever the
+ * lengths). A bf16 out's sums lose 1e-9 of themselves per row that they add up, 2e-4 over 200000.
  *   q          [B, L, H, Dh]  q_dtype (already roped)
  *   local_kv   [B, W_max, Dh] q_dtype (NULL if W_max is 0); local_len [B] int32 rows present
  *              (<= W_max); local_pos0 [B] int32 absolute position of local row 0

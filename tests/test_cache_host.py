@@ -323,3 +323,13 @@ def test_outputs_whose_heads_cross_are_refused(lib, tokens, heads, token, head):
     assert lib.hisa_rope(ctypes.byref(hb.RopeDesc(**kw)), FAKE, FAKE, FAKE, far, None, None, None) == EINVAL
     kw.update(x_token=token, x_head=token, y_head=token)   # in place, token after token at the same dims
     assert lib.hisa_rope(ctypes.byref(hb.RopeDesc(**kw)), FAKE, FAKE, FAKE, FAKE, None, None, None) == EINVAL
+
+
+def test_an_f32_output_of_long_lists_takes_more_workspace():
+    # 64 x 512 sums per CTA, where a list may have more than 16 tiles of 48 rows (the window's 3 among them)
+    build.build_library()
+    need = lambda n, out, B=304: hb.workspace_bytes(hb.OP_CACHE_ATTEND, attn_desc(  # noqa: E731
+        B=B, Np_max=n, k=0, table_cols=1 << 12, pages=1 << 12, out_dtype=out))
+    assert need(13 * 48, hb.HISA_F32) == need(13 * 48, hb.HISA_BF16)
+    assert need(13 * 48 + 1, hb.HISA_F32) == need(13 * 48 + 1, hb.HISA_BF16) + 152 * 64 * 512 * 4
+    assert need(1 << 17, hb.HISA_F32, 1) == need(1 << 17, hb.HISA_BF16, 1) + 152 * 64 * 512 * 4

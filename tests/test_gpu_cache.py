@@ -1166,3 +1166,91 @@ def test_paged_decode_combines_what_the_selection_names():
         pr = torch.softmax(turn(q[b], 4 * have[b], 1).to(torch.bfloat16).double() @ v.t() / math.sqrt(DH), -1)
         want = turn(pr @ v, 4 * have[b], -1)
         assert (out[b].double() - want).abs().max() < 0.1 * want.abs().max()
+
+
+# ------------------------------------------------------------------------------------
+# long lists in one span: what the tensor cores cut off does not add up
+# ------------------------------------------------------------------------------------
+def of_the_same_rows(c, B):
+    """Case c of one sequence for B queries over its pages, and three of them as a case of their own."""
+    d = dict(c, B=B, lens=c["lens"] * B)
+    d["q"] = randn((B, *c["q"].shape[1:]), c["qt"], 77, 2.0)
+    for k in ("local", "len", "pos0", "t0", "count", "table"):
+        d[k] = c[k].expand(B, *c[k].shape[1:]).contiguous()
+    if c["I"] is not None:
+        d["I"] = c["I"].expand(B, *c["I"].shape[1:]).contiguous()
+    pick = [0, B // 2, B - 1]
+    some = dict(d, B=3, lens=c["lens"] * 3, **{k: d[k][pick] for k in ("q", "local", "len", "pos0", "t0", "count", "table")})
+    return d, some, pick
+
+
+@pytest.mark.parametrize("B,n", [(160, 600), (160, 769), (160, 3000), (160, 12000), (16, 100000)])
+@pytest.mark.parametrize("cache", ["4bit", "bf16"])
+def test_attend_f32_output_by_norm_of_long_lists(B, n, cache):
+    # as test_attend_f32_output_by_norm: the 3e-6 of the header, and a third of it again. Sums that stayed in the tensor cores' accumulators
+    # would be 8e-6 off over 3000 rows.
+    c, some, pick = of_the_same_rows(attend_case([n], 1, 64, cache, "bf16", 64, seed=3), B)
+    out, ws = run_attend(c, "f32")
+    assert hb.device_status(ws) == 0
+    for j, b in enumerate(pick):
+        want = wanted(some, j, 0)
+        assert (out[b, 0].double() - want).norm() <= 4e-6 * want.norm(), b
+
+
+@pytest.mark.parametrize("cache", ["4bit", "bf16"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("most", [6.0, 60.0])
+def test_attend_large_logits_that_grow_over_long_lists(cache, out, most):
+    # the running maximum moves between sums that are put by, also by more than f32's exponents span
+    c = attend_case([4000], 1, 64, cache, "bf16", 64, window=0, q_std=1.0)
+    grow = torch.linspace(0.1, most, 4000, device="cuda")
+    at = slots(c["table"], 0, torch.arange(4000, device="cuda"), 64)
+    base = randn((512,), "f32", 3)
+    if cache == "bf16":
+        c["pool"].view(-1, 512)[at] = (base * grow[:, None]).to(torch.bfloat16)
+    else:
+        c["scales"].view(-1, 32)[at] = (grow[:, None] / 6).to(torch.float8_e4m3fn).expand(-1, 32).contiguous().view(torch.uint8)
+    c, some, pick = of_the_same_rows(c, 160)
+    got, ws = run_attend(c, out)
+    assert hb.device_status(ws) == 0
+    check_attend(some, got[pick], out, weight=2.0**-22 if out == "f32" else None)
+    again, _ = run_attend(c, out, ws=ws)
+    assert torch.equal(again, got)
+
+
+def test_attend_sums_that_see_nothing_yet():
+    # long lists whose first tiles are skipped ids: what is put by is nothing, and what comes later counts
+    c = attend_case([3000], 1, 64, "4bit", "bf16", 64, select=2500, window=0)
+    c["I"][0, 0, :2000] = -1
+    c, some, pick = of_the_same_rows(c, 160)
+    some["I"] = c["I"][pick]
+    out, ws = run_attend(c, "f32")
+    assert hb.device_status(ws) == 0
+    for j, b in enumerate(pick):
+        want = wanted(some, j, 0)
+        assert (out[b, 0].double() - want).norm() <= 4e-6 * want.norm(), b
+    c["I"].fill_(-1)
+    assert (run_attend(c, "f32", sinks=None)[0] == 0).all()
+
+
+@pytest.mark.parametrize("H,q", [(64, "bf16")])
+def test_attend_two_graphs_share_a_workspace(H, q):
+    # two captured calls of different shapes, one workspace, replayed in turn
+    a, _, _ = of_the_same_rows(attend_case([2000], 1, H, "4bit", q, 64, seed=3), 20)
+    b = attend_case([700, 30, 5000], 1, H, "bf16", q, 16, seed=4)
+    want = [run_attend(c, "f32")[0] for c in (a, b)]
+    out = [torch.zeros_like(w) for w in want]
+    ws = max((run_attend(c, "f32")[1] for c in (a, b)), key=lambda t: t.numel())
+    torch.cuda.synchronize()
+    graphs = []
+    for c, o in zip((a, b), out):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run_attend(c, "f32", ws=ws, out=o)
+        graphs.append(g)
+    for _ in range(3):
+        for g, o, w in zip(graphs, out, want):
+            o.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, w)
