@@ -67,6 +67,8 @@ class PagedDecode:
         self.ahead = [x.shape[0] for x in recent]
         self._order()
         self.capacity = self.top + steps
+        if any(t + self.capacity - n > 2**31 for t, n in zip(starts, self.ahead)):
+            raise ValueError("positions from 0 to 2^31 - 1 expected, for as many tokens as the window buffer takes")
         self.local = torch.zeros((B, self.capacity, DH), **bf16)
         for b, x in enumerate(recent):
             self.local[b, :x.shape[0]] = x

@@ -252,3 +252,12 @@ def test_what_no_call_would_take_is_refused_at_once(calls, kw):
     # not by the first append, when pages have changed hands
     with pytest.raises(ValueError, match="do not take"):
         layer(**kw)
+
+
+def test_positions_end_with_the_window_buffer(calls):
+    # the third sequence has room for two tokens more than steps, once the others have given their places to new ones
+    far, before = [9, 9, 2**31 - 4], [kv_rows(2), kv_rows(2), kv_rows(0)]
+    with pytest.raises(ValueError, match="positions"):
+        layer(start=far, recent=before)
+    layer(start=[9, 9, 2**31 - 6], recent=before)
+    layer(start=far)
